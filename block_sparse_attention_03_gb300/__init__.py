@@ -27,7 +27,8 @@ DTYPES = {"bf16": 0, "fp8": 1, "nvfp4": 2}
 # every symbol include/msa.h declares
 EXPORTS = ("msa_workspace_size", "msa_workspace_init", "msa_indexer_score", "msa_topk_blocks",
            "msa_sparse_attend", "msa_decode", "msa_read_device_status", "msa_status_string",
-           "msa_dequant_debug", "msa_decode_noalloc", "msa_cache_insert")
+           "msa_dequant_debug", "msa_decode_noalloc", "msa_cache_insert", "msa_dense_workspace_size",
+           "msa_dense_attend", "msa_rope_init", "msa_rope_insert", "msa_build_tables")
 
 
 class MsaError(RuntimeError):
@@ -73,6 +74,23 @@ class MsaQueryT(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("dtype", ctypes.c_int), ("scale", ctypes.c_float)]
 
 
+ROPE_LAYOUTS = {"halves": 0, "adjacent": 1}  # msa_rope_layout_t
+
+
+class MsaRopeT(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("axes", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("axis", ctypes.c_uint8 * 64), ("turns", ctypes.c_uint64 * 64)]
+
+
+class MsaRowsT(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("stride", ctypes.c_int64)]
+
+
+class MsaQkNormT(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("index_q", ctypes.c_void_p),
+                ("index_k", ctypes.c_void_p), ("eps", ctypes.c_float), ("offset", ctypes.c_float)]
+
+
 _lib_handle = None
 
 
@@ -98,8 +116,15 @@ def lib() -> ctypes.CDLL:
         h.msa_dequant_debug.argtypes = [P, ctypes.c_int32, P, ctypes.c_int32, P, P]
         h.msa_decode_noalloc.argtypes = [P, P, P, P, P, ctypes.c_int32, P, P, P, P, P]
         h.msa_cache_insert.argtypes = [P, ctypes.c_int32, P, P, P, P, P, ctypes.c_size_t, P]
+        I = ctypes.c_int32
+        h.msa_dense_workspace_size.restype = ctypes.c_size_t
+        h.msa_dense_workspace_size.argtypes = [P, P, I]
+        h.msa_dense_attend.argtypes = [P, P, P, P, I, P, P, P, ctypes.c_size_t, P]
+        h.msa_rope_init.argtypes = [P, I, ctypes.c_double, I, P, I]
+        h.msa_rope_insert.argtypes = [P, P, I, P, P, I, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P]
+        h.msa_build_tables.argtypes = [I, I, P, P, I, P, I, P, P, P, P, P, I, P, P, P, ctypes.c_size_t, P]
         for name in EXPORTS:
-            if name != "msa_workspace_size" and name != "msa_status_string":
+            if name not in ("msa_workspace_size", "msa_status_string", "msa_dense_workspace_size"):
                 getattr(h, name).restype = ctypes.c_int
         _lib_handle = h
     return _lib_handle
@@ -192,8 +217,34 @@ class Query:
         return MsaQueryT(_ptr(self.data), DTYPES[self.dtype], self.scale)
 
 
+@dataclasses.dataclass
+class QkNorm:
+    """bf16 [128] weights of the per-head RMS norm before the rotation (None: that kind is not normed)."""
+    q: object = None
+    k: object = None
+    index_q: object = None
+    index_k: object = None
+    eps: float = 1e-6
+    offset: float = 0.0   # the norm multiplies by offset + weight
+
+    def struct(self) -> MsaQkNormT:
+        return MsaQkNormT(_ptr(self.q), _ptr(self.k), _ptr(self.index_q), _ptr(self.index_k), self.eps, self.offset)
+
+
 def _ref(x):
     return ctypes.byref(x)
+
+
+def _rows(t, heads: int, tokens: int, where: str) -> Optional[MsaRowsT]:
+    """Rows of a projection: [tokens][heads][128] (or [tokens][128] for one head), the heads side by side."""
+    if t is None:
+        return None
+    shape, strides = tuple(t.shape), t.stride()
+    if len(shape) == 2 and heads == 1:
+        shape, strides = (shape[0], 1, shape[1]), (strides[0], 128, strides[1])
+    if shape != (tokens, heads, 128) or strides[2] != 1 or (heads > 1 and strides[1] != 128):
+        raise MsaError(1, where)
+    return MsaRowsT(t.data_ptr(), strides[0])
 
 
 # ---------------------------------------------------------------- entry points (same names as the C ABI)
@@ -281,12 +332,79 @@ def msa_cache_insert(cache, slot_mapping, k, v, index_k, workspace, stream=None)
                                   _stream(stream)), "msa_cache_insert")
 
 
+def msa_dense_workspace_size(cache: PagedCache, batch: Batch, num_q_heads: int) -> int:
+    c, b = cache.struct(), batch.struct()
+    n = lib().msa_dense_workspace_size(_ref(c), _ref(b), num_q_heads)
+    if n == 0:
+        raise MsaError(1, "msa_dense_workspace_size")
+    return int(n)
+
+
+def msa_dense_attend(cache, batch, cfg, q: Query, num_q_heads: int, out, lse, workspace, stream=None) -> None:
+    """Attention of each new token (up to 8 a sequence) over its whole sequence in the paged cache."""
+    c, b, f, qq = cache.struct(), batch.struct(), cfg.struct(), q.struct()
+    _check(lib().msa_dense_attend(_ref(c), _ref(b), _ref(f), _ref(qq), num_q_heads, _ptr(out), _ptr(lse),
+                                  _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)),
+           "msa_dense_attend")
+
+
+def msa_rope_init(rotary_dim: int, theta: float, sections=None, layout: str = "halves") -> MsaRopeT:
+    """Rotary positions with one axis, or with len(sections) axes of sections[a] frequency pairs each."""
+    sections = [rotary_dim // 2] if sections is None else list(sections)
+    r = MsaRopeT()
+    arr = (ctypes.c_int32 * max(1, len(sections)))(*sections)
+    _check(lib().msa_rope_init(_ref(r), rotary_dim, theta, len(sections), arr, ROPE_LAYOUTS.get(layout, -1)),
+           "msa_rope_init")
+    return r
+
+
+def msa_rope_insert(cache, rope: MsaRopeT, positions, slot_mapping, q, q_out: Query, index_q, index_q_out: Optional[Query],
+                    k, v, index_k, norm: Optional[QkNorm], workspace, stream=None) -> None:
+    """Norm and rotate q, index q, k and index k (bf16 [T][heads][128], any token stride), write the
+    queries to q_out / index_q_out and k, v, index k into the paged caches at slot_mapping (int32 [T]).
+    positions: int32 [axes][T], or [T] for one axis."""
+    where = "msa_rope_insert"
+    T, H = int(slot_mapping.numel()), cache.num_kv_heads
+    if positions.numel() != rope.axes * T or not positions.is_contiguous() or q.dim() != 3:
+        raise MsaError(1, where)
+    hq = q.shape[1]
+    if q_out.data.numel() != T * hq * 128 or not q_out.data.is_contiguous() or \
+            (index_q_out is not None and (index_q_out.data.numel() != T * H * 128 or not index_q_out.data.is_contiguous())):
+        raise MsaError(1, where)
+    c, qo = cache.struct(), q_out.struct()
+    rows = [_rows(q, hq, T, where), _rows(index_q, H, T, where), _rows(k, H, T, where), _rows(v, H, T, where),
+            _rows(index_k, 1, T, where)]
+    io = None if index_q_out is None else index_q_out.struct()
+    n = None if norm is None else norm.struct()
+    ref = [None if x is None else _ref(x) for x in rows + [io, n]]
+    _check(lib().msa_rope_insert(_ref(c), _ref(rope), T, _ptr(positions), _ptr(slot_mapping), hq, ref[0], _ref(qo), ref[1],
+                                 ref[5], ref[2], ref[3], ref[4], ref[6], _ptr(workspace),
+                                 workspace.numel() * workspace.element_size(), _stream(stream)), where)
+
+
+def msa_build_tables(num_blocks: int, cached_lens, new_lens, block_table, free_blocks, free_count, seq_lens, token_offsets,
+                     slot_mapping, positions, free_count_out, workspace, stream=None) -> None:
+    """Block tables, lengths, slots and positions of a step from the requests' lengths (all int32 on the
+    device): block_table [S][max_blocks] and the stack free_blocks are updated in place; seq_lens [S],
+    token_offsets [S + 1], slot_mapping and positions [max_tokens] and free_count_out [1] are written."""
+    S = cached_lens.numel()
+    if new_lens.numel() != S or block_table.dim() != 2 or block_table.shape[0] != S or seq_lens.numel() != S or \
+            token_offsets.numel() != S + 1 or positions.numel() != slot_mapping.numel() or not block_table.is_contiguous():
+        raise MsaError(1, "msa_build_tables")
+    _check(lib().msa_build_tables(S, num_blocks, _ptr(cached_lens), _ptr(new_lens), block_table.shape[1], _ptr(block_table),
+                                  free_blocks.numel(), _ptr(free_blocks), _ptr(free_count), _ptr(free_count_out),
+                                  _ptr(seq_lens), _ptr(token_offsets), slot_mapping.numel(), _ptr(slot_mapping),
+                                  _ptr(positions), _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                  _stream(stream)), "msa_build_tables")
+
+
 def default_config(topk: int = 16, head_dim: int = 128, index_dim: int = 128) -> Config:
     """The model's settings: index and softmax scales head_dim ** -0.5."""
     return Config(topk=topk, index_scale=index_dim ** -0.5, sm_scale=head_dim ** -0.5)
 
 
-__all__ = ["PagedCache", "Batch", "Config", "Query", "MsaError", "lib", "EXPORTS", "default_config",
+__all__ = ["PagedCache", "Batch", "Config", "Query", "QkNorm", "MsaError", "lib", "EXPORTS", "default_config",
            "msa_workspace_size", "msa_workspace_init", "msa_indexer_score", "msa_topk_blocks",
            "msa_sparse_attend", "msa_decode", "msa_read_device_status", "msa_status_string",
-           "msa_dequant_debug", "msa_decode_noalloc", "msa_cache_insert", "roofline"]
+           "msa_dequant_debug", "msa_decode_noalloc", "msa_cache_insert", "msa_dense_workspace_size", "msa_dense_attend",
+           "msa_rope_init", "msa_rope_insert", "msa_build_tables", "roofline"]

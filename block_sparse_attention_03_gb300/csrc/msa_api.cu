@@ -59,6 +59,24 @@ bool encode_rows(CUtensorMap* m, const void* base, long rows, bool bf16) {
   return r == CUDA_SUCCESS;
 }
 
+// The dense attend's maps: rows of 128 elements of an FP8 (128 B), BF16 (256 B, in
+// boxes of 128 B) or NVFP4 (64 B) cache; a box holds the rows of one unit, each
+// under the swizzle of its width (conflict-free ldmatrix).
+bool encode_unit_rows(CUtensorMap* m, const void* base, long rows, int fmt) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const bool bf16 = fmt == FMT_BF16, fp4 = fmt == FMT_NVFP4;
+  cuuint64_t dims[2] = {fp4 ? 64ull : 128ull, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {bf16 ? 256ull : (fp4 ? 64ull : 128ull)};
+  cuuint32_t box[2] = {bf16 || fp4 ? 64u : 128u, (cuuint32_t)dense_unit_keys(fmt)};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult r = fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
+                  const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  fp4 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 // ---------------------------------------------------------------- checks
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -529,6 +547,81 @@ msa_status_t run_k2q(const msa_cache_t* c, const msa_batch_t* b, const msa_confi
   return MSA_OK;
 }
 
+// ---------------------------------------------------------------- the dense attend
+
+struct DensePlan {
+  int cols = 0, CG = 0, rows = 0;
+  size_t off_info = 0, off_ml = 0, off_o = 0, total = 0;
+};
+
+msa_status_t make_dense_plan(const msa_cache_t* c, const msa_batch_t* b, int hq, DensePlan& pl) {
+  const int G = c->num_kv_heads;
+  if (hq < G || hq % G != 0) return MSA_ERR_INVALID_ARGUMENT;
+  if (hq / G > 64 || b->q_per_seq > 8) return MSA_ERR_UNSUPPORTED;
+  pl.cols = b->q_per_seq * (hq / G);
+  pl.rows = dense_rows(dense_nt(pl.cols));
+  pl.CG = (pl.cols + pl.rows - 1) / pl.rows;
+  if ((long)b->num_seqs * G * pl.CG >= (1l << 31)) return MSA_ERR_UNSUPPORTED;
+  const size_t ctas = (size_t)sm_count();
+  size_t o = 256;  // the status word
+  pl.off_info = o; o = align256(o + ctas * sizeof(int2));
+  pl.off_ml = o; o = align256(o + 2 * ctas * pl.rows * sizeof(float2));
+  pl.off_o = o; o = align256(o + 2 * ctas * pl.rows * kDim * sizeof(float));
+  pl.total = o;
+  return MSA_OK;
+}
+
+msa_status_t run_dense(const msa_cache_t* c, const msa_batch_t* b, const msa_config_t* cfg, const msa_query_t* q, int hq,
+                       void* out, float* lse, const DensePlan& pl, void* ws, cudaStream_t st) {
+  const int G = c->num_kv_heads, fmt = fmt_of(c->kv_dtype), sms = sm_count();
+  const long rows = (long)c->num_blocks * G * kBlock;
+  CUtensorMap tk, tv;
+  if (!encode_unit_rows(&tk, c->k, rows, fmt) || !encode_unit_rows(&tv, c->v, rows, fmt)) return MSA_ERR_CUDA;
+  DenseParams p;
+  p.S = b->num_seqs;
+  p.Q = b->q_per_seq;
+  p.G = G;
+  p.r = hq / G;
+  p.cols = pl.cols;
+  p.CG = pl.CG;
+  p.max_nb = b->max_blocks_per_seq;
+  p.num_blocks = c->num_blocks;
+  p.seq_lens = b->seq_lens;
+  p.block_table = b->block_table;
+  p.q = q->data;
+  p.q_fp8 = q->dtype == MSA_DTYPE_FP8_E4M3;
+  p.q_scale = p.q_fp8 ? q->scale : 1.f;
+  p.col_const = cfg->sm_scale * 1.4426950408889634f * (fmt == FMT_NVFP4 ? c->k_global : 1.f);
+  p.k_sc = static_cast<const uint8_t*>(fmt == FMT_FP8 ? static_cast<const void*>(c->k_scale) : c->k_sf);
+  p.v_sc = static_cast<const uint8_t*>(fmt == FMT_FP8 ? static_cast<const void*>(c->v_scale) : c->v_sf);
+  p.v_global = c->v_global;
+  p.info = at<int2>(ws, pl.off_info);
+  p.part_ml = at<float2>(ws, pl.off_ml);
+  p.part_o = at<float>(ws, pl.off_o);
+  p.out = out;
+  p.lse = lse;
+  p.status = at<DeviceStatus>(ws, 0);
+  cudaError_t e;
+  if (fmt == FMT_BF16) e = launch_dense_bf16(&tk, &tv, p, sms, st);
+  else if (fmt == FMT_FP8) e = launch_dense_fp8(&tk, &tv, p, sms, st);
+  else e = launch_dense_nvfp4(&tk, &tv, p, sms, c->nvfp4_mode == MSA_NVFP4_E4M3_PRODUCT, st);
+  if (e != cudaSuccess) return MSA_ERR_CUDA;
+  return cuda_status(launch_dense_combine(p, fmt != FMT_BF16, sms, st));
+}
+
+msa_status_t check_rope(const msa_rope_t* r) {
+  if (!r) return MSA_ERR_INVALID_ARGUMENT;
+  if (r->rotary_dim < 16 || r->rotary_dim > kDim || r->rotary_dim % 16 != 0) return MSA_ERR_UNSUPPORTED;
+  if (r->axes < 1 || r->axes > MSA_ROPE_MAX_AXES) return MSA_ERR_UNSUPPORTED;
+  if (r->layout != MSA_ROPE_HALVES && r->layout != MSA_ROPE_ADJACENT) return MSA_ERR_INVALID_ARGUMENT;
+  for (int i = 0; i < r->rotary_dim / 2; ++i)
+    if (r->axis[i] >= r->axes) return MSA_ERR_INVALID_ARGUMENT;
+  return MSA_OK;
+}
+
+// rows of one projection: tokens `stride` elements apart, heads side by side
+bool rows_ok(const msa_rows_t* r) { return r && r->data && aligned16(r->data) && r->stride >= 0 && r->stride % 8 == 0; }
+
 }  // namespace
 
 // ====================================================================== C ABI
@@ -673,6 +766,169 @@ msa_status_t msa_cache_insert(const msa_cache_t* cache, int32_t num_tokens, cons
   p.ig = cache->idx_global;
   p.status = static_cast<DeviceStatus*>(workspace);
   return cuda_status(launch_insert(p, sm_count(), (cudaStream_t)stream));
+}
+
+size_t msa_dense_workspace_size(const msa_cache_t* cache, const msa_batch_t* batch, int32_t num_q_heads) {
+  DensePlan pl;
+  if (check_batch(batch) != MSA_OK || check_cache(cache, false, false) != MSA_OK ||
+      make_dense_plan(cache, batch, num_q_heads, pl) != MSA_OK)
+    return 0;
+  return pl.total;
+}
+
+msa_status_t msa_dense_attend(const msa_cache_t* cache, const msa_batch_t* batch, const msa_config_t* cfg,
+                              const msa_query_t* q, int32_t num_q_heads, void* out, float* lse, void* workspace,
+                              size_t workspace_bytes, msa_stream_t stream) {
+  msa_status_t s;
+  if ((s = check_batch(batch)) != MSA_OK || (s = check_cfg(cfg)) != MSA_OK || (s = check_cache(cache, false, true)) != MSA_OK ||
+      (s = check_query(q)) != MSA_OK)
+    return s;
+  if (!out || !workspace || !aligned16(out) || !aligned16(workspace)) return MSA_ERR_INVALID_ARGUMENT;
+  DensePlan pl;
+  if ((s = make_dense_plan(cache, batch, num_q_heads, pl)) != MSA_OK) return s;
+  if (workspace_bytes < pl.total) return MSA_ERR_WORKSPACE_TOO_SMALL;
+  return run_dense(cache, batch, cfg, q, num_q_heads, out, lse, pl, workspace, (cudaStream_t)stream);
+}
+
+msa_status_t msa_rope_init(msa_rope_t* rope, int32_t rotary_dim, double theta, int32_t axes, const int32_t* sections,
+                           int32_t layout) {
+  if (!rope || !sections || !(theta > 0.0) || !std::isfinite(theta)) return MSA_ERR_INVALID_ARGUMENT;
+  if (axes < 1 || axes > MSA_ROPE_MAX_AXES || rotary_dim < 16 || rotary_dim > kDim || rotary_dim % 16 != 0)
+    return MSA_ERR_UNSUPPORTED;
+  std::memset(rope, 0, sizeof(*rope));
+  rope->rotary_dim = rotary_dim;
+  rope->axes = axes;
+  rope->layout = layout;
+  const int pairs = rotary_dim / 2;
+  int i = 0;
+  for (int a = 0; a < axes; ++a) {
+    if (sections[a] < 0 || sections[a] > pairs - i) return MSA_ERR_INVALID_ARGUMENT;
+    for (int k = 0; k < sections[a]; ++k) rope->axis[i++] = (uint8_t)a;
+  }
+  if (i != pairs) return MSA_ERR_INVALID_ARGUMENT;
+  for (i = 0; i < pairs; ++i) {
+    double turns = std::pow(theta, -2.0 * i / rotary_dim) / 6.283185307179586476925;
+    turns -= std::floor(turns);  // whole turns change nothing (theta < 1)
+    rope->turns[i] = (uint64_t)std::ldexp(turns, 64);
+  }
+  return check_rope(rope);
+}
+
+msa_status_t msa_rope_insert(const msa_cache_t* cache, const msa_rope_t* rope, int32_t num_tokens,
+                             const int32_t* positions, const int32_t* slot_mapping, int32_t num_q_heads,
+                             const msa_rows_t* q, const msa_query_t* q_out, const msa_rows_t* index_q,
+                             const msa_query_t* index_q_out, const msa_rows_t* k, const msa_rows_t* v,
+                             const msa_rows_t* index_k, const msa_qk_norm_t* norm, void* workspace,
+                             size_t workspace_bytes, msa_stream_t stream) {
+  msa_status_t s;
+  if ((s = check_cache(cache, index_k != nullptr, true)) != MSA_OK || (s = check_rope(rope)) != MSA_OK) return s;
+  if (num_tokens < 0 || !workspace) return MSA_ERR_INVALID_ARGUMENT;
+  if (workspace_bytes < 256) return MSA_ERR_WORKSPACE_TOO_SMALL;
+  if (num_q_heads < 1 || num_q_heads > 1024) return MSA_ERR_UNSUPPORTED;
+  if (num_tokens == 0) return MSA_OK;
+  if (!positions || !slot_mapping || !rows_ok(q) || !rows_ok(k) || !rows_ok(v) || (index_q && !rows_ok(index_q)) ||
+      (index_k && !rows_ok(index_k)) || (index_q != nullptr) != (index_q_out != nullptr))
+    return MSA_ERR_INVALID_ARGUMENT;
+  if ((s = check_query(q_out)) != MSA_OK || (index_q && (s = check_query(index_q_out)) != MSA_OK)) return s;
+  RopeParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.rope = *rope;
+  p.num_tokens = num_tokens;
+  p.Hq = num_q_heads;
+  p.H = cache->num_kv_heads;
+  p.Giq = index_q ? cache->num_kv_heads : 0;
+  p.Gik = index_k ? 1 : 0;
+  p.num_blocks = cache->num_blocks;
+  p.kv_fmt = fmt_of(cache->kv_dtype);
+  p.idx_fmt = index_k ? fmt_of(cache->index_dtype) : FMT_BF16;
+  p.positions = positions;
+  p.slots = slot_mapping;
+  p.q = static_cast<const __nv_bfloat16*>(q->data);
+  p.q_stride = q->stride;
+  p.k = static_cast<const __nv_bfloat16*>(k->data);
+  p.k_stride = k->stride;
+  p.v = static_cast<const __nv_bfloat16*>(v->data);
+  p.v_stride = v->stride;
+  if (index_q) {
+    p.iq = static_cast<const __nv_bfloat16*>(index_q->data);
+    p.iq_stride = index_q->stride;
+    p.iq_out = static_cast<uint8_t*>(const_cast<void*>(index_q_out->data));
+    p.iq_fp8 = index_q_out->dtype == MSA_DTYPE_FP8_E4M3;
+    p.iq_inv = p.iq_fp8 ? 1.f / index_q_out->scale : 1.f;
+  }
+  if (index_k) {
+    p.ik = static_cast<const __nv_bfloat16*>(index_k->data);
+    p.ik_stride = index_k->stride;
+  }
+  p.q_out = static_cast<uint8_t*>(const_cast<void*>(q_out->data));
+  p.q_fp8 = q_out->dtype == MSA_DTYPE_FP8_E4M3;
+  p.q_inv = p.q_fp8 ? 1.f / q_out->scale : 1.f;
+  if (!std::isfinite(p.q_inv) || !std::isfinite(p.iq_inv)) return MSA_ERR_INVALID_ARGUMENT;
+  if (norm) {
+    const void* w[4] = {norm->q, norm->index_q, norm->k, norm->index_k};
+    if (!(norm->eps >= 0.f) || !std::isfinite(norm->eps) || !std::isfinite(norm->offset)) return MSA_ERR_INVALID_ARGUMENT;
+    for (int i = 0; i < 4; ++i) {
+      if (w[i] && !aligned16(w[i])) return MSA_ERR_INVALID_ARGUMENT;
+      p.w[i] = static_cast<const __nv_bfloat16*>(w[i]);
+      p.norm |= w[i] != nullptr;
+    }
+    p.eps = norm->eps;
+    p.w_offset = norm->offset;
+  }
+  // the insert writes through the cache's pointers
+  p.kc = static_cast<uint8_t*>(const_cast<void*>(cache->k));
+  p.vc = static_cast<uint8_t*>(const_cast<void*>(cache->v));
+  p.ic = static_cast<uint8_t*>(const_cast<void*>(cache->idx));
+  p.ks = const_cast<float*>(cache->k_scale);
+  p.vs = const_cast<float*>(cache->v_scale);
+  p.is = const_cast<float*>(cache->idx_scale);
+  p.ksf = static_cast<uint8_t*>(const_cast<void*>(cache->k_sf));
+  p.vsf = static_cast<uint8_t*>(const_cast<void*>(cache->v_sf));
+  p.isf = static_cast<uint8_t*>(const_cast<void*>(cache->idx_sf));
+  p.kg = cache->k_global;
+  p.vg = cache->v_global;
+  p.ig = cache->idx_global;
+  p.status = static_cast<DeviceStatus*>(workspace);
+  return cuda_status(launch_rope(p, sm_count(), (cudaStream_t)stream));
+}
+
+msa_status_t msa_build_tables(int32_t num_seqs, int32_t num_blocks, const int32_t* cached_lens, const int32_t* new_lens,
+                              int32_t max_blocks_per_seq, int32_t* block_table, int32_t free_capacity,
+                              int32_t* free_blocks, const int32_t* free_count, int32_t* free_count_out,
+                              int32_t* seq_lens, int32_t* token_offsets, int32_t max_tokens, int32_t* slot_mapping,
+                              int32_t* positions, void* workspace, size_t workspace_bytes, msa_stream_t stream) {
+  if (num_seqs < 1 || num_blocks < 1 || max_blocks_per_seq < 1 || free_capacity < 0 || max_tokens < 0)
+    return MSA_ERR_INVALID_ARGUMENT;
+  if (num_seqs > kMaxTableSeqs || (long)num_blocks * kBlock >= (1l << 31) || (long)max_blocks_per_seq * kBlock > (1l << 30) ||
+      free_capacity >= (1 << 30) || max_tokens >= (1 << 30))
+    return MSA_ERR_UNSUPPORTED;
+  if (!cached_lens || !new_lens || !block_table || !free_count || !free_count_out || !seq_lens || !token_offsets ||
+      !workspace || (free_capacity > 0 && !free_blocks) || (max_tokens > 0 && (!slot_mapping || !positions)))
+    return MSA_ERR_INVALID_ARGUMENT;
+  // the CTAs read the inputs while others write the outputs
+  if (free_count_out == free_count || seq_lens == cached_lens || seq_lens == new_lens || token_offsets == cached_lens ||
+      token_offsets == new_lens)
+    return MSA_ERR_INVALID_ARGUMENT;
+  if (workspace_bytes < 256) return MSA_ERR_WORKSPACE_TOO_SMALL;
+  TablesParams p;
+  p.num_seqs = num_seqs;
+  p.num_blocks = num_blocks;
+  p.max_nb = max_blocks_per_seq;
+  p.free_cap = free_capacity;
+  p.max_tokens = max_tokens;
+  p.cached = cached_lens;
+  p.fresh = new_lens;
+  p.block_table = block_table;
+  p.free_blocks_in = free_blocks;
+  p.free_blocks = free_blocks;
+  p.free_count = free_count;
+  p.free_count_out = free_count_out;
+  p.seq_lens = seq_lens;
+  p.offsets = token_offsets;
+  p.slots = slot_mapping;
+  p.positions = positions;
+  p.status = static_cast<DeviceStatus*>(workspace);
+  return cuda_status(launch_tables(p, sm_count(), (cudaStream_t)stream));
 }
 
 msa_status_t msa_read_device_status(void* workspace, msa_stream_t stream, int32_t* detail) {

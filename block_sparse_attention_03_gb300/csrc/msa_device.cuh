@@ -22,6 +22,7 @@ constexpr uint32_t FLAG_BAD_BLOCK = 1u << 0;    // block-table entry outside the
 constexpr uint32_t FLAG_BAD_SEQLEN = 1u << 1;   // seq_len outside [q_per_seq, max_blocks*128]
 constexpr uint32_t FLAG_BAD_SELECT = 1u << 2;   // selected block the query cannot see
 constexpr uint32_t FLAG_TIMEOUT = 1u << 3;      // a bounded wait gave up
+constexpr uint32_t FLAG_NO_ROOM = 1u << 4;      // a request's blocks or token places are not there
 
 struct DeviceStatus {
   uint32_t flags;

@@ -224,7 +224,82 @@ struct InsertParams {
   DeviceStatus* status;
 };
 
+// Dense attend over the whole cache (msa_dense.cuh).
+struct DenseParams {
+  int32_t S, Q, G, r;         // sequences, new tokens each, KV heads, q heads per KV head
+  int32_t cols, CG;           // Q x r query columns of a (sequence, KV head), in CG groups of rows(NT) columns
+  int32_t max_nb, num_blocks;
+  const int32_t* seq_lens;
+  const int32_t* block_table;
+  const void* q;              // [S*Q][G*r][128] bf16 or e4m3 codes
+  int32_t q_fp8;
+  float q_scale;
+  float col_const;            // sm_scale * log2(e) (x NVFP4 K per-tensor scale)
+  const uint8_t* k_sc;        // per-token fp32 scales (FP8) or e4m3 group scales (NVFP4)
+  const uint8_t* v_sc;
+  float v_global;             // NVFP4 V per-tensor scale
+  int2* info;                 // [CTAs] (sequence x G x CG + group) the run begins in, 1: it began before the run
+  float* part_o;              // [2 x CTAs][rows][128] partials of cut segments
+  float2* part_ml;            // [2 x CTAs][rows] running max (log2 domain), sum
+  void* out;                  // bf16 [S*Q][G*r][128]
+  float* lse;
+  DeviceStatus* status;
+};
+// tiles of 16 query columns an instance takes (0: up to 8 columns), and the rows of its partials
+inline int dense_nt(int cols) { return cols <= 8 ? 0 : cols <= 16 ? 1 : cols <= 32 ? 2 : 4; }
+inline int dense_rows(int nt) { return nt == 0 ? 8 : 16 * nt; }
+// keys (rows of a tensor-copy box) a unit holds
+inline int dense_unit_keys(int fmt) { return fmt == FMT_BF16 ? 64 : 128; }
+
+// Rotary insert (msa_rope.cu).
+struct RopeParams {
+  msa_rope_t rope;
+  int32_t num_tokens, Hq, Giq, H, Gik;  // tokens; q, index q, K (and V), index K heads (0: none)
+  int32_t num_blocks, kv_fmt, idx_fmt;
+  int32_t chunks;                        // warps a token's rows are spread over (set by the launcher)
+  const int32_t* positions;              // [axes][num_tokens]
+  const int32_t* slots;                  // [num_tokens], < 0: no insert
+  const __nv_bfloat16 *q, *iq, *k, *v, *ik;
+  int64_t q_stride, iq_stride, k_stride, v_stride, ik_stride;  // elements between tokens
+  uint8_t *q_out, *iq_out;               // [num_tokens][heads][128] bf16 or e4m3 codes
+  int32_t q_fp8, iq_fp8;
+  float q_inv, iq_inv;                   // 1 / per-tensor scale
+  int32_t norm;
+  const __nv_bfloat16* w[4];             // norm weights of q, index q, k, index k (null: none)
+  float eps, w_offset;
+  uint8_t *kc, *vc, *ic;
+  float *ks, *vs, *is;
+  uint8_t *ksf, *vsf, *isf;
+  float kg, vg, ig;
+  DeviceStatus* status;
+};
+
+// Block tables from request lengths (msa_tables.cu).
+struct TablesParams {
+  int32_t num_seqs, num_blocks, max_nb, free_cap, max_tokens;
+  const int32_t* cached;          // [S] tokens in the cache
+  const int32_t* fresh;           // [S] tokens new, -1: the request has ended
+  int32_t* block_table;           // [S][max_nb]
+  const int32_t* free_blocks_in;  // [free_cap] the stack (same memory as free_blocks)
+  int32_t* free_blocks;
+  const int32_t* free_count;
+  int32_t* free_count_out;
+  int32_t* seq_lens;              // [S]
+  int32_t* offsets;               // [S + 1]
+  int32_t* slots;                 // [max_tokens]
+  int32_t* positions;             // [max_tokens]
+  DeviceStatus* status;
+};
+constexpr int kMaxTableSeqs = 8192;  // four sums a request in shared memory
+
 // launchers (return cudaGetLastError())
+cudaError_t launch_rope(RopeParams p, int num_sms, cudaStream_t st);
+cudaError_t launch_tables(const TablesParams& p, int num_sms, cudaStream_t st);
+cudaError_t launch_dense_bf16(const CUtensorMap* tk, const CUtensorMap* tv, const DenseParams& p, int num_sms, cudaStream_t st);
+cudaError_t launch_dense_fp8(const CUtensorMap* tk, const CUtensorMap* tv, const DenseParams& p, int num_sms, cudaStream_t st);
+cudaError_t launch_dense_nvfp4(const CUtensorMap* tk, const CUtensorMap* tv, const DenseParams& p, int num_sms,
+                               bool round_e4m3, cudaStream_t st);
+cudaError_t launch_dense_combine(const DenseParams& p, bool f16p, int num_sms, cudaStream_t st);
 cudaError_t launch_insert(const InsertParams& p, int num_sms, cudaStream_t st);
 cudaError_t launch_k2q_build(const K2qParams& p, int num_sms, cudaStream_t st);    // count, scan, fill
 cudaError_t launch_k2q_attend(const CUtensorMap* tk, const CUtensorMap* tv, const K2qParams& p, int num_sms,

@@ -1,0 +1,215 @@
+// Block tables, slot maps, positions and lengths of a step, from the requests'
+// lengths and a stack of free blocks, in one launch and without the host.
+//
+// With c_s tokens cached and n_s new (n_s = -1: the request has ended):
+//   wants_s = ceil((c_s + n_s) / 128) - ceil(c_s / 128)   blocks it takes
+//   back_s  = ceil(c_s / 128) if it has ended             blocks it gives back
+// and three exclusive sums over the requests (tokens, wants, back) say where each
+// one's tokens, new blocks and returned blocks lie.  The returned blocks go on
+// top of the stack in the requests' order, the new ones come off its top in the
+// same order: the i-th block taken is the stack's entry total - 1 - i.
+//
+// Latency is all there is (some kilobytes): every CTA computes the sums by
+// itself in shared memory, so there is no second launch and no wait between
+// CTAs, and then takes its share of the tokens, new blocks and returned blocks,
+// finding the request of each by bisection.  A new token's slot is computed from
+// the stack, not read from the table entry another CTA writes.
+#include "msa_device.cuh"
+#include "msa_internal.h"
+
+namespace msa {
+
+namespace {
+
+constexpr int kTabThreads = 512;
+
+// Exclusive sums in place of three arrays of n values (n <= kMaxTableSeqs); the
+// totals land at [n].  Summed in 64 bits and clamped at kMost when stored (past
+// any count that can be granted), so that no set of lengths wraps around.
+constexpr long kMost = 1l << 30;
+
+__device__ void scan3(int* a, int* b, int* c, int n, long* warp_sums) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (n + kTabThreads - 1) / kTabThreads;
+  const int i0 = min(n, tid * per), i1 = min(n, i0 + per);
+  long v[3] = {0, 0, 0};
+  for (int i = i0; i < i1; ++i) {
+    v[0] += a[i];
+    v[1] += b[i];
+    v[2] += c[i];
+  }
+  long x[3] = {v[0], v[1], v[2]};
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const long t = __shfl_up_sync(0xffffffffu, x[k], o);
+      if (lane >= o) x[k] += t;
+    }
+  if (lane == 31)
+#pragma unroll
+    for (int k = 0; k < 3; ++k) warp_sums[k * 32 + warp] = x[k];
+  __syncthreads();
+  long base[3];
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    base[k] = x[k] - v[k];
+    long all = 0;
+    for (int w = 0; w < kTabThreads / 32; ++w) {
+      const long t = warp_sums[k * 32 + w];
+      if (w < warp) base[k] += t;
+      all += t;
+    }
+    if (tid == 0) (k == 0 ? a : k == 1 ? b : c)[n] = (int)min(all, kMost);
+  }
+  for (int i = i0; i < i1; ++i) {
+    const int ta = a[i], tb = b[i], tc = c[i];
+    a[i] = (int)min(base[0], kMost);
+    b[i] = (int)min(base[1], kMost);
+    c[i] = (int)min(base[2], kMost);
+    base[0] += ta;
+    base[1] += tb;
+    base[2] += tc;
+  }
+  __syncthreads();
+}
+
+// The last s with at[s] <= x (at: n + 1 exclusive sums, at[0] = 0 <= x < at[n]); among equal sums the one that holds x.
+__device__ __forceinline__ int owner(const int* at, int n, int x) {
+  int lo = 0, hi = n;  // at[lo] <= x < at[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (at[mid] <= x) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ int blocks_of(int t) { return (t + kBlock - 1) / kBlock; }
+
+__global__ void __launch_bounds__(kTabThreads) tables_kernel(const TablesParams p) {
+  extern __shared__ int sm[];
+  __shared__ long warp_sums[96];
+  __shared__ int s_taken;
+  const int S = p.num_seqs, tid = threadIdx.x;
+  int* tok = sm;               // [S + 1] first token of each request
+  int* want = tok + S + 1;     // [S + 1] first new block
+  int* back = want + S + 1;    // [S + 1] first returned block
+  int* cached = back + S + 1;  // [S] -1: malformed
+  const long limit = (long)p.max_nb * kBlock;
+  if (tid == 0) s_taken = 0;
+  for (int s = tid; s < S; s += kTabThreads) {
+    const int c = __ldg(p.cached + s), n = __ldg(p.fresh + s);
+    const bool good = c >= 0 && n >= -1 && (long)c + max(n, 0) <= limit;
+    if (!good && blockIdx.x == 0) raise_flag(p.status, FLAG_BAD_SEQLEN, s);
+    const int add = good ? max(n, 0) : 0;
+    cached[s] = good ? c : -1;
+    tok[s] = add;
+    want[s] = add > 0 ? blocks_of(c + add) - blocks_of(c) : 0;
+    back[s] = good && n < 0 ? blocks_of(c) : 0;
+  }
+  __syncthreads();
+  scan3(tok, want, back, S, warp_sums);
+  const int count = min(max(__ldg(p.free_count), 0), p.free_cap);
+  const int room = p.free_cap - count;
+  if (blockIdx.x == 0 && tid == 0 && count != __ldg(p.free_count)) raise_flag(p.status, FLAG_BAD_BLOCK, count);
+  const int given = min(back[S], room);  // returned blocks the stack has room for
+  const int total = count + given;
+  // the blocks taken: those of the requests that are granted, a prefix of all
+  // (a request is granted if its blocks are there and its tokens have places)
+  for (int s = tid; s < S; s += kTabThreads)
+    if (want[s + 1] <= total && tok[s + 1] <= p.max_tokens) atomicMax(&s_taken, want[s + 1]);
+  __syncthreads();
+  const int taken = s_taken;
+  const int gtid = blockIdx.x * kTabThreads + tid, gn = gridDim.x * kTabThreads;
+
+  // the i-th block taken; -1 (and the flag) if the stack names a block outside the pool
+  auto stack_at = [&](int i) -> int {
+    const int at = total - 1 - i;
+    int b;
+    if (at < count) {
+      b = __ldg(p.free_blocks_in + at);
+    } else {
+      const int r = at - count, s = owner(back, S, r);
+      b = p.block_table[(size_t)s * p.max_nb + (r - back[s])];
+    }
+    if (b < 0 || b >= p.num_blocks) {
+      raise_flag(p.status, FLAG_BAD_BLOCK, b);
+      return -1;
+    }
+    return b;
+  };
+  auto granted = [&](int s) { return want[s + 1] <= total && tok[s + 1] <= p.max_tokens; };
+
+  // lengths and token offsets
+  for (int s = gtid; s < S; s += gn) {
+    const int add = tok[s + 1] - tok[s];
+    const int c = cached[s];
+    const bool ends = back[s + 1] > back[s] || (c >= 0 && __ldg(p.fresh + s) < 0);
+    int len = c < 0 || ends ? 0 : c;
+    if (add > 0) {
+      if (granted(s)) len = c + add;
+      else raise_flag(p.status, FLAG_NO_ROOM, s);
+    }
+    p.seq_lens[s] = len;
+    p.offsets[s] = tok[s];
+  }
+  if (gtid == 0) {
+    p.offsets[S] = tok[S];
+    *p.free_count_out = total - taken;
+    if (back[S] > room) raise_flag(p.status, FLAG_NO_ROOM, -1);
+  }
+  // slots and positions of the new tokens, padding behind them
+  for (int t = gtid; t < p.max_tokens; t += gn) {
+    int slot = -1, pos = 0;
+    if (t < tok[S]) {
+      const int s = owner(tok, S, t);
+      const int c = cached[s];
+      pos = c + (t - tok[s]);
+      if (granted(s)) {
+        const int b = pos / kBlock, had = blocks_of(c);
+        int blk;
+        if (b < had) {
+          blk = p.block_table[(size_t)s * p.max_nb + b];
+          if (blk < 0 || blk >= p.num_blocks) {
+            raise_flag(p.status, FLAG_BAD_BLOCK, blk);
+            blk = -1;
+          }
+        } else {
+          blk = stack_at(want[s] + b - had);
+        }
+        if (blk >= 0) slot = blk * kBlock + pos % kBlock;
+      }
+    }
+    p.slots[t] = slot;
+    p.positions[t] = pos;
+  }
+  // the new blocks into the tables
+  for (int i = gtid; i < taken; i += gn) {
+    const int s = owner(want, S, i);
+    p.block_table[(size_t)s * p.max_nb + blocks_of(cached[s]) + (i - want[s])] = stack_at(i);
+  }
+  // the returned blocks that stay on the stack (entries at and above `count`:
+  // nothing reads those in this call)
+  for (int r = gtid; r < min(given, total - taken - count); r += gn) {
+    const int s = owner(back, S, r);
+    p.free_blocks[count + r] = p.block_table[(size_t)s * p.max_nb + (r - back[s])];
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_tables(const TablesParams& p, int num_sms, cudaStream_t st) {
+  const size_t smem = ((size_t)p.num_seqs * 4 + 3) * sizeof(int);
+  cudaError_t e = cudaFuncSetAttribute(tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  // a CTA's sums cost as much as some thousand tokens' slots: four tokens a thread
+  const long work = p.max_tokens > p.num_seqs ? p.max_tokens : p.num_seqs;
+  long grid = (work + 4 * kTabThreads - 1) / (4 * kTabThreads);
+  if (grid > num_sms) grid = num_sms;
+  if (grid < 1) grid = 1;
+  tables_kernel<<<(unsigned)grid, kTabThreads, smem, st>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace msa

@@ -279,6 +279,130 @@ msa_status_t msa_cache_insert(const msa_cache_t* cache, int32_t num_tokens, cons
                               const void* k, const void* v, const void* index_k, void* workspace,
                               size_t workspace_bytes, msa_stream_t stream);
 
+/* Dense attend: the layers of the model that select no blocks.  For query head
+ * h of KV head g = h / (num_q_heads / num_kv_heads), exact softmax attention over
+ * every visible key of the sequence, logits scaled by cfg->sm_scale (the only
+ * field of cfg it reads; the others must be valid).
+ * q, out, lse: as in msa_sparse_attend.  q_per_seq <= 8 and num_q_heads /
+ * num_kv_heads <= 64, else MSA_ERR_UNSUPPORTED.
+ * Lengths: seq_lens[s] from 0 up.  0 is a padding row of the batch: out 0, lse
+ * -inf.  With 0 < seq_lens[s] < q_per_seq the first new tokens sit at negative
+ * positions, see no key, and get out 0, lse -inf.  A length below 0 or beyond
+ * max_blocks_per_seq * 128 raises the device fault flag; its rows get out 0, lse
+ * -inf.  A block-table entry outside the pool is flagged and its keys are left
+ * out.  Entries past a sequence's last block are not read.
+ * What the cache holds past a sequence's end (NaN or infinity among it) and what
+ * the tokens after a query's own position hold reaches no output of that query.
+ * The result does not depend on timing: equal calls give equal bits on one GPU.
+ * workspace: msa_dense_workspace_size bytes, 16-byte aligned, msa_workspace_init
+ * as for the other entry points (and it may be shared with them); calls that
+ * overlap on the GPU need workspaces of their own. */
+size_t msa_dense_workspace_size(const msa_cache_t* cache, const msa_batch_t* batch, int32_t num_q_heads);
+msa_status_t msa_dense_attend(const msa_cache_t* cache, const msa_batch_t* batch, const msa_config_t* cfg,
+                              const msa_query_t* q, int32_t num_q_heads, void* out, float* lse, void* workspace,
+                              size_t workspace_bytes, msa_stream_t stream);
+
+/* Rotary positions (model page, MiniMaxM3SparseAttention: partial rotary
+ * positions; with several axes -- time, height, width -- for images and video).
+ * Pair i of a row's first rotary_dim elements turns by
+ *   2 pi * positions[axis[i]][t] * turns[i] / 2^64
+ * (a, b) -> (a cos - b sin, a sin + b cos).  The pair is elements (i, i +
+ * rotary_dim / 2) (MSA_ROPE_HALVES) or (2i, 2i + 1) (MSA_ROPE_ADJACENT).
+ * msa_rope_init fills the struct on the host: frequencies theta^(-2i /
+ * rotary_dim), the pairs given to the axes in consecutive sections (sections[a]
+ * pairs for axis a, rotary_dim / 2 in all).  A caller with other frequencies
+ * or another order of axes writes `turns` and `axis` itself (turns a position x
+ * 2^64, modulo 2^64; a negative frequency is its two's complement). */
+#define MSA_ROPE_MAX_AXES 4
+typedef enum {
+  MSA_ROPE_HALVES = 0,
+  MSA_ROPE_ADJACENT = 1
+} msa_rope_layout_t;
+typedef struct {
+  int32_t rotary_dim;  /* 16 to 128, a multiple of 16 */
+  int32_t axes;        /* 1 to MSA_ROPE_MAX_AXES */
+  int32_t layout;      /* msa_rope_layout_t */
+  uint8_t axis[64];
+  uint64_t turns[64];
+} msa_rope_t;
+msa_status_t msa_rope_init(msa_rope_t* rope, int32_t rotary_dim, double theta, int32_t axes, const int32_t* sections,
+                           int32_t layout);
+
+/* bf16 rows of a projection: element d of head h of token t at data[t * stride +
+ * h * 128 + d] (a slice of a fused projection's output).  data 16-byte aligned,
+ * stride a multiple of 8 elements. */
+typedef struct {
+  const void* data;
+  int64_t stride;
+} msa_rows_t;
+
+/* Per-head RMS norm before the rotation: y = x * rsqrt(mean x^2 + eps) * (offset
+ * + w), w bf16 [128], 16-byte aligned, shared by the heads of a kind (offset 1 for
+ * weights stored around zero, as the model's Gemma-style norm does, else 0).  A
+ * null weight: that kind is not normed. */
+typedef struct {
+  const void* q;
+  const void* k;
+  const void* index_q;
+  const void* index_k;
+  float eps;
+  float offset;
+} msa_qk_norm_t;
+
+/* Rotary insert: the step between the projections and the path.  Norm (norm may
+ * be NULL) and rotation of q, index q, k and index k in fp32, then one rounding:
+ *   q_out, index_q_out  [num_tokens][heads][128], bf16, or E4M3 codes of y * (1 /
+ *                       scale) (fp32, round to nearest even, saturating);
+ *   k, v, index k       into the caches through slot_mapping, by the formats'
+ *                       rules of msa_cache_insert (v is neither normed nor turned).
+ * positions: device int32 [axes][num_tokens], any values.
+ * slot_mapping: as in msa_cache_insert (negative: that token's keys and values
+ *   are not stored, its queries are still written; beyond the pool: the same,
+ *   and flagged).  Two tokens mapped to one slot race.
+ * index_q / index_q_out (num_kv_heads heads) may both be NULL, as may index_k.
+ * q_out may be q's own memory when q is dense (stride = heads * 128) and bf16.
+ * The call writes through q_out's, index_q_out's and the cache's pointers.
+ * workspace: at least 256 bytes; only its status word is used. */
+msa_status_t msa_rope_insert(const msa_cache_t* cache, const msa_rope_t* rope, int32_t num_tokens,
+                             const int32_t* positions, const int32_t* slot_mapping, int32_t num_q_heads,
+                             const msa_rows_t* q, const msa_query_t* q_out, const msa_rows_t* index_q,
+                             const msa_query_t* index_q_out, const msa_rows_t* k, const msa_rows_t* v,
+                             const msa_rows_t* index_k, const msa_qk_norm_t* norm, void* workspace,
+                             size_t workspace_bytes, msa_stream_t stream);
+
+/* Block tables, lengths, slots and positions of one step, from the requests'
+ * lengths, on the GPU.
+ * Request s has cached_lens[s] tokens in the cache (its row of block_table names
+ * their blocks) and new_lens[s] new ones: 0 for a request that waits, -1 for one
+ * that has ended.  free_blocks[0 .. *free_count) is a stack of free blocks.
+ *   1. The blocks of the ended requests go on top of the stack, in the order of
+ *      the requests; their rows of block_table are left as they are.
+ *   2. Each request takes the blocks its new tokens need beyond those it has off
+ *      the top of the stack, in the order of the requests, into its row.
+ * Outputs:
+ *   seq_lens       [num_seqs] cached + new (0 for an ended request): the batch's lengths
+ *   token_offsets  [num_seqs + 1] exclusive sums of the new tokens
+ *   slot_mapping, positions  [max_tokens] for new token i of request s, at
+ *                  token_offsets[s] + i: its slot and its position cached + i;
+ *                  -1 and 0 behind the last token
+ *   free_count_out the stack's new size.  Must not be free_count (the call reads
+ *                  its inputs while it writes); seq_lens and token_offsets must not
+ *                  overlap the input lengths either.
+ * A request whose blocks are not there, or whose tokens end beyond max_tokens,
+ * is refused (and so is every later one that wants tokens behind it): its length
+ * stays cached_lens[s], its slots are -1, it takes no block, and the device fault
+ * flag is raised.  A malformed request (a length below 0, new_lens below -1, more
+ * than max_blocks_per_seq * 128 tokens) is flagged and counts as length 0.  Blocks
+ * outside [0, num_blocks) are flagged; their slots are -1.  Returned blocks beyond
+ * free_capacity are dropped and flagged.
+ * num_seqs <= 8192, max_tokens < 2^30.  Deterministic.  workspace: at least 256
+ * bytes; only its status word is used. */
+msa_status_t msa_build_tables(int32_t num_seqs, int32_t num_blocks, const int32_t* cached_lens, const int32_t* new_lens,
+                              int32_t max_blocks_per_seq, int32_t* block_table, int32_t free_capacity,
+                              int32_t* free_blocks, const int32_t* free_count, int32_t* free_count_out,
+                              int32_t* seq_lens, int32_t* token_offsets, int32_t max_tokens, int32_t* slot_mapping,
+                              int32_t* positions, void* workspace, size_t workspace_bytes, msa_stream_t stream);
+
 /* Synchronise `stream`, read and clear the workspace's status word.
  * Returns MSA_OK, MSA_ERR_DEVICE_FAULT or MSA_ERR_TIMEOUT; *detail (optional,
  * host pointer) receives the raw flag bits. */
