@@ -11,6 +11,8 @@ from __future__ import annotations
 import ctypes
 import dataclasses
 import os
+import struct as _struct
+import threading
 from typing import Optional
 
 from . import roofline  # noqa: F401  (host-side byte model)
@@ -97,7 +99,7 @@ _lib_handle = None
 def lib() -> ctypes.CDLL:
     """Load libmsa.so (built in-tree by __graft_entry__.build()); raises if absent."""
     global _lib_handle
-    if _lib_handle is None:
+    if _lib_handle is None:  # (every call after the first returns at once)
         if not os.path.exists(LIB_PATH):
             raise RuntimeError(f"{LIB_PATH} is not built; run __graft_entry__.build() first "
                                "(there is no non-CUDA implementation)")
@@ -134,10 +136,18 @@ def _ptr(t) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
+_raw_stream = None
+
+
 def _stream(stream) -> Optional[int]:
-    import torch
     if stream is None:
-        stream = torch.cuda.current_stream()
+        global _raw_stream
+        if _raw_stream is None:
+            import torch
+            # the current stream's handle without a Stream object around it (a microsecond less)
+            raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), torch.cuda.current_device
+            _raw_stream = (lambda: raw(device())) if raw else (lambda: torch.cuda.current_stream().cuda_stream)
+        return _raw_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -235,16 +245,62 @@ def _ref(x):
     return ctypes.byref(x)
 
 
-def _rows(t, heads: int, tokens: int, where: str) -> Optional[MsaRowsT]:
-    """Rows of a projection: [tokens][heads][128] (or [tokens][128] for one head), the heads side by side."""
-    if t is None:
-        return None
-    shape, strides = tuple(t.shape), t.stride()
-    if len(shape) == 2 and heads == 1:
-        shape, strides = (shape[0], 1, shape[1]), (strides[0], 128, strides[1])
-    if shape != (tokens, heads, 128) or strides[2] != 1 or (heads > 1 and strides[1] != 128):
+# The structs of the serving calls, packed side by side into a per-thread host
+# buffer in one go (a ctypes object for each costs several microseconds a
+# call, as long as the kernels of a decode step).  The library copies what it needs before it returns.
+_tls = threading.local()
+_CACHE, _BATCH, _CONFIG, _QUERY, _ROWS, _NORM = "7i9P3fi", "3i2P", "3i2f2i", "Pif", "Pq", "4P2f"
+
+
+class _Layout:
+    """Consecutive structs, each 8-byte aligned: the packer and each one's offset."""
+
+    def __init__(self, *formats):
+        self.offsets, fmt = [], "@"
+        for f in formats:
+            fmt += "0P"
+            self.offsets.append(_struct.calcsize(fmt))
+            fmt += f
+        self.packer = _struct.Struct(fmt + "0P")
+
+    def pack(self, *values):
+        """Pack into this thread's buffer; returns the address of its start."""
+        buf = getattr(_tls, "buf", None)
+        if buf is None:
+            _tls.buf = buf = ctypes.create_string_buffer(1024)
+            _tls.addr = ctypes.addressof(buf)
+        self.packer.pack_into(buf, 0, *values)
+        return _tls.addr
+
+
+def _p(t) -> int:
+    return 0 if t is None else t.data_ptr()
+
+
+def _cache_values(c: PagedCache):
+    return (DTYPES[c.kv_dtype], DTYPES[c.index_dtype], c.num_blocks, 128, c.num_kv_heads, c.head_dim, c.index_dim,
+            c.k.data_ptr(), c.v.data_ptr(), _p(c.k_sf), _p(c.v_sf), _p(c.k_scale), _p(c.v_scale), _p(c.idx), _p(c.idx_sf),
+            _p(c.idx_scale), c.k_global, c.v_global, c.idx_global, NVFP4_MODES.get(c.nvfp4_mode, -1))
+
+
+_DENSE = _Layout(_CACHE, _BATCH, _CONFIG, _QUERY)
+_ROPE = _Layout(_CACHE, _ROWS, _QUERY, _ROWS, _QUERY, _ROWS, _ROWS, _ROWS, _NORM)
+
+
+def _rows(t, heads: int, tokens: int, where: str):
+    """(pointer, token stride) of a projection's rows: [tokens][heads][128] (or [tokens][128] for
+    one head), the heads side by side."""
+    shape, strides = t.shape, t.stride()
+    if len(shape) == 3:
+        if shape[0] != tokens or shape[1] != heads or shape[2] != 128 or strides[2] != 1 or (heads > 1 and strides[1] != 128):
+            raise MsaError(1, where)
+    elif len(shape) != 2 or heads != 1 or shape[0] != tokens or shape[1] != 128 or strides[1] != 1:
         raise MsaError(1, where)
-    return MsaRowsT(t.data_ptr(), strides[0])
+    return t.data_ptr(), strides[0]
+
+
+def _nbytes(t) -> int:
+    return t.numel() * t.element_size()
 
 
 # ---------------------------------------------------------------- entry points (same names as the C ABI)
@@ -342,10 +398,14 @@ def msa_dense_workspace_size(cache: PagedCache, batch: Batch, num_q_heads: int) 
 
 def msa_dense_attend(cache, batch, cfg, q: Query, num_q_heads: int, out, lse, workspace, stream=None) -> None:
     """Attention of each new token (up to 8 a sequence) over its whole sequence in the paged cache."""
-    c, b, f, qq = cache.struct(), batch.struct(), cfg.struct(), q.struct()
-    _check(lib().msa_dense_attend(_ref(c), _ref(b), _ref(f), _ref(qq), num_q_heads, _ptr(out), _ptr(lse),
-                                  _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)),
-           "msa_dense_attend")
+    lens, table = batch.seq_lens, batch.block_table
+    at = _DENSE.pack(*_cache_values(cache), lens.shape[0], batch.q_per_seq, table.shape[1], lens.data_ptr(), table.data_ptr(),
+                     cfg.topk, cfg.init_blocks, cfg.local_blocks, cfg.index_scale, cfg.sm_scale,
+                     SCORE_TYPES.get(cfg.score_type, -1), PREFILL_SELECT.get(cfg.prefill_select, -1),
+                     q.data.data_ptr(), DTYPES[q.dtype], q.scale)
+    o = _DENSE.offsets
+    _check(lib().msa_dense_attend(at + o[0], at + o[1], at + o[2], at + o[3], num_q_heads, out.data_ptr(), _p(lse),
+                                  workspace.data_ptr(), _nbytes(workspace), _stream(stream)), "msa_dense_attend")
 
 
 def msa_rope_init(rotary_dim: int, theta: float, sections=None, layout: str = "halves") -> MsaRopeT:
@@ -364,22 +424,28 @@ def msa_rope_insert(cache, rope: MsaRopeT, positions, slot_mapping, q, q_out: Qu
     queries to q_out / index_q_out and k, v, index k into the paged caches at slot_mapping (int32 [T]).
     positions: int32 [axes][T], or [T] for one axis."""
     where = "msa_rope_insert"
-    T, H = int(slot_mapping.numel()), cache.num_kv_heads
-    if positions.numel() != rope.axes * T or not positions.is_contiguous() or q.dim() != 3:
+    T, H = slot_mapping.numel(), cache.num_kv_heads
+    if q.dim() != 3 or positions.numel() != rope.axes * T or not positions.is_contiguous():
         raise MsaError(1, where)
     hq = q.shape[1]
-    if q_out.data.numel() != T * hq * 128 or not q_out.data.is_contiguous() or \
-            (index_q_out is not None and (index_q_out.data.numel() != T * H * 128 or not index_q_out.data.is_contiguous())):
+    if q_out.data.numel() != T * hq * 128 or not q_out.data.is_contiguous():
         raise MsaError(1, where)
-    c, qo = cache.struct(), q_out.struct()
-    rows = [_rows(q, hq, T, where), _rows(index_q, H, T, where), _rows(k, H, T, where), _rows(v, H, T, where),
-            _rows(index_k, 1, T, where)]
-    io = None if index_q_out is None else index_q_out.struct()
-    n = None if norm is None else norm.struct()
-    ref = [None if x is None else _ref(x) for x in rows + [io, n]]
-    _check(lib().msa_rope_insert(_ref(c), _ref(rope), T, _ptr(positions), _ptr(slot_mapping), hq, ref[0], _ref(qo), ref[1],
-                                 ref[5], ref[2], ref[3], ref[4], ref[6], _ptr(workspace),
-                                 workspace.numel() * workspace.element_size(), _stream(stream)), where)
+    none = (0, 0)
+    iqo = (0, 0, 0.0)
+    if index_q_out is not None:
+        if index_q_out.data.numel() != T * H * 128 or not index_q_out.data.is_contiguous():
+            raise MsaError(1, where)
+        iqo = (index_q_out.data.data_ptr(), DTYPES[index_q_out.dtype], index_q_out.scale)
+    w = (0, 0, 0, 0, 0.0, 0.0) if norm is None else (_p(norm.q), _p(norm.k), _p(norm.index_q), _p(norm.index_k), norm.eps,
+                                                     norm.offset)
+    at = _ROPE.pack(*_cache_values(cache), *_rows(q, hq, T, where), q_out.data.data_ptr(), DTYPES[q_out.dtype], q_out.scale,
+                    *(none if index_q is None else _rows(index_q, H, T, where)), *iqo, *_rows(k, H, T, where),
+                    *_rows(v, H, T, where), *(none if index_k is None else _rows(index_k, 1, T, where)), *w)
+    o = _ROPE.offsets
+    _check(lib().msa_rope_insert(at, ctypes.byref(rope), T, positions.data_ptr(), slot_mapping.data_ptr(), hq, at + o[1], at + o[2],
+                                 0 if index_q is None else at + o[3], 0 if index_q_out is None else at + o[4], at + o[5],
+                                 at + o[6], 0 if index_k is None else at + o[7], 0 if norm is None else at + o[8],
+                                 workspace.data_ptr(), _nbytes(workspace), _stream(stream)), where)
 
 
 def msa_build_tables(num_blocks: int, cached_lens, new_lens, block_table, free_blocks, free_count, seq_lens, token_offsets,
@@ -387,15 +453,15 @@ def msa_build_tables(num_blocks: int, cached_lens, new_lens, block_table, free_b
     """Block tables, lengths, slots and positions of a step from the requests' lengths (all int32 on the
     device): block_table [S][max_blocks] and the stack free_blocks are updated in place; seq_lens [S],
     token_offsets [S + 1], slot_mapping and positions [max_tokens] and free_count_out [1] are written."""
-    S = cached_lens.numel()
-    if new_lens.numel() != S or block_table.dim() != 2 or block_table.shape[0] != S or seq_lens.numel() != S or \
+    S, shape = cached_lens.numel(), block_table.shape
+    if new_lens.numel() != S or len(shape) != 2 or shape[0] != S or seq_lens.numel() != S or \
             token_offsets.numel() != S + 1 or positions.numel() != slot_mapping.numel() or not block_table.is_contiguous():
         raise MsaError(1, "msa_build_tables")
-    _check(lib().msa_build_tables(S, num_blocks, _ptr(cached_lens), _ptr(new_lens), block_table.shape[1], _ptr(block_table),
-                                  free_blocks.numel(), _ptr(free_blocks), _ptr(free_count), _ptr(free_count_out),
-                                  _ptr(seq_lens), _ptr(token_offsets), slot_mapping.numel(), _ptr(slot_mapping),
-                                  _ptr(positions), _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                  _stream(stream)), "msa_build_tables")
+    _check(lib().msa_build_tables(S, num_blocks, cached_lens.data_ptr(), new_lens.data_ptr(), shape[1], block_table.data_ptr(),
+                                  free_blocks.numel(), free_blocks.data_ptr(), free_count.data_ptr(), free_count_out.data_ptr(),
+                                  seq_lens.data_ptr(), token_offsets.data_ptr(), slot_mapping.numel(), slot_mapping.data_ptr(),
+                                  positions.data_ptr(), workspace.data_ptr(), _nbytes(workspace), _stream(stream)),
+           "msa_build_tables")
 
 
 def default_config(topk: int = 16, head_dim: int = 128, index_dim: int = 128) -> Config:

@@ -550,7 +550,7 @@ msa_status_t run_k2q(const msa_cache_t* c, const msa_batch_t* b, const msa_confi
 // ---------------------------------------------------------------- the dense attend
 
 struct DensePlan {
-  int cols = 0, CG = 0, rows = 0;
+  int cols = 0, CG = 0, cper = 0, rows = 0;
   size_t off_info = 0, off_ml = 0, off_o = 0, total = 0;
 };
 
@@ -559,10 +559,12 @@ msa_status_t make_dense_plan(const msa_cache_t* c, const msa_batch_t* b, int hq,
   if (hq < G || hq % G != 0) return MSA_ERR_INVALID_ARGUMENT;
   if (hq / G > 64 || b->q_per_seq > 8) return MSA_ERR_UNSUPPORTED;
   pl.cols = b->q_per_seq * (hq / G);
-  pl.rows = dense_rows(dense_nt(pl.cols));
-  pl.CG = (pl.cols + pl.rows - 1) / pl.rows;
+  pl.CG = (pl.cols + 63) / 64;
+  pl.cper = (pl.cols + pl.CG - 1) / pl.CG;
+  const DenseShape sh = dense_shape(pl.cper);
+  pl.rows = dense_rows(sh.nn, sh.ncg);
   if ((long)b->num_seqs * G * pl.CG >= (1l << 31)) return MSA_ERR_UNSUPPORTED;
-  const size_t ctas = (size_t)sm_count();
+  const size_t ctas = (size_t)sm_count() * dense_teams(fmt_of(c->kv_dtype), sh.nn);  // runs
   size_t o = 256;  // the status word
   pl.off_info = o; o = align256(o + ctas * sizeof(int2));
   pl.off_ml = o; o = align256(o + 2 * ctas * pl.rows * sizeof(float2));
@@ -584,6 +586,7 @@ msa_status_t run_dense(const msa_cache_t* c, const msa_batch_t* b, const msa_con
   p.r = hq / G;
   p.cols = pl.cols;
   p.CG = pl.CG;
+  p.cper = pl.cper;
   p.max_nb = b->max_blocks_per_seq;
   p.num_blocks = c->num_blocks;
   p.seq_lens = b->seq_lens;
@@ -604,9 +607,10 @@ msa_status_t run_dense(const msa_cache_t* c, const msa_batch_t* b, const msa_con
   cudaError_t e;
   if (fmt == FMT_BF16) e = launch_dense_bf16(&tk, &tv, p, sms, st);
   else if (fmt == FMT_FP8) e = launch_dense_fp8(&tk, &tv, p, sms, st);
-  else e = launch_dense_nvfp4(&tk, &tv, p, sms, c->nvfp4_mode == MSA_NVFP4_E4M3_PRODUCT, st);
+  else if (c->nvfp4_mode == MSA_NVFP4_E4M3_PRODUCT) e = launch_dense_nvfp4_rounded(&tk, &tv, p, sms, st);
+  else e = launch_dense_nvfp4(&tk, &tv, p, sms, st);
   if (e != cudaSuccess) return MSA_ERR_CUDA;
-  return cuda_status(launch_dense_combine(p, fmt != FMT_BF16, sms, st));
+  return cuda_status(launch_dense_combine(p, fmt, sms, st));
 }
 
 msa_status_t check_rope(const msa_rope_t* r) {

@@ -16,7 +16,7 @@ namespace {
 
 constexpr int kJoinWarps = 16;
 
-// rows: of a partial; F16P: l carries P's scale of 2^14.
+// rows: of a partial; shift: log2 of P's scale, which l carries.
 __global__ void __launch_bounds__(32 * kJoinWarps) dense_combine_kernel(const DenseParams p, int rows, float shift) {
   __shared__ float so[kJoinWarps][132];
   __shared__ float sm[kJoinWarps][2];
@@ -41,8 +41,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) dense_combine_kernel(const De
   const int parts = s_parts - c + 1;
   const int gc = me.x % (p.G * p.CG), s = me.x / (p.G * p.CG);
   const int g = gc / p.CG, cg = gc - g * p.CG;
-  const int c0 = cg * rows;
-  const int nrows = p.cols - c0 < rows ? p.cols - c0 : rows;
+  const int c0 = cg * p.cper;
+  const int nrows = p.cols - c0 < p.cper ? p.cols - c0 : p.cper;
   // few rows: several warps share a row's partials
   int ns = 1;
   while (ns < kJoinWarps && nrows * ns * 2 <= kJoinWarps) ns *= 2;
@@ -129,9 +129,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) dense_combine_kernel(const De
 
 }  // namespace
 
-cudaError_t launch_dense_combine(const DenseParams& p, bool f16p, int num_sms, cudaStream_t st) {
+cudaError_t launch_dense_combine(const DenseParams& p, int fmt, int num_sms, cudaStream_t st) {
+  const DenseShape sh = dense_shape(p.cper);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)num_sms);
+  cfg.gridDim = dim3((unsigned)(num_sms * dense_teams(fmt, sh.nn)));
   cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -139,7 +140,8 @@ cudaError_t launch_dense_combine(const DenseParams& p, bool f16p, int num_sms, c
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, dense_combine_kernel, p, dense_rows(dense_nt(p.cols)), f16p ? kDensePShift : 0.f);
+  return cudaLaunchKernelEx(&cfg, dense_combine_kernel, p, dense_rows(sh.nn, sh.ncg),
+                            fmt != FMT_BF16 ? kDensePShift : 0.f);
 }
 
 }  // namespace msa

@@ -13,35 +13,45 @@
 // its group: 8 flop a byte at 4 columns over FP8, far below the tensor rate, so
 // the design is a stream of K / V tiles with as much in flight as fits.
 //
-// Split.  A unit is SK keys of one (sequence, group); the units of the batch,
-// in (sequence, group, position) order, are cut into equal contiguous runs, one
-// per CTA (one CTA an SM), whatever the lengths are: the lengths stay on the
-// device and every CTA does the same work to within a unit.  A run crosses
-// (sequence, group) borders; a segment it holds whole is written out at once,
-// a cut one leaves its partial in the workspace (at most two a CTA), joined by
-// the combine kernel.  No atomics: the result does not depend on timing.
+// Split.  A unit is SK keys of one (sequence, group of heads); the units of the
+// batch, in (sequence, group, position) order, are cut into equal contiguous
+// runs, one per team, whatever the lengths are: the lengths stay on the device
+// and every team does the same work to within a unit.  A run crosses (sequence,
+// group) borders; a segment it holds whole is written out at once, a cut one
+// leaves its partial in the workspace (at most two a run), joined by the
+// combine kernel.  No atomics: the result does not depend on timing.
 //
-// A CTA has one producer warp, which walks the run, publishes each segment's
-// facts and query rows in one of two slots and streams the tiles through a
-// ring of stages (tensor copies, mbarriers), and two groups of four consumer
-// warps that take alternate units.  In a group the warps divide the unit as NT
-// tiles of 16 columns x key ranges.
+// A team is one producer warp and four consumer warps with a ring of their own;
+// a CTA (one an SM) holds two or three, so that one team's segment ends (the
+// join of its warps, the output) pass behind the others' work.  The producer
+// walks the run, publishes each segment's facts and query rows in one of two
+// slots and streams the tiles through the ring (tensor copies, mbarriers).  The
+// consumers divide a unit as NCG groups of 8 NN columns x key ranges; a warp takes
+// up to 32 columns, so that the tile it has converted serves them all.
 //
-// Tensor-core mapping (mma.sync: 4 to 64 columns are far too few for a 128-row
-// tile), queries as the 16 rows, so that P leaves the softmax in the layout in
-// which it enters the second product, with no exchange between lanes:
-//   S[col][key] = Q[col][:] . K[key][:]     (A = Q, B = K)
-//   O[col][d]  += sum_key P[col][key] V[key][d]  (A = P, B = V)
+// Tensor-core mapping (mma.sync: up to 64 columns are too few for a 128-row
+// tile).  The queries are the rows of the first product and the columns of the
+// second, so that P leaves the softmax in the lanes and order in which it enters
+// the second product, with no exchange between lanes, and with up to 8 columns
+// the output takes 32 registers and no MMA works on empty columns:
+//   S[col][key]   = Q[col][:] . K[key][:]             (A = Q, B = K)
+//   O^T[d][col]  += sum_key V[key][d] P[col][key]     (A = V^T, B = P)
 //   FP8    K enters e4m3 MMAs as it is, a bf16 query as e4m3 hi + lo terms after
 //          a power-of-two row scale (exact to 2^-10 of the row's 448); with up
 //          to 8 columns the lo terms are the tile's rows 8 to 15 and cost
-//          nothing.  V becomes f16 (exact) and P x vscale f16 (11 bits).
+//          nothing, with up to 16 a second MMA.  With more the tensor pipe would
+//          be the bound (an e4m3 k32 MMA takes as long as two f16 k16 ones:
+//          4.2 and 2.1 cycles an SM, from the pipe's counters), so K becomes f16
+//          there.  V becomes f16 (exact), P x vscale f16 (11 bits).
 //   NVFP4  K and V become f16 in registers (e2m1 x e4m3 fits 6 bits: exact).
-//   BF16   as it is; P enters as bf16 hi + lo terms (16 bits; with up to 8
-//          columns again in the rows 8 to 15), since one bf16 term alone would
-//          add an error as large as the output's own rounding.
-// P is scaled by 2^14 where it becomes f16, l with it, so that f16's range
-// reaches 2^-28 of the row's largest weight before it loses bits.
+//   BF16   as it is; P enters as bf16 hi + lo terms (16 bits), since one bf16
+//          term alone would add an error near the output's own rounding.
+//
+// The running maximum is lazy: m moves only when a logit passes it by 2^8, so
+// that the output is rescaled a few times a segment and the lanes of a row need
+// not agree on a maximum at every step (one vote instead).  P is scaled by 2^7
+// where it becomes f16, l with it: at most 2^15, and 2^-21 of the row's
+// reference weight before f16 loses bits.
 //
 // A masked key's logit is replaced, not multiplied; in units that hold masked
 // keys V is masked in registers too, so NaN or infinity in rows past the end of a
@@ -53,12 +63,18 @@
 
 namespace msa {
 
-constexpr int kDenseGroups = 2;   // consumer groups, alternate units
-constexpr int kDenseWpg = 4;      // warps a group
-constexpr int kDenseWarps = kDenseGroups * kDenseWpg;
-constexpr int kDenseConsumers = 32 * kDenseWarps;
-constexpr int kDenseThreads = kDenseConsumers + 32;
-constexpr float kDensePShift = 14.f;  // log2 of the scale of P (f16 formats)
+constexpr int kDenseWpg = 4;             // consumer warps of a team
+constexpr float kDensePShift = 7.f;      // log2 of the scale of P (f16 formats)
+constexpr float kDenseLazy = 8.f;        // a logit (log2) above the reference by this moves it
+
+// How the query meets K.
+enum QMode : int {
+  QM_16 = 0,    // BF16 and NVFP4 caches: 16-bit MMAs
+  QM_E4 = 1,    // FP8: e4m3 queries as they are
+  QM_E4X2 = 2,  // FP8: bf16 queries as two e4m3 terms, two MMAs
+  QM_ROWS = 3,  // FP8: the two terms in rows 0-7 and 8-15 of one tile
+  QM_F16K = 4   // FP8: K widened to f16, f16 queries
+};
 
 template <int FMT>
 struct DenseTraits;
@@ -84,45 +100,63 @@ struct DenseFacts {
   int32_t pad;
 };
 
-// NT: tiles of 16 query columns; R8: NT = 1 and at most 8 columns.
-template <int FMT, int NT, bool R8>
+// NN: tiles of 8 query columns a warp takes; NCG: groups of such columns in a unit.
+template <int FMT, int NN, int NCG>
 struct DenseLayout {
   using T = DenseTraits<FMT>;
-  static constexpr int ROWS = R8 ? 8 : 16 * NT;  // columns (query rows) of a unit
-  static constexpr int TR = R8 ? 8 : 16;         // of one warp
+  // Narrow instances need under 128 registers a thread; NVFP4's dequantization
+  // keeps three teams busy where two are enough for the others.
+  static constexpr int TEAMS = (NN == 1 && FMT == FMT_NVFP4) ? 3 : 2;
+  // Wide ones need more than a CTA of ten warps can give each thread (168): their
+  // warps come in fours (the producers' four hold two idle ones) and the
+  // consumers take registers over from the producers.
+  static constexpr bool WIDE = NN >= 3;
+  static constexpr int CONSUMERS = 32 * kDenseWpg * TEAMS;
+  static constexpr int THREADS = CONSUMERS + (WIDE ? 128 : 32 * TEAMS);
+  static constexpr int MT = (NN + 1) / 2;        // 16-row tiles of a warp's queries
+  static constexpr int WROWS = 8 * NN;           // columns of a warp
+  static constexpr int ROWS = WROWS * NCG;       // of a unit
+  static constexpr int KGW = kDenseWpg / NCG;    // warps that share a group's columns, each its keys
   static constexpr size_t STAGE = 2 * (size_t)T::TILE;  // K tile, V tile
   static constexpr size_t SCALES = 2 * (size_t)T::SC;   // their scales, in a region of their own
-  static constexpr int DCH = R8 ? 64 : 32;       // output dims a merge pass takes
+  static constexpr int DCH = NN == 1 ? 64 : (NN == 2 || NCG == 1 || FMT == FMT_NVFP4) ? 32 : 16;  // output dims a merge pass takes
   static constexpr int MROW = DCH + 4;           // padded row of the merge area
-  static constexpr size_t MERGE_BYTES = (size_t)kDenseWarps * TR * MROW * 4;
-  static constexpr size_t ML_BYTES = (size_t)kDenseWarps * TR * 8;
   static constexpr int QROW = 272;               // a query row, padded (conflict-free reads)
+  // per team
+  static constexpr size_t MERGE_BYTES = (size_t)kDenseWpg * WROWS * MROW * 4;
+  static constexpr size_t ML_BYTES = (size_t)kDenseWpg * WROWS * 8;
   static constexpr size_t QSLOT = (size_t)ROWS * QROW;
-  static constexpr size_t FIXED = MERGE_BYTES + ML_BYTES + 2 * QSLOT + 2 * sizeof(DenseFacts) + 512;
-  // Ring stages: an even number, so that a stage always belongs to the same
-  // consumer group and the group sees every phase of its barriers.
-  static constexpr int NST = (int)((227 * 1024 - 1024 - FIXED) / (STAGE + SCALES)) / 2 * 2;
-  static constexpr size_t SC = STAGE * NST;
+  static constexpr size_t CF_BYTES = (ROWS * 4 + 15) / 16 * 16;
+  static constexpr size_t FIXED = MERGE_BYTES + ML_BYTES + 2 * QSLOT + CF_BYTES + 2 * sizeof(DenseFacts) + 320;
+  static constexpr int NST_FIT = (int)(((227 * 1024 - 1024) / TEAMS - FIXED) / (STAGE + SCALES));
+  static constexpr int NST = NST_FIT < 8 ? NST_FIT : 8;  // ring stages of a team
+  // the tiles of all teams first (1 KB alignment), then each team's block
+  static constexpr size_t TILES = STAGE * NST * TEAMS;
+  static constexpr size_t SC = 0;
   static constexpr size_t MERGE = SC + SCALES * NST;
   static constexpr size_t ML = MERGE + MERGE_BYTES;
   static constexpr size_t Q = ML + ML_BYTES;
-  static constexpr size_t FACTS = Q + 2 * QSLOT;
+  static constexpr size_t CF = Q + 2 * QSLOT;
+  static constexpr size_t FACTS = CF + CF_BYTES;
   static constexpr size_t BARS = FACTS + 2 * sizeof(DenseFacts);
-  static constexpr size_t TOTAL = BARS + 8 * (2 * NST + 4) + 4 * NST + 16;
-  static constexpr size_t SMEM = TOTAL + 1024;
-  static_assert(SMEM <= 227 * 1024 && NST >= 4 && NST <= 16 && NST % kDenseGroups == 0, "stages");
+  static constexpr size_t TEAM = (BARS + 8 * (2 * NST + 4) + 4 * NST + 16 + 127) / 128 * 128;
+  static constexpr size_t SMEM = TILES + TEAMS * TEAM + 1024;
+  static_assert(SMEM <= 227 * 1024 && NST >= 2, "stages");
   static_assert(STAGE % 1024 == 0 && MERGE_BYTES % 16 == 0 && ML_BYTES % 16 == 0 && QSLOT % 16 == 0, "alignment");
 };
 
-namespace dense {
+// One team's shared memory.
+struct DenseTeam {
+  uint8_t* tiles;   // ring of stages
+  uint8_t* mem;     // scales, merge area, queries, facts
+  uint64_t *full, *empty, *ifull, *iempty;
+  int* stage_ok;
+  int* dead;
+  DenseFacts* facts;
+  int id;           // team of the grid: the run it takes
+};
 
-__device__ __forceinline__ uint32_t swz128(uint32_t base, int row, int chunk) {
-  return base + row * 128 + ((chunk ^ (row & 7)) << 4);
-}
-// 64-byte rows under the 64-byte swizzle
-__device__ __forceinline__ uint32_t swz64(uint32_t base, int row, int chunk) {
-  return base + row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4);
-}
+namespace dense {
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -152,6 +186,30 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
+// two fp32 operations at once
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{ .reg .b64 x, y, z; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mul.rn.f32x2 z, x, y; mov.b64 {%0, %1}, z; }"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{ .reg .b64 x, y, z; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; add.rn.f32x2 z, x, y; mov.b64 {%0, %1}, z; }"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{ .reg .b64 x, y, z, w; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mov.b64 z, {%6, %7}; fma.rn.f32x2 w, x, y, z; "
+      "mov.b64 {%0, %1}, w; }"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(a, fmaxf(b, c)); }
 __device__ __forceinline__ float2 lds_f2(const float* p) { return *reinterpret_cast<const float2*>(p); }
 
 __device__ __forceinline__ bool is_dead(const int* flag) { return *reinterpret_cast<const volatile int*>(flag) != 0; }
@@ -186,22 +244,24 @@ __device__ __forceinline__ long warp_scan(long v, int lane) {  // inclusive
 
 // ---------------------------------------------------------------- the producer warp
 
-template <int FMT, int NT, bool R8>
-__device__ void producer(const CUtensorMap* tmk, const CUtensorMap* tmv, const DenseParams& p, uint8_t* base,
-                         uint64_t* full, uint64_t* empty, uint64_t* ifull, uint64_t* iempty, int* dead,
-                         DenseFacts* facts, int* stage_ok, int lane) {
+template <int FMT, int NN, int NCG>
+__device__ void producer(const CUtensorMap* tmk, const CUtensorMap* tmv, const DenseParams& p, const DenseTeam& tm,
+                         int lane) {
   using TR = DenseTraits<FMT>;
-  using LY = DenseLayout<FMT, NT, R8>;
+  using LY = DenseLayout<FMT, NN, NCG>;
   constexpr int NST = LY::NST;
+  uint64_t *full = tm.full, *empty = tm.empty, *ifull = tm.ifull, *iempty = tm.iempty;
+  int* dead = tm.dead;
   const int S = p.S, max_nb = p.max_nb;
   const long GC = (long)p.G * p.CG;
-  // units in all, then the run of this CTA: [u0, u1)
+  // units in all, then the run of this team: [u0, u1)
   long total = 0;
 #pragma unroll 4
   for (int s = lane; s < S; s += 32) total += units_of<TR::SK>(__ldg(p.seq_lens + s), max_nb);
   total = warp_sum(total) * GC;
-  const long grid = total < (long)gridDim.x ? total : (long)gridDim.x;
-  const long c = blockIdx.x;
+  const long teams = (long)gridDim.x * LY::TEAMS;
+  const long grid = total < teams ? total : teams;
+  const long c = tm.id;
   long u0 = 0, u1 = 0;
   if (c < grid) {
     u0 = c * total / grid;
@@ -255,10 +315,10 @@ __device__ void producer(const CUtensorMap* tmk, const CUtensorMap* tmv, const D
       break;
     }
     const int qrow_bytes = p.q_fp8 ? 128 : 256;
-    const int c0 = cg * LY::ROWS;
-    const int nrows = p.cols - c0 < LY::ROWS ? p.cols - c0 : LY::ROWS;
+    const int c0 = cg * p.cper;
+    const int nrows = p.cols - c0 < p.cper ? p.cols - c0 : p.cper;
     if (lane == 0) {
-      DenseFacts& f = facts[slot];
+      DenseFacts& f = tm.facts[slot];
       f.s = s;
       f.g = g;
       f.cg = cg;
@@ -270,10 +330,11 @@ __device__ void producer(const CUtensorMap* tmk, const CUtensorMap* tmv, const D
       mbar_expect_tx(&ifull[slot], (uint32_t)(nrows * qrow_bytes));
     }
     __syncwarp();
+    fence_proxy_async();
     for (int row = lane; row < nrows; row += 32) {
       const int col = c0 + row, i = col / p.r, h = col - i * p.r;
       const size_t src = ((size_t)s * p.Q + i) * ((size_t)p.G * p.r) + (size_t)g * p.r + h;
-      bulk_g2s(base + LY::Q + (size_t)slot * LY::QSLOT + (size_t)row * LY::QROW,
+      bulk_g2s(tm.mem + LY::Q + (size_t)slot * LY::QSLOT + (size_t)row * LY::QROW,
                static_cast<const uint8_t*>(p.q) + src * qrow_bytes, (uint32_t)qrow_bytes, &ifull[slot]);
     }
     ++ii;
@@ -302,9 +363,9 @@ __device__ void producer(const CUtensorMap* tmk, const CUtensorMap* tmv, const D
         break;
       }
       if (lane == 0) {
-        stage_ok[st] = ph >= 0 ? 1 : 0;
+        tm.stage_ok[st] = ph >= 0 ? 1 : 0;
         if (ph >= 0) {
-          uint8_t* stg = base + (size_t)st * LY::STAGE;
+          uint8_t* stg = tm.tiles + (size_t)st * LY::STAGE;
           const size_t tile = (size_t)ph * p.G + g;
           const int y = (int)(tile * kBlock) + half * TR::SK;
           fence_proxy_async();
@@ -317,7 +378,7 @@ __device__ void producer(const CUtensorMap* tmk, const CUtensorMap* tmv, const D
           } else {
             tma_load_2d(stg, tmk, 0, y, &full[st]);
             tma_load_2d(stg + TR::TILE, tmv, 0, y, &full[st]);
-            uint8_t* sc = base + LY::SC + (size_t)st * LY::SCALES;
+            uint8_t* sc = tm.mem + LY::SC + (size_t)st * LY::SCALES;
             bulk_g2s(sc, p.k_sc + tile * TR::SC, TR::SC, &full[st]);
             bulk_g2s(sc + TR::SC, p.v_sc + tile * TR::SC, TR::SC, &full[st]);
           }
@@ -338,7 +399,7 @@ __device__ void producer(const CUtensorMap* tmk, const CUtensorMap* tmv, const D
     if (use > 0 && !ring_wait(&iempty[slot], (uint32_t)((use - 1) & 1), dead)) {
       set_dead(dead, p.status, -1);
     } else if (lane == 0) {
-      facts[slot].n = -1;
+      tm.facts[slot].n = -1;
       mbar_arrive(&ifull[slot]);
     }
     ++ii;
@@ -359,218 +420,270 @@ __device__ void producer(const CUtensorMap* tmk, const CUtensorMap* tmv, const D
 
 // ---------------------------------------------------------------- consumer pieces
 
-// The A fragments of a warp's 16 query columns (rows g8 and g8 + 8 of the
-// tile) from the raw query rows in shared memory, and the factor of each row's
-// logits (log2 domain).
-//   FP8    a[0]: hi terms (R8: rows 8-15 the lo terms of columns 0-7), a[1]: lo
-//   16-bit a[0][ks]: k slots of lane j as in slot_dim()
-template <int FMT>
+template <int QM>
 struct QRegs {
-  static constexpr int KS = FMT == FMT_FP8 ? 4 : 8;
+  static constexpr bool E4 = QM == QM_E4 || QM == QM_E4X2 || QM == QM_ROWS;
+  static constexpr int KS = E4 ? 4 : 8;             // k steps of the first product
+  static constexpr int SP = QM == QM_E4X2 ? 2 : 1;  // terms
 };
-
-template <int FMT>
-__device__ __forceinline__ int slot_dim(int ks, int hi, int j) {  // first dim of k slots 2j (hi = 0) or 2j + 8
-  if constexpr (FMT == FMT_FP8) return 32 * ks + 16 * hi + 4 * j;
-  else if constexpr (FMT == FMT_BF16) return 16 * ks + 8 * hi + 2 * j;
-  else return 32 * j + 4 * ks + 2 * hi;  // NVFP4: a lane's 32 consecutive dims
-}
 
 __device__ __forceinline__ float2 bf16x2_to_float2(uint32_t w) {
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 
-// qs: the rows of the segment's columns, QROW bytes apart.
-template <int FMT, bool R8, int SP, int QROW>
-__device__ __forceinline__ void load_q(const uint8_t* qs, int row0, int nrows, bool q_fp8, float q_scale, float cst,
-                                       int lane, uint32_t (&a)[SP][QRegs<FMT>::KS][4], float (&colf)[2]) {
-  constexpr int KS = QRegs<FMT>::KS;
-  constexpr int W = FMT == FMT_FP8 ? 2 : 1;  // words of two elements a (k step, half) takes
-  const int g8 = lane >> 2, j = lane & 3;
-#pragma unroll
-  for (int rr = 0; rr < (R8 ? 1 : 2); ++rr) {
-    const int row = row0 + g8 + 8 * rr;
-    const bool have = row < nrows;
-    const uint8_t* src = qs + (size_t)row * QROW;
-    if (q_fp8) {
-      // E4M3 codes: as they are, or widened exactly
-      colf[rr] = q_scale * cst;
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-        for (int hi = 0; hi < 2; ++hi) {
-          const int d = slot_dim<FMT>(ks, hi, j);
-          uint32_t w = 0;
-          if constexpr (FMT == FMT_FP8) {
-            if (have) w = *reinterpret_cast<const uint32_t*>(src + d);
-          } else {
-            const uint32_t c2 = have ? *reinterpret_cast<const uint16_t*>(src + d) : 0u;
-            if constexpr (FMT == FMT_BF16) {
-              const float2 v = e4m3x2_to_float2((uint16_t)c2);
-              w = pack_bf16x2(v.x, v.y);
-            } else {
-              w = e4m3x2_to_f16x2(c2);
-            }
-          }
-          a[0][ks][rr + 2 * hi] = w;
-          if constexpr (R8) a[0][ks][1 + 2 * hi] = 0u;
-          else if constexpr (SP == 2) a[1][ks][rr + 2 * hi] = 0u;
-        }
+// Where dim d of a query row is kept, so that a k step's 16 (e4m3: 32) columns
+// are the dims K's fragments hold in the same slots.  The order of the dims is
+// free as long as both agree; d even, pairs stay together.
+template <int FMT, int QM>
+__device__ __forceinline__ int q_place(int d) {
+  if constexpr (QM == QM_F16K) {  // K's slots 2j, 2j + 1 and 2j + 8, 2j + 9 hold dims 4j .. 4j + 3
+    const int ks = d >> 4, j = (d >> 2) & 3, hi = (d >> 1) & 1;
+    return 16 * ks + 8 * hi + 2 * j;
+  } else if constexpr (FMT == FMT_NVFP4) {  // a lane's 32 consecutive dims, four a step
+    const int j = d >> 5, ks = (d >> 2) & 7, hi = (d >> 1) & 1;
+    return 16 * ks + 8 * hi + 2 * j;
+  } else {
+    return d;
+  }
+}
+
+// The segment's query rows, in place, into the form of their fragments (16-bit
+// rows of 256 bytes, or e4m3 rows with the lo terms 128 bytes behind the hi
+// terms), and each row's logit factor (log2 domain).  One warp a row.
+template <int FMT, int QM, int QROW>
+__device__ __forceinline__ void convert_q(uint8_t* qs, float* cf, int nrows, int rows, bool q_fp8, float q_scale, float cst,
+                                          int warp, int lane) {
+#pragma unroll 1
+  for (int row = warp; row < rows; row += kDenseWpg) {
+    uint8_t* r = qs + (size_t)row * QROW;
+    if (row >= nrows) {  // no such column: zeros
+      *reinterpret_cast<uint2*>(r + 8 * lane) = make_uint2(0u, 0u);
+      if (lane == 0) cf[row] = 1.f;
       continue;
     }
-    uint32_t raw[KS][2][W];
-    float amax = 0.f;
-    bool bad = false;
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-      for (int hi = 0; hi < 2; ++hi) {
-        const uint8_t* at = src + 2 * slot_dim<FMT>(ks, hi, j);
-        if constexpr (FMT == FMT_FP8) {
-          const uint2 w = have ? *reinterpret_cast<const uint2*>(at) : make_uint2(0u, 0u);
-          raw[ks][hi][0] = w.x;
-          raw[ks][hi][W - 1] = w.y;
+    if (q_fp8) {
+      if constexpr (!QRegs<QM>::E4) {  // widened exactly
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(r + 4 * lane);
+        __syncwarp();
+        uint32_t h[2];
+        if constexpr (FMT == FMT_BF16) {
+          const float2 a = e4m3x2_to_float2((uint16_t)w), b = e4m3x2_to_float2((uint16_t)(w >> 16));
+          h[0] = pack_bf16x2(a.x, a.y);
+          h[1] = pack_bf16x2(b.x, b.y);
         } else {
-          raw[ks][hi][0] = have ? *reinterpret_cast<const uint32_t*>(at) : 0u;
+          h[0] = e4m3x2_to_f16x2(w);
+          h[1] = e4m3x2_hi_to_f16x2(w);
         }
-        if constexpr (FMT != FMT_BF16) {
-#pragma unroll
-          for (int t = 0; t < W; ++t) {
-            const float2 v = bf16x2_to_float2(raw[ks][hi][t] & 0x7fff7fffu);
-            amax = fmaxf(amax, fmaxf(v.x, v.y));
-            bad |= !(v.x <= 3.4e38f) || !(v.y <= 3.4e38f);
-          }
-        }
+        *reinterpret_cast<uint32_t*>(r + 2 * q_place<FMT, QM>(4 * lane)) = h[0];
+        *reinterpret_cast<uint32_t*>(r + 2 * q_place<FMT, QM>(4 * lane + 2)) = h[1];
+      } else {
+        *reinterpret_cast<uint32_t*>(r + 128 + 4 * lane) = 0u;  // no lo terms
       }
-    float ps = 1.f, back = 1.f;
-    if constexpr (FMT != FMT_BF16) {
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-      bad = ((__ballot_sync(0xffffffffu, bad) >> (4 * g8)) & 0xfu) != 0;
-      int e = pow2_fit(amax, FMT == FMT_FP8 ? 448.f : 16384.f);
-      e = e < -126 ? -126 : (e > 126 ? 126 : e);
-      ps = pow2i(e);
-      back = pow2i(-e);
+      if (lane == 0) cf[row] = fmaxf(q_scale * cst, 1.2e-38f);
+      continue;
     }
-    // a query row that is not finite has no finite logits; the reduced formats would hide that
-    colf[rr] = bad ? __int_as_float(0x7fc00000) : back * cst;
+    if constexpr (FMT == FMT_BF16) {
+      if (lane == 0) cf[row] = fmaxf(cst, 1.2e-38f);
+      continue;  // as they are
+    }
+    const uint2 w = *reinterpret_cast<const uint2*>(r + 8 * lane);
+    __syncwarp();
+    const float2 a = bf16x2_to_float2(w.x), b = bf16x2_to_float2(w.y);
+    float amax = fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(b.x), fabsf(b.y)));
+    const bool bad = !(fabsf(a.x) <= 3.4e38f) || !(fabsf(a.y) <= 3.4e38f) || !(fabsf(b.x) <= 3.4e38f) || !(fabsf(b.y) <= 3.4e38f);
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-      for (int hi = 0; hi < 2; ++hi) {
-        uint32_t h = 0, l = 0;
-        if constexpr (FMT == FMT_FP8) {
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const float2 x = bf16x2_to_float2(raw[ks][hi][t]);
-            const uint16_t hw = pack_e4m3x2(x.x * ps, x.y * ps);
-            const float2 hv = e4m3x2_to_float2(hw);
-            h |= (uint32_t)hw << (16 * t);
-            l |= (uint32_t)pack_e4m3x2(x.x * ps - hv.x, x.y * ps - hv.y) << (16 * t);
-          }
-        } else if constexpr (FMT == FMT_BF16) {
-          h = raw[ks][hi][0];
-        } else {
-          const float2 x = bf16x2_to_float2(raw[ks][hi][0]);
-          h = pack_f16x2(x.x * ps, x.y * ps);
-        }
-        a[0][ks][rr + 2 * hi] = h;
-        if constexpr (R8) a[0][ks][1 + 2 * hi] = l;
-        else if constexpr (SP == 2) a[1][ks][rr + 2 * hi] = l;
-      }
+    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    int e = pow2_fit(amax, QRegs<QM>::E4 ? 448.f : 16384.f);
+    e = e < -126 ? -126 : (e > 126 ? 126 : e);
+    const float ps = pow2i(e);
+    if constexpr (QRegs<QM>::E4) {
+      const uint16_t h0 = pack_e4m3x2(a.x * ps, a.y * ps), h1 = pack_e4m3x2(b.x * ps, b.y * ps);
+      const float2 v0 = e4m3x2_to_float2(h0), v1 = e4m3x2_to_float2(h1);
+      *reinterpret_cast<uint32_t*>(r + 4 * lane) = (uint32_t)h0 | ((uint32_t)h1 << 16);
+      *reinterpret_cast<uint32_t*>(r + 128 + 4 * lane) =
+          (uint32_t)pack_e4m3x2(a.x * ps - v0.x, a.y * ps - v0.y) |
+          ((uint32_t)pack_e4m3x2(b.x * ps - v1.x, b.y * ps - v1.y) << 16);
+    } else {
+      *reinterpret_cast<uint32_t*>(r + 2 * q_place<FMT, QM>(4 * lane)) = pack_f16x2(a.x * ps, a.y * ps);
+      *reinterpret_cast<uint32_t*>(r + 2 * q_place<FMT, QM>(4 * lane + 2)) = pack_f16x2(b.x * ps, b.y * ps);
+    }
+    // A query row that is not finite has no finite logits; the reduced formats
+    // would hide that.  (The factor is kept off zero: it multiplies -inf.)
+    const bool any_bad = __any_sync(0xffffffffu, bad);
+    if (lane == 0) cf[row] = any_bad ? __int_as_float(0x7fc00000) : fmaxf(pow2i(-e) * cst, 1.2e-38f);
   }
-  if constexpr (R8) colf[1] = 0.f;
 }
 
-// S of KC keys from key row kb of the tile.
-template <int FMT, bool R8, int SP, bool NVR, int KC>
-__device__ __forceinline__ void logits(const uint8_t* stg, const uint8_t* sc, int kb, int lane,
-                                       const uint32_t (&a)[SP][QRegs<FMT>::KS][4], float (&sacc)[KC / 8][4]) {
+// Lane addresses into a stage's tiles.  Rows are swizzled: the 16-byte chunk c of
+// row r sits at chunk c ^ (r & 7) (128-byte rows) or c ^ ((r >> 1) & 3) (64-byte
+// rows), so stepping through a row is an XOR on bits 4 to 6 of the address and
+// stepping by 8 rows leaves the swizzle alone.
+template <int FMT>
+__device__ __forceinline__ uint32_t k_lane(uint32_t tile, int lane) {
+  if constexpr (FMT == FMT_NVFP4) {
+    const int g8 = lane >> 2, j = lane & 3;  // 16 bytes of key g8
+    return tile + g8 * 64 + ((j ^ ((g8 >> 1) & 3)) << 4);
+  } else {
+    return tile + (lane & 7) * 128 + (((lane >> 3) ^ (lane & 7)) << 4);  // ldmatrix: 8 keys x 4 chunks
+  }
+}
+template <int FMT>
+__device__ __forceinline__ uint32_t v_lane(uint32_t tile, int lane) {  // ldmatrix.trans: 16 keys x 2 chunks
+  const int row = (lane & 7) + (lane & 8);
+  if constexpr (FMT == FMT_NVFP4) return tile + row * 64 + (((lane >> 4) ^ ((lane >> 1) & 3)) << 4);
+  else return tile + row * 128 + (((lane >> 4) ^ (lane & 7)) << 4);
+}
+
+// S of KC keys from key row kb of the tile.  kl: k_lane of the tile; ql[m]: this
+// lane's ldmatrix address of the query rows of tile m.  REG: the fragments are in aq.
+template <int FMT, int QM, bool NVR, int KC, int MT, bool REG>
+__device__ __forceinline__ void logits(uint32_t kl, const uint8_t* ksc, const uint32_t (&ql)[MT], int kb, int lane,
+                                       const uint32_t (&aq)[QRegs<QM>::KS][4], float (&sacc)[KC / 8][MT][4]) {
   using TR = DenseTraits<FMT>;
-  const uint32_t kt = smem_u32(stg);
+  constexpr int NT = KC / 8;
+  kl += kb * (FMT == FMT_NVFP4 ? 64 : 128);
 #pragma unroll
-  for (int t = 0; t < KC / 8; ++t) {
-    sacc[t][0] = sacc[t][1] = sacc[t][2] = sacc[t][3] = 0.f;
-    if constexpr (FMT == FMT_FP8) {
-      const int row = kb + 8 * t + (lane & 7);
+  for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int kp = 0; kp < 2; ++kp) {
-        uint32_t b[4];
-        ldmatrix_x4(b, swz128(kt, row, 4 * kp + (lane >> 3)));
-        mma_e4m3_k32(sacc[t], a[0][2 * kp], b[0], b[1]);
-        mma_e4m3_k32(sacc[t], a[0][2 * kp + 1], b[2], b[3]);
-        if constexpr (SP == 2) {
-          mma_e4m3_k32(sacc[t], a[1][2 * kp], b[0], b[1]);
-          mma_e4m3_k32(sacc[t], a[1][2 * kp + 1], b[2], b[3]);
-        }
-      }
-    } else if constexpr (FMT == FMT_BF16) {
-      const int row = kb + 8 * t + (lane & 7);
-      float s2[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int m = 0; m < MT; ++m) sacc[t][m][0] = sacc[t][m][1] = sacc[t][m][2] = sacc[t][m][3] = 0.f;
+  if constexpr (FMT == FMT_NVFP4) {
+    const uint8_t* sc = ksc + (kb + (lane >> 2)) * 8 + 2 * (lane & 3);
+    uint32_t w[NT][4], s2[NT];
 #pragma unroll
-      for (int kp = 0; kp < 4; ++kp) {
-        uint32_t b[4];
-        ldmatrix_x4(b, swz128(kt + (kp >> 1) * (TR::SK * 128), row, 4 * (kp & 1) + (lane >> 3)));
-        mma_bf16_k16(sacc[t], a[0][2 * kp], b[0], b[1]);
-        mma_bf16_k16(s2, a[0][2 * kp + 1], b[2], b[3]);
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) sacc[t][e] += s2[e];
-    } else {
-      const int g8 = lane >> 2, j = lane & 3;
-      const int row = kb + 8 * t + g8;
-      uint4 w;
+    for (int t = 0; t < NT; ++t) {
       asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                   : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
-                   : "r"(swz64(kt, row, j)));
-      const uint32_t s2 = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(sc + row * 8 + 2 * j));
-      const uint32_t sA = __byte_perm(s2, s2, 0x1010), sB = __byte_perm(s2, s2, 0x3232);
-      const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+                   : "=r"(w[t][0]), "=r"(w[t][1]), "=r"(w[t][2]), "=r"(w[t][3])
+                   : "r"(kl + t * 512));
+      s2[t] = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(sc + t * 64));
+    }
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {  // 8 dims: two k steps
+    for (int q = 0; q < 4; ++q) {  // 8 dims: two k steps
+      uint32_t a[2][MT][4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          if constexpr (REG) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) a[i][m][e] = aq[2 * q + i][e];
+          } else {
+            ldmatrix_x4(a[i][m], ql[m] + (2 * q + i) * 32);
+          }
+        }
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const uint32_t sd = q < 2 ? __byte_perm(s2[t], s2[t], 0x1010) : __byte_perm(s2[t], s2[t], 0x3232);
         uint32_t h[4];
-        e2m1x8_to_f16(ww[q], h);
+        e2m1x8_to_f16(w[t][q], h);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          h[i] = hmul2(h[i], q < 2 ? sA : sB);
+          h[i] = hmul2(h[i], sd);
           if constexpr (NVR) h[i] = e4m3_round_f16x2(h[i]);
         }
-        mma_f16_k16(sacc[t], a[0][2 * q], h[0], h[1]);
-        mma_f16_k16(sacc[t], a[0][2 * q + 1], h[2], h[3]);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          mma_f16_k16(sacc[t][m], a[0][m], h[0], h[1]);
+          mma_f16_k16(sacc[t][m], a[1][m], h[2], h[3]);
+        }
+      }
+    }
+  } else if constexpr (QRegs<QM>::E4) {
+#pragma unroll
+    for (int kp = 0; kp < 2; ++kp) {
+      uint32_t a[2][2][MT][4];  // [step][term]
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          if constexpr (REG) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) a[i][0][m][e] = aq[2 * kp + i][e];
+          } else {
+            ldmatrix_x4(a[i][0][m], ql[m] + (2 * kp + i) * 32);
+            if constexpr (QM == QM_E4X2) ldmatrix_x4(a[i][1][m], ql[m] + 128 + (2 * kp + i) * 32);
+          }
+        }
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        uint32_t b[4];
+        ldmatrix_x4(b, (kl ^ (kp << 6)) + t * 1024);
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            mma_e4m3_k32(sacc[t][m], a[i][0][m], b[2 * i], b[2 * i + 1]);
+            if constexpr (QM == QM_E4X2) mma_e4m3_k32(sacc[t][m], a[i][1][m], b[2 * i], b[2 * i + 1]);
+          }
+      }
+    }
+  } else {
+    // 16-bit steps: a load brings two (BF16) or four (FP8 widened) of them
+    constexpr int STEPS = QM == QM_F16K ? 4 : 2;
+#pragma unroll
+    for (int kp = 0; kp < 8 / STEPS; ++kp) {
+      uint32_t a[STEPS][MT][4];
+#pragma unroll
+      for (int i = 0; i < STEPS; ++i)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          if constexpr (REG) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) a[i][m][e] = aq[STEPS * kp + i][e];
+          } else {
+            ldmatrix_x4(a[i][m], ql[m] + (STEPS * kp + i) * 32);
+          }
+        }
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        uint32_t b[4];
+        if constexpr (QM == QM_F16K) {
+          ldmatrix_x4(b, (kl ^ (kp << 6)) + t * 1024);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t b0 = e4m3x2_to_f16x2(b[i]), b1 = e4m3x2_hi_to_f16x2(b[i]);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) mma_f16_k16(sacc[t][m], a[i][m], b0, b1);
+          }
+        } else {
+          ldmatrix_x4(b, (kl ^ ((kp & 1) << 6)) + (kp >> 1) * (TR::SK * 128) + t * 1024);
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int m = 0; m < MT; ++m) mma_bf16_k16(sacc[t][m], a[i][m], b[2 * i], b[2 * i + 1]);
+        }
       }
     }
   }
 }
 
-// One accumulator tile += A B.  MASK: only the rows that are kept (0 x NaN is NaN
-// in every row of a product).
-template <int FMT, bool R8, bool MASK>
-__device__ __forceinline__ void mma_rows(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, bool keep0,
-                                         bool keep1) {
-  if constexpr (!MASK) {
+// One accumulator tile += A B.  SOME: only the columns 2j (keep 1) and 2j + 1
+// (keep 2) that are named (0 x NaN is NaN in every column of a product).
+template <int FMT, bool SOME>
+__device__ __forceinline__ void mma_cols(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, int keep) {
+  if constexpr (!SOME) {
     if constexpr (FMT == FMT_BF16) mma_bf16_k16(d, a, b0, b1);
     else mma_f16_k16(d, a, b0, b1);
   } else {
     float t[4] = {d[0], d[1], d[2], d[3]};
     if constexpr (FMT == FMT_BF16) mma_bf16_k16(t, a, b0, b1);
     else mma_f16_k16(t, a, b0, b1);
-    d[0] = keep0 ? t[0] : d[0];
-    d[1] = keep0 ? t[1] : d[1];
-    d[2] = (R8 ? keep0 : keep1) ? t[2] : d[2];
-    d[3] = (R8 ? keep0 : keep1) ? t[3] : d[3];
+    d[0] = keep & 1 ? t[0] : d[0];
+    d[1] = keep & 2 ? t[1] : d[1];
+    d[2] = keep & 1 ? t[2] : d[2];
+    d[3] = keep & 2 ? t[3] : d[3];
   }
 }
 
-// O += P V over 16 keys from key row kb; pa (and pl, the lo terms of bf16) are
-// P's A fragments.  MASK: V of the keys beyond row klim of the tile counts as 0,
-// and only the lane's rows g8 (keep0) and g8 + 8 (keep1) are added to.
-template <int FMT, bool R8, bool NVR, bool MASK>
-__device__ __forceinline__ void pv16(const uint8_t* stg, const uint8_t* vs, int kb, int klim, int lane, const uint32_t (&pa)[4],
-                                     const uint32_t (&pl)[4], float (&o)[16][4], bool keep0, bool keep1) {
+// O^T += V^T P over 16 keys from key row kb.  vl: v_lane of the tile; pb[n][2]: P's
+// B fragments of column tile n (pl: the lo terms of bf16).  MASK: V of the keys
+// beyond row klim of the tile counts as 0, and keep[n] names the columns added to.
+template <int FMT, int NN, bool NVR, bool MASK>
+__device__ __forceinline__ void pv16(uint32_t vl, const uint8_t* vs, int kb, int klim, int lane,
+                                     const uint32_t (&pb)[NN][2], const uint32_t (&pl)[NN][2], float (&o)[8][NN][4],
+                                     const int (&keep)[NN]) {
   using TR = DenseTraits<FMT>;
-  const uint32_t vt = smem_u32(stg + TR::TILE);
   const int j = lane & 3;
-  const int mrow = kb + (lane & 7) + ((lane >> 3) & 1) * 8, mch = lane >> 4;
+  vl += kb * (FMT == FMT_NVFP4 ? 64 : 128);
   uint32_t m0 = 0xffffffffu, m1 = 0xffffffffu;  // keys 2j, 2j + 1 and 2j + 8, 2j + 9 of the step
   if constexpr (MASK) {
     const int k = kb + 2 * j;
@@ -581,38 +694,38 @@ __device__ __forceinline__ void pv16(const uint8_t* stg, const uint8_t* vs, int 
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       uint32_t r[4];
-      ldmatrix_x4_trans(r, swz128(vt, mrow, 2 * c + mch));
+      ldmatrix_x4_trans(r, vl ^ (c << 5));
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
+        // a register holds two dims of two keys: rows g8 take the even dim, rows g8 + 8 the odd one
         const uint32_t x0 = __byte_perm(r[2 * q], 0u, 0x3120), x1 = __byte_perm(r[2 * q + 1], 0u, 0x3120);
-        uint32_t b0 = e4m3x2_to_f16x2(x0), b1 = e4m3x2_to_f16x2(x1);
-        uint32_t d0 = e4m3x2_hi_to_f16x2(x0), d1 = e4m3x2_hi_to_f16x2(x1);
+        uint32_t a[4] = {e4m3x2_to_f16x2(x0), e4m3x2_hi_to_f16x2(x0), e4m3x2_to_f16x2(x1), e4m3x2_hi_to_f16x2(x1)};
         if constexpr (MASK) {
-          b0 &= m0;
-          d0 &= m0;
-          b1 &= m1;
-          d1 &= m1;
+          a[0] &= m0;
+          a[1] &= m0;
+          a[2] &= m1;
+          a[3] &= m1;
         }
-        mma_rows<FMT, R8, MASK>(o[2 * (2 * c + q)], pa, b0, b1, keep0, keep1);
-        mma_rows<FMT, R8, MASK>(o[2 * (2 * c + q) + 1], pa, d0, d1, keep0, keep1);
+#pragma unroll
+        for (int n = 0; n < NN; ++n) mma_cols<FMT, MASK>(o[2 * c + q][n], a, pb[n][0], pb[n][1], keep[n]);
       }
     }
   } else if constexpr (FMT == FMT_BF16) {
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
       uint32_t r[4];
-      ldmatrix_x4_trans(r, swz128(vt + (c >> 2) * (TR::SK * 128), mrow, 2 * (c & 3) + mch));
+      ldmatrix_x4_trans(r, (vl ^ ((c & 3) << 5)) + (c >> 2) * (TR::SK * 128));
+      uint32_t a[4] = {r[0], r[2], r[1], r[3]};
       if constexpr (MASK) {
-        r[0] &= m0;
-        r[1] &= m1;
-        r[2] &= m0;
-        r[3] &= m1;
+        a[0] &= m0;
+        a[1] &= m0;
+        a[2] &= m1;
+        a[3] &= m1;
       }
-      mma_rows<FMT, R8, MASK>(o[2 * c], pa, r[0], r[1], keep0, keep1);
-      mma_rows<FMT, R8, MASK>(o[2 * c + 1], pa, r[2], r[3], keep0, keep1);
-      if constexpr (!R8) {
-        mma_rows<FMT, R8, MASK>(o[2 * c], pl, r[0], r[1], keep0, keep1);
-        mma_rows<FMT, R8, MASK>(o[2 * c + 1], pl, r[2], r[3], keep0, keep1);
+#pragma unroll
+      for (int n = 0; n < NN; ++n) {
+        mma_cols<FMT, MASK>(o[c][n], a, pb[n][0], pb[n][1], keep[n]);
+        mma_cols<FMT, MASK>(o[c][n], a, pl[n][0], pl[n][1], keep[n]);
       }
     }
   } else {
@@ -642,11 +755,11 @@ __device__ __forceinline__ void pv16(const uint8_t* stg, const uint8_t* vs, int 
 #pragma unroll
     for (int cp = 0; cp < 2; ++cp) {
       uint32_t r[4];
-      ldmatrix_x4_trans(r, swz64(vt, mrow, 2 * cp + mch));
+      ldmatrix_x4_trans(r, vl ^ (cp << 5));
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         const int c = 2 * cp + q;
-        uint32_t bb[2][4];
+        uint32_t bb[2][4];  // [key half][dim 4 g8 + i of chunk c]
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t x[4];  // key 2j: dims 0,1 / 2,3; key 2j + 1: dims 0,1 / 2,3
@@ -661,7 +774,11 @@ __device__ __forceinline__ void pv16(const uint8_t* stg, const uint8_t* vs, int 
           }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) mma_rows<FMT, R8, MASK>(o[4 * c + i], pa, bb[0][i], bb[1][i], keep0, keep1);
+        for (int u = 0; u < 2; ++u) {
+          const uint32_t a[4] = {bb[0][2 * u], bb[0][2 * u + 1], bb[1][2 * u], bb[1][2 * u + 1]};
+#pragma unroll
+          for (int n = 0; n < NN; ++n) mma_cols<FMT, MASK>(o[2 * c + u][n], a, pb[n][0], pb[n][1], keep[n]);
+        }
       }
     }
   }
@@ -690,289 +807,330 @@ __device__ __forceinline__ bool v_not_finite(const uint8_t* stg, const uint8_t* 
   return __any_sync(0xffffffffu, bad);
 }
 
-// The first of the consecutive dims that o[t][0..3] of lane j belong to is
-//   FP8    16 (t / 2) + 4j + (t & 1) + 2e   BF16  8 t + 2j + e   NVFP4  32 (t / 4) + 8j + (t & 3) + 4e
-// for the accumulator columns e = 0, 1.
+// The output dim of accumulator tile mt's row g8 (half 0) or g8 + 8 (half 1).
 template <int FMT>
-__device__ __forceinline__ int out_dim(int t, int e, int j) {
-  if constexpr (FMT == FMT_FP8) return 16 * (t >> 1) + 4 * j + (t & 1) + 2 * e;
-  else if constexpr (FMT == FMT_BF16) return 8 * t + 2 * j + e;
-  else return 32 * (t >> 2) + 8 * j + (t & 3) + 4 * e;
+__device__ __forceinline__ int out_dim(int mt, int half, int g8) {
+  if constexpr (FMT == FMT_FP8) return 16 * mt + 2 * g8 + half;
+  else if constexpr (FMT == FMT_BF16) return 16 * mt + 8 * half + g8;
+  else return 32 * (mt >> 1) + 4 * g8 + 2 * (mt & 1) + half;
 }
 
-template <int FMT, int NT, bool R8, int SP, bool NVR>
-__device__ void consumer(const DenseParams& p, uint8_t* base, uint64_t* full, uint64_t* empty, uint64_t* ifull,
-                         uint64_t* iempty, int* dead, const DenseFacts* facts, const int* stage_ok, int warp, int lane) {
+template <int FMT, int NN, int NCG, int QM, bool NVR>
+__device__ void consumer(const DenseParams& p, const DenseTeam& tm, int bar, int warp, int lane) {
   using TR = DenseTraits<FMT>;
-  using LY = DenseLayout<FMT, NT, R8>;
-  constexpr int NST = LY::NST;
-  constexpr int KGW = kDenseWpg / NT;          // warps of a group that share a column tile
+  using LY = DenseLayout<FMT, NN, NCG>;
+  constexpr int NST = LY::NST, MT = LY::MT, KGW = LY::KGW;
   constexpr int KW = TR::SK / KGW;             // keys of a warp in a unit
   constexpr int KC = KW < 32 ? KW : 32;        // keys a softmax step takes
-  constexpr int NR = R8 ? 1 : 2;               // rows of a lane
   constexpr bool F16P = FMT != FMT_BF16;
-  const int grp = warp / kDenseWpg, sub = warp % kDenseWpg;
-  const int ct = sub / KGW, kw = (sub % KGW) * KW;
+  constexpr float SHIFT = F16P ? kDensePShift : 0.f;
+  constexpr bool REG = NN == 1;                // query fragments held in registers
+  constexpr int TEAM_THREADS = 32 * kDenseWpg;
+  const int ct = warp / KGW, kw = (warp % KGW) * KW;  // column group, first key
   const int tid = warp * 32 + lane;
   const int g8 = lane >> 2, j = lane & 3;
   const int H = p.G * p.r;
-  float* mo = reinterpret_cast<float*>(base + LY::MERGE);   // [warps][TR rows][MROW]
-  float* ml = reinterpret_cast<float*>(base + LY::ML);      // [warps][TR rows][2]
-  int bi = 0;
+  int* dead = tm.dead;
+  float* mo = reinterpret_cast<float*>(tm.mem + LY::MERGE);   // [warps][WROWS][MROW]
+  float* ml = reinterpret_cast<float*>(tm.mem + LY::ML);      // [warps][WROWS][2]
+  float* cf = reinterpret_cast<float*>(tm.mem + LY::CF);      // [ROWS]
+  int st = 0;
+  uint32_t par = 0;
 #pragma unroll 1
   for (int ii = 0;; ++ii) {
     const int slot = ii & 1;
-    const bool got = ring_wait(&ifull[slot], (uint32_t)((ii >> 1) & 1), dead);
+    const bool got = ring_wait(&tm.ifull[slot], (uint32_t)((ii >> 1) & 1), dead);
     if (!got) set_dead(dead, p.status, ii);
-    if (named_bar_or(1, kDenseConsumers, !got)) break;  // every consumer warp leaves together
-    const DenseFacts f = facts[slot];
+    if (named_bar_or(bar, TEAM_THREADS, !got)) break;  // the team's consumers leave together
+    const DenseFacts f = tm.facts[slot];
     if (f.n < 0) break;
-    const int c0 = f.cg * LY::ROWS;
-    const int nrows = p.cols - c0 < LY::ROWS ? p.cols - c0 : LY::ROWS;
-    uint32_t aq[SP][QRegs<FMT>::KS][4];
-    float colf[2];
-    load_q<FMT, R8, SP, LY::QROW>(base + LY::Q + (size_t)slot * LY::QSLOT, 16 * ct, nrows, p.q_fp8 != 0, p.q_scale, p.col_const,
-                        lane, aq, colf);
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&iempty[slot]);
-
-    int qi[2], qlim[2];
-    float m_run[2], l_run[2];
+    const int c0 = f.cg * p.cper;
+    const int nrows = p.cols - c0 < p.cper ? p.cols - c0 : p.cper;
+    uint8_t* qs = tm.mem + LY::Q + (size_t)slot * LY::QSLOT;
+    convert_q<FMT, QM, LY::QROW>(qs, cf, nrows, LY::ROWS, p.q_fp8 != 0, p.q_scale, p.col_const, warp, lane);
+    named_bar_sync(bar, TEAM_THREADS);
+    // ldmatrix addresses of the query tiles: row (lane & 7) + (lane & 8), column half
+    // lane >> 4.  Where a tile has 8 rows only, the other 8 are the lo terms
+    // (QM_ROWS) or repeat them and are not used.
+    uint32_t ql[MT];
 #pragma unroll
-    for (int rr = 0; rr < 2; ++rr) {
-      const int row = 16 * ct + g8 + 8 * rr;
-      qi[rr] = (c0 + row) / p.r;
-      qlim[rr] = row < nrows ? f.T - p.Q + qi[rr] : -1;
-      m_run[rr] = -INFINITY;
-      l_run[rr] = 0.f;
+    for (int m = 0; m < MT; ++m) {
+      const bool half = 2 * m + 1 == NN;
+      int off = (lane >> 4) * 16;
+      if (half && QM == QM_ROWS && (lane & 8)) off += 128;
+      ql[m] = smem_u32(qs) + (ct * LY::WROWS + 16 * m + (lane & 7) + (half ? 0 : (lane & 8))) * LY::QROW + off;
     }
-    float o[16][4];
+    uint32_t aq[QRegs<QM>::KS][4];
+    if constexpr (REG) {
 #pragma unroll
-    for (int t = 0; t < 16; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
+      for (int ks = 0; ks < QRegs<QM>::KS; ++ks) {
+        ldmatrix_x4(aq[ks], ql[0] + ks * 32);
+        if constexpr (QM != QM_ROWS) aq[ks][1] = aq[ks][3] = 0u;
+      }
+    }
+
+    // row state: the reference m_run (log2 domain) and the raw logit that moves it
+    float m_run[NN], msub[NN], ylim[NN], colf[NN];
+    float2 l_run[NN];
+#pragma unroll
+    for (int n = 0; n < NN; ++n) {
+      m_run[n] = -INFINITY;
+      ylim[n] = -INFINITY;
+      msub[n] = 0.f;
+      l_run[n] = make_float2(0.f, 0.f);
+      colf[n] = cf[ct * LY::WROWS + 8 * n + g8];
+    }
+    float o[8][NN][4];
+#pragma unroll
+    for (int t = 0; t < 8; ++t)
+#pragma unroll
+      for (int n = 0; n < NN; ++n) o[t][n][0] = o[t][n][1] = o[t][n][2] = o[t][n][3] = 0.f;
     int ev = 0;           // FP8: P carries vscale x 2^ev
-    bool ev_set = false;
+    float fe = 0.f;       // 2^ev, 0: not chosen yet
     const int lim0 = f.T - p.Q;  // every row sees the keys up to here
 
 #pragma unroll 1
-    for (int k = f.k0; k < f.k0 + f.n; ++k, ++bi) {
-      if ((bi & (kDenseGroups - 1)) != grp) continue;
-      const int st = bi % NST;
-      const bool have = ring_wait(&full[st], (uint32_t)((bi / NST) & 1), dead);
+    for (int k = f.k0; k < f.k0 + f.n; ++k) {
+      const bool have = ring_wait(&tm.full[st], par, dead);
       if (!have) set_dead(dead, p.status, f.s);
-      const uint8_t* stg = base + (size_t)st * LY::STAGE;
-      const uint8_t* ksc = base + LY::SC + (size_t)st * LY::SCALES;  // scales of K, then of V
+      const uint32_t stg = smem_u32(tm.tiles + (size_t)st * LY::STAGE);
+      const uint8_t* ksc = tm.mem + LY::SC + (size_t)st * LY::SCALES;  // scales of K, then of V
       const uint8_t* vsb = ksc + TR::SC;
-      if (have && stage_ok[st]) {
+      if (have && tm.stage_ok[st]) {
+        const uint32_t kl = k_lane<FMT>(stg, lane), vl = v_lane<FMT>(stg + TR::TILE, lane);
 #pragma unroll 1
         for (int kb = kw; kb < kw + KW; kb += KC) {
           const int key0 = k * TR::SK + kb;  // position of the step's first key
           if (key0 >= f.T) break;
-          float sacc[KC / 8][4];
-          logits<FMT, R8, SP, NVR, KC>(stg, ksc, kb, lane, aq, sacc);
+          float sacc[KC / 8][MT][4];
+          logits<FMT, QM, NVR, KC, MT, REG>(kl, ksc, ql, kb, lane, aq, sacc);
           const bool masked = key0 + KC - 1 > lim0;
-          // ---- scale and mask, the row's new maximum
-          float mx[2] = {-INFINITY, -INFINITY};
+          // ---- raw logits y (x = y colf), masked; does any pass the reference?
+          float2 y[KC / 8][NN];
 #pragma unroll
           for (int t = 0; t < KC / 8; ++t) {
             float2 ks = make_float2(1.f, 1.f);
-            if constexpr (FMT == FMT_FP8)
-              ks = lds_f2(reinterpret_cast<const float*>(ksc) + kb + 8 * t + 2 * j);
-            if constexpr (R8 && FMT == FMT_FP8) {  // hi + lo terms
-              sacc[t][0] += sacc[t][2];
-              sacc[t][1] += sacc[t][3];
-            }
+            if constexpr (FMT == FMT_FP8) ks = lds_f2(reinterpret_cast<const float*>(ksc) + kb + 8 * t + 2 * j);
 #pragma unroll
-            for (int rr = 0; rr < NR; ++rr) {
-              float x0 = sacc[t][2 * rr] * (ks.x * colf[rr]), x1 = sacc[t][2 * rr + 1] * (ks.y * colf[rr]);
-              if (masked) {
-                const int key = key0 + 8 * t + 2 * j;
-                x0 = key <= qlim[rr] ? x0 : -INFINITY;
-                x1 = key + 1 <= qlim[rr] ? x1 : -INFINITY;
+            for (int n = 0; n < NN; ++n) {
+              float2 v = make_float2(sacc[t][n >> 1][2 * (n & 1)], sacc[t][n >> 1][2 * (n & 1) + 1]);
+              if constexpr (QM == QM_ROWS) v = add2(v, make_float2(sacc[t][0][2], sacc[t][0][3]));  // hi + lo terms
+              if constexpr (FMT == FMT_FP8) v = mul2(v, ks);
+              y[t][n] = v;
+            }
+          }
+          if (masked) {
+#pragma unroll
+            for (int n = 0; n < NN; ++n) {
+              const int row = ct * LY::WROWS + 8 * n + g8;
+              const int lim = row < nrows ? lim0 + (c0 + row) / p.r - key0 : -1;
+#pragma unroll
+              for (int t = 0; t < KC / 8; ++t) {
+                if (8 * t + 2 * j > lim) y[t][n].x = -INFINITY;
+                if (8 * t + 2 * j + 1 > lim) y[t][n].y = -INFINITY;
               }
-              sacc[t][2 * rr] = x0;
-              sacc[t][2 * rr + 1] = x1;
-              mx[rr] = fmaxf(mx[rr], fmaxf(x0, x1));
             }
           }
-          float msub[2], alpha[2];
-          bool grew = false;
+          float mx[NN];
+          bool over = false;
 #pragma unroll
-          for (int rr = 0; rr < NR; ++rr) {
-            mx[rr] = fmaxf(mx[rr], __shfl_xor_sync(0xffffffffu, mx[rr], 1));
-            mx[rr] = fmaxf(mx[rr], __shfl_xor_sync(0xffffffffu, mx[rr], 2));
-            const float mnew = fmaxf(m_run[rr], mx[rr]);
-            msub[rr] = mnew == -INFINITY ? 0.f : mnew;
-            alpha[rr] = ex2(m_run[rr] - msub[rr]);
-            grew |= mnew != m_run[rr];
-            m_run[rr] = mnew;
-            if constexpr (F16P) msub[rr] -= kDensePShift;
+          for (int n = 0; n < NN; ++n) {
+            mx[n] = fmaxf(y[0][n].x, y[0][n].y);
+#pragma unroll
+            for (int t = 1; t < KC / 8; ++t) mx[n] = max3(mx[n], y[t][n].x, y[t][n].y);
+            over |= mx[n] > ylim[n];
           }
-          // ---- FP8: the power of two that keeps P x vscale in f16's range
-          float resc = 1.f;
-          const float* vsc = reinterpret_cast<const float*>(vsb) + kb;
-          float fe = 1.f;
+          // ---- FP8: V's scales; does P x vscale x 2^ev keep to f16's range?
+          float2 vs[KC / 8];
           if constexpr (FMT == FMT_FP8) {
             float vm = 0.f;
-            if (lane < KC && key0 + lane < f.T) vm = fabsf(vsc[lane]);
-            vm = vm <= 3.0e38f ? vm : 0.f;
 #pragma unroll
-            for (int s = 16; s > 0; s >>= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, s));
-            const float cur = vm * pow2i(ev);
-            if (!ev_set || cur > 2.f || cur < 0.00390625f) {
-              if (vm > 0.f) {
+            for (int t = 0; t < KC / 8; ++t) {
+              vs[t] = lds_f2(reinterpret_cast<const float*>(vsb) + kb + 8 * t + 2 * j);
+              if (masked) {  // the scale of a row that holds no key may be anything
+                if (key0 + 8 * t + 2 * j >= f.T) vs[t].x = 0.f;
+                if (key0 + 8 * t + 2 * j + 1 >= f.T) vs[t].y = 0.f;
+              }
+              vm = max3(vm, fabsf(vs[t].x), fabsf(vs[t].y));
+            }
+            over |= vm * fe > 1.f || fe == 0.f;
+            if (!__any_sync(0xffffffffu, vm * fe >= 0.00390625f)) over = true;
+          }
+          if (__any_sync(0xffffffffu, over)) {
+            // the row's new reference, and the power of two of V's scales
+            float resc = 1.f;
+            if constexpr (FMT == FMT_FP8) {
+              float vm = 0.f;
+#pragma unroll
+              for (int t = 0; t < KC / 8; ++t) {
+                const float v0 = fabsf(vs[t].x), v1 = fabsf(vs[t].y);
+                vm = max3(vm, v0 <= 3.0e38f ? v0 : 0.f, v1 <= 3.0e38f ? v1 : 0.f);
+              }
+              vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 1));
+              vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 2));
+              const float cur = vm * fe;
+              if (vm > 0.f && (fe == 0.f || cur > 1.f || cur < 0.00390625f)) {
                 const int be = (int)(__float_as_uint(vm) >> 23) - 127;  // vm in [2^be, 2^(be + 1))
                 int en = -3 - be;                                      // vm x 2^en in [1/8, 1/4)
                 en = en < -126 ? -126 : (en > 120 ? 120 : en);
-                if (ev_set) {
-                  const int de = en - ev < -126 ? -126 : (en - ev > 126 ? 126 : en - ev);
-                  resc = pow2i(de);
-                  grew = true;
-                }
+                const int de = en - ev < -126 ? -126 : (en - ev > 126 ? 126 : en - ev);
+                if (fe != 0.f) resc = pow2i(de);
                 ev = en;
-                ev_set = true;
+                fe = pow2i(en);
               }
             }
-            fe = pow2i(ev);
-          }
-          if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
-            for (int rr = 0; rr < NR; ++rr) {
-              l_run[rr] *= alpha[rr];
-              const float w = alpha[rr] * resc;
+            for (int n = 0; n < NN; ++n) {
+              mx[n] = fmaxf(mx[n], __shfl_xor_sync(0xffffffffu, mx[n], 1));
+              mx[n] = fmaxf(mx[n], __shfl_xor_sync(0xffffffffu, mx[n], 2));
+              const float mnew = fmaxf(m_run[n], mx[n] * colf[n]);
+              const float ref = mnew == -INFINITY ? 0.f : mnew;
+              const float alpha = ex2(m_run[n] - ref);  // the first time 0 x 0
+              m_run[n] = mnew;
+              msub[n] = ref - SHIFT;
+              ylim[n] = (mnew + kDenseLazy) / colf[n];
+              l_run[n].x *= alpha;
+              l_run[n].y *= alpha;
+              // the accumulators hold the columns 2j, 2j + 1
+              const float w0 = __shfl_sync(0xffffffffu, alpha, 8 * j) * resc;
+              const float w1 = __shfl_sync(0xffffffffu, alpha, 8 * j + 4) * resc;
 #pragma unroll
-              for (int t = 0; t < 16; ++t) {
-                o[t][2 * rr] *= w;
-                o[t][2 * rr + 1] *= w;
-                if constexpr (R8 && FMT == FMT_BF16) {  // the lo terms' rows belong to the same column
-                  o[t][2] *= w;
-                  o[t][3] *= w;
-                }
+              for (int t = 0; t < 8; ++t) {
+                o[t][n][0] *= w0;
+                o[t][n][1] *= w1;
+                o[t][n][2] *= w0;
+                o[t][n][3] *= w1;
               }
             }
           }
           // ---- P, its row sums, and P's fragments: keys 2j, 2j + 1 of tile t
-          uint32_t ph[KC / 8][2], plo[KC / 8][2];
+          uint32_t ph[KC / 8][NN], plo[KC / 8][NN];
 #pragma unroll
           for (int t = 0; t < KC / 8; ++t) {
-            float2 vs = make_float2(fe, fe);
-            if constexpr (FMT == FMT_FP8) {
-              const float2 v = lds_f2(vsc + 8 * t + 2 * j);
-              vs.x *= v.x;
-              vs.y *= v.y;
-              if (masked) {  // the scale of a row that holds no key may be anything
-                const int key = key0 + 8 * t + 2 * j;
-                vs.x = key < f.T ? vs.x : 0.f;
-                vs.y = key + 1 < f.T ? vs.y : 0.f;
-              }
-            }
+            float2 w = make_float2(1.f, 1.f);
+            if constexpr (FMT == FMT_FP8) w = mul2(vs[t], make_float2(fe, fe));
 #pragma unroll
-            for (int rr = 0; rr < NR; ++rr) {
-              float p0 = ex2(sacc[t][2 * rr] - msub[rr]), p1 = ex2(sacc[t][2 * rr + 1] - msub[rr]);
-              l_run[rr] += p0 + p1;
+            for (int n = 0; n < NN; ++n) {
+              const float2 x = fma2(y[t][n], make_float2(colf[n], colf[n]), make_float2(-msub[n], -msub[n]));
+              float2 q = make_float2(ex2(x.x), ex2(x.y));
+              l_run[n] = add2(l_run[n], q);
               if constexpr (FMT == FMT_FP8) {
+                const float2 v = mul2(q, w);
                 if (masked) {  // a masked weight stays 0 beside a scale that is not finite
-                  p0 = p0 == 0.f ? 0.f : p0 * vs.x;
-                  p1 = p1 == 0.f ? 0.f : p1 * vs.y;
+                  q.x = q.x == 0.f ? 0.f : v.x;
+                  q.y = q.y == 0.f ? 0.f : v.y;
                 } else {
-                  p0 *= vs.x;
-                  p1 *= vs.y;
+                  q = v;
                 }
               }
               if constexpr (F16P) {
-                ph[t][rr] = pack_f16x2(p0, p1);
-                plo[t][rr] = 0u;
+                ph[t][n] = pack_f16x2(q.x, q.y);
+                plo[t][n] = 0u;
               } else {
-                const uint32_t h = pack_bf16x2(p0, p1);
-                ph[t][rr] = h;
-                plo[t][rr] = pack_bf16x2(p0 - __uint_as_float(h << 16), p1 - __uint_as_float(h & 0xffff0000u));
+                const uint32_t h = pack_bf16x2(q.x, q.y);
+                const float2 hv = bf16x2_to_float2(h);
+                ph[t][n] = h;
+                plo[t][n] = pack_bf16x2(q.x - hv.x, q.y - hv.y);
               }
             }
           }
-          // ---- O += P V
-#define MSA_DENSE_PV(MASK, KLIM, KEEP0, KEEP1)                                               \
-  _Pragma("unroll") for (int h = 0; h < KC / 16; ++h) {                                      \
-    /* R8: rows 8 to 15 hold the lo terms of rows 0 to 7 */                                  \
-    const uint32_t pa[4] = {ph[2 * h][0], R8 ? plo[2 * h][0] : ph[2 * h][NR - 1],            \
-                            ph[2 * h + 1][0], R8 ? plo[2 * h + 1][0] : ph[2 * h + 1][NR - 1]}; \
-    const uint32_t pl[4] = {plo[2 * h][0], plo[2 * h][NR - 1], plo[2 * h + 1][0], plo[2 * h + 1][NR - 1]}; \
-    pv16<FMT, R8, NVR, MASK>(stg, vsb, kb + 16 * h, KLIM, lane, pa, pl, o, KEEP0, KEEP1);    \
+          // ---- O^T += V^T P
+#define MSA_DENSE_PV(MASK, KLIM, KEEP)                                                        \
+  _Pragma("unroll") for (int h = 0; h < KC / 16; ++h) {                                       \
+    uint32_t pb[NN][2], pl[NN][2];                                                            \
+    _Pragma("unroll") for (int n = 0; n < NN; ++n) {                                          \
+      pb[n][0] = ph[2 * h][n];                                                                \
+      pb[n][1] = ph[2 * h + 1][n];                                                            \
+      pl[n][0] = plo[2 * h][n];                                                               \
+      pl[n][1] = plo[2 * h + 1][n];                                                           \
+    }                                                                                         \
+    pv16<FMT, NN, NVR, MASK>(vl, vsb, kb + 16 * h, KLIM, lane, pb, pl, o, KEEP);              \
   }
+          int keep[NN];
+#pragma unroll
+          for (int n = 0; n < NN; ++n) keep[n] = 3;
           if (!masked) {
-            MSA_DENSE_PV(false, 0, true, true)
+            MSA_DENSE_PV(false, 0, keep)
           } else {
             // tile rows up to the last key of the sequence; with several new tokens a
-            // row between lim0 and there is seen by some of them only
+            // row between lim0 and there is seen by some of them only, and if its V is
+            // not finite each token goes by itself, up to its own position
             const int klast = f.T - 1 - k * TR::SK;
             int r0 = lim0 + 1 - k * TR::SK, r1 = klast + 1;
             r0 = r0 < kb ? kb : r0;
             r1 = r1 > kb + KC ? kb + KC : r1;
-            if (p.Q == 1 || !v_not_finite<FMT>(stg, vsb, r0, r1, lane)) {
-              MSA_DENSE_PV(true, klast, true, true)
-            } else {
-              // a later token's V is not finite: each token by itself, up to its own position
+            const bool apart =
+                p.Q > 1 && v_not_finite<FMT>(tm.tiles + (size_t)st * LY::STAGE, vsb, r0, r1, lane);
 #pragma unroll 1
-              for (int i = 0; i < p.Q; ++i) {
-                MSA_DENSE_PV(true, klast - (p.Q - 1 - i), qi[0] == i, qi[1] == i)
+            for (int i = apart ? 0 : p.Q - 1; i < p.Q; ++i) {
+              if (apart) {
+#pragma unroll
+                for (int n = 0; n < NN; ++n) {
+                  const int col = c0 + ct * LY::WROWS + 8 * n + 2 * j;
+                  keep[n] = (col / p.r == i ? 1 : 0) | ((col + 1) / p.r == i ? 2 : 0);
+                }
               }
+              MSA_DENSE_PV(true, klast - (p.Q - 1 - i), keep)
             }
           }
 #undef MSA_DENSE_PV
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[st]);
-    }
-
-    // ---------------- the segment's result: the warps of a column tile hold different keys
-#pragma unroll
-    for (int rr = 0; rr < NR; ++rr) {
-      l_run[rr] += __shfl_xor_sync(0xffffffffu, l_run[rr], 1);
-      l_run[rr] += __shfl_xor_sync(0xffffffffu, l_run[rr], 2);
-      if (j == 0) {
-        ml[(warp * LY::TR + g8 + 8 * rr) * 2] = m_run[rr];
-        ml[(warp * LY::TR + g8 + 8 * rr) * 2 + 1] = l_run[rr];
+      if (lane == 0) mbar_arrive(&tm.empty[st]);
+      if (++st == NST) {
+        st = 0;
+        par ^= 1u;
       }
+    }
+    fence_proxy_async();  // the query rows were rewritten in place; the next copy into them comes after that
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&tm.iempty[slot]);
+
+    // ---------------- the segment's result: the warps of a column group hold different keys
+#pragma unroll
+    for (int n = 0; n < NN; ++n) {
+      float l = l_run[n].x + l_run[n].y;
+      l += __shfl_xor_sync(0xffffffffu, l, 1);
+      l += __shfl_xor_sync(0xffffffffu, l, 2);
+      if (j == 0) *reinterpret_cast<float2*>(ml + (warp * LY::WROWS + 8 * n + g8) * 2) = make_float2(m_run[n], l);
     }
     const float osc = FMT == FMT_FP8 ? pow2i(-ev) : (FMT == FMT_NVFP4 ? p.v_global : 1.f);
     const bool whole = f.part < 0;
     constexpr int D4 = LY::DCH / 4;
+    constexpr int MTP = LY::DCH / 16;  // accumulator tiles a pass takes (their dims are consecutive)
+    static_assert(FMT != FMT_NVFP4 || LY::DCH >= 32, "a pass holds whole 32-dim chunks");
 #pragma unroll
     for (int pass = 0; pass < 128 / LY::DCH; ++pass) {
-      // the dims of accumulators [pass * 16 / passes, ...) are consecutive from pass * DCH
 #pragma unroll
-      for (int tt = 0; tt < 16 * LY::DCH / 128; ++tt) {
-        const int t = pass * (16 * LY::DCH / 128) + tt;
+      for (int tt = 0; tt < MTP; ++tt) {
+        const int mt = pass * MTP + tt;
 #pragma unroll
-        for (int rr = 0; rr < NR; ++rr)
+        for (int n = 0; n < NN; ++n)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float v = o[t][2 * rr + e];
-            if constexpr (R8 && FMT == FMT_BF16) v += o[t][2 + e];
-            mo[(warp * LY::TR + g8 + 8 * rr) * LY::MROW + out_dim<FMT>(t, e, j) - pass * LY::DCH] = v * osc;
-          }
+          for (int e = 0; e < 4; ++e)  // column 2j + (e & 1), row half e >> 1
+            mo[(warp * LY::WROWS + 8 * n + 2 * j + (e & 1)) * LY::MROW + out_dim<FMT>(mt, e >> 1, g8) - pass * LY::DCH] =
+                o[mt][n][e] * osc;
       }
-      named_bar_sync(1, kDenseConsumers);
+      named_bar_sync(bar, TEAM_THREADS);
 #pragma unroll 1
-      for (int x = tid; x < LY::ROWS * D4; x += kDenseConsumers) {
+      for (int x = tid; x < LY::ROWS * D4; x += TEAM_THREADS) {
         const int row = x / D4, d = 4 * (x - row * D4);
         if (row >= nrows) continue;
-        const int tile = R8 ? 0 : row >> 4, tr = R8 ? row : row & 15;
+        const int cgi = row / LY::WROWS, tr = row - cgi * LY::WROWS;
         float M = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kDenseGroups * KGW; ++w) {
-          const int src = (w / KGW) * kDenseWpg + tile * KGW + w % KGW;
-          M = fmaxf(M, ml[(src * LY::TR + tr) * 2]);
-        }
+        for (int w = 0; w < KGW; ++w) M = fmaxf(M, ml[((cgi * KGW + w) * LY::WROWS + tr) * 2]);
         const float ms = M == -INFINITY ? 0.f : M;
         float L = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < kDenseGroups * KGW; ++w) {
-          const int src = (w / KGW) * kDenseWpg + tile * KGW + w % KGW;
-          const float2 v = lds_f2(ml + (src * LY::TR + tr) * 2);
+        for (int w = 0; w < KGW; ++w) {
+          const int src = (cgi * KGW + w) * LY::WROWS + tr;
+          const float2 v = lds_f2(ml + src * 2);
           const float fw = ex2(v.x - ms);
           L += fw * v.y;
-          const float4 ov = *reinterpret_cast<const float4*>(mo + (src * LY::TR + tr) * LY::MROW + d);
+          const float4 ov = *reinterpret_cast<const float4*>(mo + src * LY::MROW + d);
           acc.x += fw * ov.x;
           acc.y += fw * ov.y;
           acc.z += fw * ov.z;
@@ -988,54 +1146,65 @@ __device__ void consumer(const DenseParams& p, uint8_t* base, uint64_t* full, ui
           pk.y = pack_bf16x2(acc.z * inv, acc.w * inv);
           *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + orow * kDim + dim) = pk;
           if (dim == 0 && p.lse)
-            p.lse[orow] = L == 0.f ? -INFINITY : (M - (F16P ? kDensePShift : 0.f) + log2f(L)) * 0.69314718055994531f;
+            p.lse[orow] = L == 0.f ? -INFINITY : (M - SHIFT + log2f(L)) * 0.69314718055994531f;
         } else {
           *reinterpret_cast<float4*>(p.part_o + ((size_t)f.part * LY::ROWS + row) * kDim + dim) = acc;
           if (dim == 0) p.part_ml[(size_t)f.part * LY::ROWS + row] = make_float2(M, L);
         }
       }
-      named_bar_sync(1, kDenseConsumers);  // the merge area is free again
+      named_bar_sync(bar, TEAM_THREADS);  // the merge area is free again
     }
   }
 }
 
-// 9 warps a CTA, one CTA an SM: up to 224 registers a thread.
-template <int FMT, int NT, bool R8, int SP, bool NVR>
-__global__ void __launch_bounds__(kDenseThreads, 1)
+// One CTA an SM.  Ten warps (two teams): up to 168 registers a thread; fifteen
+// (three teams): 128; WIDE: twelve warps launched with 168, of which the
+// producers' four keep 40 and the consumers' eight take 232 (384 x 168 = 128 x
+// 40 + 256 x 232 = 64,512 registers).
+template <int FMT, int NN, int NCG, int QM, bool NVR>
+__global__ void __launch_bounds__(DenseLayout<FMT, NN, NCG>::THREADS, 1)
     dense_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv, const DenseParams p) {
-  using LY = DenseLayout<FMT, NT, R8>;
-  constexpr int NST = LY::NST;
+  using LY = DenseLayout<FMT, NN, NCG>;
+  constexpr int NST = LY::NST, TEAMS = LY::TEAMS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(base + LY::BARS);
-  uint64_t* empty = full + NST;
-  uint64_t* ifull = empty + NST;
-  uint64_t* iempty = ifull + 2;
-  int* stage_ok = reinterpret_cast<int*>(iempty + 2);
-  int* dead = stage_ok + NST;
-  DenseFacts* facts = reinterpret_cast<DenseFacts*>(base + LY::FACTS);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) {
+  const bool consumes = warp < TEAMS * kDenseWpg;
+  const int team = consumes ? warp / kDenseWpg : warp - TEAMS * kDenseWpg;
+  DenseTeam tm;
+  tm.tiles = base + (size_t)team * NST * LY::STAGE;
+  tm.mem = base + LY::TILES + (size_t)team * LY::TEAM;
+  tm.full = reinterpret_cast<uint64_t*>(tm.mem + LY::BARS);
+  tm.empty = tm.full + NST;
+  tm.ifull = tm.empty + NST;
+  tm.iempty = tm.ifull + 2;
+  tm.stage_ok = reinterpret_cast<int*>(tm.iempty + 2);
+  tm.dead = tm.stage_ok + NST;
+  tm.facts = reinterpret_cast<DenseFacts*>(tm.mem + LY::FACTS);
+  tm.id = blockIdx.x * TEAMS + team;
+  if (!consumes && team < TEAMS && lane == 0) {
     for (int st = 0; st < NST; ++st) {
-      mbar_init(&full[st], 1);
-      mbar_init(&empty[st], kDenseWpg);
+      mbar_init(&tm.full[st], 1);
+      mbar_init(&tm.empty[st], kDenseWpg);
     }
     for (int sl = 0; sl < 2; ++sl) {
-      mbar_init(&ifull[sl], 1);
-      mbar_init(&iempty[sl], kDenseWarps);
+      mbar_init(&tm.ifull[sl], 1);
+      mbar_init(&tm.iempty[sl], kDenseWpg);
     }
-    *dead = 0;
+    *tm.dead = 0;
     fence_mbar_init();
     prefetch_tmap(&tmk);
     prefetch_tmap(&tmv);
   }
   __syncthreads();
   pdl_launch_dependents();  // the combine's CTAs may take their place as soon as this grid's leave room
-  if (warp == kDenseWarps) {
-    producer<FMT, NT, R8>(&tmk, &tmv, p, base, full, empty, ifull, iempty, dead, facts, stage_ok, lane);
+  if (!consumes) {
+    if constexpr (LY::WIDE) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if (team < TEAMS) producer<FMT, NN, NCG>(&tmk, &tmv, p, tm, lane);
   } else {
+    if constexpr (LY::WIDE) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
     // sequences without keys (and malformed ones) have no units: their rows here
-    for (int s = blockIdx.x + warp * gridDim.x; s < p.S; s += gridDim.x * kDenseWarps) {
+    for (int s = blockIdx.x + warp * gridDim.x; s < p.S; s += gridDim.x * TEAMS * kDenseWpg) {
       const int T = __ldg(p.seq_lens + s);
       if (T >= 1 && T <= p.max_nb * kBlock) continue;
       if (T != 0 && lane == 0) raise_flag(p.status, FLAG_BAD_SEQLEN, T);
@@ -1045,17 +1214,18 @@ __global__ void __launch_bounds__(kDenseThreads, 1)
       if (p.lse)
         for (long x = lane; x < rows; x += 32) p.lse[(size_t)s * rows + x] = -INFINITY;
     }
-    consumer<FMT, NT, R8, SP, NVR>(p, base, full, empty, ifull, iempty, dead, facts, stage_ok, warp, lane);
+    consumer<FMT, NN, NCG, QM, NVR>(p, tm, 1 + team, warp % kDenseWpg, lane);
   }
 }
 
-template <int FMT, int NT, bool R8, int SP, bool NVR>
+template <int FMT, int NN, int NCG, int QM, bool NVR>
 cudaError_t launch_one(const CUtensorMap* tk, const CUtensorMap* tv, const DenseParams& p, int num_sms, cudaStream_t st) {
-  constexpr size_t smem = DenseLayout<FMT, NT, R8>::SMEM;
-  auto kern = dense_kernel<FMT, NT, R8, SP, NVR>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  using LY = DenseLayout<FMT, NN, NCG>;
+  static_assert(LY::ROWS == dense_rows(NN, NCG) && LY::TEAMS == dense_teams(FMT, NN), "the plan's sizes");
+  auto kern = dense_kernel<FMT, NN, NCG, QM, NVR>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)LY::SMEM);
   if (e != cudaSuccess) return e;
-  kern<<<(unsigned)num_sms, kDenseThreads, smem, st>>>(*tk, *tv, p);
+  kern<<<(unsigned)num_sms, LY::THREADS, LY::SMEM, st>>>(*tk, *tv, p);
   return cudaGetLastError();
 }
 

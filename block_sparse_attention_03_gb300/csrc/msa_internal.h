@@ -227,7 +227,7 @@ struct InsertParams {
 // Dense attend over the whole cache (msa_dense.cuh).
 struct DenseParams {
   int32_t S, Q, G, r;         // sequences, new tokens each, KV heads, q heads per KV head
-  int32_t cols, CG;           // Q x r query columns of a (sequence, KV head), in CG groups of rows(NT) columns
+  int32_t cols, CG, cper;     // Q x r query columns of a (sequence, KV head), in CG groups of cper
   int32_t max_nb, num_blocks;
   const int32_t* seq_lens;
   const int32_t* block_table;
@@ -238,16 +238,24 @@ struct DenseParams {
   const uint8_t* k_sc;        // per-token fp32 scales (FP8) or e4m3 group scales (NVFP4)
   const uint8_t* v_sc;
   float v_global;             // NVFP4 V per-tensor scale
-  int2* info;                 // [CTAs] (sequence x G x CG + group) the run begins in, 1: it began before the run
-  float* part_o;              // [2 x CTAs][rows][128] partials of cut segments
-  float2* part_ml;            // [2 x CTAs][rows] running max (log2 domain), sum
+  int2* info;                 // [teams] (sequence x G x CG + group) the run begins in, 1: it began before the run
+  float* part_o;              // [2 x teams][rows][128] partials of cut segments
+  float2* part_ml;            // [2 x teams][rows] reference (log2 domain), sum
   void* out;                  // bf16 [S*Q][G*r][128]
   float* lse;
   DeviceStatus* status;
 };
-// tiles of 16 query columns an instance takes (0: up to 8 columns), and the rows of its partials
-inline int dense_nt(int cols) { return cols <= 8 ? 0 : cols <= 16 ? 1 : cols <= 32 ? 2 : 4; }
-inline int dense_rows(int nt) { return nt == 0 ? 8 : 16 * nt; }
+// The instance for `cper` columns: tiles of 8 columns a warp takes (nn) and
+// groups of such warps (ncg); the rows of its partials and its teams an SM.
+struct DenseShape {
+  int nn, ncg;
+};
+inline DenseShape dense_shape(int cper) {
+  if (cper <= 32) return {cper <= 8 ? 1 : cper <= 16 ? 2 : cper <= 24 ? 3 : 4, 1};
+  return {cper <= 48 ? 3 : 4, 2};
+}
+constexpr int dense_rows(int nn, int ncg) { return 8 * nn * ncg; }
+constexpr int dense_teams(int fmt, int nn) { return nn == 1 && fmt == FMT_NVFP4 ? 3 : 2; }
 // keys (rows of a tensor-copy box) a unit holds
 inline int dense_unit_keys(int fmt) { return fmt == FMT_BF16 ? 64 : 128; }
 
@@ -298,8 +306,10 @@ cudaError_t launch_tables(const TablesParams& p, int num_sms, cudaStream_t st);
 cudaError_t launch_dense_bf16(const CUtensorMap* tk, const CUtensorMap* tv, const DenseParams& p, int num_sms, cudaStream_t st);
 cudaError_t launch_dense_fp8(const CUtensorMap* tk, const CUtensorMap* tv, const DenseParams& p, int num_sms, cudaStream_t st);
 cudaError_t launch_dense_nvfp4(const CUtensorMap* tk, const CUtensorMap* tv, const DenseParams& p, int num_sms,
-                               bool round_e4m3, cudaStream_t st);
-cudaError_t launch_dense_combine(const DenseParams& p, bool f16p, int num_sms, cudaStream_t st);
+                               cudaStream_t st);
+cudaError_t launch_dense_nvfp4_rounded(const CUtensorMap* tk, const CUtensorMap* tv, const DenseParams& p, int num_sms,
+                                       cudaStream_t st);
+cudaError_t launch_dense_combine(const DenseParams& p, int fmt, int num_sms, cudaStream_t st);
 cudaError_t launch_insert(const InsertParams& p, int num_sms, cudaStream_t st);
 cudaError_t launch_k2q_build(const K2qParams& p, int num_sms, cudaStream_t st);    // count, scan, fill
 cudaError_t launch_k2q_attend(const CUtensorMap* tk, const CUtensorMap* tv, const K2qParams& p, int num_sms,
