@@ -287,14 +287,11 @@ _DENSE = _Layout(_CACHE, _BATCH, _CONFIG, _QUERY)
 _ROPE = _Layout(_CACHE, _ROWS, _QUERY, _ROWS, _QUERY, _ROWS, _ROWS, _ROWS, _NORM)
 
 
-def _rows(t, heads: int, tokens: int, where: str):
-    """(pointer, token stride) of a projection's rows: [tokens][heads][128] (or [tokens][128] for
-    one head), the heads side by side."""
-    shape, strides = t.shape, t.stride()
-    if len(shape) == 3:
-        if shape[0] != tokens or shape[1] != heads or shape[2] != 128 or strides[2] != 1 or (heads > 1 and strides[1] != 128):
-            raise MsaError(1, where)
-    elif len(shape) != 2 or heads != 1 or shape[0] != tokens or shape[1] != 128 or strides[1] != 1:
+def _rows(t, shape, where: str):
+    """(pointer, token stride) of a projection's rows of the given shape ([tokens][heads][128], or
+    [tokens][128] for one head), the heads side by side."""
+    strides = t.stride()
+    if t.shape != shape or strides[-1] != 1 or (len(shape) == 3 and strides[1] != 128 and shape[1] != 1):
         raise MsaError(1, where)
     return t.data_ptr(), strides[0]
 
@@ -430,7 +427,7 @@ def msa_rope_insert(cache, rope: MsaRopeT, positions, slot_mapping, q, q_out: Qu
     hq = q.shape[1]
     if q_out.data.numel() != T * hq * 128 or not q_out.data.is_contiguous():
         raise MsaError(1, where)
-    none = (0, 0)
+    none, kv = (0, 0), (T, H, 128)
     iqo = (0, 0, 0.0)
     if index_q_out is not None:
         if index_q_out.data.numel() != T * H * 128 or not index_q_out.data.is_contiguous():
@@ -438,9 +435,9 @@ def msa_rope_insert(cache, rope: MsaRopeT, positions, slot_mapping, q, q_out: Qu
         iqo = (index_q_out.data.data_ptr(), DTYPES[index_q_out.dtype], index_q_out.scale)
     w = (0, 0, 0, 0, 0.0, 0.0) if norm is None else (_p(norm.q), _p(norm.k), _p(norm.index_q), _p(norm.index_k), norm.eps,
                                                      norm.offset)
-    at = _ROPE.pack(*_cache_values(cache), *_rows(q, hq, T, where), q_out.data.data_ptr(), DTYPES[q_out.dtype], q_out.scale,
-                    *(none if index_q is None else _rows(index_q, H, T, where)), *iqo, *_rows(k, H, T, where),
-                    *_rows(v, H, T, where), *(none if index_k is None else _rows(index_k, 1, T, where)), *w)
+    at = _ROPE.pack(*_cache_values(cache), *_rows(q, (T, hq, 128), where), q_out.data.data_ptr(), DTYPES[q_out.dtype], q_out.scale,
+                    *(none if index_q is None else _rows(index_q, kv, where)), *iqo, *_rows(k, kv, where),
+                    *_rows(v, kv, where), *(none if index_k is None else _rows(index_k, (T, 128) if index_k.dim() == 2 else (T, 1, 128), where)), *w)
     o = _ROPE.offsets
     _check(lib().msa_rope_insert(at, ctypes.byref(rope), T, positions.data_ptr(), slot_mapping.data_ptr(), hq, at + o[1], at + o[2],
                                  0 if index_q is None else at + o[3], 0 if index_q_out is None else at + o[4], at + o[5],

@@ -256,8 +256,13 @@ __device__ void producer(const CUtensorMap* tmk, const CUtensorMap* tmv, const D
   const long GC = (long)p.G * p.CG;
   // units in all, then the run of this team: [u0, u1)
   long total = 0;
+  int mine0 = 0;  // the length of sequence `lane`: a batch of up to 32 is read once
 #pragma unroll 4
-  for (int s = lane; s < S; s += 32) total += units_of<TR::SK>(__ldg(p.seq_lens + s), max_nb);
+  for (int s0 = 0; s0 < S; s0 += 32) {
+    const int T = s0 + lane < S ? __ldg(p.seq_lens + s0 + lane) : 0;
+    if (s0 == 0) mine0 = T;
+    total += units_of<TR::SK>(T, max_nb);
+  }
   total = warp_sum(total) * GC;
   const long teams = (long)gridDim.x * LY::TEAMS;
   const long grid = total < teams ? total : teams;
@@ -272,7 +277,8 @@ __device__ void producer(const CUtensorMap* tmk, const CUtensorMap* tmv, const D
   long sb = 0;
   if (u1 > u0) {
     for (int s0 = 0; s0 < S; s0 += 32) {
-      const long mine = s0 + lane < S ? GC * units_of<TR::SK>(__ldg(p.seq_lens + s0 + lane), max_nb) : 0;
+      const int T = s0 == 0 ? mine0 : s0 + lane < S ? __ldg(p.seq_lens + s0 + lane) : 0;
+      const long mine = GC * units_of<TR::SK>(T, max_nb);
       const long incl = warp_scan(mine, lane);
       const uint32_t over = __ballot_sync(0xffffffffu, sb + incl > u0);
       if (over) {
@@ -292,7 +298,7 @@ __device__ void producer(const CUtensorMap* tmk, const CUtensorMap* tmv, const D
   if (u1 <= u0 && lane == 0) p.info[c] = make_int2(-1, 0);
 #pragma unroll 1
   while (u < u1 && ok) {
-    const int T = __ldg(p.seq_lens + s);
+    const int T = s < 32 ? __shfl_sync(0xffffffffu, mine0, s & 31) : __ldg(p.seq_lens + s);
     const int un = units_of<TR::SK>(T, max_nb);
     if (un == 0) {  // an empty sequence holds no units
       ++s;
@@ -307,6 +313,11 @@ __device__ void producer(const CUtensorMap* tmk, const CUtensorMap* tmv, const D
     const int sg = (int)((long)s * GC + gc);
     if (first && lane == 0) p.info[c] = make_int2(sg, cut_start ? 1 : 0);
     first = false;
+    // the first 32 block-table entries, on their way while the segment is published
+    const int32_t* row = p.block_table + (size_t)s * max_nb;
+    constexpr int UPB = kBlock / TR::SK;  // units a block
+    int b_have = k0 / UPB;                // entries [b_have, b_have + 32), one a lane
+    int entry = (b_have + lane) * UPB < k0 + n ? __ldg(row + b_have + lane) : -1;
     // publish the segment and its query rows
     const int slot = ii & 1, use = ii >> 1;
     if (use > 0 && !ring_wait(&iempty[slot], (uint32_t)((use - 1) & 1), dead)) {
@@ -338,24 +349,21 @@ __device__ void producer(const CUtensorMap* tmk, const CUtensorMap* tmv, const D
                static_cast<const uint8_t*>(p.q) + src * qrow_bytes, (uint32_t)qrow_bytes, &ifull[slot]);
     }
     ++ii;
-    // its tiles, 32 block-table entries at a time
-    const int32_t* row = p.block_table + (size_t)s * max_nb;
-    constexpr int UPB = kBlock / TR::SK;  // units a block
-    int b_have = -1, phys = -1;           // entries [b_have, b_have + 32) one per lane
+    // its tiles
 #pragma unroll 1
     for (int k = k0; k < k0 + n; ++k) {
       const int b = k / UPB, half = k - b * UPB;
-      if (b_have < 0 || b >= b_have + 32) {
+      if (b >= b_have + 32) {
         b_have = b;
-        const int mine = b + lane;
-        phys = -1;
-        if (mine * UPB < k0 + n) {
-          const int ph = __ldg(row + mine);
-          if (ph < 0 || ph >= p.num_blocks) raise_flag(p.status, FLAG_BAD_BLOCK, ph);
-          else phys = ph;
+        entry = (b + lane) * UPB < k0 + n ? __ldg(row + b + lane) : -1;
+      }
+      if (b == b_have && (k == k0 || half == 0)) {  // new entries: the ones outside the pool
+        if ((b + lane) * UPB < k0 + n && (entry < 0 || entry >= p.num_blocks)) {
+          raise_flag(p.status, FLAG_BAD_BLOCK, entry);
+          entry = -1;
         }
       }
-      const int ph = __shfl_sync(0xffffffffu, phys, b - b_have);
+      const int ph = __shfl_sync(0xffffffffu, entry, b - b_have);
       const int st = bi % NST, ub = bi / NST;
       if (ub > 0 && !ring_wait(&empty[st], (uint32_t)((ub - 1) & 1), dead)) {
         set_dead(dead, p.status, sg);

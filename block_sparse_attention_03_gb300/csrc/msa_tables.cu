@@ -23,53 +23,59 @@ namespace {
 
 constexpr int kTabThreads = 512;
 
-// Exclusive sums in place of three arrays of n values (n <= kMaxTableSeqs); the
-// totals land at [n].  Summed in 64 bits and clamped at kMost when stored (past
-// any count that can be granted), so that no set of lengths wraps around.
-constexpr long kMost = 1l << 30;
+// Sums saturate at kMost, past any count that can be granted, so that no set of
+// lengths wraps around (a saturating sum of sizes is associative).
+constexpr int kMost = 1 << 30;
+__device__ __forceinline__ int sat_add(int a, int b) { return min(a + b, kMost); }  // 0 <= a, b <= kMost
 
-__device__ void scan3(int* a, int* b, int* c, int n, long* warp_sums) {
+// Exclusive sums in place of three arrays of n sizes <= kMost (n <= kMaxTableSeqs);
+// the totals land at [n].
+__device__ void scan3(int* a, int* b, int* c, int n, int* warp_sums) {
+  constexpr int W = kTabThreads / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (n + kTabThreads - 1) / kTabThreads;
   const int i0 = min(n, tid * per), i1 = min(n, i0 + per);
-  long v[3] = {0, 0, 0};
+  int x[3] = {0, 0, 0};
   for (int i = i0; i < i1; ++i) {
-    v[0] += a[i];
-    v[1] += b[i];
-    v[2] += c[i];
+    x[0] = sat_add(x[0], a[i]);
+    x[1] = sat_add(x[1], b[i]);
+    x[2] = sat_add(x[2], c[i]);
   }
-  long x[3] = {v[0], v[1], v[2]};
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1)
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
-      const long t = __shfl_up_sync(0xffffffffu, x[k], o);
-      if (lane >= o) x[k] += t;
+      const int t = __shfl_up_sync(0xffffffffu, x[k], o);
+      if (lane >= o) x[k] = sat_add(x[k], t);
     }
   if (lane == 31)
 #pragma unroll
-    for (int k = 0; k < 3; ++k) warp_sums[k * 32 + warp] = x[k];
+    for (int k = 0; k < 3; ++k) warp_sums[k * W + warp] = x[k];
   __syncthreads();
-  long base[3];
+  int base[3];
 #pragma unroll
   for (int k = 0; k < 3; ++k) {
-    base[k] = x[k] - v[k];
-    long all = 0;
-    for (int w = 0; w < kTabThreads / 32; ++w) {
-      const long t = warp_sums[k * 32 + w];
-      if (w < warp) base[k] += t;
-      all += t;
+    // every warp scans the warps' sums by itself
+    int w = lane < W ? warp_sums[k * W + lane] : 0;
+#pragma unroll
+    for (int o = 1; o < W; o <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, w, o);
+      if (lane >= o) w = sat_add(w, t);
     }
-    if (tid == 0) (k == 0 ? a : k == 1 ? b : c)[n] = (int)min(all, kMost);
+    const int all = __shfl_sync(0xffffffffu, w, W - 1);
+    const int before = __shfl_sync(0xffffffffu, w, max(warp - 1, 0));
+    const int left = __shfl_up_sync(0xffffffffu, x[k], 1);
+    base[k] = sat_add(warp > 0 ? before : 0, lane > 0 ? left : 0);
+    if (tid == 0) (k == 0 ? a : k == 1 ? b : c)[n] = all;
   }
   for (int i = i0; i < i1; ++i) {
     const int ta = a[i], tb = b[i], tc = c[i];
-    a[i] = (int)min(base[0], kMost);
-    b[i] = (int)min(base[1], kMost);
-    c[i] = (int)min(base[2], kMost);
-    base[0] += ta;
-    base[1] += tb;
-    base[2] += tc;
+    a[i] = base[0];
+    b[i] = base[1];
+    c[i] = base[2];
+    base[0] = sat_add(base[0], ta);
+    base[1] = sat_add(base[1], tb);
+    base[2] = sat_add(base[2], tc);
   }
   __syncthreads();
 }
@@ -89,7 +95,7 @@ __device__ __forceinline__ int blocks_of(int t) { return (t + kBlock - 1) / kBlo
 
 __global__ void __launch_bounds__(kTabThreads) tables_kernel(const TablesParams p) {
   extern __shared__ int sm[];
-  __shared__ long warp_sums[96];
+  __shared__ int warp_sums[3 * kTabThreads / 32];
   __shared__ int s_taken;
   const int S = p.num_seqs, tid = threadIdx.x;
   int* tok = sm;               // [S + 1] first token of each request
@@ -98,6 +104,7 @@ __global__ void __launch_bounds__(kTabThreads) tables_kernel(const TablesParams 
   int* cached = back + S + 1;  // [S] -1: malformed
   const long limit = (long)p.max_nb * kBlock;
   if (tid == 0) s_taken = 0;
+  const int count_in = __ldg(p.free_count);
   for (int s = tid; s < S; s += kTabThreads) {
     const int c = __ldg(p.cached + s), n = __ldg(p.fresh + s);
     const bool good = c >= 0 && n >= -1 && (long)c + max(n, 0) <= limit;
@@ -110,9 +117,9 @@ __global__ void __launch_bounds__(kTabThreads) tables_kernel(const TablesParams 
   }
   __syncthreads();
   scan3(tok, want, back, S, warp_sums);
-  const int count = min(max(__ldg(p.free_count), 0), p.free_cap);
+  const int count = min(max(count_in, 0), p.free_cap);
   const int room = p.free_cap - count;
-  if (blockIdx.x == 0 && tid == 0 && count != __ldg(p.free_count)) raise_flag(p.status, FLAG_BAD_BLOCK, count);
+  if (blockIdx.x == 0 && tid == 0 && count != count_in) raise_flag(p.status, FLAG_BAD_BLOCK, count);
   const int given = min(back[S], room);  // returned blocks the stack has room for
   const int total = count + given;
   // the blocks taken: those of the requests that are granted, a prefix of all
@@ -203,10 +210,12 @@ cudaError_t launch_tables(const TablesParams& p, int num_sms, cudaStream_t st) {
   const size_t smem = ((size_t)p.num_seqs * 4 + 3) * sizeof(int);
   cudaError_t e = cudaFuncSetAttribute(tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  // a CTA's sums cost as much as some thousand tokens' slots: four tokens a thread
+  // one token a thread, up to two CTAs an SM: a thread's chain of dependent
+  // reads (bisection, table, stack) is the kernel's time, so each has one
+  // (253 requests, 64K tokens: 9.2 us with four tokens a thread)
   const long work = p.max_tokens > p.num_seqs ? p.max_tokens : p.num_seqs;
-  long grid = (work + 4 * kTabThreads - 1) / (4 * kTabThreads);
-  if (grid > num_sms) grid = num_sms;
+  long grid = (work + kTabThreads - 1) / kTabThreads;
+  if (grid > 2 * num_sms) grid = 2 * num_sms;
   if (grid < 1) grid = 1;
   tables_kernel<<<(unsigned)grid, kTabThreads, smem, st>>>(p);
   return cudaGetLastError();
