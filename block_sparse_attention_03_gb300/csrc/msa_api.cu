@@ -874,7 +874,6 @@ msa_status_t msa_rope_insert(const msa_cache_t* cache, const msa_rope_t* rope, i
     for (int i = 0; i < 4; ++i) {
       if (w[i] && !aligned16(w[i])) return MSA_ERR_INVALID_ARGUMENT;
       p.w[i] = static_cast<const __nv_bfloat16*>(w[i]);
-      p.norm |= w[i] != nullptr;
     }
     p.eps = norm->eps;
     p.w_offset = norm->offset;

@@ -264,7 +264,6 @@ struct RopeParams {
   msa_rope_t rope;
   int32_t num_tokens, Hq, Giq, H, Gik;  // tokens; q, index q, K (and V), index K heads (0: none)
   int32_t num_blocks, kv_fmt, idx_fmt;
-  int32_t chunks;                        // warps a token's rows are spread over (set by the launcher)
   const int32_t* positions;              // [axes][num_tokens]
   const int32_t* slots;                  // [num_tokens], < 0: no insert
   const __nv_bfloat16 *q, *iq, *k, *v, *ik;
@@ -272,7 +271,6 @@ struct RopeParams {
   uint8_t *q_out, *iq_out;               // [num_tokens][heads][128] bf16 or e4m3 codes
   int32_t q_fp8, iq_fp8;
   float q_inv, iq_inv;                   // 1 / per-tensor scale
-  int32_t norm;
   const __nv_bfloat16* w[4];             // norm weights of q, index q, k, index k (null: none)
   float eps, w_offset;
   uint8_t *kc, *vc, *ic;
@@ -301,7 +299,7 @@ struct TablesParams {
 constexpr int kMaxTableSeqs = 8192;  // four sums a request in shared memory
 
 // launchers (return cudaGetLastError())
-cudaError_t launch_rope(RopeParams p, int num_sms, cudaStream_t st);
+cudaError_t launch_rope(const RopeParams& p, int num_sms, cudaStream_t st);
 cudaError_t launch_tables(const TablesParams& p, int num_sms, cudaStream_t st);
 cudaError_t launch_dense_bf16(const CUtensorMap* tk, const CUtensorMap* tv, const DenseParams& p, int num_sms, cudaStream_t st);
 cudaError_t launch_dense_fp8(const CUtensorMap* tk, const CUtensorMap* tv, const DenseParams& p, int num_sms, cudaStream_t st);

@@ -15,11 +15,27 @@
 // (turns_i: turns a position x 2^64), exact for any 32-bit position to 2^-32 of
 // a turn, with no table of cosines to read and no largest position.
 //
-// Bound: HBM (a token's rows are read once and written once).  Half a warp takes
-// a row, 16 bytes a lane; a warp takes one token and, for many tokens, all of its
-// rows, so that its 64 sines and cosines (two a lane, exchanged through shared
-// memory) are used for every head; with few tokens its rows are spread over
-// several warps, which compute them again.
+// Bound: HBM (a token's rows are read once and written once), with the issue
+// slots close behind, so instructions per element are what counts.  A quarter of
+// a warp takes a row, 16 elements a lane, chosen so that both elements of a pair
+// are in one lane (eight at i and eight at i + rotary_dim / 2; no exchange between
+// lanes); a warp takes four heads of one kind at a time, so that what a row is is
+// a uniform branch and finding it, its loads, sums and stores are shared by
+// many elements; fp32 operations go two at a time (f32x2).  What the loop needs to
+// know of a row comes from a table that the CTA writes once.
+//
+// Split: the quads of rows of all tokens, in order, are cut into equal runs, one
+// per warp of a grid that fills the GPU: a prompt leaves no uneven last wave, and
+// a decode step's few tokens still spread over as many warps as they have quads.
+// A warp computes a token's 64 sines and cosines (two a lane, exchanged through
+// shared memory) once for all its quads of that token.
+//
+// The formats' rules divide by the row's (or group's) scale.  The quotient is
+// formed by Markstein's method (Computation of elementary functions on the IBM
+// RISC System/6000, 1990): with y = RN(1/s), q = RN(x y), r = RN(x - q s) exact,
+// RN(q + r y) is the correctly rounded quotient, so the codes are those of an
+// IEEE division at three operations an element; scales near the ends of fp32's
+// range, where r could underflow or y overflow, take the division itself.
 #include "msa_device.cuh"
 #include "msa_internal.h"
 
@@ -27,8 +43,8 @@ namespace msa {
 
 namespace {
 
-constexpr int kRopeWarps = 4;
-constexpr int kBatch = 4;  // row pairs a warp has in flight
+constexpr int kRopeWarps = 8;
+constexpr int kRopeCtas = 3;  // CTAs an SM (registers)
 
 // e2m1 codes of (lo, hi), round to nearest even, saturating at +-6, +0 for zero magnitudes.
 __device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
@@ -39,263 +55,349 @@ __device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
   return r;
 }
 
-__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
-  return (uint32_t)pack_e4m3x2(a, b) | ((uint32_t)pack_e4m3x2(c, d) << 16);
+__device__ __forceinline__ uint32_t e4m3x4(float2 a, float2 b) {
+  return (uint32_t)pack_e4m3x2(a.x, a.y) | ((uint32_t)pack_e4m3x2(b.x, b.y) << 16);
+}
+
+// y[i] / s, correctly rounded (see above).
+template <int N>
+__device__ __forceinline__ void divide(const float2 (&y)[N], float s, float2 (&z)[N]) {
+  if (s >= 8.27e-25f && s <= 1.2e24f) {  // 2^-80 to 2^80
+    const float r = __frcp_rn(s);
+    const float2 r2 = make_float2(r, r), n2 = make_float2(-s, -s);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float2 q = mul2(y[i], r2);
+      z[i] = fma2(fma2(q, n2, y[i]), r2, q);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) z[i] = make_float2(__fdiv_rn(y[i].x, s), __fdiv_rn(y[i].y, s));
+  }
 }
 
 // What a row is.
-enum Kind : int { KIND_Q = 0, KIND_IQ = 1, KIND_K = 2, KIND_IK = 3, KIND_V = 4, KIND_NONE = 5 };
+enum Kind : int { KIND_Q = 0, KIND_IQ = 1, KIND_K = 2, KIND_IK = 3, KIND_V = 4 };
 
-struct Row {
-  int kind, head;
+// What the loop needs to know of a row (of one head of one kind).
+struct __align__(16) RowDesc {
+  const uint8_t* src;   // token 0
+  long src_step;        // bytes between tokens
+  uint8_t* out;         // queries: token 0 of the output; caches: the data (null: no such head)
+  int out_step;         // queries: bytes between tokens; caches: the head's first row
+  int kind;             // of all rows of a quad
 };
-// rows of a token in the order q, index q, k, v, index k
-__device__ __forceinline__ Row row_of(const RopeParams& p, int r) {
-  if (r < p.Hq) return {KIND_Q, r};
-  r -= p.Hq;
-  if (r < p.Giq) return {KIND_IQ, r};
-  r -= p.Giq;
-  if (r < p.H) return {KIND_K, r};
-  r -= p.H;
-  if (r < p.H) return {KIND_V, r};
-  r -= p.H;
-  if (r < p.Gik) return {KIND_IK, 0};
-  return {KIND_NONE, 0};
+
+__device__ __forceinline__ uint4 bf16x8(const float2* y) {
+  return make_uint4(pack_bf16x2(y[0].x, y[0].y), pack_bf16x2(y[1].x, y[1].y), pack_bf16x2(y[2].x, y[2].y),
+                    pack_bf16x2(y[3].x, y[3].y));
+}
+__device__ __forceinline__ uint2 e4m3x8(const float2* y) { return make_uint2(e4m3x4(y[0], y[1]), e4m3x4(y[2], y[3])); }
+__device__ __forceinline__ float amax8(const float2* y) {
+  return fmaxf(fmaxf(fmaxf(fabsf(y[0].x), fabsf(y[0].y)), fmaxf(fabsf(y[1].x), fabsf(y[1].y))),
+               fmaxf(fmaxf(fabsf(y[2].x), fabsf(y[2].y)), fmaxf(fabsf(y[3].x), fabsf(y[3].y))));
 }
 
-__device__ __forceinline__ const __nv_bfloat16* row_src(const RopeParams& p, long t, Row w) {
-  switch (w.kind) {
-    case KIND_Q: return p.q + t * p.q_stride + w.head * kDim;
-    case KIND_IQ: return p.iq + t * p.iq_stride + w.head * kDim;
-    case KIND_K: return p.k + t * p.k_stride + w.head * kDim;
-    case KIND_V: return p.v + t * p.v_stride + w.head * kDim;
-    default: return p.ik + t * p.ik_stride;
-  }
-}
-
-// One cache row of 16 lanes x 8 elements (every lane of the warp takes part in
-// the shuffles; `put` says whether this half stores).
+// One cache row of 8 lanes, elements [dA, dA + 8) (y[0..3]) and [dB, dB + 8) a lane
+// (every lane of the warp takes part in the exchanges; `put`: this row is stored).
 template <int FMT>
-__device__ __forceinline__ void put_row(const float (&y)[8], bool put, uint8_t* __restrict__ data,
-                                        float* __restrict__ scale, uint8_t* __restrict__ sf, float g, long row, int l16) {
+__device__ __forceinline__ void put_row(const float2 (&y)[8], int dA, int dB, bool put, uint8_t* __restrict__ data,
+                                        float* __restrict__ scale, uint8_t* __restrict__ sf, float g, long row,
+                                        float* chunk_max, int l8) {
   if constexpr (FMT == FMT_BF16) {
-    if (!put) return;
-    uint4 w;
-    w.x = pack_bf16x2(y[0], y[1]);
-    w.y = pack_bf16x2(y[2], y[3]);
-    w.z = pack_bf16x2(y[4], y[5]);
-    w.w = pack_bf16x2(y[6], y[7]);
-    *reinterpret_cast<uint4*>(data + row * 256 + 16 * l16) = w;
+    if (put) {
+      *reinterpret_cast<uint4*>(data + row * 256 + 2 * dA) = bf16x8(y);
+      *reinterpret_cast<uint4*>(data + row * 256 + 2 * dB) = bf16x8(y + 4);
+    }
     return;
   }
-  float m = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(y[i]));
+  const float ma = amax8(y), mb = amax8(y + 4);
   if constexpr (FMT == FMT_FP8) {
+    float m = fmaxf(ma, mb);
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     if (!put) return;
     const float s = m > 0.f ? __fdiv_rn(m, 448.f) : 1.f;
-    float z[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) z[i] = __fdiv_rn(y[i], s);
-    uint2 w;
-    w.x = e4m3x4(z[0], z[1], z[2], z[3]);
-    w.y = e4m3x4(z[4], z[5], z[6], z[7]);
-    *reinterpret_cast<uint2*>(data + row * 128 + 8 * l16) = w;
-    if (l16 == 0) scale[row] = s;
+    float2 z[8];
+    divide(y, s, z);
+    *reinterpret_cast<uint2*>(data + row * 128 + dA) = e4m3x8(z);
+    *reinterpret_cast<uint2*>(data + row * 128 + dB) = e4m3x8(z + 4);
+    if (l8 == 0) scale[row] = s;
   } else {
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));  // 16 elements: two lanes
+    // the largest of each 16-element group, from those of its two 8-element chunks
+    // (in the row's order in shared memory; a group may lie in two halves)
+    chunk_max[dA >> 3] = ma;
+    chunk_max[dB >> 3] = mb;
+    __syncwarp();
+    const float2 a2 = *reinterpret_cast<const float2*>(chunk_max + (dA >> 4) * 2);
+    const float2 b2 = *reinterpret_cast<const float2*>(chunk_max + (dB >> 4) * 2);
+    __syncwarp();
     if (!put) return;
-    const uint32_t code = pack_e4m3x2(__fdiv_rn(m, __fmul_rn(6.f, g)), 0.f) & 0xffu;
-    const float den = __fmul_rn(e4m3_to_float((uint8_t)code), g);
-    uint32_t w = 0;
-    if (den > 0.f) {
+    const float g6 = __fmul_rn(6.f, g);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w |= e2m1x2(__fdiv_rn(y[2 * i], den), __fdiv_rn(y[2 * i + 1], den)) << (8 * i);
+    for (int k = 0; k < 2; ++k) {
+      const float m = k ? fmaxf(b2.x, b2.y) : fmaxf(a2.x, a2.y);
+      const int d = k ? dB : dA;
+      const uint32_t code = pack_e4m3x2(__fdiv_rn(m, g6), 0.f) & 0xffu;
+      const float den = __fmul_rn(e4m3_to_float((uint8_t)code), g);
+      uint32_t w = 0;
+      if (den > 0.f) {
+        const float2 v[4] = {y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]};
+        float2 z[4];
+        divide(v, den, z);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w |= e2m1x2(z[i].x, z[i].y) << (8 * i);
+      }
+      *reinterpret_cast<uint32_t*>(data + row * 64 + (d >> 1)) = w;
+      if ((d & 8) == 0) sf[row * 8 + (d >> 4)] = (uint8_t)code;
     }
-    *reinterpret_cast<uint32_t*>(data + row * 64 + 4 * l16) = w;
-    if ((l16 & 1) == 0) sf[row * 8 + (l16 >> 1)] = (uint8_t)code;
   }
 }
 
-template <int KVF, int IF>
-__global__ void __launch_bounds__(32 * kRopeWarps) rope_kernel(const __grid_constant__ RopeParams p) {
+template <int KVF, int IF, bool ADJ>
+__global__ void __launch_bounds__(32 * kRopeWarps, kRopeCtas) rope_kernel(const __grid_constant__ RopeParams p) {
+  extern __shared__ RowDesc s_rows[];  // four a quad
   __shared__ uint64_t s_turns[64];
   __shared__ int s_axis[64];
-  __shared__ float2 s_cs[kRopeWarps][64];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l16 = lane & 15, half = lane >> 4;
+  __shared__ __align__(16) float s_w[4][kDim];           // offset + norm weight
+  __shared__ __align__(16) float2 s_cs[kRopeWarps][64];  // cosines, sines
+  __shared__ __align__(16) float s_max[kRopeWarps][4][16];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l8 = lane & 7, sub = lane >> 3;
   const int pairs = p.rope.rotary_dim >> 1;
   if (threadIdx.x < 64) {
     s_turns[threadIdx.x] = p.rope.turns[threadIdx.x];
     s_axis[threadIdx.x] = p.rope.axis[threadIdx.x];
   }
+  for (int i = threadIdx.x; i < 4 * kDim; i += 32 * kRopeWarps) {
+    const __nv_bfloat16* w = p.w[i / kDim];
+    s_w[i / kDim][i % kDim] = w ? __bfloat162float(w[i % kDim]) + p.w_offset : 1.f;
+  }
+  // quads of rows, kind after kind: where each ends
+  const int e0 = (p.Hq + 3) >> 2, e1 = e0 + ((p.Giq + 3) >> 2), e2 = e1 + ((p.H + 3) >> 2), e3 = e2 + ((p.H + 3) >> 2),
+            e4 = e3 + p.Gik;
+  for (int r = threadIdx.x; r < 4 * e4; r += 32 * kRopeWarps) {
+    const int qd = r >> 2;
+    RowDesc d;
+    const int h = r - 4 * (qd < e0 ? 0 : qd < e1 ? e0 : qd < e2 ? e1 : qd < e3 ? e2 : e3);
+    int heads = p.H;
+    const __nv_bfloat16* src;
+    long step;
+    d.out = nullptr;
+    if (qd < e1) {
+      const bool q = qd < e0;
+      d.kind = q ? KIND_Q : KIND_IQ;
+      heads = q ? p.Hq : p.Giq;
+      src = q ? p.q : p.iq;
+      step = q ? p.q_stride : p.iq_stride;
+      const int es = (q ? p.q_fp8 : p.iq_fp8) ? 1 : 2;
+      if (h < heads) d.out = (q ? p.q_out : p.iq_out) + (size_t)h * kDim * es;
+      d.out_step = heads * kDim * es;
+    } else {
+      d.kind = qd < e2 ? KIND_K : qd < e3 ? KIND_V : KIND_IK;
+      if (qd >= e3) heads = 1;
+      src = qd < e2 ? p.k : qd < e3 ? p.v : p.ik;
+      step = qd < e2 ? p.k_stride : qd < e3 ? p.v_stride : p.ik_stride;
+      if (h < heads) d.out = qd < e2 ? p.kc : qd < e3 ? p.vc : p.ic;
+      d.out_step = h * kBlock;
+    }
+    // (a quarter without a head reads the last one's row again)
+    d.src = reinterpret_cast<const uint8_t*>(src + (long)min(h, heads - 1) * kDim);
+    d.src_step = 2 * step;
+    s_rows[r] = d;
+  }
   __syncthreads();
-  const int rows = p.Hq + p.Giq + 2 * p.H + p.Gik;
-  const int row_pairs = (rows + 1) >> 1;
-  const int per = (row_pairs + p.chunks - 1) / p.chunks;  // row pairs a warp takes
-  const long items = (long)p.num_tokens * p.chunks;
-  const bool adjacent = p.rope.layout == MSA_ROPE_ADJACENT;
-  // this lane's 8 dims: the pairs they belong to, and whether they are the second of them
-  const int d0 = 8 * l16;
-  const bool rot = d0 < 2 * pairs;
-  const int shift = pairs >> 3;  // lanes between the halves of a pair ("halves" layout)
-  const bool second = d0 >= pairs;
-  const int partner = (lane & 16) | ((second ? l16 - shift : l16 + shift) & 15);
+  // this lane's elements [dA, dA + 8) and [dB, dB + 8)
+  int dA, dB;
+  bool rot;
+  if constexpr (ADJ) {
+    dA = 16 * l8;
+    dB = dA + 8;
+    rot = dA < 2 * pairs;
+  } else {
+    const int rl = pairs >> 3;  // lanes that hold pairs; the others the rest of the row
+    rot = l8 < rl;
+    dA = rot ? 8 * l8 : 2 * pairs + 8 * (l8 - rl);
+    dB = rot ? pairs + 8 * l8 : kDim / 2 + pairs + 8 * (l8 - rl);
+  }
+
+  // this warp's run of quads, [u, u1) of num_tokens x e4
+  const long quads = (long)p.num_tokens * e4, warps = (long)gridDim.x * kRopeWarps;
+  const long w = (long)blockIdx.x * kRopeWarps + warp;
+  const long u0 = w * quads / warps, u1 = (w + 1) * quads / warps;
+  if (u0 >= u1) return;
+  long t = u0 / e4;
+  int qd = (int)(u0 - t * e4);
+  int left = (int)(u1 - u0);
+
+  // the slot and positions of a token, and the raw elements of a quad's rows, are
+  // read one ahead
+  int slot_n, pos_n[2] = {0, 0};
+  auto fetch = [&](long tt) {
+    slot_n = __ldg(p.slots + tt);
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      if (lane + 32 * k < pairs) pos_n[k] = __ldg(p.positions + (size_t)s_axis[lane + 32 * k] * p.num_tokens + tt);
+  };
+  uint4 a1, b1;
+  auto load = [&](long tt, int q) {
+    const RowDesc& d = s_rows[4 * q + sub];
+    const uint8_t* src = d.src + tt * d.src_step;
+    a1 = *reinterpret_cast<const uint4*>(src + 2 * dA);
+    b1 = *reinterpret_cast<const uint4*>(src + 2 * dB);
+  };
+  fetch(t);
+  load(t, qd);
 #pragma unroll 1
-  for (long it = (long)blockIdx.x * kRopeWarps + warp; it < items; it += (long)gridDim.x * kRopeWarps) {
-    const long t = it / p.chunks;
-    const int ch = (int)(it - t * p.chunks);
-    const int pr0 = ch * per, pr1 = min(row_pairs, pr0 + per);
-    const int slot = __ldg(p.slots + t);
+  while (left > 0) {
+    const int slot = slot_n;
     // cosines and sines of this token: pairs lane, lane + 32
     __syncwarp();
 #pragma unroll
-    for (int i = lane; i < 64; i += 32) {
+    for (int k = 0; k < 2; ++k) {
+      const int i = lane + 32 * k;
       if (i < pairs) {
-        const int pos = __ldg(p.positions + (size_t)s_axis[i] * p.num_tokens + t);
-        const uint64_t f = (uint64_t)(int64_t)pos * s_turns[i];
+        const uint64_t f = (uint64_t)(int64_t)pos_n[k] * s_turns[i];
         float sn, cs;
         sincospif((float)(int32_t)(f >> 32) * 4.656612873077393e-10f, &sn, &cs);  // x 2^-31: half turns
         s_cs[warp][i] = make_float2(cs, sn);
       }
     }
     __syncwarp();
-    float c[8], s[8];
+    if (left > e4 - qd) fetch(t + 1);
+    // halves: pair dA + i for element i of both parts; adjacent: each pair's sine and cosine
+    float2 c[4], s[4], cb[ADJ ? 4 : 1], sb[ADJ ? 4 : 1];
+    if (rot) {
+      const int first = ADJ ? dA >> 1 : dA;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float2 v = make_float2(1.f, 0.f);
-      if (rot) {
-        const int dim = d0 + i;
-        const int pair = adjacent ? dim >> 1 : (second ? dim - pairs : dim);
-        v = s_cs[warp][pair];
-        // out = own x cos + partner x sin, the first of a pair taking -sin
-        if (adjacent ? (i & 1) == 0 : !second) v.y = -v.y;
+      for (int i = 0; i < 4; ++i) {
+        const float4 v = *reinterpret_cast<const float4*>(&s_cs[warp][first + 2 * i]);
+        if constexpr (ADJ) {
+          // pairs first + 2i and first + 2i + 1: out = own x cos + other x (-sin, sin)
+          float2* cc = i < 2 ? c + 2 * i : cb + 2 * (i - 2);
+          float2* ss = i < 2 ? s + 2 * i : sb + 2 * (i - 2);
+          cc[0] = make_float2(v.x, v.x);
+          ss[0] = make_float2(-v.y, v.y);
+          cc[1] = make_float2(v.z, v.z);
+          ss[1] = make_float2(-v.w, v.w);
+        } else {
+          c[i] = make_float2(v.x, v.z);
+          s[i] = make_float2(v.y, v.w);
+        }
       }
-      c[i] = v.x;
-      s[i] = v.y;
     }
     const bool live = slot >= 0;
     const int blk = slot >> 7, off = slot & 127;
-    if (live && blk >= p.num_blocks && ch == 0 && lane == 0) raise_flag(p.status, FLAG_BAD_BLOCK, slot);
+    if (live && blk >= p.num_blocks && qd == 0 && lane == 0) raise_flag(p.status, FLAG_BAD_BLOCK, slot);
     const bool store = live && blk < p.num_blocks;
+    const long row0 = (long)blk * p.H * kBlock + off;
+
+    const int end = min(e4, qd + left);
+    left -= end - qd;
 #pragma unroll 1
-    for (int pr = pr0; pr < pr1; pr += kBatch) {
-      uint4 raw[kBatch];
+    for (; qd < end; ++qd) {
+      const uint32_t u[8] = {a1.x, a1.y, a1.z, a1.w, b1.x, b1.y, b1.z, b1.w};
+      if (qd + 1 < end) load(t, qd + 1);
+      else if (left > 0) load(t + 1, 0);
+      const RowDesc& d = s_rows[4 * qd + sub];
+      const int kind = d.kind;  // the same in all rows of the quad
+      uint8_t* const out = d.out;
+      float2 y[8];
 #pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        const int r = 2 * (pr + b) + half;
-        raw[b] = make_uint4(0u, 0u, 0u, 0u);
-        if (pr + b < pr1 && r < rows)
-          raw[b] = *reinterpret_cast<const uint4*>(row_src(p, t, row_of(p, r)) + d0);
+      for (int i = 0; i < 8; ++i) y[i] = make_float2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u));
+      if (kind != KIND_V) {
+        if (p.w[kind]) {
+          float2 q2 = mul2(y[0], y[0]), q3 = mul2(y[4], y[4]);
+#pragma unroll
+          for (int i = 1; i < 4; ++i) {
+            q2 = fma2(y[i], y[i], q2);
+            q3 = fma2(y[4 + i], y[4 + i], q3);
+          }
+          q2 = add2(q2, q3);
+          float q = q2.x + q2.y;
+#pragma unroll
+          for (int o = 4; o > 0; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
+          const float inv = rsqrtf(fmaf(q, 1.f / kDim, p.eps));
+          const float2 i2 = make_float2(inv, inv);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float4 g = *reinterpret_cast<const float4*>(&s_w[kind][(i < 2 ? dA : dB - 8) + 4 * i]);
+            y[2 * i] = mul2(mul2(y[2 * i], i2), make_float2(g.x, g.y));
+            y[2 * i + 1] = mul2(mul2(y[2 * i + 1], i2), make_float2(g.z, g.w));
+          }
+        }
+        if (rot) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 a = y[i], b = y[4 + i];
+            if constexpr (ADJ) {
+              y[i] = fma2(a, c[i], mul2(make_float2(a.y, a.x), s[i]));
+              y[4 + i] = fma2(b, cb[i], mul2(make_float2(b.y, b.x), sb[i]));
+            } else {
+              y[i] = fma2(a, c[i], mul2(b, make_float2(-s[i].x, -s[i].y)));
+              y[4 + i] = fma2(b, c[i], mul2(a, s[i]));
+            }
+          }
+        }
       }
+      if (kind <= KIND_IQ) {
+        uint8_t* const o = out + t * d.out_step;
+        if (kind == KIND_Q ? p.q_fp8 : p.iq_fp8) {
+          const float iv = kind == KIND_Q ? p.q_inv : p.iq_inv;
 #pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        if (pr + b >= pr1) break;
-        const int r = 2 * (pr + b) + half;
-        const Row w = r < rows ? row_of(p, r) : Row{KIND_NONE, 0};
-        const uint32_t u[4] = {raw[b].x, raw[b].y, raw[b].z, raw[b].w};
-        float y[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          y[2 * i] = __uint_as_float(u[i] << 16);
-          y[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-        }
-        const bool turns = w.kind <= KIND_IK;
-        if (p.norm) {
-          float q = 0.f;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) q = fmaf(y[i], y[i], q);
-#pragma unroll
-          for (int o = 8; o > 0; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
-          const __nv_bfloat16* wp = turns ? p.w[w.kind] : nullptr;
-          if (wp) {
-            const float inv = rsqrtf(fmaf(q, 1.f / kDim, p.eps));
-            const uint4 ww = __ldg(reinterpret_cast<const uint4*>(wp + d0));
-            const uint32_t g[4] = {ww.x, ww.y, ww.z, ww.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              y[2 * i] = y[2 * i] * inv * (__uint_as_float(g[i] << 16) + p.w_offset);
-              y[2 * i + 1] = y[2 * i + 1] * inv * (__uint_as_float(g[i] & 0xffff0000u) + p.w_offset);
-            }
+          for (int i = 0; i < 8; ++i) y[i] = mul2(y[i], make_float2(iv, iv));
+          if (out) {
+            *reinterpret_cast<uint2*>(o + dA) = e4m3x8(y);
+            *reinterpret_cast<uint2*>(o + dB) = e4m3x8(y + 4);
           }
+        } else if (out) {
+          *reinterpret_cast<uint4*>(o + 2 * dA) = bf16x8(y);
+          *reinterpret_cast<uint4*>(o + 2 * dB) = bf16x8(y + 4);
         }
-        if (adjacent) {
-          if (turns && rot) {
-#pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-              const float a = y[i], d = y[i + 1];
-              y[i] = fmaf(a, c[i], d * s[i]);
-              y[i + 1] = fmaf(d, c[i + 1], a * s[i + 1]);
-            }
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float o = __shfl_sync(0xffffffffu, y[i], partner);
-            if (turns && rot) y[i] = fmaf(y[i], c[i], o * s[i]);
-          }
-        }
-        // ---- out
-        const bool query = w.kind <= KIND_IQ;
-        if (query) {
-          const int heads = w.kind == KIND_Q ? p.Hq : p.Giq;
-          uint8_t* out = w.kind == KIND_Q ? p.q_out : p.iq_out;
-          const bool fp8 = (w.kind == KIND_Q ? p.q_fp8 : p.iq_fp8) != 0;
-          const size_t e = ((size_t)t * heads + w.head) * kDim + d0;
-          if (fp8) {
-            const float iv = w.kind == KIND_Q ? p.q_inv : p.iq_inv;
-            uint2 o;
-            o.x = e4m3x4(y[0] * iv, y[1] * iv, y[2] * iv, y[3] * iv);
-            o.y = e4m3x4(y[4] * iv, y[5] * iv, y[6] * iv, y[7] * iv);
-            *reinterpret_cast<uint2*>(out + e) = o;
-          } else {
-            uint4 o;
-            o.x = pack_bf16x2(y[0], y[1]);
-            o.y = pack_bf16x2(y[2], y[3]);
-            o.z = pack_bf16x2(y[4], y[5]);
-            o.w = pack_bf16x2(y[6], y[7]);
-            *reinterpret_cast<uint4*>(out + 2 * e) = o;
-          }
-        }
-        const bool kv = w.kind == KIND_K || w.kind == KIND_V, ik = w.kind == KIND_IK;
-        if (__any_sync(0xffffffffu, kv)) {
-          const long row = ((long)blk * p.H + w.head) * kBlock + off;
-          const bool isk = w.kind == KIND_K;
-          put_row<KVF>(y, kv && store, isk ? p.kc : p.vc, isk ? p.ks : p.vs, isk ? p.ksf : p.vsf, isk ? p.kg : p.vg, row,
-                       l16);
-        }
-        if (__any_sync(0xffffffffu, ik))
-          put_row<IF>(y, ik && store, p.ic, p.is, p.isf, p.ig, (long)blk * kBlock + off, l16);
+      } else if (kind == KIND_IK) {
+        put_row<IF>(y, dA, dB, store && out, out, p.is, p.isf, p.ig, (long)blk * kBlock + off, s_max[warp][sub], l8);
+      } else {
+        const bool isk = kind == KIND_K;
+        put_row<KVF>(y, dA, dB, store && out, out, isk ? p.ks : p.vs, isk ? p.ksf : p.vsf, isk ? p.kg : p.vg, row0 + d.out_step,
+                     s_max[warp][sub], l8);
       }
     }
+    qd = 0;
+    ++t;
   }
+}
+
+int rope_quads(const RopeParams& p) {
+  return (p.Hq + 3) / 4 + (p.Giq + 3) / 4 + 2 * ((p.H + 3) / 4) + p.Gik;
+}
+
+template <int KVF, int IF>
+cudaError_t launch_layout(const RopeParams& p, unsigned grid, cudaStream_t st) {
+  const size_t smem = 4 * (size_t)rope_quads(p) * sizeof(RowDesc);
+  auto kern = p.rope.layout == MSA_ROPE_ADJACENT ? rope_kernel<KVF, IF, true> : rope_kernel<KVF, IF, false>;
+  if (smem > 32768) {  // with the static part more than the 48 KB a launch has unasked
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  kern<<<grid, 32 * kRopeWarps, smem, st>>>(p);
+  return cudaGetLastError();
 }
 
 template <int KVF>
 cudaError_t launch_kv(const RopeParams& p, unsigned grid, cudaStream_t st) {
   switch (p.idx_fmt) {
-    case FMT_BF16: rope_kernel<KVF, FMT_BF16><<<grid, 32 * kRopeWarps, 0, st>>>(p); break;
-    case FMT_FP8: rope_kernel<KVF, FMT_FP8><<<grid, 32 * kRopeWarps, 0, st>>>(p); break;
-    case FMT_NVFP4: rope_kernel<KVF, FMT_NVFP4><<<grid, 32 * kRopeWarps, 0, st>>>(p); break;
+    case FMT_BF16: return launch_layout<KVF, FMT_BF16>(p, grid, st);
+    case FMT_FP8: return launch_layout<KVF, FMT_FP8>(p, grid, st);
+    case FMT_NVFP4: return launch_layout<KVF, FMT_NVFP4>(p, grid, st);
     default: return cudaErrorInvalidValue;
   }
-  return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_rope(RopeParams p, int num_sms, cudaStream_t st) {
-  // one warp a token where that fills the GPU (32 warps an SM); with fewer
-  // tokens a token's rows go to as many warps as there are row pairs at most
-  const int row_pairs = (p.Hq + p.Giq + 2 * p.H + p.Gik + 1) / 2;
-  long chunks = ((long)num_sms * 32 + p.num_tokens - 1) / p.num_tokens;
-  if (chunks > row_pairs) chunks = row_pairs;
-  if (chunks < 1) chunks = 1;
-  p.chunks = (int)chunks;
-  const long items = (long)p.num_tokens * chunks;
-  long grid = (items + kRopeWarps - 1) / kRopeWarps;
-  const long cap = (long)num_sms * 64;
+cudaError_t launch_rope(const RopeParams& p, int num_sms, cudaStream_t st) {
+  const long quads = (long)p.num_tokens * rope_quads(p);
+  long grid = (quads + kRopeWarps - 1) / kRopeWarps;
+  const long cap = (long)num_sms * kRopeCtas;
   if (grid > cap) grid = cap;
   switch (p.kv_fmt) {
     case FMT_BF16: return launch_kv<FMT_BF16>(p, (unsigned)grid, st);
