@@ -36,13 +36,12 @@
 // the output takes 32 registers and no MMA works on empty columns:
 //   S[col][key]   = Q[col][:] . K[key][:]             (A = Q, B = K)
 //   O^T[d][col]  += sum_key V[key][d] P[col][key]     (A = V^T, B = P)
-//   FP8    K enters e4m3 MMAs as it is, a bf16 query as e4m3 hi + lo terms after
-//          a power-of-two row scale (exact to 2^-10 of the row's 448); with up
-//          to 8 columns the lo terms are the tile's rows 8 to 15 and cost
-//          nothing, with up to 16 a second MMA.  With more the tensor pipe would
-//          be the bound (an e4m3 k32 MMA takes as long as two f16 k16 ones:
-//          4.2 and 2.1 cycles an SM, from the pipe's counters), so K becomes f16
-//          there.  V becomes f16 (exact), P x vscale f16 (11 bits).
+//   FP8    K and V become f16 (exact); a bf16 query f16 after a power-of-two row
+//          scale (11 bits, exact to 2^-25 of 16,384 below it), P x vscale f16.
+//          K as it is against the query's two e4m3 terms takes as long with 4
+//          columns (330 us over 4 x 131,072 tokens both ways) and longer with
+//          more: 105 to 97 us with 16 columns and 222 to 133 with 32 over 64 x
+//          8,192, since each e4m3 k32 MMA costs the pipe what two f16 k16 do.
 //   NVFP4  K and V become f16 in registers (e2m1 x e4m3 fits 6 bits: exact).
 //   BF16   as it is; P enters as bf16 hi + lo terms (16 bits), since one bf16
 //          term alone would add an error near the output's own rounding.
@@ -64,17 +63,11 @@
 namespace msa {
 
 constexpr int kDenseWpg = 4;             // consumer warps of a team
+// An MMA's sum is ready after 21 cycles, and a scheduler could start one every 8:
+// a warp alternates this many sums.
+constexpr int kDenseChains = 4;
 constexpr float kDensePShift = 7.f;      // log2 of the scale of P (f16 formats)
 constexpr float kDenseLazy = 8.f;        // a logit (log2) above the reference by this moves it
-
-// How the query meets K.
-enum QMode : int {
-  QM_16 = 0,    // BF16 and NVFP4 caches: 16-bit MMAs
-  QM_E4 = 1,    // FP8: e4m3 queries as they are
-  QM_E4X2 = 2,  // FP8: bf16 queries as two e4m3 terms, two MMAs
-  QM_ROWS = 3,  // FP8: the two terms in rows 0-7 and 8-15 of one tile
-  QM_F16K = 4   // FP8: K widened to f16, f16 queries
-};
 
 template <int FMT>
 struct DenseTraits;
@@ -194,7 +187,18 @@ __device__ __forceinline__ void set_dead(int* flag, DeviceStatus* st, int detail
   if (!is_dead(flag)) raise_flag(st, FLAG_TIMEOUT, detail);
   *reinterpret_cast<volatile int*>(flag) = 1;
 }
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile("{ .reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+               : "=r"(done)
+               : "r"(smem_u32(bar)), "r"(parity)
+               : "memory");
+  return done != 0;
+}
+// Bounded wait of a warp.  A plain test first: a try_wait may suspend, which takes
+// some 200 cycles even where the phase is complete.
 __device__ __forceinline__ bool ring_wait(uint64_t* bar, uint32_t parity, const int* dead) {
+  if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
   if (is_dead(dead)) return false;
   return mbar_wait_warp(bar, parity);
 }
@@ -405,23 +409,18 @@ __device__ void producer(const CUtensorMap* tmk, const CUtensorMap* tmv, const D
 
 // ---------------------------------------------------------------- consumer pieces
 
-template <int QM>
-struct QRegs {
-  static constexpr bool E4 = QM == QM_E4 || QM == QM_E4X2 || QM == QM_ROWS;
-  static constexpr int KS = E4 ? 4 : 8;             // k steps of the first product
-  static constexpr int SP = QM == QM_E4X2 ? 2 : 1;  // terms
-};
+constexpr int kDenseKSteps = 8;  // 16-dim steps of the first product
 
 __device__ __forceinline__ float2 bf16x2_to_float2(uint32_t w) {
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 
-// Where dim d of a query row is kept, so that a k step's 16 (e4m3: 32) columns
-// are the dims K's fragments hold in the same slots.  The order of the dims is
-// free as long as both agree; d even, pairs stay together.
-template <int FMT, int QM>
+// Where dim d of a query row is kept, so that a k step's 16 columns are the dims
+// K's fragments hold in the same slots.  The order of the dims is free as long as
+// both agree; d even, pairs stay together.
+template <int FMT>
 __device__ __forceinline__ int q_place(int d) {
-  if constexpr (QM == QM_F16K) {  // K's slots 2j, 2j + 1 and 2j + 8, 2j + 9 hold dims 4j .. 4j + 3
+  if constexpr (FMT == FMT_FP8) {  // K's slots 2j, 2j + 1 and 2j + 8, 2j + 9 hold dims 4j .. 4j + 3
     const int ks = d >> 4, j = (d >> 2) & 3, hi = (d >> 1) & 1;
     return 16 * ks + 8 * hi + 2 * j;
   } else if constexpr (FMT == FMT_NVFP4) {  // a lane's 32 consecutive dims, four a step
@@ -433,9 +432,8 @@ __device__ __forceinline__ int q_place(int d) {
 }
 
 // The segment's query rows, in place, into the form of their fragments (16-bit
-// rows of 256 bytes, or e4m3 rows with the lo terms 128 bytes behind the hi
-// terms), and each row's logit factor (log2 domain).  One warp a row.
-template <int FMT, int QM, int QROW>
+// rows of 256 bytes), and each row's logit factor (log2 domain).  One warp a row.
+template <int FMT, int QROW>
 __device__ __forceinline__ void convert_q(uint8_t* qs, float* cf, int nrows, int rows, bool q_fp8, float q_scale, float cst,
                                           int warp, int lane) {
 #pragma unroll 1
@@ -447,23 +445,20 @@ __device__ __forceinline__ void convert_q(uint8_t* qs, float* cf, int nrows, int
       continue;
     }
     if (q_fp8) {
-      if constexpr (!QRegs<QM>::E4) {  // widened exactly
-        const uint32_t w = *reinterpret_cast<const uint32_t*>(r + 4 * lane);
-        __syncwarp();
-        uint32_t h[2];
-        if constexpr (FMT == FMT_BF16) {
-          const float2 a = e4m3x2_to_float2((uint16_t)w), b = e4m3x2_to_float2((uint16_t)(w >> 16));
-          h[0] = pack_bf16x2(a.x, a.y);
-          h[1] = pack_bf16x2(b.x, b.y);
-        } else {
-          h[0] = e4m3x2_to_f16x2(w);
-          h[1] = e4m3x2_hi_to_f16x2(w);
-        }
-        *reinterpret_cast<uint32_t*>(r + 2 * q_place<FMT, QM>(4 * lane)) = h[0];
-        *reinterpret_cast<uint32_t*>(r + 2 * q_place<FMT, QM>(4 * lane + 2)) = h[1];
+      // widened exactly
+      const uint32_t w = *reinterpret_cast<const uint32_t*>(r + 4 * lane);
+      __syncwarp();
+      uint32_t h[2];
+      if constexpr (FMT == FMT_BF16) {
+        const float2 a = e4m3x2_to_float2((uint16_t)w), b = e4m3x2_to_float2((uint16_t)(w >> 16));
+        h[0] = pack_bf16x2(a.x, a.y);
+        h[1] = pack_bf16x2(b.x, b.y);
       } else {
-        *reinterpret_cast<uint32_t*>(r + 128 + 4 * lane) = 0u;  // no lo terms
+        h[0] = e4m3x2_to_f16x2(w);
+        h[1] = e4m3x2_hi_to_f16x2(w);
       }
+      *reinterpret_cast<uint32_t*>(r + 2 * q_place<FMT>(4 * lane)) = h[0];
+      *reinterpret_cast<uint32_t*>(r + 2 * q_place<FMT>(4 * lane + 2)) = h[1];
       if (lane == 0) cf[row] = fmaxf(q_scale * cst, 1.2e-38f);
       continue;
     }
@@ -478,20 +473,11 @@ __device__ __forceinline__ void convert_q(uint8_t* qs, float* cf, int nrows, int
     const bool bad = !(fabsf(a.x) <= 3.4e38f) || !(fabsf(a.y) <= 3.4e38f) || !(fabsf(b.x) <= 3.4e38f) || !(fabsf(b.y) <= 3.4e38f);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    int e = pow2_fit(amax, QRegs<QM>::E4 ? 448.f : 16384.f);
+    int e = pow2_fit(amax, 16384.f);
     e = e < -126 ? -126 : (e > 126 ? 126 : e);
     const float ps = pow2i(e);
-    if constexpr (QRegs<QM>::E4) {
-      const uint16_t h0 = pack_e4m3x2(a.x * ps, a.y * ps), h1 = pack_e4m3x2(b.x * ps, b.y * ps);
-      const float2 v0 = e4m3x2_to_float2(h0), v1 = e4m3x2_to_float2(h1);
-      *reinterpret_cast<uint32_t*>(r + 4 * lane) = (uint32_t)h0 | ((uint32_t)h1 << 16);
-      *reinterpret_cast<uint32_t*>(r + 128 + 4 * lane) =
-          (uint32_t)pack_e4m3x2(a.x * ps - v0.x, a.y * ps - v0.y) |
-          ((uint32_t)pack_e4m3x2(b.x * ps - v1.x, b.y * ps - v1.y) << 16);
-    } else {
-      *reinterpret_cast<uint32_t*>(r + 2 * q_place<FMT, QM>(4 * lane)) = pack_f16x2(a.x * ps, a.y * ps);
-      *reinterpret_cast<uint32_t*>(r + 2 * q_place<FMT, QM>(4 * lane + 2)) = pack_f16x2(b.x * ps, b.y * ps);
-    }
+    *reinterpret_cast<uint32_t*>(r + 2 * q_place<FMT>(4 * lane)) = pack_f16x2(a.x * ps, a.y * ps);
+    *reinterpret_cast<uint32_t*>(r + 2 * q_place<FMT>(4 * lane + 2)) = pack_f16x2(b.x * ps, b.y * ps);
     // A query row that is not finite has no finite logits; the reduced formats
     // would hide that.  (The factor is kept off zero: it multiplies -inf.)
     const bool any_bad = __any_sync(0xffffffffu, bad);
@@ -521,11 +507,12 @@ __device__ __forceinline__ uint32_t v_lane(uint32_t tile, int lane) {  // ldmatr
 
 // S of KC keys from key row kb of the tile.  kl: k_lane of the tile; ql[m]: this
 // lane's ldmatrix address of the query rows of tile m.  REG: the fragments are in aq.
-template <int FMT, int QM, bool NVR, int KC, int MT, bool REG>
+template <int FMT, bool NVR, int KC, int MT, bool REG>
 __device__ __forceinline__ void logits(uint32_t kl, const uint8_t* ksc, const uint32_t (&ql)[MT], int kb, int lane,
-                                       const uint32_t (&aq)[QRegs<QM>::KS][4], float (&sacc)[KC / 8][MT][4]) {
+                                       const uint32_t (&aq)[kDenseKSteps][4], float (&sacc)[KC / 8][MT][4]) {
   using TR = DenseTraits<FMT>;
   constexpr int NT = KC / 8;
+  constexpr int TG = NT < kDenseChains / MT ? NT : kDenseChains / MT;  // key tiles whose MMAs alternate
   kl += kb * (FMT == FMT_NVFP4 ? 64 : 128);
 #pragma unroll
   for (int t = 0; t < NT; ++t)
@@ -556,86 +543,79 @@ __device__ __forceinline__ void logits(uint32_t kl, const uint8_t* ksc, const ui
           }
         }
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const uint32_t sd = q < 2 ? __byte_perm(s2[t], s2[t], 0x1010) : __byte_perm(s2[t], s2[t], 0x3232);
-        uint32_t h[4];
-        e2m1x8_to_f16(w[t][q], h);
+      for (int t0 = 0; t0 < NT; t0 += TG) {
+        uint32_t h[TG][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          h[i] = hmul2(h[i], sd);
-          if constexpr (NVR) h[i] = e4m3_round_f16x2(h[i]);
+        for (int u = 0; u < TG; ++u) {
+          const uint32_t sx = s2[t0 + u], sd = q < 2 ? __byte_perm(sx, sx, 0x1010) : __byte_perm(sx, sx, 0x3232);
+          e2m1x8_to_f16(w[t0 + u][q], h[u]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            h[u][i] = hmul2(h[u][i], sd);
+            if constexpr (NVR) h[u][i] = e4m3_round_f16x2(h[u][i]);
+          }
         }
 #pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int u = 0; u < TG; ++u)
+#pragma unroll
+            for (int m = 0; m < MT; ++m) mma_f16_k16(sacc[t0 + u][m], a[i][m], h[u][2 * i], h[u][2 * i + 1]);
+      }
+    }
+  } else if constexpr (FMT == FMT_FP8) {  // a register's four dims of a key: both halves of a k step
+#pragma unroll
+    for (int kp = 0; kp < 2; ++kp) {
+      uint32_t b[NT][4];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) ldmatrix_x4(b[t], (kl ^ (kp << 6)) + t * 1024);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t a[MT][4];
+#pragma unroll
         for (int m = 0; m < MT; ++m) {
-          mma_f16_k16(sacc[t][m], a[0][m], h[0], h[1]);
-          mma_f16_k16(sacc[t][m], a[1][m], h[2], h[3]);
+          if constexpr (REG) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) a[m][e] = aq[4 * kp + i][e];
+          } else {
+            ldmatrix_x4(a[m], ql[m] + (4 * kp + i) * 32);
+          }
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const uint32_t b0 = e4m3x2_to_f16x2(b[t][i]), b1 = e4m3x2_hi_to_f16x2(b[t][i]);
+#pragma unroll
+          for (int m = 0; m < MT; ++m) mma_f16_k16(sacc[t][m], a[m], b0, b1);
         }
       }
     }
-  } else if constexpr (QRegs<QM>::E4) {
+  } else {
 #pragma unroll
-    for (int kp = 0; kp < 2; ++kp) {
-      uint32_t a[2][2][MT][4];  // [step][term]
+    for (int kp = 0; kp < 4; ++kp) {
+      uint32_t a[2][MT][4];
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
           if constexpr (REG) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) a[i][0][m][e] = aq[2 * kp + i][e];
+            for (int e = 0; e < 4; ++e) a[i][m][e] = aq[2 * kp + i][e];
           } else {
-            ldmatrix_x4(a[i][0][m], ql[m] + (2 * kp + i) * 32);
-            if constexpr (QM == QM_E4X2) ldmatrix_x4(a[i][1][m], ql[m] + 128 + (2 * kp + i) * 32);
+            ldmatrix_x4(a[i][m], ql[m] + (2 * kp + i) * 32);
           }
         }
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        uint32_t b[4];
-        ldmatrix_x4(b, (kl ^ (kp << 6)) + t * 1024);
+      for (int t0 = 0; t0 < NT; t0 += TG) {
+        uint32_t b[TG][4];
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int u = 0; u < TG; ++u)
+          ldmatrix_x4(b[u], (kl ^ ((kp & 1) << 6)) + (kp >> 1) * (TR::SK * 128) + (t0 + u) * 1024);
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            mma_e4m3_k32(sacc[t][m], a[i][0][m], b[2 * i], b[2 * i + 1]);
-            if constexpr (QM == QM_E4X2) mma_e4m3_k32(sacc[t][m], a[i][1][m], b[2 * i], b[2 * i + 1]);
-          }
-      }
-    }
-  } else {
-    // 16-bit steps: a load brings two (BF16) or four (FP8 widened) of them
-    constexpr int STEPS = QM == QM_F16K ? 4 : 2;
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int kp = 0; kp < 8 / STEPS; ++kp) {
-      uint32_t a[STEPS][MT][4];
+          for (int u = 0; u < TG; ++u)
 #pragma unroll
-      for (int i = 0; i < STEPS; ++i)
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          if constexpr (REG) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) a[i][m][e] = aq[STEPS * kp + i][e];
-          } else {
-            ldmatrix_x4(a[i][m], ql[m] + (STEPS * kp + i) * 32);
-          }
-        }
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        uint32_t b[4];
-        if constexpr (QM == QM_F16K) {
-          ldmatrix_x4(b, (kl ^ (kp << 6)) + t * 1024);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t b0 = e4m3x2_to_f16x2(b[i]), b1 = e4m3x2_hi_to_f16x2(b[i]);
-#pragma unroll
-            for (int m = 0; m < MT; ++m) mma_f16_k16(sacc[t][m], a[i][m], b0, b1);
-          }
-        } else {
-          ldmatrix_x4(b, (kl ^ ((kp & 1) << 6)) + (kp >> 1) * (TR::SK * 128) + t * 1024);
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int m = 0; m < MT; ++m) mma_bf16_k16(sacc[t][m], a[i][m], b[2 * i], b[2 * i + 1]);
-        }
+            for (int m = 0; m < MT; ++m) mma_bf16_k16(sacc[t0 + u][m], a[i][m], b[u][2 * i], b[u][2 * i + 1]);
       }
     }
   }
@@ -708,10 +688,9 @@ __device__ __forceinline__ void pv16(uint32_t vl, const uint8_t* vs, int kb, int
         a[3] &= m1;
       }
 #pragma unroll
-      for (int n = 0; n < NN; ++n) {
-        mma_cols<FMT, MASK>(o[c][n], a, pb[n][0], pb[n][1], keep[n]);
-        mma_cols<FMT, MASK>(o[c][n], a, pl[n][0], pl[n][1], keep[n]);
-      }
+      for (int n = 0; n < NN; ++n) mma_cols<FMT, MASK>(o[c][n], a, pb[n][0], pb[n][1], keep[n]);
+#pragma unroll
+      for (int n = 0; n < NN; ++n) mma_cols<FMT, MASK>(o[c][n], a, pl[n][0], pl[n][1], keep[n]);
     }
   } else {
     // the scales of this lane's keys (2j, 2j + 1, 2j + 8, 2j + 9), of the groups 2c + (g8 >> 2)
@@ -800,7 +779,7 @@ __device__ __forceinline__ int out_dim(int mt, int half, int g8) {
   else return 32 * (mt >> 1) + 4 * g8 + 2 * (mt & 1) + half;
 }
 
-template <int FMT, int NN, int NCG, int QM, bool NVR>
+template <int FMT, int NN, int NCG, bool NVR>
 __device__ void consumer(const DenseParams& p, const DenseTeam& tm, int bar, int warp, int lane) {
   using TR = DenseTraits<FMT>;
   using LY = DenseLayout<FMT, NN, NCG>;
@@ -832,25 +811,22 @@ __device__ void consumer(const DenseParams& p, const DenseTeam& tm, int bar, int
     const int c0 = f.cg * p.cper;
     const int nrows = p.cols - c0 < p.cper ? p.cols - c0 : p.cper;
     uint8_t* qs = tm.mem + LY::Q + (size_t)slot * LY::QSLOT;
-    convert_q<FMT, QM, LY::QROW>(qs, cf, nrows, LY::ROWS, p.q_fp8 != 0, p.q_scale, p.col_const, warp, lane);
+    convert_q<FMT, LY::QROW>(qs, cf, nrows, LY::ROWS, p.q_fp8 != 0, p.q_scale, p.col_const, warp, lane);
     named_bar_sync(bar, TEAM_THREADS);
     // ldmatrix addresses of the query tiles: row (lane & 7) + (lane & 8), column half
-    // lane >> 4.  Where a tile has 8 rows only, the other 8 are the lo terms
-    // (QM_ROWS) or repeat them and are not used.
+    // lane >> 4.  Where a tile has 8 rows only, the other 8 repeat them and are not used.
     uint32_t ql[MT];
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       const bool half = 2 * m + 1 == NN;
-      int off = (lane >> 4) * 16;
-      if (half && QM == QM_ROWS && (lane & 8)) off += 128;
-      ql[m] = smem_u32(qs) + (ct * LY::WROWS + 16 * m + (lane & 7) + (half ? 0 : (lane & 8))) * LY::QROW + off;
+      ql[m] = smem_u32(qs) + (ct * LY::WROWS + 16 * m + (lane & 7) + (half ? 0 : (lane & 8))) * LY::QROW + (lane >> 4) * 16;
     }
-    uint32_t aq[QRegs<QM>::KS][4];
+    uint32_t aq[kDenseKSteps][4];
     if constexpr (REG) {
 #pragma unroll
-      for (int ks = 0; ks < QRegs<QM>::KS; ++ks) {
+      for (int ks = 0; ks < kDenseKSteps; ++ks) {
         ldmatrix_x4(aq[ks], ql[0] + ks * 32);
-        if constexpr (QM != QM_ROWS) aq[ks][1] = aq[ks][3] = 0u;
+        aq[ks][1] = aq[ks][3] = 0u;
       }
     }
 
@@ -888,7 +864,7 @@ __device__ void consumer(const DenseParams& p, const DenseTeam& tm, int bar, int
           const int key0 = k * TR::SK + kb;  // position of the step's first key
           if (key0 >= f.T) break;
           float sacc[KC / 8][MT][4];
-          logits<FMT, QM, NVR, KC, MT, REG>(kl, ksc, ql, kb, lane, aq, sacc);
+          logits<FMT, NVR, KC, MT, REG>(kl, ksc, ql, kb, lane, aq, sacc);
           const bool masked = key0 + KC - 1 > lim0;
           // ---- raw logits y (x = y colf), masked; does any pass the reference?
           float2 y[KC / 8][NN];
@@ -899,7 +875,6 @@ __device__ void consumer(const DenseParams& p, const DenseTeam& tm, int bar, int
 #pragma unroll
             for (int n = 0; n < NN; ++n) {
               float2 v = make_float2(sacc[t][n >> 1][2 * (n & 1)], sacc[t][n >> 1][2 * (n & 1) + 1]);
-              if constexpr (QM == QM_ROWS) v = add2(v, make_float2(sacc[t][0][2], sacc[t][0][3]));  // hi + lo terms
               if constexpr (FMT == FMT_FP8) v = mul2(v, ks);
               y[t][n] = v;
             }
@@ -1146,7 +1121,7 @@ __device__ void consumer(const DenseParams& p, const DenseTeam& tm, int bar, int
 // (three teams): 128; WIDE: twelve warps launched with 168, of which the
 // producers' four keep 40 and the consumers' eight take 232 (384 x 168 = 128 x
 // 40 + 256 x 232 = 64,512 registers).
-template <int FMT, int NN, int NCG, int QM, bool NVR>
+template <int FMT, int NN, int NCG, bool NVR>
 __global__ void __launch_bounds__(DenseLayout<FMT, NN, NCG>::THREADS, 1)
     dense_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv, const DenseParams p) {
   using LY = DenseLayout<FMT, NN, NCG>;
@@ -1199,15 +1174,15 @@ __global__ void __launch_bounds__(DenseLayout<FMT, NN, NCG>::THREADS, 1)
       if (p.lse)
         for (long x = lane; x < rows; x += 32) p.lse[(size_t)s * rows + x] = -INFINITY;
     }
-    consumer<FMT, NN, NCG, QM, NVR>(p, tm, 1 + team, warp % kDenseWpg, lane);
+    consumer<FMT, NN, NCG, NVR>(p, tm, 1 + team, warp % kDenseWpg, lane);
   }
 }
 
-template <int FMT, int NN, int NCG, int QM, bool NVR>
+template <int FMT, int NN, int NCG, bool NVR>
 cudaError_t launch_one(const CUtensorMap* tk, const CUtensorMap* tv, const DenseParams& p, int num_sms, cudaStream_t st) {
   using LY = DenseLayout<FMT, NN, NCG>;
   static_assert(LY::ROWS == dense_rows(NN, NCG) && LY::TEAMS == dense_teams(FMT, NN), "the plan's sizes");
-  auto kern = dense_kernel<FMT, NN, NCG, QM, NVR>;
+  auto kern = dense_kernel<FMT, NN, NCG, NVR>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)LY::SMEM);
   if (e != cudaSuccess) return e;
   kern<<<(unsigned)num_sms, LY::THREADS, LY::SMEM, st>>>(*tk, *tv, p);

@@ -5,14 +5,9 @@ namespace msa {
 
 namespace {
 
-// E4M3 queries as they are; bf16 ones as two e4m3 terms (in the spare rows of
-// the tile, or by a second MMA), and against K widened to f16 where the second
-// MMA would make the tensor pipe the bound (more than 16 columns).
 template <int NN, int NCG>
 cudaError_t launch(const CUtensorMap* tk, const CUtensorMap* tv, const DenseParams& p, int num_sms, cudaStream_t st) {
-  if constexpr (NN == 1) return dense::launch_one<FMT_FP8, NN, NCG, QM_ROWS, false>(tk, tv, p, num_sms, st);
-  else if (p.q_fp8) return dense::launch_one<FMT_FP8, NN, NCG, QM_E4, false>(tk, tv, p, num_sms, st);
-  else return dense::launch_one<FMT_FP8, NN, NCG, NN == 2 ? QM_E4X2 : QM_F16K, false>(tk, tv, p, num_sms, st);
+  return dense::launch_one<FMT_FP8, NN, NCG, false>(tk, tv, p, num_sms, st);
 }
 
 }  // namespace
