@@ -112,12 +112,13 @@ struct DenseLayout {
   static constexpr int KGW = kDenseWpg / NCG;    // warps that share a group's columns, each its keys
   static constexpr size_t STAGE = 2 * (size_t)T::TILE;  // K tile, V tile
   static constexpr size_t SCALES = 2 * (size_t)T::SC;   // their scales, in a region of their own
-  static constexpr int DCH = NN == 1 ? 64 : (NN == 2 || NCG == 1 || FMT == FMT_NVFP4) ? 32 : 16;  // output dims a merge pass takes
-  static constexpr int MROW = DCH + 4;           // padded row of the merge area
+  static constexpr int END = NN == 1 ? 2 : NN == 2 ? 3 : 4;  // what a segment's end takes, in units
+  static constexpr int MT_OWN = 8 / KGW;         // output tiles a warp takes when the warps of a group join (NN > 1)
+  static constexpr int DCH = 64, MROW = DCH + 4;  // output dims of a pass of that join, padded (NN = 1)
   static constexpr int QROW = 272;               // a query row, padded (conflict-free reads)
   // per team
-  static constexpr size_t MERGE_BYTES = (size_t)kDenseWpg * WROWS * MROW * 4;
-  static constexpr size_t ML_BYTES = (size_t)kDenseWpg * WROWS * 8;
+  static constexpr size_t MERGE_BYTES = NN == 1 ? kDenseWpg * WROWS * MROW * 4 : kDenseWpg * (KGW - 1) * MT_OWN * 512;
+  static constexpr size_t ML_BYTES = (size_t)kDenseWpg * WROWS * 16;  // m, l, a weight
   static constexpr size_t QSLOT = (size_t)ROWS * QROW;
   static constexpr size_t CF_BYTES = (ROWS * 4 + 15) / 16 * 16;
   static constexpr size_t FIXED = MERGE_BYTES + ML_BYTES + 2 * QSLOT + CF_BYTES + 2 * sizeof(DenseFacts) + 320;
@@ -209,6 +210,13 @@ __device__ __forceinline__ int units_of(int T, int max_nb) {
   return (T < 1 || T > max_nb * kBlock) ? 0 : (T + SK - 1) / SK;
 }
 
+// The same with END more for the segment's end.
+template <int SK, int END>
+__device__ __forceinline__ int slots_of(int T, int max_nb) {
+  const int un = units_of<SK>(T, max_nb);
+  return un > 0 ? un + END : 0;
+}
+
 __device__ __forceinline__ long warp_sum(long v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -235,14 +243,17 @@ __device__ void producer(const CUtensorMap* tmk, const CUtensorMap* tmv, const D
   int* dead = tm.dead;
   const int S = p.S, max_nb = p.max_nb;
   const long GC = (long)p.G * p.CG;
-  // units in all, then the run of this team: [u0, u1)
+  // Units in all, then the run of this team: [u0, u1).  Every segment has END units
+  // more than its keys, which stand for its end (the join, the output, the next
+  // one's start), so that runs with many short segments are not the last: 61 ragged
+  // sequences of 48 columns take 88 us, and 100 where only keys are counted.
   long total = 0;
   int mine0 = 0;  // the length of sequence `lane`: a batch of up to 32 is read once
 #pragma unroll 4
   for (int s0 = 0; s0 < S; s0 += 32) {
     const int T = s0 + lane < S ? __ldg(p.seq_lens + s0 + lane) : 0;
     if (s0 == 0) mine0 = T;
-    total += units_of<TR::SK>(T, max_nb);
+    total += slots_of<TR::SK, LY::END>(T, max_nb);
   }
   total = warp_sum(total) * GC;
   const long teams = (long)gridDim.x * LY::TEAMS;
@@ -259,7 +270,7 @@ __device__ void producer(const CUtensorMap* tmk, const CUtensorMap* tmv, const D
   if (u1 > u0) {
     for (int s0 = 0; s0 < S; s0 += 32) {
       const int T = s0 == 0 ? mine0 : s0 + lane < S ? __ldg(p.seq_lens + s0 + lane) : 0;
-      const long mine = GC * units_of<TR::SK>(T, max_nb);
+      const long mine = GC * slots_of<TR::SK, LY::END>(T, max_nb);
       const long incl = warp_scan(mine, lane);
       const uint32_t over = __ballot_sync(0xffffffffu, sb + incl > u0);
       if (over) {
@@ -276,7 +287,6 @@ __device__ void producer(const CUtensorMap* tmk, const CUtensorMap* tmv, const D
   int bi = 0, ii = 0;
   bool ok = true;
   bool first = true;
-  if (u1 <= u0 && lane == 0) p.info[c] = make_int2(-1, 0);
 #pragma unroll 1
   while (u < u1 && ok) {
     const int T = s < 32 ? __shfl_sync(0xffffffffu, mine0, s & 31) : __ldg(p.seq_lens + s);
@@ -286,7 +296,15 @@ __device__ void producer(const CUtensorMap* tmk, const CUtensorMap* tmv, const D
       continue;
     }
     const long in_s = u - sb;
-    const int gc = (int)(in_s / un), k0 = (int)(in_s - (long)gc * un);
+    const int span = un + LY::END, gc = (int)(in_s / span), k0 = (int)(in_s - (long)gc * span);
+    if (k0 >= un) {  // another run's segment end
+      u += span - k0;
+      if (gc + 1 == GC) {
+        sb += (long)span * GC;
+        ++s;
+      }
+      continue;
+    }
     const long left = u1 - u;
     const int n = left < (long)(un - k0) ? (int)left : un - k0;
     const int g = gc / p.CG, cg = gc - g * p.CG;
@@ -377,12 +395,9 @@ __device__ void producer(const CUtensorMap* tmk, const CUtensorMap* tmv, const D
       }
       ++bi;
     }
-    u += n;
-    if (u >= sb + (long)un * GC) {
-      sb += (long)un * GC;
-      ++s;
-    }
+    u += n;  // from the last key's unit on, the next round passes the segment's end
   }
+  if (first && lane == 0) p.info[c] = make_int2(-1, 0);  // a run without keys
   if (ok) {
     const int slot = ii & 1, use = ii >> 1;
     if (use > 0 && !ring_wait(&iempty[slot], (uint32_t)((use - 1) & 1), dead)) {
@@ -795,8 +810,7 @@ __device__ void consumer(const DenseParams& p, const DenseTeam& tm, int bar, int
   const int g8 = lane >> 2, j = lane & 3;
   const int H = p.G * p.r;
   int* dead = tm.dead;
-  float* mo = reinterpret_cast<float*>(tm.mem + LY::MERGE);   // [warps][WROWS][MROW]
-  float* ml = reinterpret_cast<float*>(tm.mem + LY::ML);      // [warps][WROWS][2]
+  float4* ml = reinterpret_cast<float4*>(tm.mem + LY::ML);  // [warps][WROWS]: m, l, the scale of O or its weight
   float* cf = reinterpret_cast<float*>(tm.mem + LY::CF);      // [ROWS]
   int st = 0;
   uint32_t par = 0;
@@ -1048,71 +1062,193 @@ __device__ void consumer(const DenseParams& p, const DenseTeam& tm, int bar, int
     if (lane == 0) mbar_arrive(&tm.iempty[slot]);
 
     // ---------------- the segment's result: the warps of a column group hold different keys
+    const float osc = FMT == FMT_FP8 ? pow2i(-ev) : (FMT == FMT_NVFP4 ? p.v_global : 1.f);
 #pragma unroll
     for (int n = 0; n < NN; ++n) {
       float l = l_run[n].x + l_run[n].y;
       l += __shfl_xor_sync(0xffffffffu, l, 1);
       l += __shfl_xor_sync(0xffffffffu, l, 2);
-      if (j == 0) *reinterpret_cast<float2*>(ml + (warp * LY::WROWS + 8 * n + g8) * 2) = make_float2(m_run[n], l);
+      if (j == 0) ml[warp * LY::WROWS + 8 * n + g8] = make_float4(m_run[n], l, osc, 0.f);
     }
-    const float osc = FMT == FMT_FP8 ? pow2i(-ev) : (FMT == FMT_NVFP4 ? p.v_global : 1.f);
     const bool whole = f.part < 0;
-    constexpr int D4 = LY::DCH / 4;
-    constexpr int MTP = LY::DCH / 16;  // accumulator tiles a pass takes (their dims are consecutive)
-    static_assert(FMT != FMT_NVFP4 || LY::DCH >= 32, "a pass holds whole 32-dim chunks");
-#pragma unroll
-    for (int pass = 0; pass < 128 / LY::DCH; ++pass) {
-#pragma unroll
-      for (int tt = 0; tt < MTP; ++tt) {
-        const int mt = pass * MTP + tt;
-#pragma unroll
-        for (int n = 0; n < NN; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)  // column 2j + (e & 1), row half e >> 1
-            mo[(warp * LY::WROWS + 8 * n + 2 * j + (e & 1)) * LY::MROW + out_dim<FMT>(mt, e >> 1, g8) - pass * LY::DCH] =
-                o[mt][n][e] * osc;
-      }
-      named_bar_sync(bar, TEAM_THREADS);
+    if constexpr (NN == 1) {
+      // Few columns: half the dims at a time, then a thread a row and four dims.  The
+      // code runs once a segment, so its size counts (instruction fetches): only the
+      // stores out of the accumulators are unrolled.  256 sequences of 100 to 1,000
+      // tokens: 49.7 us, and 53.0 the other way.
+      float* mo = reinterpret_cast<float*>(tm.mem + LY::MERGE);  // [warps][WROWS][MROW]
+      constexpr int D4 = LY::DCH / 4;
+      constexpr int MTP = LY::DCH / 16;  // accumulator tiles a pass takes (their dims are consecutive)
+      static_assert(FMT != FMT_NVFP4 || LY::DCH >= 32, "a pass holds whole 32-dim chunks");
 #pragma unroll 1
-      for (int x = tid; x < LY::ROWS * D4; x += TEAM_THREADS) {
-        const int row = x / D4, d = 4 * (x - row * D4);
-        if (row >= nrows) continue;
-        const int cgi = row / LY::WROWS, tr = row - cgi * LY::WROWS;
-        float M = -INFINITY;
+      for (int pass = 0; pass < 128 / LY::DCH; ++pass) {
 #pragma unroll
-        for (int w = 0; w < KGW; ++w) M = fmaxf(M, ml[((cgi * KGW + w) * LY::WROWS + tr) * 2]);
-        const float ms = M == -INFINITY ? 0.f : M;
-        float L = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int ps = 0; ps < 128 / LY::DCH; ++ps)
+          if (ps == pass) {
+#pragma unroll
+            for (int n = 0; n < NN; ++n)
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {  // column 2j + c
+                float* row = mo + (warp * LY::WROWS + 8 * n + 2 * j + c) * LY::MROW;
+#pragma unroll
+                for (int tt = 0; tt < MTP; ++tt) {
+                  const float(&v)[4] = o[ps * MTP + tt][n];
+                  const int d = out_dim<FMT>(tt, 0, g8);  // within the chunk
+                  if constexpr (FMT == FMT_NVFP4) {
+                    const float(&v1)[4] = o[ps * MTP + (tt | 1)][n];
+                    if (!(tt & 1)) *reinterpret_cast<float4*>(row + d) = make_float4(v[c], v[c + 2], v1[c], v1[c + 2]);
+                  } else if constexpr (FMT == FMT_FP8) {
+                    *reinterpret_cast<float2*>(row + d) = make_float2(v[c], v[c + 2]);
+                  } else {
+                    row[d] = v[c];
+                    row[out_dim<FMT>(tt, 1, g8)] = v[c + 2];
+                  }
+                }
+              }
+          }
+        named_bar_sync(bar, TEAM_THREADS);
+#pragma unroll 1
+        for (int x = tid; x < LY::ROWS * D4; x += TEAM_THREADS) {
+          const int row = x / D4, d = 4 * (x - row * D4);
+          if (row >= nrows) continue;
+          const int cgi = row / LY::WROWS, tr = row - cgi * LY::WROWS;
+          float4 v[KGW];
+          float M = -INFINITY;
+#pragma unroll
+          for (int w = 0; w < KGW; ++w) {
+            v[w] = ml[(cgi * KGW + w) * LY::WROWS + tr];
+            M = fmaxf(M, v[w].x);
+          }
+          const float ms = M == -INFINITY ? 0.f : M;
+          float L = 0.f;
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int w = 0; w < KGW; ++w) {
+            const float fw = ex2(v[w].x - ms);
+            L += fw * v[w].y;
+            const float4 ov = *reinterpret_cast<const float4*>(mo + ((cgi * KGW + w) * LY::WROWS + tr) * LY::MROW + d);
+            acc.x += fw * (ov.x * v[w].z);
+            acc.y += fw * (ov.y * v[w].z);
+            acc.z += fw * (ov.z * v[w].z);
+            acc.w += fw * (ov.w * v[w].z);
+          }
+          const int dim = pass * LY::DCH + d;
+          if (whole) {
+            const float inv = L == 0.f ? 0.f : 1.f / L;
+            const int col = c0 + row, i = col / p.r, h = col - i * p.r;
+            const size_t orow = ((size_t)f.s * p.Q + i) * H + (size_t)f.g * p.r + h;
+            uint2 pk;
+            pk.x = pack_bf16x2(acc.x * inv, acc.y * inv);
+            pk.y = pack_bf16x2(acc.z * inv, acc.w * inv);
+            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + orow * kDim + dim) = pk;
+            if (dim == 0 && p.lse)
+              p.lse[orow] = L == 0.f ? -INFINITY : (M - SHIFT + log2f(L)) * 0.69314718055994531f;
+          } else {
+            *reinterpret_cast<float4*>(p.part_o + ((size_t)f.part * LY::ROWS + row) * kDim + dim) = acc;
+            if (dim == 0) p.part_ml[(size_t)f.part * LY::ROWS + row] = make_float2(M, L);
+          }
+        }
+        named_bar_sync(bar, TEAM_THREADS);  // the merge area is free again
+      }
+    } else {
+      // Many columns: each warp takes 1 / KGW of the output tiles from the others, as
+      // they lie in the lanes (16 bytes a lane, no bank conflicts), and writes them.
+      // 61 ragged sequences of 48 columns: 93.4 us, and 100 the other way.
+      float4* mo = reinterpret_cast<float4*>(tm.mem + LY::MERGE);  // [warps][receivers][tiles][lanes]
+      named_bar_sync(bar, TEAM_THREADS);
+      if (tid < LY::ROWS) {  // a thread a column: the weights of its group's warps
+        const int at = tid / LY::WROWS * KGW * LY::WROWS + tid % LY::WROWS;
+        float4 v[KGW];
+        float M = -INFINITY, L = 0.f;
 #pragma unroll
         for (int w = 0; w < KGW; ++w) {
-          const int src = (cgi * KGW + w) * LY::WROWS + tr;
-          const float2 v = lds_f2(ml + src * 2);
-          const float fw = ex2(v.x - ms);
-          L += fw * v.y;
-          const float4 ov = *reinterpret_cast<const float4*>(mo + src * LY::MROW + d);
-          acc.x += fw * ov.x;
-          acc.y += fw * ov.y;
-          acc.z += fw * ov.z;
-          acc.w += fw * ov.w;
+          v[w] = ml[at + w * LY::WROWS];
+          M = fmaxf(M, v[w].x);
         }
-        const int dim = pass * LY::DCH + d;
-        if (whole) {
-          const float inv = L == 0.f ? 0.f : 1.f / L;
-          const int col = c0 + row, i = col / p.r, h = col - i * p.r;
-          const size_t orow = ((size_t)f.s * p.Q + i) * H + (size_t)f.g * p.r + h;
-          uint2 pk;
-          pk.x = pack_bf16x2(acc.x * inv, acc.y * inv);
-          pk.y = pack_bf16x2(acc.z * inv, acc.w * inv);
-          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + orow * kDim + dim) = pk;
-          if (dim == 0 && p.lse)
-            p.lse[orow] = L == 0.f ? -INFINITY : (M - SHIFT + log2f(L)) * 0.69314718055994531f;
-        } else {
-          *reinterpret_cast<float4*>(p.part_o + ((size_t)f.part * LY::ROWS + row) * kDim + dim) = acc;
-          if (dim == 0) p.part_ml[(size_t)f.part * LY::ROWS + row] = make_float2(M, L);
+        const float ms = M == -INFINITY ? 0.f : M;
+#pragma unroll
+        for (int w = 0; w < KGW; ++w) {
+          v[w].x = ex2(v[w].x - ms);
+          L += v[w].x * v[w].y;
+        }
+        const float inv = whole ? (L == 0.f ? 0.f : 1.f / L) : 1.f;
+#pragma unroll
+        for (int w = 0; w < KGW; ++w) ml[at + w * LY::WROWS].w = v[w].x * inv;
+        if (tid < nrows) {
+          if (!whole) {
+            p.part_ml[(size_t)f.part * LY::ROWS + tid] = make_float2(M, L);
+          } else if (p.lse) {
+            const int col = c0 + tid, i = col / p.r, h = col - i * p.r;
+            p.lse[((size_t)f.s * p.Q + i) * H + (size_t)f.g * p.r + h] =
+                L == 0.f ? -INFINITY : (M - SHIFT + log2f(L)) * 0.69314718055994531f;
+          }
         }
       }
-      named_bar_sync(bar, TEAM_THREADS);  // the merge area is free again
+      named_bar_sync(bar, TEAM_THREADS);
+      const int me = warp % KGW, grp = warp - me;
+#pragma unroll
+      for (int n = 0; n < NN; ++n) {
+        const float4* own = ml + warp * LY::WROWS + 8 * n + 2 * j;
+        const float2 wc = make_float2(own[0].w, own[1].w);  // columns 2j, 2j + 1
+        // where this lane writes: BF16 lanes hold dims 8 apart and pair up with a neighbour's, one column each
+        size_t at[2];
+        bool live[2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int row = ct * LY::WROWS + 8 * n + 2 * j + (FMT == FMT_BF16 ? (g8 & 1) : c);
+          live[c] = row < nrows;
+          const int col = c0 + row, i = col / p.r, h = col - i * p.r;
+          at[c] = whole ? (((size_t)f.s * p.Q + i) * H + (size_t)f.g * p.r + h) * kDim
+                        : ((size_t)f.part * LY::ROWS + row) * kDim;
+        }
+#pragma unroll
+        for (int w = 0; w < KGW; ++w)
+#pragma unroll
+          for (int u = 0; u < LY::MT_OWN; ++u) {
+            float(&v)[4] = o[w * LY::MT_OWN + u][n];
+            v[0] = v[0] * osc * wc.x;
+            v[1] = v[1] * osc * wc.y;
+            v[2] = v[2] * osc * wc.x;
+            v[3] = v[3] * osc * wc.y;
+            if (w != me)
+              mo[((warp * (KGW - 1) + (w < me ? w : w - 1)) * LY::MT_OWN + u) * 32 + lane] = make_float4(v[0], v[1], v[2], v[3]);
+          }
+        named_bar_sync(bar, TEAM_THREADS);
+#pragma unroll
+        for (int u = 0; u < LY::MT_OWN; ++u) {
+          float a[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int w = 0; w < KGW; ++w) {  // in the order of the keys
+            const float(&mine)[4] = o[w * LY::MT_OWN + u][n];
+            float4 x = make_float4(mine[0], mine[1], mine[2], mine[3]);
+            if (w != me) x = mo[(((grp + w) * (KGW - 1) + (me < w ? me : me - 1)) * LY::MT_OWN + u) * 32 + lane];
+            a[0] += x.x;
+            a[1] += x.y;
+            a[2] += x.z;
+            a[3] += x.w;
+          }
+          const int mt = me * LY::MT_OWN + u;
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float2 v;
+            int dim;
+            if constexpr (FMT == FMT_BF16) {
+              const bool odd = g8 & 1;
+              const float got = __shfl_xor_sync(0xffffffffu, odd ? a[2 * c] : a[2 * c + 1], 4);
+              v = odd ? make_float2(got, a[2 * c + 1]) : make_float2(a[2 * c], got);
+              dim = out_dim<FMT>(mt, c, g8 & ~1);
+            } else {
+              v = make_float2(a[c], a[c + 2]);
+              dim = out_dim<FMT>(mt, 0, g8);
+            }
+            if (live[c]) {
+              if (whole) *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + at[c] + dim) = pack_bf16x2(v.x, v.y);
+              else *reinterpret_cast<float2*>(p.part_o + at[c] + dim) = v;
+            }
+          }
+        }
+        named_bar_sync(bar, TEAM_THREADS);  // the merge area is free again
+      }
     }
   }
 }
