@@ -19,13 +19,13 @@ namespace {
 
 constexpr int kJoinWarps = 8;
 constexpr int kJoinThreads = 32 * kJoinWarps;
-constexpr int kJoinBatch = 8;  // partials of a row a warp has in flight
 
 // runs: in the grid of the attend; rows: of a partial; cta_rows: a CTA's share of
 // them (blockIdx.y); shift: log2 of P's scale, which l carries.
 template <bool BY_SEGMENT>
-__global__ void __launch_bounds__(kJoinThreads) dense_combine_kernel(const DenseParams p, int runs, int rows, int cta_rows,
+__global__ void __launch_bounds__(kJoinThreads, BY_SEGMENT ? 3 : 5) dense_combine_kernel(const DenseParams p, int runs, int rows, int cta_rows,
                                                                      float shift) {
+  constexpr int kJoinBatch = BY_SEGMENT ? 8 : 4;  // partials of a row a warp has in flight
   __shared__ float so[kJoinWarps][132];
   __shared__ float sm[kJoinWarps][2];
   __shared__ int s_first, s_end;
@@ -164,7 +164,7 @@ cudaError_t launch_dense_combine(const DenseParams& p, int fmt, int num_sms, cud
   const float shift = fmt != FMT_BF16 ? kDensePShift : 0.f;
   // few segments: each has many partials, so its rows go to CTAs of their own
   const bool by_segment = segments <= runs / 4;
-  const int cta_rows = by_segment ? (p.cper <= 8 ? 1 : kJoinWarps) : (p.cper <= kJoinWarps ? p.cper : 2 * kJoinWarps);
+  const int cta_rows = by_segment && p.cper <= 8 ? 1 : (p.cper < kJoinWarps ? p.cper : kJoinWarps);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(by_segment ? segments : runs - 1), (unsigned)((p.cper + cta_rows - 1) / cta_rows));
   cfg.blockDim = dim3(kJoinThreads);
