@@ -837,6 +837,9 @@ msa_status_t msa_rope_insert(const msa_cache_t* cache, const msa_rope_t* rope, i
   RopeParams p;
   std::memset(&p, 0, sizeof(p));
   p.rope = *rope;
+  static_assert(MSA_ROPE_MAX_AXES <= 4, "two bits an axis");
+  for (int i = 0; i < rope->rotary_dim / 2; ++i)
+    for (int b = 0; b < 2; ++b) p.axis_bits[b][i >> 5] |= (uint32_t)(rope->axis[i] >> b & 1) << (i & 31);
   p.num_tokens = num_tokens;
   p.Hq = num_q_heads;
   p.H = cache->num_kv_heads;

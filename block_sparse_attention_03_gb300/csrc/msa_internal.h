@@ -262,6 +262,7 @@ inline int dense_unit_keys(int fmt) { return fmt == FMT_BF16 ? 64 : 128; }
 // Rotary insert (msa_rope.cu).
 struct RopeParams {
   msa_rope_t rope;
+  uint32_t axis_bits[2][2];             // bit b of the axis of pair 32 k + i: bit i of [b][k]
   int32_t num_tokens, Hq, Giq, H, Gik;  // tokens; q, index q, K (and V), index K heads (0: none)
   int32_t num_blocks, kv_fmt, idx_fmt;
   const int32_t* positions;              // [axes][num_tokens]

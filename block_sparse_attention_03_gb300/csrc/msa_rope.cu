@@ -158,24 +158,15 @@ template <int KVF, int IF, bool ADJ>
 __global__ void __launch_bounds__(32 * kRopeWarps, kRopeCtas) rope_kernel(const __grid_constant__ RopeParams p) {
   extern __shared__ RowDesc s_rows[];  // four a quad
   __shared__ uint64_t s_turns[64];
-  __shared__ int s_axis[64];
   __shared__ __align__(16) float s_w[4][kDim];           // offset + norm weight
   __shared__ __align__(16) float2 s_cs[kRopeWarps][64];  // cosines, sines
   __shared__ __align__(16) float s_max[kRopeWarps][4][16];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l8 = lane & 7, sub = lane >> 3;
   const int pairs = p.rope.rotary_dim >> 1;
-  if (threadIdx.x < 64) {
-    s_turns[threadIdx.x] = p.rope.turns[threadIdx.x];
-    s_axis[threadIdx.x] = p.rope.axis[threadIdx.x];
-  }
-  for (int i = threadIdx.x; i < 4 * kDim; i += 32 * kRopeWarps) {
-    const __nv_bfloat16* w = p.w[i / kDim];
-    s_w[i / kDim][i % kDim] = w ? __bfloat162float(w[i % kDim]) + p.w_offset : 1.f;
-  }
   // quads of rows, kind after kind: where each ends
   const int e0 = (p.Hq + 3) >> 2, e1 = e0 + ((p.Giq + 3) >> 2), e2 = e1 + ((p.H + 3) >> 2), e3 = e2 + ((p.H + 3) >> 2),
             e4 = e3 + p.Gik;
-  for (int r = threadIdx.x; r < 4 * e4; r += 32 * kRopeWarps) {
+  auto describe = [&](int r) {
     const int qd = r >> 2;
     RowDesc d;
     const int h = r - 4 * (qd < e0 ? 0 : qd < e1 ? e0 : qd < e2 ? e1 : qd < e3 ? e2 : e3);
@@ -203,9 +194,8 @@ __global__ void __launch_bounds__(32 * kRopeWarps, kRopeCtas) rope_kernel(const 
     // (a quarter without a head reads the last one's row again)
     d.src = reinterpret_cast<const uint8_t*>(src + (long)min(h, heads - 1) * kDim);
     d.src_step = 2 * step;
-    s_rows[r] = d;
-  }
-  __syncthreads();
+    return d;
+  };
   // this lane's elements [dA, dA + 8) and [dB, dB + 8)
   int dA, dB;
   bool rot;
@@ -223,30 +213,44 @@ __global__ void __launch_bounds__(32 * kRopeWarps, kRopeCtas) rope_kernel(const 
   // this warp's run of quads, [u, u1) of num_tokens x e4
   const long quads = (long)p.num_tokens * e4, warps = (long)gridDim.x * kRopeWarps;
   const long w = (long)blockIdx.x * kRopeWarps + warp;
-  const long u0 = w * quads / warps, u1 = (w + 1) * quads / warps;
-  if (u0 >= u1) return;
-  long t = u0 / e4;
-  int qd = (int)(u0 - t * e4);
+  // (w quads / warps, in parts that keep the divisions to 32 bits where the total is)
+  const bool small = (quads >> 32) == 0;
+  const long each = small ? (long)((uint32_t)quads / (uint32_t)warps) : quads / warps;
+  const uint32_t rest = (uint32_t)(quads - each * warps);  // warps are at most some thousands
+  const long u0 = w * each + (uint32_t)w * rest / (uint32_t)warps;
+  const long u1 = (w + 1) * each + (uint32_t)(w + 1) * rest / (uint32_t)warps;
+  int t = small ? (int)((uint32_t)u0 / (uint32_t)e4) : (int)(u0 / e4);
+  int qd = (int)(u0 - (long)t * e4);
   int left = (int)(u1 - u0);
 
+  // The first reads, of memory, and then what the CTA keeps of the heads and weights.
+  int axis[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) axis[k] = (p.axis_bits[0][k] >> lane & 1) | (p.axis_bits[1][k] >> lane & 1) << 1;
   // the slot and positions of a token, and the raw elements of a quad's rows, are
   // read one ahead
-  int slot_n, pos_n[2] = {0, 0};
-  auto fetch = [&](long tt) {
+  int slot_n = -1, pos_n[2] = {0, 0};
+  auto fetch = [&](int tt) {
     slot_n = __ldg(p.slots + tt);
 #pragma unroll
     for (int k = 0; k < 2; ++k)
-      if (lane + 32 * k < pairs) pos_n[k] = __ldg(p.positions + (size_t)s_axis[lane + 32 * k] * p.num_tokens + tt);
+      if (lane + 32 * k < pairs) pos_n[k] = __ldg(p.positions + (size_t)axis[k] * p.num_tokens + tt);
   };
   uint4 a1, b1;
-  auto load = [&](long tt, int q) {
-    const RowDesc& d = s_rows[4 * q + sub];
+  auto load = [&](int tt, const RowDesc& d) {
     const uint8_t* src = d.src + tt * d.src_step;
     a1 = *reinterpret_cast<const uint4*>(src + 2 * dA);
     b1 = *reinterpret_cast<const uint4*>(src + 2 * dB);
   };
-  fetch(t);
-  load(t, qd);
+  if (left > 0) fetch(t);
+  if (threadIdx.x < 64) s_turns[threadIdx.x] = p.rope.turns[threadIdx.x];
+  for (int i = threadIdx.x; i < 4 * kDim; i += 32 * kRopeWarps) {
+    const __nv_bfloat16* w = p.w[i / kDim];
+    s_w[i / kDim][i % kDim] = w ? __bfloat162float(w[i % kDim]) + p.w_offset : 1.f;
+  }
+  for (int r = threadIdx.x; r < 4 * e4; r += 32 * kRopeWarps) s_rows[r] = describe(r);
+  __syncthreads();
+  if (left > 0) load(t, s_rows[4 * qd + sub]);
 #pragma unroll 1
   while (left > 0) {
     const int slot = slot_n;
@@ -264,25 +268,16 @@ __global__ void __launch_bounds__(32 * kRopeWarps, kRopeCtas) rope_kernel(const 
     }
     __syncwarp();
     if (left > e4 - qd) fetch(t + 1);
-    // halves: pair dA + i for element i of both parts; adjacent: each pair's sine and cosine
-    float2 c[4], s[4], cb[ADJ ? 4 : 1], sb[ADJ ? 4 : 1];
-    if (rot) {
-      const int first = ADJ ? dA >> 1 : dA;
+    // Halves: pair dA + i for element i of both parts, held for the token.  Adjacent
+    // layouts need twice as many and read them for each quad instead (16,384 tokens
+    // into NVFP4 with three axes: 78.0 us, and 82.0 held; halves into BF16 51.8 held, 55.6 read).
+    float2 c[4], s[4];
+    if (!ADJ && rot) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float4 v = *reinterpret_cast<const float4*>(&s_cs[warp][first + 2 * i]);
-        if constexpr (ADJ) {
-          // pairs first + 2i and first + 2i + 1: out = own x cos + other x (-sin, sin)
-          float2* cc = i < 2 ? c + 2 * i : cb + 2 * (i - 2);
-          float2* ss = i < 2 ? s + 2 * i : sb + 2 * (i - 2);
-          cc[0] = make_float2(v.x, v.x);
-          ss[0] = make_float2(-v.y, v.y);
-          cc[1] = make_float2(v.z, v.z);
-          ss[1] = make_float2(-v.w, v.w);
-        } else {
-          c[i] = make_float2(v.x, v.z);
-          s[i] = make_float2(v.y, v.w);
-        }
+        const float4 v = *reinterpret_cast<const float4*>(&s_cs[warp][dA + 2 * i]);
+        c[i] = make_float2(v.x, v.z);
+        s[i] = make_float2(v.y, v.w);
       }
     }
     const bool live = slot >= 0;
@@ -296,8 +291,8 @@ __global__ void __launch_bounds__(32 * kRopeWarps, kRopeCtas) rope_kernel(const 
 #pragma unroll 1
     for (; qd < end; ++qd) {
       const uint32_t u[8] = {a1.x, a1.y, a1.z, a1.w, b1.x, b1.y, b1.z, b1.w};
-      if (qd + 1 < end) load(t, qd + 1);
-      else if (left > 0) load(t + 1, 0);
+      if (qd + 1 < end) load(t, s_rows[4 * (qd + 1) + sub]);
+      else if (left > 0) load(t + 1, s_rows[sub]);
       const RowDesc& d = s_rows[4 * qd + sub];
       const int kind = d.kind;  // the same in all rows of the quad
       uint8_t* const out = d.out;
@@ -328,11 +323,13 @@ __global__ void __launch_bounds__(32 * kRopeWarps, kRopeCtas) rope_kernel(const 
         if (rot) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float2 a = y[i], b = y[4 + i];
-            if constexpr (ADJ) {
-              y[i] = fma2(a, c[i], mul2(make_float2(a.y, a.x), s[i]));
-              y[4 + i] = fma2(b, cb[i], mul2(make_float2(b.y, b.x), sb[i]));
+            if constexpr (ADJ) {  // elements 2i and 2i + 1 are pairs: own x cos + other x (-sin, sin)
+              const float4 v = *reinterpret_cast<const float4*>(&s_cs[warp][(dA >> 1) + 2 * i]);
+              float2* z = y + 2 * i;
+              z[0] = fma2(z[0], make_float2(v.x, v.x), mul2(make_float2(z[0].y, z[0].x), make_float2(-v.y, v.y)));
+              z[1] = fma2(z[1], make_float2(v.z, v.z), mul2(make_float2(z[1].y, z[1].x), make_float2(-v.w, v.w)));
             } else {
+              const float2 a = y[i], b = y[4 + i];
               y[i] = fma2(a, c[i], mul2(b, make_float2(-s[i].x, -s[i].y)));
               y[4 + i] = fma2(b, c[i], mul2(a, s[i]));
             }
@@ -340,7 +337,7 @@ __global__ void __launch_bounds__(32 * kRopeWarps, kRopeCtas) rope_kernel(const 
         }
       }
       if (kind <= KIND_IQ) {
-        uint8_t* const o = out + t * d.out_step;
+        uint8_t* const o = out + (long)t * d.out_step;
         if (kind == KIND_Q ? p.q_fp8 : p.iq_fp8) {
           const float iv = kind == KIND_Q ? p.q_inv : p.iq_inv;
 #pragma unroll
