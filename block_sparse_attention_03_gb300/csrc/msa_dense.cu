@@ -164,7 +164,7 @@ cudaError_t launch_dense_combine(const DenseParams& p, int fmt, int num_sms, cud
   const float shift = fmt != FMT_BF16 ? kDensePShift : 0.f;
   // few segments: each has many partials, so its rows go to CTAs of their own
   const bool by_segment = segments <= runs / 4;
-  const int cta_rows = by_segment && p.cper <= 8 ? 1 : (p.cper < kJoinWarps ? p.cper : kJoinWarps);
+  const int cta_rows = by_segment ? (p.cper <= 8 ? 1 : 4) : (p.cper < kJoinWarps ? p.cper : kJoinWarps);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(by_segment ? segments : runs - 1), (unsigned)((p.cper + cta_rows - 1) / cta_rows));
   cfg.blockDim = dim3(kJoinThreads);

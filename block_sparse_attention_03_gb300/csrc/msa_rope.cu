@@ -268,16 +268,25 @@ __global__ void __launch_bounds__(32 * kRopeWarps, kRopeCtas) rope_kernel(const 
     }
     __syncwarp();
     if (left > e4 - qd) fetch(t + 1);
-    // Halves: pair dA + i for element i of both parts, held for the token.  Adjacent
-    // layouts need twice as many and read them for each quad instead (16,384 tokens
-    // into NVFP4 with three axes: 78.0 us, and 82.0 held; halves into BF16 51.8 held, 55.6 read).
-    float2 c[4], s[4];
-    if (!ADJ && rot) {
+    // halves: pair dA + i for element i of both parts; adjacent: each pair's sine and cosine
+    float2 c[4], s[4], cb[ADJ ? 4 : 1], sb[ADJ ? 4 : 1];
+    if (rot) {
+      const int first = ADJ ? dA >> 1 : dA;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float4 v = *reinterpret_cast<const float4*>(&s_cs[warp][dA + 2 * i]);
-        c[i] = make_float2(v.x, v.z);
-        s[i] = make_float2(v.y, v.w);
+        const float4 v = *reinterpret_cast<const float4*>(&s_cs[warp][first + 2 * i]);
+        if constexpr (ADJ) {
+          // pairs first + 2i and first + 2i + 1: out = own x cos + other x (-sin, sin)
+          float2* cc = i < 2 ? c + 2 * i : cb + 2 * (i - 2);
+          float2* ss = i < 2 ? s + 2 * i : sb + 2 * (i - 2);
+          cc[0] = make_float2(v.x, v.x);
+          ss[0] = make_float2(-v.y, v.y);
+          cc[1] = make_float2(v.z, v.z);
+          ss[1] = make_float2(-v.w, v.w);
+        } else {
+          c[i] = make_float2(v.x, v.z);
+          s[i] = make_float2(v.y, v.w);
+        }
       }
     }
     const bool live = slot >= 0;
@@ -323,13 +332,11 @@ __global__ void __launch_bounds__(32 * kRopeWarps, kRopeCtas) rope_kernel(const 
         if (rot) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            if constexpr (ADJ) {  // elements 2i and 2i + 1 are pairs: own x cos + other x (-sin, sin)
-              const float4 v = *reinterpret_cast<const float4*>(&s_cs[warp][(dA >> 1) + 2 * i]);
-              float2* z = y + 2 * i;
-              z[0] = fma2(z[0], make_float2(v.x, v.x), mul2(make_float2(z[0].y, z[0].x), make_float2(-v.y, v.y)));
-              z[1] = fma2(z[1], make_float2(v.z, v.z), mul2(make_float2(z[1].y, z[1].x), make_float2(-v.w, v.w)));
+            const float2 a = y[i], b = y[4 + i];
+            if constexpr (ADJ) {
+              y[i] = fma2(a, c[i], mul2(make_float2(a.y, a.x), s[i]));
+              y[4 + i] = fma2(b, cb[i], mul2(make_float2(b.y, b.x), sb[i]));
             } else {
-              const float2 a = y[i], b = y[4 + i];
               y[i] = fma2(a, c[i], mul2(b, make_float2(-s[i].x, -s[i].y)));
               y[4 + i] = fma2(b, c[i], mul2(a, s[i]));
             }
