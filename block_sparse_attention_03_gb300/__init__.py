@@ -139,15 +139,16 @@ def _ptr(t) -> Optional[int]:
 _raw_stream = None
 
 
-def _stream(stream) -> Optional[int]:
+def _stream(stream, device=None) -> Optional[int]:
     if stream is None:
         global _raw_stream
         if _raw_stream is None:
             import torch
             # the current stream's handle without a Stream object around it (a microsecond less)
-            raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), torch.cuda.current_device
-            _raw_stream = (lambda: raw(device())) if raw else (lambda: torch.cuda.current_stream().cuda_stream)
-        return _raw_stream()
+            raw, current = getattr(torch._C, "_cuda_getCurrentRawStream", None), torch.cuda.current_device
+            _raw_stream = (lambda d: raw(current() if d is None else d)) if raw else \
+                (lambda d: torch.cuda.current_stream(d).cuda_stream)
+        return _raw_stream(device)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -287,11 +288,24 @@ _DENSE = _Layout(_CACHE, _BATCH, _CONFIG, _QUERY)
 _ROPE = _Layout(_CACHE, _ROWS, _QUERY, _ROWS, _QUERY, _ROWS, _ROWS, _ROWS, _NORM)
 
 
+_int32 = _bf16 = _device = None
+
+
+def _torch_names() -> None:
+    global _int32, _bf16, _device
+    import torch
+    _int32, _bf16, _device = torch.int32, torch.bfloat16, torch.cuda.current_device
+
+
+# The serving calls refuse what the kernels would misread: other types, strides and
+# sizes, and tensors that are not on the current device, where the kernels run.  The
+# checks stand in one expression a call (a helper's call costs as much as a check).
+
 def _rows(t, shape, where: str):
-    """(pointer, token stride) of a projection's rows of the given shape ([tokens][heads][128], or
+    """(pointer, token stride) of a projection's bf16 rows of the given shape ([tokens][heads][128], or
     [tokens][128] for one head), the heads side by side."""
     strides = t.stride()
-    if t.shape != shape or strides[-1] != 1 or (len(shape) == 3 and strides[1] != 128 and shape[1] != 1):
+    if t.shape != shape or strides[-1] != 1 or (len(shape) == 3 and strides[1] != 128 and shape[1] != 1) or t.dtype is not _bf16:
         raise MsaError(1, where)
     return t.data_ptr(), strides[0]
 
@@ -394,15 +408,26 @@ def msa_dense_workspace_size(cache: PagedCache, batch: Batch, num_q_heads: int) 
 
 
 def msa_dense_attend(cache, batch, cfg, q: Query, num_q_heads: int, out, lse, workspace, stream=None) -> None:
-    """Attention of each new token (up to 8 a sequence) over its whole sequence in the paged cache."""
-    lens, table = batch.seq_lens, batch.block_table
-    at = _DENSE.pack(*_cache_values(cache), lens.shape[0], batch.q_per_seq, table.shape[1], lens.data_ptr(), table.data_ptr(),
+    """Attention of each new token (up to 8 a sequence) over its whole sequence in the paged cache.
+    q.data, out: [S * q_per_seq][num_q_heads][128], lse: fp32 [S * q_per_seq][num_q_heads] or None, all dense."""
+    if _int32 is None:
+        _torch_names()
+    lens, table, data = batch.seq_lens, batch.block_table, q.data
+    shape, rows, dev = table.shape, lens.numel() * batch.q_per_seq * num_q_heads, cache.k.get_device()
+    if (dev < 0 or dev != _device() or len(shape) != 2 or shape[0] != lens.numel()
+            or lens.dtype is not _int32 or table.dtype is not _int32 or not lens.is_contiguous() or not table.is_contiguous()
+            or data.numel() != rows * 128 or not data.is_contiguous() or data.element_size() != (1 if q.dtype == "fp8" else 2)
+            or out.numel() != rows * 128 or not out.is_contiguous() or out.dtype is not _bf16
+            or (lse is not None and (lse.numel() != rows or not lse.is_contiguous() or lse.element_size() != 4))
+            or lens.get_device() != dev or table.get_device() != dev or data.get_device() != dev or out.get_device() != dev):
+        raise MsaError(1, "msa_dense_attend")
+    at = _DENSE.pack(*_cache_values(cache), shape[0], batch.q_per_seq, shape[1], lens.data_ptr(), table.data_ptr(),
                      cfg.topk, cfg.init_blocks, cfg.local_blocks, cfg.index_scale, cfg.sm_scale,
                      SCORE_TYPES.get(cfg.score_type, -1), PREFILL_SELECT.get(cfg.prefill_select, -1),
-                     q.data.data_ptr(), DTYPES[q.dtype], q.scale)
+                     data.data_ptr(), DTYPES[q.dtype], q.scale)
     o = _DENSE.offsets
     _check(lib().msa_dense_attend(at + o[0], at + o[1], at + o[2], at + o[3], num_q_heads, out.data_ptr(), _p(lse),
-                                  workspace.data_ptr(), _nbytes(workspace), _stream(stream)), "msa_dense_attend")
+                                  workspace.data_ptr(), _nbytes(workspace), _stream(stream, dev)), "msa_dense_attend")
 
 
 def msa_rope_init(rotary_dim: int, theta: float, sections=None, layout: str = "halves") -> MsaRopeT:
@@ -417,32 +442,42 @@ def msa_rope_init(rotary_dim: int, theta: float, sections=None, layout: str = "h
 
 def msa_rope_insert(cache, rope: MsaRopeT, positions, slot_mapping, q, q_out: Query, index_q, index_q_out: Optional[Query],
                     k, v, index_k, norm: Optional[QkNorm], workspace, stream=None) -> None:
-    """Norm and rotate q, index q, k and index k (bf16 [T][heads][128], any token stride), write the
-    queries to q_out / index_q_out and k, v, index k into the paged caches at slot_mapping (int32 [T]).
+    """Norm and rotate q, index q, k and index k (bf16 [T][H][128], any token stride), write the
+    queries to q_out / index_q_out (dense) and k, v, index k into the paged caches at slot_mapping (int32 [T]).
     positions: int32 [axes][T], or [T] for one axis."""
+    if _int32 is None:
+        _torch_names()
     where = "msa_rope_insert"
-    T, H = slot_mapping.numel(), cache.num_kv_heads
-    if q.dim() != 3 or positions.numel() != rope.axes * T or not positions.is_contiguous():
+    T, H, dev, qd = slot_mapping.numel(), cache.num_kv_heads, cache.k.get_device(), q_out.data
+    if (dev < 0 or dev != _device() or q.dim() != 3
+            or positions.numel() != rope.axes * T or positions.dtype is not _int32 or not positions.is_contiguous()
+            or slot_mapping.dtype is not _int32 or not slot_mapping.is_contiguous()
+            or qd.numel() != q.numel() or not qd.is_contiguous() or qd.element_size() != (1 if q_out.dtype == "fp8" else 2)
+            or positions.get_device() != dev or slot_mapping.get_device() != dev or q.get_device() != dev or k.get_device() != dev
+            or v.get_device() != dev):
         raise MsaError(1, where)
     hq = q.shape[1]
-    if q_out.data.numel() != T * hq * 128 or not q_out.data.is_contiguous():
-        raise MsaError(1, where)
     none, kv = (0, 0), (T, H, 128)
-    iqo = (0, 0, 0.0)
+    iqo, w = (0, 0, 0.0), (0, 0, 0, 0, 0.0, 0.0)
     if index_q_out is not None:
-        if index_q_out.data.numel() != T * H * 128 or not index_q_out.data.is_contiguous():
+        x = index_q_out.data
+        if x.numel() != T * H * 128 or not x.is_contiguous() or x.element_size() != (1 if index_q_out.dtype == "fp8" else 2):
             raise MsaError(1, where)
-        iqo = (index_q_out.data.data_ptr(), DTYPES[index_q_out.dtype], index_q_out.scale)
-    w = (0, 0, 0, 0, 0.0, 0.0) if norm is None else (_p(norm.q), _p(norm.k), _p(norm.index_q), _p(norm.index_k), norm.eps,
-                                                     norm.offset)
-    at = _ROPE.pack(*_cache_values(cache), *_rows(q, (T, hq, 128), where), q_out.data.data_ptr(), DTYPES[q_out.dtype], q_out.scale,
+        iqo = (x.data_ptr(), DTYPES[index_q_out.dtype], index_q_out.scale)
+    if norm is not None:
+        w = norm.q, norm.k, norm.index_q, norm.index_k
+        for x in w:
+            if x is not None and (x.numel() != 128 or x.dtype is not _bf16 or not x.is_contiguous()):
+                raise MsaError(1, where)
+        w = (_p(norm.q), _p(norm.k), _p(norm.index_q), _p(norm.index_k), norm.eps, norm.offset)
+    at = _ROPE.pack(*_cache_values(cache), *_rows(q, (T, hq, 128), where), qd.data_ptr(), DTYPES[q_out.dtype], q_out.scale,
                     *(none if index_q is None else _rows(index_q, kv, where)), *iqo, *_rows(k, kv, where),
                     *_rows(v, kv, where), *(none if index_k is None else _rows(index_k, (T, 128) if index_k.dim() == 2 else (T, 1, 128), where)), *w)
     o = _ROPE.offsets
     _check(lib().msa_rope_insert(at, ctypes.byref(rope), T, positions.data_ptr(), slot_mapping.data_ptr(), hq, at + o[1], at + o[2],
                                  0 if index_q is None else at + o[3], 0 if index_q_out is None else at + o[4], at + o[5],
                                  at + o[6], 0 if index_k is None else at + o[7], 0 if norm is None else at + o[8],
-                                 workspace.data_ptr(), _nbytes(workspace), _stream(stream)), where)
+                                 workspace.data_ptr(), _nbytes(workspace), _stream(stream, dev)), where)
 
 
 def msa_build_tables(num_blocks: int, cached_lens, new_lens, block_table, free_blocks, free_count, seq_lens, token_offsets,
@@ -450,15 +485,21 @@ def msa_build_tables(num_blocks: int, cached_lens, new_lens, block_table, free_b
     """Block tables, lengths, slots and positions of a step from the requests' lengths (all int32 on the
     device): block_table [S][max_blocks] and the stack free_blocks are updated in place; seq_lens [S],
     token_offsets [S + 1], slot_mapping and positions [max_tokens] and free_count_out [1] are written."""
-    S, shape = cached_lens.numel(), block_table.shape
-    if new_lens.numel() != S or len(shape) != 2 or shape[0] != S or seq_lens.numel() != S or \
-            token_offsets.numel() != S + 1 or positions.numel() != slot_mapping.numel() or not block_table.is_contiguous():
-        raise MsaError(1, "msa_build_tables")
+    if _int32 is None:
+        _torch_names()
+    where, dev = "msa_build_tables", block_table.get_device()
+    S, shape, tokens = cached_lens.numel(), block_table.shape, slot_mapping.numel()
+    if (dev < 0 or dev != _device() or new_lens.numel() != S or len(shape) != 2 or shape[0] != S
+            or seq_lens.numel() != S or token_offsets.numel() != S + 1 or positions.numel() != tokens or cached_lens.get_device() != dev or seq_lens.get_device() != dev):
+        raise MsaError(1, where)
+    for t in (cached_lens, new_lens, block_table, free_blocks, free_count, seq_lens, token_offsets, slot_mapping, positions,
+              free_count_out):
+        if t.dtype is not _int32 or not t.is_contiguous():
+            raise MsaError(1, where)
     _check(lib().msa_build_tables(S, num_blocks, cached_lens.data_ptr(), new_lens.data_ptr(), shape[1], block_table.data_ptr(),
                                   free_blocks.numel(), free_blocks.data_ptr(), free_count.data_ptr(), free_count_out.data_ptr(),
-                                  seq_lens.data_ptr(), token_offsets.data_ptr(), slot_mapping.numel(), slot_mapping.data_ptr(),
-                                  positions.data_ptr(), workspace.data_ptr(), _nbytes(workspace), _stream(stream)),
-           "msa_build_tables")
+                                  seq_lens.data_ptr(), token_offsets.data_ptr(), tokens, slot_mapping.data_ptr(),
+                                  positions.data_ptr(), workspace.data_ptr(), _nbytes(workspace), _stream(stream, dev)), where)
 
 
 def default_config(topk: int = 16, head_dim: int = 128, index_dim: int = 128) -> Config:
