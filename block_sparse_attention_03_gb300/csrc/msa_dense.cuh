@@ -38,10 +38,10 @@
 //   O^T[d][col]  += sum_key V[key][d] P[col][key]     (A = V^T, B = P)
 //   FP8    K and V become f16 (exact); a bf16 query f16 after a power-of-two row
 //          scale (11 bits, exact to 2^-25 of 16,384 below it), P x vscale f16.
-//          K as it is against the query's two e4m3 terms takes as long with 4
-//          columns (330 us over 4 x 131,072 tokens both ways) and longer with
-//          more: 105 to 97 us with 16 columns and 222 to 133 with 32 over 64 x
-//          8,192, since each e4m3 k32 MMA costs the pipe what two f16 k16 do.
+//          K as it is, against the query's two e4m3 terms (e4m3 k32 MMAs), takes
+//          as long with 4 columns (4 x 524,288 tokens: 330 us both ways) and
+//          longer with more: 105 us against 97 with 16 columns (16 x 32,768), 222
+//          against 133 with 32 (8 x 65,536).
 //   NVFP4  K and V become f16 in registers (e2m1 x e4m3 fits 6 bits: exact).
 //   BF16   as it is; P enters as bf16 hi + lo terms (16 bits), since one bf16
 //          term alone would add an error near the output's own rounding.
@@ -51,6 +51,14 @@
 // not agree on a maximum at every step (one vote instead).  P is scaled by 2^7
 // where it becomes f16, l with it: at most 2^15, and 2^-21 of the row's
 // reference weight before f16 loses bits.
+//
+// Measured (one GPU, launches back to back; shares of the measured copy rate,
+// 6,779 GB/s): 4 columns, FP8 32 x 16K-32K tokens 135 us (91%), 4 x 512K 329 us
+// (99%), BF16 32 x 16K-32K 240 us (100%), NVFP4 32 x 16K-64K 180 us (63%: the dequantization's
+// issue slots); 32 columns (8 new tokens), BF16 8 x 64K 185 us (86%), FP8 128 us
+// (64%), NVFP4 8 x 128K 235 us (38%; tensor pipe 42%, issue slots 39%, two warps a
+// scheduler waiting for each other's results); 61 ragged BF16 sequences of 48
+// columns 88 us (47%; tensor pipe 50%); one sequence of 4K tokens 9.3 us.
 //
 // A masked key's logit is replaced, not multiplied; in units that hold masked
 // keys V is masked in registers too, so NaN or infinity in rows past the end of a

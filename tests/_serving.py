@@ -115,7 +115,8 @@ def plain_dense(c, skip_blocks=()):
 
     The error bound of a logit: q.k is summed in fp32 (128 products in tensor-core
     order: at most 136 roundings of partial sums below sum |q k|), a bf16 query
-    meeting e4m3 keys is held to 2^-10 / 224 of its row's largest element, and
+    meeting e4m3 keys is held in f16 after a scale that brings its row's largest
+    element to 2^13 or more (exact above 2^-14, off by 2^-25 at most below: 2^-38 of the largest), and
     the scaled logit takes three more roundings in the log2 domain."""
     q = c["q"].cpu()
     q = q.view(torch.int16).numpy().view(np.uint16) if c["qd"] == "bf16" else q.numpy()
@@ -141,7 +142,7 @@ def plain_dense(c, skip_blocks=()):
                     qv = q[row, hh]
                     x = K[see] @ qv * scale
                     mass = np.abs(K[see]) @ np.abs(qv) * scale
-                    split = 2.0 ** -10 / 224 * np.abs(qv).max() * np.abs(K[see]).sum(1) * scale if c["kv"] == "fp8" and c["qd"] == "bf16" else 0.0
+                    split = 2.0 ** -38 * np.abs(qv).max() * np.abs(K[see]).sum(1) * scale if c["kv"] == "fp8" and c["qd"] == "bf16" else 0.0
                     ex[row, hh] = (mass * 136 * 2.0 ** -24 + split + np.abs(x) * 3 * 2.0 ** -23).max()
                     m = x.max()
                     p = np.exp(x - m)
