@@ -110,8 +110,16 @@ def _host_rows(c, name, s, h, upto):
     return np.concatenate(got)[:upto] if got else np.zeros((0, DIM))
 
 
+def _scales(c, name, s, h, upto):
+    """fp32 scales of the first `upto` tokens of sequence s (FP8)."""
+    index = {int(p): i for i, p in enumerate(c["perm"])}
+    got = [c["rows_" + name + "_scale"][index[int(c["table"][s, b])], h].numpy() for b in range(-(-upto // BLOCK))]
+    return np.concatenate(got)[:upto].astype(np.float64)
+
+
 def plain_dense(c, skip_blocks=()):
-    """(out, lse, |v| average, logit error bound, keys) of every row, in 64 bits.
+    """(out, lse, |v| average, logit error bound, keys, bound for weights below f16's normal range) of
+    every row, in 64 bits.
 
     The error bound of a logit: q.k is summed in fp32 (128 products in tensor-core
     order: at most 136 roundings of partial sums below sum |q k|), a bf16 query
@@ -124,13 +132,17 @@ def plain_dense(c, skip_blocks=()):
     Q, Hq, H = c["Q"], c["Hq"], c["H"]
     R, r = len(c["lens"]) * Q, Hq // H
     out, lse = np.zeros((R, Hq, DIM)), np.full((R, Hq), -np.inf)
-    size, ex, n = np.zeros((R, Hq, DIM)), np.zeros((R, Hq)), np.zeros((R, Hq))
+    size, ex, n, low = np.zeros((R, Hq, DIM)), np.zeros((R, Hq)), np.zeros((R, Hq)), np.zeros((R, Hq, DIM))
     scale = DIM ** -0.5
     for s, T in enumerate(c["lens"]):
         if T <= 0:
             continue
         for h in range(H):
             K, V = _host_rows(c, "k", s, h, T), _host_rows(c, "v", s, h, T)
+            A = np.abs(V)
+            if c["kv"] == "fp8":
+                vs = _scales(c, "v", s, h, T)
+                A = A * (vs.max() / vs * 2.0 ** 8)[:, None]
             for i in range(Q):
                 see = np.arange(T) <= T - Q + i
                 for b in skip_blocks:
@@ -150,20 +162,24 @@ def plain_dense(c, skip_blocks=()):
                     out[row, hh] = p @ V[see] / p.sum()
                     size[row, hh] = p @ np.abs(V[see]) / p.sum()
                     n[row, hh] = see.sum()
-    return out, lse, size, ex, n
+                    low[row, hh] = 0 if c["kv"] == "bf16" else 2.0 ** -32 * A[see].sum(0)
+    return out, lse, size, ex, n, low
 
 
 def check_dense(c, out, lse, ref, rows=None):
     """Against plain_dense.  out: half a step of bf16; before it every weight is off by the logit's
     error twice (itself and the sum's), ex2's 2^-22 and its own rounding (2^-11 as f16, 2^-16 as two bf16
-    terms), and the sums over n keys in fp32 by at most n / 8 roundings of a lane's run of them."""
-    o, l, size, ex, n = ref
+    terms), and the sums over n keys in fp32 by at most n / 8 roundings of a lane's run of them.
+    As f16 a weight is kept as 2^7 w where the row's reference has w = 1 (its sum is 1 or more), so
+    below 2^-14 it is off by half of 2^-24: 2^-32 |v| a key.  FP8 keeps 2^7 w times the key's scale over
+    one that is at most 2^8 the largest: that much more, over the key's own scale."""
+    o, l, size, ex, n, low = ref
     rows = slice(None) if rows is None else rows
     got, gl = out.float().cpu().numpy().astype(np.float64)[rows], lse.cpu().numpy().astype(np.float64)[rows]
-    o, l, size, ex, n = o[rows], l[rows], size[rows], ex[rows], n[rows]
+    o, l, size, ex, n, low = o[rows], l[rows], size[rows], ex[rows], n[rows], low[rows]
     sums = (n / 8 + 64) * 2.0 ** -24
     weight = (2.0 ** -16 if c["kv"] == "bf16" else 2.0 ** -11) + 2 * ex + 2.0 ** -21 + 2 * sums
-    tol = HALF["bf16"] * np.abs(o) + (1 + HALF["bf16"]) * size * weight[..., None] + 1e-37
+    tol = HALF["bf16"] * np.abs(o) + (1 + HALF["bf16"]) * size * weight[..., None] + (1 + HALF["bf16"]) * low + 1e-37
     assert np.isfinite(got).all()
     err = np.abs(got - o)
     assert (err <= tol).all(), (np.argwhere(err > tol)[:4], (err / tol).max())

@@ -48,6 +48,18 @@ def test_long_sequence_is_joined(kv, qd, Q, r):
     check_dense(c, *run_dense(c), plain_dense(c))
 
 
+@pytest.mark.parametrize("kv", ["bf16", "fp8", "nvfp4"])
+@pytest.mark.parametrize("Q,r,H", [(1, 4, 2), (2, 6, 1), (6, 4, 1), (8, 4, 1), (3, 16, 1), (8, 8, 1)])
+def test_as_many_segments_as_teams(kv, Q, r, H):
+    # 1 to 64 columns; about as many short sequences as there are teams, so that runs begin and end
+    # inside, before and behind the places that stand for segment ends, beside one that spans many runs
+    rng = np.random.default_rng(100 * Q + r)
+    lens = [int(x) for x in rng.choice([0, 1, 2, 63, 64, 65, 128, 129, 200, 257], 320 // H)] + [4003]
+    rng.shuffle(lens)
+    c = paged_case(lens, kv, Q=Q, Hq=r * H, H=H, seed=Q + r)
+    check_dense(c, *run_dense(c), plain_dense(c))
+
+
 def test_large_logits_and_uneven_scales():
     # a few keys take nearly all of the weight, and V's scales span 2^20
     c = paged_case([5000, 129], "fp8", Hq=4, H=2, seed=9, spread=2.5, qsize=6.0)
@@ -190,6 +202,32 @@ def test_captured_calls_on_another_stream():
         check_dense(x, out, lse, plain_dense(x))
         assert torch.equal(out, out2)
         c["q"].copy_(saved)
+
+
+def test_two_graphs_share_a_workspace():
+    # of different column counts, so that they lay it out differently, replayed in turn
+    a, b = paged_case([5000, 77], "fp8", Hq=4, H=2, seed=21), paged_case([900, 3000, 0], "nvfp4", Q=8, Hq=8, H=2, seed=22)
+    cfg, calls = msa.default_config(), []
+    for c in (a, b):
+        cache, batch, q = bind_dense(c)
+        calls.append((c, cache, batch, q, c["Hq"], *dense_outputs(c)))
+    ws = torch.full((max(msa.msa_dense_workspace_size(x[1], x[2], x[4]) for x in calls),), 0x5a, dtype=torch.uint8, device="cuda")
+    msa.msa_workspace_init(ws)
+    graphs = []
+    for c, cache, batch, q, hq, out, lse in calls:
+        msa.msa_dense_attend(cache, batch, cfg, q, hq, out, lse, ws)
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            msa.msa_dense_attend(cache, batch, cfg, q, hq, out, lse, ws)
+    refs = [plain_dense(c) for c, *_ in calls]
+    for n in (0, 1, 1, 0, 1):
+        calls[n][5].fill_(3)
+        calls[n][6].fill_(3)
+        graphs[n].replay()
+        torch.cuda.synchronize()
+        check_dense(calls[n][0], calls[n][5], calls[n][6], refs[n])
+    assert msa.msa_read_device_status(ws)[1] == 0
 
 
 def test_equals_the_sparse_attend_that_selects_every_block():
