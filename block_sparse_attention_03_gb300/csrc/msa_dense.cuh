@@ -122,7 +122,7 @@ struct DenseLayout {
   static constexpr size_t SCALES = 2 * (size_t)T::SC;   // their scales, in a region of their own
   static constexpr int END = NN == 1 ? 2 : NN == 2 ? 3 : 4;  // what a segment's end takes, in units
   static constexpr int MT_OWN = 8 / KGW;         // output tiles a warp takes when the warps of a group join (NN > 1)
-  static constexpr int DCH = 64, MROW = DCH + 4;  // output dims of a pass of that join, padded (NN = 1)
+  static constexpr int MROW = kDim + 4;          // padded row of that join's area (NN = 1)
   static constexpr int QROW = 272;               // a query row, padded (conflict-free reads)
   // per team
   static constexpr size_t MERGE_BYTES = NN == 1 ? kDenseWpg * WROWS * MROW * 4 : kDenseWpg * (KGW - 1) * MT_OWN * 512;
@@ -130,8 +130,10 @@ struct DenseLayout {
   static constexpr size_t QSLOT = (size_t)ROWS * QROW;
   static constexpr size_t CF_BYTES = (ROWS * 4 + 15) / 16 * 16;
   static constexpr size_t FIXED = MERGE_BYTES + ML_BYTES + 2 * QSLOT + CF_BYTES + 2 * sizeof(DenseFacts) + 320;
-  static constexpr int NST_FIT = (int)(((227 * 1024 - 1024) / TEAMS - FIXED) / (STAGE + SCALES));
-  static constexpr int NST = NST_FIT < 8 ? NST_FIT : 8;  // ring stages of a team
+  // Two stages a team: some 20 MB on their way over the GPU.  More make the memory
+  // slower, not faster: 4 x 512K FP8 tokens 320 us with two, 335 with three, NVFP4
+  // verify 226 with two and 236 with the four that fit.
+  static constexpr int NST = 2;
   // the tiles of all teams first (1 KB alignment), then each team's block
   static constexpr size_t TILES = STAGE * NST * TEAMS;
   static constexpr size_t SC = 0;
@@ -143,7 +145,7 @@ struct DenseLayout {
   static constexpr size_t BARS = FACTS + 2 * sizeof(DenseFacts);
   static constexpr size_t TEAM = (BARS + 8 * (2 * NST + 4) + 4 * NST + 16 + 127) / 128 * 128;
   static constexpr size_t SMEM = TILES + TEAMS * TEAM + 1024;
-  static_assert(SMEM <= 227 * 1024 && NST >= 2, "stages");
+  static_assert(SMEM <= 227 * 1024, "stages");
   static_assert(STAGE % 1024 == 0 && MERGE_BYTES % 16 == 0 && ML_BYTES % 16 == 0 && QSLOT % 16 == 0, "alignment");
 };
 
@@ -1080,84 +1082,68 @@ __device__ void consumer(const DenseParams& p, const DenseTeam& tm, int bar, int
     }
     const bool whole = f.part < 0;
     if constexpr (NN == 1) {
-      // Few columns: half the dims at a time, then a thread a row and four dims.  The
-      // code runs once a segment, so its size counts (instruction fetches): only the
-      // stores out of the accumulators are unrolled.  256 sequences of 100 to 1,000
-      // tokens: 49.7 us, and 53.0 the other way.
+      // Few columns: all of them through shared memory, then a thread a row and four
+      // dims.  The code runs once a segment, so its size counts (instruction fetches):
+      // only the stores out of the accumulators are unrolled.  256 sequences of 100 to
+      // 1,000 tokens: 41.9 us, 43.1 in two halves, and 53 in the other way (below).
       float* mo = reinterpret_cast<float*>(tm.mem + LY::MERGE);  // [warps][WROWS][MROW]
-      constexpr int D4 = LY::DCH / 4;
-      constexpr int MTP = LY::DCH / 16;  // accumulator tiles a pass takes (their dims are consecutive)
-      static_assert(FMT != FMT_NVFP4 || LY::DCH >= 32, "a pass holds whole 32-dim chunks");
-#pragma unroll 1
-      for (int pass = 0; pass < 128 / LY::DCH; ++pass) {
 #pragma unroll
-        for (int ps = 0; ps < 128 / LY::DCH; ++ps)
-          if (ps == pass) {
+      for (int c = 0; c < 2; ++c) {  // column 2j + c
+        float* row = mo + (warp * LY::WROWS + 2 * j + c) * LY::MROW;
 #pragma unroll
-            for (int n = 0; n < NN; ++n)
-#pragma unroll
-              for (int c = 0; c < 2; ++c) {  // column 2j + c
-                float* row = mo + (warp * LY::WROWS + 8 * n + 2 * j + c) * LY::MROW;
-#pragma unroll
-                for (int tt = 0; tt < MTP; ++tt) {
-                  const float(&v)[4] = o[ps * MTP + tt][n];
-                  const int d = out_dim<FMT>(tt, 0, g8);  // within the chunk
-                  if constexpr (FMT == FMT_NVFP4) {
-                    const float(&v1)[4] = o[ps * MTP + (tt | 1)][n];
-                    if (!(tt & 1)) *reinterpret_cast<float4*>(row + d) = make_float4(v[c], v[c + 2], v1[c], v1[c + 2]);
-                  } else if constexpr (FMT == FMT_FP8) {
-                    *reinterpret_cast<float2*>(row + d) = make_float2(v[c], v[c + 2]);
-                  } else {
-                    row[d] = v[c];
-                    row[out_dim<FMT>(tt, 1, g8)] = v[c + 2];
-                  }
-                }
-              }
-          }
-        named_bar_sync(bar, TEAM_THREADS);
-#pragma unroll 1
-        for (int x = tid; x < LY::ROWS * D4; x += TEAM_THREADS) {
-          const int row = x / D4, d = 4 * (x - row * D4);
-          if (row >= nrows) continue;
-          const int cgi = row / LY::WROWS, tr = row - cgi * LY::WROWS;
-          float4 v[KGW];
-          float M = -INFINITY;
-#pragma unroll
-          for (int w = 0; w < KGW; ++w) {
-            v[w] = ml[(cgi * KGW + w) * LY::WROWS + tr];
-            M = fmaxf(M, v[w].x);
-          }
-          const float ms = M == -INFINITY ? 0.f : M;
-          float L = 0.f;
-          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-          for (int w = 0; w < KGW; ++w) {
-            const float fw = ex2(v[w].x - ms);
-            L += fw * v[w].y;
-            const float4 ov = *reinterpret_cast<const float4*>(mo + ((cgi * KGW + w) * LY::WROWS + tr) * LY::MROW + d);
-            acc.x += fw * (ov.x * v[w].z);
-            acc.y += fw * (ov.y * v[w].z);
-            acc.z += fw * (ov.z * v[w].z);
-            acc.w += fw * (ov.w * v[w].z);
-          }
-          const int dim = pass * LY::DCH + d;
-          if (whole) {
-            const float inv = L == 0.f ? 0.f : 1.f / L;
-            const int col = c0 + row, i = col / p.r, h = col - i * p.r;
-            const size_t orow = ((size_t)f.s * p.Q + i) * H + (size_t)f.g * p.r + h;
-            uint2 pk;
-            pk.x = pack_bf16x2(acc.x * inv, acc.y * inv);
-            pk.y = pack_bf16x2(acc.z * inv, acc.w * inv);
-            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + orow * kDim + dim) = pk;
-            if (dim == 0 && p.lse)
-              p.lse[orow] = L == 0.f ? -INFINITY : (M - SHIFT + log2f(L)) * 0.69314718055994531f;
+        for (int mt = 0; mt < 8; ++mt) {
+          const float(&v)[4] = o[mt][0];
+          const int d = out_dim<FMT>(mt, 0, g8);
+          if constexpr (FMT == FMT_NVFP4) {
+            const float(&v1)[4] = o[mt | 1][0];
+            if (!(mt & 1)) *reinterpret_cast<float4*>(row + d) = make_float4(v[c], v[c + 2], v1[c], v1[c + 2]);
+          } else if constexpr (FMT == FMT_FP8) {
+            *reinterpret_cast<float2*>(row + d) = make_float2(v[c], v[c + 2]);
           } else {
-            *reinterpret_cast<float4*>(p.part_o + ((size_t)f.part * LY::ROWS + row) * kDim + dim) = acc;
-            if (dim == 0) p.part_ml[(size_t)f.part * LY::ROWS + row] = make_float2(M, L);
+            row[d] = v[c];
+            row[out_dim<FMT>(mt, 1, g8)] = v[c + 2];
           }
         }
-        named_bar_sync(bar, TEAM_THREADS);  // the merge area is free again
       }
+      named_bar_sync(bar, TEAM_THREADS);
+#pragma unroll 1
+      for (int x = tid; x < nrows * 32; x += TEAM_THREADS) {
+        const int row = x >> 5, d = 4 * (x & 31);
+        float4 v[KGW];
+        float M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < KGW; ++w) {
+          v[w] = ml[w * LY::WROWS + row];
+          M = fmaxf(M, v[w].x);
+        }
+        const float ms = M == -INFINITY ? 0.f : M;
+        float L = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < KGW; ++w) {
+          const float fw = ex2(v[w].x - ms);
+          L += fw * v[w].y;
+          const float4 ov = *reinterpret_cast<const float4*>(mo + (w * LY::WROWS + row) * LY::MROW + d);
+          acc.x += fw * (ov.x * v[w].z);
+          acc.y += fw * (ov.y * v[w].z);
+          acc.z += fw * (ov.z * v[w].z);
+          acc.w += fw * (ov.w * v[w].z);
+        }
+        if (whole) {
+          const float inv = L == 0.f ? 0.f : 1.f / L;
+          const int col = c0 + row, i = col / p.r, h = col - i * p.r;
+          const size_t orow = ((size_t)f.s * p.Q + i) * H + (size_t)f.g * p.r + h;
+          uint2 pk;
+          pk.x = pack_bf16x2(acc.x * inv, acc.y * inv);
+          pk.y = pack_bf16x2(acc.z * inv, acc.w * inv);
+          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + orow * kDim + d) = pk;
+          if (d == 0 && p.lse) p.lse[orow] = L == 0.f ? -INFINITY : (M - SHIFT + log2f(L)) * 0.69314718055994531f;
+        } else {
+          *reinterpret_cast<float4*>(p.part_o + ((size_t)f.part * LY::ROWS + row) * kDim + d) = acc;
+          if (d == 0) p.part_ml[(size_t)f.part * LY::ROWS + row] = make_float2(M, L);
+        }
+      }
+      named_bar_sync(bar, TEAM_THREADS);  // the merge area is free again
     } else {
       // Many columns: each warp takes 1 / KGW of the output tiles from the others, as
       // they lie in the lanes (16 bytes a lane, no bank conflicts), and writes them.
