@@ -238,6 +238,7 @@ struct DenseParams {
   const uint8_t* k_sc;        // per-token fp32 scales (FP8) or e4m3 group scales (NVFP4)
   const uint8_t* v_sc;
   float v_global;             // NVFP4 V per-tensor scale
+  int32_t stream;             // the cache may be larger than the L2: its lines are the first to go
   int2* info;                 // [teams] (sequence x G x CG + group) the run begins in, 1: it began before the run
   float* part_o;              // [2 x teams][rows][128] partials of cut segments
   float2* part_ml;            // [2 x teams][rows] reference (log2 domain), sum
