@@ -13,7 +13,7 @@
 // row's partials where rows are few, and each has eight partials in flight (four
 // where segments are many and have few partials each).  Measured behind the attend:
 // 3 to 5 us after its last CTA.  Rows a CTA: one up to 8 columns, then four (8 x
-// 64K tokens of 32 columns: 127.5 us in all, 128.9 with eight, 131.8 with one).
+// 64K tokens of 32 columns: 1.4 us longer in all with eight, 4.3 with one).
 #include "msa_dense.cuh"
 
 namespace msa {

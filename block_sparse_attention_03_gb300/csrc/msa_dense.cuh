@@ -53,12 +53,13 @@
 // reference weight before f16 loses bits.
 //
 // Measured (one GPU, launches back to back; shares of the measured copy rate,
-// 6,779 GB/s): 4 columns, FP8 32 x 16K-32K tokens 135 us (91%), 4 x 512K 329 us
-// (99%), BF16 32 x 16K-32K 240 us (100%), NVFP4 32 x 16K-64K 180 us (63%: the dequantization's
-// issue slots); 32 columns (8 new tokens), BF16 8 x 64K 185 us (86%), FP8 128 us
-// (64%), NVFP4 8 x 128K 235 us (38%; tensor pipe 42%, issue slots 39%, two warps a
-// scheduler waiting for each other's results); 61 ragged BF16 sequences of 48
-// columns 88 us (47%; tensor pipe 50%); one sequence of 4K tokens 9.3 us.
+// 6,779 GB/s): 4 columns, FP8 32 x 16K-32K tokens 131 us (94%), 4 x 512K 318 us
+// (103%), BF16 32 x 16K-32K 237 us (101%), NVFP4 32 x 16K-64K 173 us (65%: the
+// dequantization's issue slots); 16 columns, FP8 16 x 32K 95 us (86%), NVFP4 8 x 64K 86
+// us (52%); 32 columns (8 new tokens), BF16 8 x 64K 182 us (87%), FP8 126 us (65%),
+// NVFP4 8 x 128K 226 us (40%; tensor pipe 43%, issue slots 40%, two warps a scheduler
+// waiting for each other's results); 61 ragged BF16 sequences of 48 columns 86 us
+// (48%; tensor pipe 50%); one sequence of 4K tokens 9.1 us.
 //
 // A masked key's logit is replaced, not multiplied; in units that hold masked
 // keys V is masked in registers too, so NaN or infinity in rows past the end of a
@@ -105,15 +106,18 @@ struct DenseFacts {
 template <int FMT, int NN, int NCG>
 struct DenseLayout {
   using T = DenseTraits<FMT>;
-  // Narrow instances need under 128 registers a thread; NVFP4's dequantization
-  // keeps three teams busy where two are enough for the others.
-  static constexpr int TEAMS = (NN == 1 && FMT == FMT_NVFP4) ? 3 : 2;
-  // Wide ones need more than a CTA of ten warps can give each thread (168): their
-  // warps come in fours (the producers' four hold two idle ones) and the
-  // consumers take registers over from the producers.
-  static constexpr bool WIDE = NN >= 3;
+  // NVFP4's dequantization keeps three teams busy where two are enough for the
+  // others (one token 173 us, 188 with two; 16 columns 86 and 93); with 24 columns
+  // and more the accumulators leave no room for a third.
+  static constexpr int TEAMS = (NN <= 2 && FMT == FMT_NVFP4) ? 3 : 2;
+  // Where an equal share is too small, the consumers take registers over from the
+  // producers; their warps come in fours then (the producers' four hold idle ones).
+  // Three teams of one column tile do better with equal shares (173 us, 182 so).
+  static constexpr bool WIDE = NN >= 3, MOVE = WIDE || (TEAMS == 3 && NN == 2);
+  static constexpr int REGS_P = WIDE ? 40 : 56, REGS_C = WIDE ? 232 : 152;
   static constexpr int CONSUMERS = 32 * kDenseWpg * TEAMS;
-  static constexpr int THREADS = CONSUMERS + (WIDE ? 128 : 32 * TEAMS);
+  static constexpr int THREADS = CONSUMERS + (MOVE ? 128 : 32 * TEAMS);
+  static_assert(!MOVE || 128 * REGS_P + CONSUMERS * REGS_C <= (65536 / THREADS / 8 * 8) * THREADS, "shares of the launch's registers");
   static constexpr int MT = (NN + 1) / 2;        // 16-row tiles of a warp's queries
   static constexpr int WROWS = 8 * NN;           // columns of a warp
   static constexpr int ROWS = WROWS * NCG;       // of a unit
@@ -255,8 +259,8 @@ __device__ void producer(const CUtensorMap* tmk, const CUtensorMap* tmv, const D
   const long GC = (long)p.G * p.CG;
   // Units in all, then the run of this team: [u0, u1).  Every segment has END units
   // more than its keys, which stand for its end (the join, the output, the next
-  // one's start), so that runs with many short segments are not the last: 61 ragged
-  // sequences of 48 columns take 88 us, and 100 where only keys are counted.
+  // one's start), so that runs with many short segments are not the last: without it
+  // 61 ragged sequences of 48 columns take 14% longer.
   long total = 0;
   int mine0 = 0;  // the length of sequence `lane`: a batch of up to 32 is read once
 #pragma unroll 4
@@ -1149,7 +1153,7 @@ __device__ void consumer(const DenseParams& p, const DenseTeam& tm, int bar, int
     } else {
       // Many columns: each warp takes 1 / KGW of the output tiles from the others, as
       // they lie in the lanes (16 bytes a lane, no bank conflicts), and writes them.
-      // 61 ragged sequences of 48 columns: 93.4 us, and 100 the other way.
+      // 61 ragged sequences of 48 columns take 7% longer the other way.
       float4* mo = reinterpret_cast<float4*>(tm.mem + LY::MERGE);  // [warps][receivers][tiles][lanes]
       named_bar_sync(bar, TEAM_THREADS);
       if (tid < LY::ROWS) {  // a thread a column: the weights of its group's warps
@@ -1249,10 +1253,11 @@ __device__ void consumer(const DenseParams& p, const DenseTeam& tm, int bar, int
   }
 }
 
-// One CTA an SM.  Ten warps (two teams): up to 168 registers a thread; fifteen
-// (three teams): 128; WIDE: twelve warps launched with 168, of which the
-// producers' four keep 40 and the consumers' eight take 232 (384 x 168 = 128 x
-// 40 + 256 x 232 = 64,512 registers).
+// One CTA an SM.  Two teams are ten warps with up to 168 registers a thread, or, WIDE,
+// twelve launched with 168, of which the producers' four keep 40 and the consumers'
+// eight take 232 (128 x 40 + 256 x 232 = 384 x 168 = 64,512 registers); three teams
+// are fifteen with up to 128, or sixteen launched with 128, the producers' four with 56
+// then and the consumers' twelve with 152 (128 x 56 + 384 x 152 = 512 x 128).
 template <int FMT, int NN, int NCG, bool NVR>
 __global__ void __launch_bounds__(DenseLayout<FMT, NN, NCG>::THREADS, 1)
     dense_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv, const DenseParams p) {
@@ -1291,10 +1296,10 @@ __global__ void __launch_bounds__(DenseLayout<FMT, NN, NCG>::THREADS, 1)
   __syncthreads();
   pdl_launch_dependents();  // the combine's CTAs may take their place as soon as this grid's leave room
   if (!consumes) {
-    if constexpr (LY::WIDE) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if constexpr (LY::MOVE) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(LY::REGS_P));
     if (team < TEAMS) producer<FMT, NN, NCG>(&tmk, &tmv, p, tm, lane);
   } else {
-    if constexpr (LY::WIDE) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+    if constexpr (LY::MOVE) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(LY::REGS_C));
     // sequences without keys (and malformed ones) have no units: their rows here
     for (int s = blockIdx.x + warp * gridDim.x; s < p.S; s += gridDim.x * TEAMS * kDenseWpg) {
       const int T = __ldg(p.seq_lens + s);
@@ -1317,6 +1322,14 @@ cudaError_t launch_one(const CUtensorMap* tk, const CUtensorMap* tv, const Dense
   auto kern = dense_kernel<FMT, NN, NCG, NVR>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)LY::SMEM);
   if (e != cudaSuccess) return e;
+  if constexpr (LY::MOVE) {
+    // the consumers would wait for ever for registers that the launch did not bring
+    static const int regs = [&] {
+      cudaFuncAttributes fa;
+      return cudaFuncGetAttributes(&fa, kern) == cudaSuccess ? fa.numRegs : 0;
+    }();
+    if (regs / 8 * 8 * LY::THREADS < 128 * LY::REGS_P + LY::CONSUMERS * LY::REGS_C) return cudaErrorLaunchOutOfResources;
+  }
   kern<<<(unsigned)num_sms, LY::THREADS, LY::SMEM, st>>>(*tk, *tv, p);
   return cudaGetLastError();
 }

@@ -256,7 +256,7 @@ inline DenseShape dense_shape(int cper) {
   return {cper <= 48 ? 3 : 4, 2};
 }
 constexpr int dense_rows(int nn, int ncg) { return 8 * nn * ncg; }
-constexpr int dense_teams(int fmt, int nn) { return nn == 1 && fmt == FMT_NVFP4 ? 3 : 2; }
+constexpr int dense_teams(int fmt, int nn) { return nn <= 2 && fmt == FMT_NVFP4 ? 3 : 2; }
 // keys (rows of a tensor-copy box) a unit holds
 inline int dense_unit_keys(int fmt) { return fmt == FMT_BF16 ? 64 : 128; }
 
