@@ -598,9 +598,10 @@ msa_status_t run_dense(const msa_cache_t* c, const msa_batch_t* b, const msa_con
   p.k_sc = static_cast<const uint8_t*>(fmt == FMT_FP8 ? static_cast<const void*>(c->k_scale) : c->k_sf);
   p.v_sc = static_cast<const uint8_t*>(fmt == FMT_FP8 ? static_cast<const void*>(c->v_scale) : c->v_sf);
   p.v_global = c->v_global;
-  // A cache of some 10 MB stays in the L2 by itself (one BF16 sequence of 4K tokens 12.4 us, 13.3 with
-  // its lines first to go); a larger one is a stream that would push the partials out
-  // (61 ragged BF16 sequences 88.7 us, 85.4 so; 256 short FP8 ones 42.0 and 40.6; NVFP4 verify 226.1 and 224.9).
+  // A small cache stays in the 129 MB L2 by itself; a larger one is a stream that would push the
+  // partials and the next kernels' code out, so its lines are the first to go.  Four BF16
+  // sequences, default and so: 16 MB 12.6 and 14.5 us, 32 MB 16.6 and 16.5, 64 MB 22.7 and 21.7, 128 MB
+  // 32.9 and 31.4 (with a cold L2 41.5 and 37.0).  The table's width bounds what the device holds.
   const double row = fmt == FMT_BF16 ? 512. : fmt == FMT_FP8 ? 264. : 144.;
   p.stream = (double)p.S * p.max_nb * kBlock * G * row > 32e6;
   p.info = at<int2>(ws, pl.off_info);

@@ -73,7 +73,7 @@ namespace msa {
 
 constexpr int kDenseWpg = 4;             // consumer warps of a team
 // An MMA's sum is ready after 21 cycles, and a scheduler could start one every 8:
-// a warp alternates this many sums.
+// a warp alternates this many sums (with two or eight the operator takes as long).
 constexpr int kDenseChains = 4;
 constexpr float kDensePShift = 7.f;      // log2 of the scale of P (f16 formats)
 constexpr float kDenseLazy = 8.f;        // a logit (log2) above the reference by this moves it
