@@ -301,11 +301,12 @@ def _torch_names() -> None:
 # sizes, and tensors that are not on the current device, where the kernels run.  The
 # checks stand in one expression a call (a helper's call costs as much as a check).
 
-def _rows(t, shape, where: str):
+def _rows(t, shape, where: str, dev: int):
     """(pointer, token stride) of a projection's bf16 rows of the given shape ([tokens][heads][128], or
     [tokens][128] for one head), the heads side by side."""
     strides = t.stride()
-    if t.shape != shape or strides[-1] != 1 or (len(shape) == 3 and strides[1] != 128 and shape[1] != 1) or t.dtype is not _bf16:
+    if t.shape != shape or strides[-1] != 1 or (len(shape) == 3 and strides[1] != 128 and shape[1] != 1) or t.dtype is not _bf16 \
+            or t.get_device() != dev:
         raise MsaError(1, where)
     return t.data_ptr(), strides[0]
 
@@ -418,8 +419,10 @@ def msa_dense_attend(cache, batch, cfg, q: Query, num_q_heads: int, out, lse, wo
             or lens.dtype is not _int32 or table.dtype is not _int32 or not lens.is_contiguous() or not table.is_contiguous()
             or data.numel() != rows * 128 or not data.is_contiguous() or data.element_size() != (1 if q.dtype == "fp8" else 2)
             or out.numel() != rows * 128 or not out.is_contiguous() or out.dtype is not _bf16
-            or (lse is not None and (lse.numel() != rows or not lse.is_contiguous() or lse.element_size() != 4))
-            or lens.get_device() != dev or table.get_device() != dev or data.get_device() != dev or out.get_device() != dev):
+            or (lse is not None and (lse.numel() != rows or not lse.is_contiguous() or lse.element_size() != 4
+                                    or lse.get_device() != dev))
+            or lens.get_device() != dev or table.get_device() != dev or data.get_device() != dev or out.get_device() != dev
+            or workspace.get_device() != dev):
         raise MsaError(1, "msa_dense_attend")
     at = _DENSE.pack(*_cache_values(cache), shape[0], batch.q_per_seq, shape[1], lens.data_ptr(), table.data_ptr(),
                      cfg.topk, cfg.init_blocks, cfg.local_blocks, cfg.index_scale, cfg.sm_scale,
@@ -453,26 +456,28 @@ def msa_rope_insert(cache, rope: MsaRopeT, positions, slot_mapping, q, q_out: Qu
             or positions.numel() != rope.axes * T or positions.dtype is not _int32 or not positions.is_contiguous()
             or slot_mapping.dtype is not _int32 or not slot_mapping.is_contiguous()
             or qd.numel() != q.numel() or not qd.is_contiguous() or qd.element_size() != (1 if q_out.dtype == "fp8" else 2)
-            or positions.get_device() != dev or slot_mapping.get_device() != dev or q.get_device() != dev or k.get_device() != dev
-            or v.get_device() != dev):
+            or positions.get_device() != dev or slot_mapping.get_device() != dev or q.get_device() != dev or qd.get_device() != dev
+            or workspace.get_device() != dev):
         raise MsaError(1, where)
     hq = q.shape[1]
     none, kv = (0, 0), (T, H, 128)
     iqo, w = (0, 0, 0.0), (0, 0, 0, 0, 0.0, 0.0)
     if index_q_out is not None:
         x = index_q_out.data
-        if x.numel() != T * H * 128 or not x.is_contiguous() or x.element_size() != (1 if index_q_out.dtype == "fp8" else 2):
+        if x.numel() != T * H * 128 or not x.is_contiguous() or x.element_size() != (1 if index_q_out.dtype == "fp8" else 2) \
+                or x.get_device() != dev:
             raise MsaError(1, where)
         iqo = (x.data_ptr(), DTYPES[index_q_out.dtype], index_q_out.scale)
     if norm is not None:
         w = norm.q, norm.k, norm.index_q, norm.index_k
         for x in w:
-            if x is not None and (x.numel() != 128 or x.dtype is not _bf16 or not x.is_contiguous()):
+            if x is not None and (x.numel() != 128 or x.dtype is not _bf16 or not x.is_contiguous() or x.get_device() != dev):
                 raise MsaError(1, where)
         w = (_p(norm.q), _p(norm.k), _p(norm.index_q), _p(norm.index_k), norm.eps, norm.offset)
-    at = _ROPE.pack(*_cache_values(cache), *_rows(q, (T, hq, 128), where), qd.data_ptr(), DTYPES[q_out.dtype], q_out.scale,
-                    *(none if index_q is None else _rows(index_q, kv, where)), *iqo, *_rows(k, kv, where),
-                    *_rows(v, kv, where), *(none if index_k is None else _rows(index_k, (T, 128) if index_k.dim() == 2 else (T, 1, 128), where)), *w)
+    at = _ROPE.pack(*_cache_values(cache), *_rows(q, (T, hq, 128), where, dev), qd.data_ptr(), DTYPES[q_out.dtype], q_out.scale,
+                    *(none if index_q is None else _rows(index_q, kv, where, dev)), *iqo, *_rows(k, kv, where, dev),
+                    *_rows(v, kv, where, dev), *(none if index_k is None else
+                                             _rows(index_k, (T, 128) if index_k.dim() == 2 else (T, 1, 128), where, dev)), *w)
     o = _ROPE.offsets
     _check(lib().msa_rope_insert(at, ctypes.byref(rope), T, positions.data_ptr(), slot_mapping.data_ptr(), hq, at + o[1], at + o[2],
                                  0 if index_q is None else at + o[3], 0 if index_q_out is None else at + o[4], at + o[5],
@@ -490,11 +495,11 @@ def msa_build_tables(num_blocks: int, cached_lens, new_lens, block_table, free_b
     where, dev = "msa_build_tables", block_table.get_device()
     S, shape, tokens = cached_lens.numel(), block_table.shape, slot_mapping.numel()
     if (dev < 0 or dev != _device() or new_lens.numel() != S or len(shape) != 2 or shape[0] != S
-            or seq_lens.numel() != S or token_offsets.numel() != S + 1 or positions.numel() != tokens or cached_lens.get_device() != dev or seq_lens.get_device() != dev):
+            or seq_lens.numel() != S or token_offsets.numel() != S + 1 or positions.numel() != tokens or workspace.get_device() != dev):
         raise MsaError(1, where)
     for t in (cached_lens, new_lens, block_table, free_blocks, free_count, seq_lens, token_offsets, slot_mapping, positions,
               free_count_out):
-        if t.dtype is not _int32 or not t.is_contiguous():
+        if t.dtype is not _int32 or t.get_device() != dev or not t.is_contiguous():
             raise MsaError(1, where)
     _check(lib().msa_build_tables(S, num_blocks, cached_lens.data_ptr(), new_lens.data_ptr(), shape[1], block_table.data_ptr(),
                                   free_blocks.numel(), free_blocks.data_ptr(), free_count.data_ptr(), free_count_out.data_ptr(),

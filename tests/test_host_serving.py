@@ -170,12 +170,14 @@ def test_python_refuses_what_the_kernels_would_misread(on_device_0):
         c = msa.PagedCache("bf16", "bf16", 2, 2, k, cache.v, None)
         msa.msa_dense_attend(c, msa.Batch(lens, table, 2), msa.Config(), msa.Query(q), 4, out, lse, ws, stream=0)
 
-    _refused(msa, dense, dict(lens=z(3, dt=i32), table=z(3, 5, dt=i32), q=z(6, 4, 128), out=z(6, 4, 128), lse=z(6, 4, dt=torch.float32)),
+    _refused(msa, dense, dict(lens=z(3, dt=i32), table=z(3, 5, dt=i32), q=z(6, 4, 128), out=z(6, 4, 128),
+                              lse=z(6, 4, dt=torch.float32)),
              [("lens", z(3, dt=torch.int64)), ("lens", cut(3)), ("lens", z(3, dt=i32, at=1)), ("table", z(2, 5, dt=i32)),
               ("table", z(15, dt=i32)), ("table", cut(3, 5)), ("table", z(3, 5, dt=torch.int64)), ("q", z(3, 4, 128)),
               ("q", z(6, 4, 128, dt=torch.float32)), ("q", z(6, 4, 128, at=-1)), ("out", z(6, 4, 64)),
               ("out", z(6, 4, 128, dt=torch.float32)), ("out", cut(6, 4, 128, dt=bf)), ("lse", z(6, 4)),
-              ("lse", z(3, 4, dt=torch.float32)), ("k", z(2, 2, 128, 128, at=1)), ("k", z(2, 2, 128, 128, at=-1))])
+              ("lse", z(3, 4, dt=torch.float32)), ("lse", z(6, 4, dt=torch.float32, at=-1)),
+              ("k", z(2, 2, 128, 128, at=1)), ("k", z(2, 2, 128, 128, at=-1))])
 
     rope = msa.MsaRopeT()
     rope.axes = 2
@@ -183,11 +185,12 @@ def test_python_refuses_what_the_kernels_would_misread(on_device_0):
     def insert(pos, slots, q, qo, k, v, w):
         msa.msa_rope_insert(cache, rope, pos, slots, q, msa.Query(qo), None, None, k, v, None, msa.QkNorm(q=w), ws, stream=0)
 
-    _refused(msa, insert, dict(pos=z(2, 3, dt=i32), slots=z(3, dt=i32), q=z(3, 4, 128), qo=z(3, 4, 128), k=z(3, 2, 128), v=z(3, 2, 128),
-                               w=z(128)),
+    _refused(msa, insert, dict(pos=z(2, 3, dt=i32), slots=z(3, dt=i32), q=z(3, 4, 128), qo=z(3, 4, 128),
+                               k=z(3, 2, 128), v=z(3, 2, 128), w=z(128)),
              [("pos", z(2, 3, dt=torch.int64)), ("pos", cut(2, 3)), ("slots", cut(3)), ("slots", z(3, dt=torch.int64)),
               ("slots", z(3, dt=i32, at=1)), ("q", z(3, 4, 128, dt=torch.float16)), ("qo", z(3, 4, 128, dt=u8)),
-              ("qo", cut(3, 4, 128, dt=bf)), ("k", z(3, 2, 128, dt=torch.float32)), ("v", z(3, 2, 128, at=1)), ("w", z(64)),
+              ("qo", cut(3, 4, 128, dt=bf)), ("k", z(3, 2, 128, dt=torch.float32)), ("v", z(3, 2, 128, at=1)),
+              ("qo", z(3, 4, 128, at=1)), ("k", z(3, 2, 128, at=-1)), ("w", z(64)), ("w", z(128, at=-1)),
               ("w", z(128, dt=torch.float32)), ("w", cut(128, dt=bf))])
 
     names = ("cached_lens", "new_lens", "block_table", "free_blocks", "free_count", "seq_lens", "token_offsets", "slot_mapping",
@@ -195,7 +198,9 @@ def test_python_refuses_what_the_kernels_would_misread(on_device_0):
     sizes = ((3,), (3,), (3, 5), (9,), (1,), (3,), (4,), (7,), (7,), (1,))
     good = {n: z(*s, dt=i32) for n, s in zip(names, sizes)}
     _refused(msa, lambda **a: msa.msa_build_tables(10, workspace=ws, stream=0, **a), good,
-             [(n, z(*s, dt=torch.int64)) for n, s in zip(names, sizes)] + [(n, cut(*s)) for n, s in zip(names, sizes) if s != (1,)] +
+             [(n, z(*s, dt=torch.int64)) for n, s in zip(names, sizes)] +
+             [(n, z(*s, dt=i32, at=-1)) for n, s in zip(names, sizes)] +
+             [(n, cut(*s)) for n, s in zip(names, sizes) if s != (1,)] +
              [("block_table", z(3, 5, dt=i32, at=1)), ("block_table", z(3, 5, dt=i32, at=-1)), ("block_table", z(2, 5, dt=i32)),
               ("seq_lens", z(2, dt=i32)), ("token_offsets", z(3, dt=i32)), ("positions", z(6, dt=i32)), ("new_lens", z(4, dt=i32))])
 
