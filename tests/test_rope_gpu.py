@@ -150,6 +150,11 @@ def test_rotations(rotary, sections, layout):
     _run(70, 5, 1, rotary=rotary, sections=sections, layout=layout, seed=rotary)
 
 
+@pytest.mark.parametrize("layout", ["halves", "adjacent"])
+def test_four_axes(layout):
+    _run(45, 4, 2, "fp8", "fp8", rotary=128, sections=[7, 21, 13, 23], layout=layout, far=100000, seed=12)
+
+
 @pytest.mark.parametrize("Hq,H", [(1, 1), (3, 3), (7, 7), (64, 4), (16, 8)])
 def test_head_counts(Hq, H):
     _run(40, Hq, H, "fp8", "fp8", seed=Hq)
