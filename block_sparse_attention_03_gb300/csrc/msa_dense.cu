@@ -164,7 +164,7 @@ cudaError_t launch_dense_combine(const DenseParams& p, int fmt, int num_sms, cud
   const DenseShape sh = dense_shape(p.cper);
   const int runs = num_sms * dense_teams(fmt, sh.nn), rows = dense_rows(sh.nn, sh.ncg);
   const long segments = (long)p.S * p.G * p.CG;
-  const float shift = fmt != FMT_BF16 ? kDensePShift : 0.f;
+  const float shift = fmt == FMT_NVFP4 ? kDensePShift : 0.f;
   // few segments: each has many partials, so its rows go to CTAs of their own
   const bool by_segment = segments <= runs / 4;
   const int cta_rows = by_segment ? (p.cper <= 8 ? 1 : 4) : (p.cper < kJoinWarps ? p.cper : kJoinWarps);

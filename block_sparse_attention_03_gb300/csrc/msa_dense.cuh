@@ -37,7 +37,7 @@
 //   S[col][key]   = Q[col][:] . K[key][:]             (A = Q, B = K)
 //   O^T[d][col]  += sum_key V[key][d] P[col][key]     (A = V^T, B = P)
 //   FP8    K and V become f16 (exact); a bf16 query f16 after a power-of-two row
-//          scale (11 bits, exact to 2^-25 of 16,384 below it), P x vscale f16.
+//          scale (11 bits, exact to 2^-25 of 16,384 below it), P x vscale f16 (below).
 //          K as it is, against the query's two e4m3 terms (e4m3 k32 MMAs), takes
 //          as long with 4 columns (4 x 524,288 tokens: 330 us both ways) and
 //          longer with more: 105 us against 97 with 16 columns (16 x 32,768), 222
@@ -48,15 +48,23 @@
 //
 // The running maximum is lazy: m moves only when a logit passes it by 2^8, so
 // that the output is rescaled a few times a segment and the lanes of a row need
-// not agree on a maximum at every step (one vote instead).  P is scaled by 2^7
-// where it becomes f16, l with it: at most 2^15, and 2^-21 of the row's
+// not agree on a maximum at every step (one vote instead).  NVFP4's P is scaled by
+// 2^7 where it becomes f16, l with it: at most 2^15, and 2^-21 of the row's
 // reference weight before f16 loses bits.
+//
+// FP8's P enters with V's scale in it, and scales may be of any size, those of
+// keys that a row does not see or that weigh nothing among them.  So every column
+// has a factor fe of its own that puts the largest p x vscale it has met (decayed
+// with m, looked at where m or the bound below moves) at 4: 2^-16 of that product
+// before f16 loses bits, off by 2^-27 of it below.  A step whose scales could
+// pass 2^15 (vscale above 2^5 times that product) has its products looked at first.  O is
+// rescaled by old over new product, never above 1, so that it cannot overflow.
 //
 // Measured (one GPU, launches back to back; shares of the measured copy rate,
 // 6,779 GB/s): 4 columns, FP8 32 x 16K-32K tokens 131 us (94%), 4 x 512K 318 us
 // (103%), BF16 32 x 16K-32K 237 us (101%), NVFP4 32 x 16K-64K 173 us (65%: the
 // dequantization's issue slots); 16 columns, FP8 16 x 32K 95 us (86%), NVFP4 8 x 64K 86
-// us (52%); 32 columns (8 new tokens), BF16 8 x 64K 182 us (87%), FP8 126 us (65%),
+// us (52%); 32 columns (8 new tokens), BF16 8 x 64K 182 us (87%), FP8 130 us (63%),
 // NVFP4 8 x 128K 226 us (40%; tensor pipe 43%, issue slots 40%, two warps a scheduler
 // waiting for each other's results); 61 ragged BF16 sequences of 48 columns 86 us
 // (48%; tensor pipe 50%); one sequence of 4K tokens 9.1 us.
@@ -75,8 +83,10 @@ constexpr int kDenseWpg = 4;             // consumer warps of a team
 // An MMA's sum is ready after 21 cycles, and a scheduler could start one every 8:
 // a warp alternates this many sums (with two or eight the operator takes as long).
 constexpr int kDenseChains = 4;
-constexpr float kDensePShift = 7.f;      // log2 of the scale of P (f16 formats)
+constexpr float kDensePShift = 7.f;      // log2 of the scale of P (NVFP4)
+constexpr float kDenseTop = 4.f;         // FP8: P x vscale of a column's largest product so far
 constexpr float kDenseLazy = 8.f;        // a logit (log2) above the reference by this moves it
+constexpr float kDenseNone = -3.0e38f;   // FP8: the reference before a row's first key
 
 template <int FMT>
 struct DenseTraits;
@@ -818,7 +828,7 @@ __device__ void consumer(const DenseParams& p, const DenseTeam& tm, int bar, int
   constexpr int KW = TR::SK / KGW;             // keys of a warp in a unit
   constexpr int KC = KW < 32 ? KW : 32;        // keys a softmax step takes
   constexpr bool F16P = FMT != FMT_BF16;
-  constexpr float SHIFT = F16P ? kDensePShift : 0.f;
+  constexpr float SHIFT = FMT == FMT_NVFP4 ? kDensePShift : 0.f;
   constexpr bool REG = NN == 1;                // query fragments held in registers
   constexpr int TEAM_THREADS = 32 * kDenseWpg;
   const int ct = warp / KGW, kw = (warp % KGW) * KW;  // column group, first key
@@ -860,14 +870,17 @@ __device__ void consumer(const DenseParams& p, const DenseTeam& tm, int bar, int
       }
     }
 
-    // row state: the reference m_run (log2 domain) and the raw logit that moves it
+    // row state: the reference m_run (log2 domain), what is subtracted, and the raw logit that
+    // moves it.  (FP8 subtracts m_run itself: four registers fewer where they spill, 32 columns
+    // 130.2 us for 132.5.)
+    constexpr bool SAME = FMT == FMT_FP8;
     float m_run[NN], msub[NN], ylim[NN], colf[NN];
     float2 l_run[NN];
 #pragma unroll
     for (int n = 0; n < NN; ++n) {
-      m_run[n] = -INFINITY;
+      m_run[n] = SAME ? kDenseNone : -INFINITY;
       ylim[n] = -INFINITY;
-      msub[n] = 0.f;
+      msub[n] = SAME ? m_run[n] : 0.f;
       l_run[n] = make_float2(0.f, 0.f);
       colf[n] = cf[ct * LY::WROWS + 8 * n + g8];
     }
@@ -876,8 +889,11 @@ __device__ void consumer(const DenseParams& p, const DenseTeam& tm, int bar, int
     for (int t = 0; t < 8; ++t)
 #pragma unroll
       for (int n = 0; n < NN; ++n) o[t][n][0] = o[t][n][1] = o[t][n][2] = o[t][n][3] = 0.f;
-    int ev = 0;           // FP8: P carries vscale x 2^ev
-    float fe = 0.f;       // 2^ev, 0: not chosen yet
+    // FP8: P enters as P x vscale x fe, O is kept times fe (0: no product yet); vlim: the
+    // largest scale that keeps every column within f16's range
+    float fe[NN], vlim = -1.f;
+#pragma unroll
+    for (int n = 0; n < NN; ++n) fe[n] = 0.f;
     const int lim0 = f.T - p.Q;  // every row sees the keys up to here
 
 #pragma unroll 1
@@ -930,7 +946,7 @@ __device__ void consumer(const DenseParams& p, const DenseTeam& tm, int bar, int
             for (int t = 1; t < KC / 8; ++t) mx[n] = max3(mx[n], y[t][n].x, y[t][n].y);
             over |= mx[n] > ylim[n];
           }
-          // ---- FP8: V's scales; does P x vscale x 2^ev keep to f16's range?
+          // ---- FP8: V's scales; does P x vscale x fe keep to f16's range?
           float2 vs[KC / 8];
           if constexpr (FMT == FMT_FP8) {
             float vm = 0.f;
@@ -943,47 +959,44 @@ __device__ void consumer(const DenseParams& p, const DenseTeam& tm, int bar, int
               }
               vm = max3(vm, fabsf(vs[t].x), fabsf(vs[t].y));
             }
-            over |= vm * fe > 1.f || fe == 0.f;
-            if (!__any_sync(0xffffffffu, vm * fe >= 0.00390625f)) over = true;
+            over |= vm > vlim;
           }
           if (__any_sync(0xffffffffu, over)) {
-            // the row's new reference, and the power of two of V's scales
-            float resc = 1.f;
-            if constexpr (FMT == FMT_FP8) {
-              float vm = 0.f;
-#pragma unroll
-              for (int t = 0; t < KC / 8; ++t) {
-                const float v0 = fabsf(vs[t].x), v1 = fabsf(vs[t].y);
-                vm = max3(vm, v0 <= 3.0e38f ? v0 : 0.f, v1 <= 3.0e38f ? v1 : 0.f);
-              }
-              vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 1));
-              vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, 2));
-              const float cur = vm * fe;
-              if (vm > 0.f && (fe == 0.f || cur > 1.f || cur < 0.00390625f)) {
-                const int be = (int)(__float_as_uint(vm) >> 23) - 127;  // vm in [2^be, 2^(be + 1))
-                int en = -3 - be;                                      // vm x 2^en in [1/8, 1/4)
-                en = en < -126 ? -126 : (en > 120 ? 120 : en);
-                const int de = en - ev < -126 ? -126 : (en - ev > 126 ? 126 : en - ev);
-                if (fe != 0.f) resc = pow2i(de);
-                ev = en;
-                fe = pow2i(en);
-              }
-            }
+            // the row's new reference and, for FP8, the column's largest product
+            if constexpr (FMT == FMT_FP8) vlim = 3.3e35f;  // 2^118: 2^8 x vscale stays finite
 #pragma unroll
             for (int n = 0; n < NN; ++n) {
               mx[n] = fmaxf(mx[n], __shfl_xor_sync(0xffffffffu, mx[n], 1));
               mx[n] = fmaxf(mx[n], __shfl_xor_sync(0xffffffffu, mx[n], 2));
               const float mnew = fmaxf(m_run[n], mx[n] * colf[n]);
-              const float ref = mnew == -INFINITY ? 0.f : mnew;
+              const float ref = !SAME && mnew == -INFINITY ? 0.f : mnew;
               const float alpha = ex2(m_run[n] - ref);  // the first time 0 x 0
               m_run[n] = mnew;
               msub[n] = ref - SHIFT;
               ylim[n] = (mnew + kDenseLazy) / colf[n];
               l_run[n].x *= alpha;
               l_run[n].y *= alpha;
+              float w = alpha;  // of O
+              if constexpr (FMT == FMT_FP8) {
+                float top = 0.f;
+#pragma unroll
+                for (int t = 0; t < KC / 8; ++t) {
+                  const float2 x = fma2(y[t][n], make_float2(colf[n], colf[n]), make_float2(-(SAME ? m_run : msub)[n], -(SAME ? m_run : msub)[n]));
+                  const float a = fabsf(ex2(x.x) * vs[t].x), b = fabsf(ex2(x.y) * vs[t].y);
+                  top = max3(top, a < INFINITY ? a : 0.f, b < INFINITY ? b : 0.f);
+                }
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const float kept = fe[n] > 0.f ? alpha * (kDenseTop * __frcp_rn(fe[n])) : 0.f;  // the former one
+                const float most = fminf(fmaxf(fmaxf(kept, top), 3.0e-36f), 3.0e38f);
+                const float inv = __frcp_rn(most);
+                w = kept == most ? 1.f : kept * inv;  // never above 1
+                if (w != 1.f || alpha != 1.f) fe[n] = fmaxf(kept, top) > 0.f ? kDenseTop * inv : 0.f;
+                vlim = fminf(vlim, fe[n] > 0.f ? 128.f * __frcp_rn(fe[n]) : -1.f);  // a weight is 2^8 at most
+              }
               // the accumulators hold the columns 2j, 2j + 1
-              const float w0 = __shfl_sync(0xffffffffu, alpha, 8 * j) * resc;
-              const float w1 = __shfl_sync(0xffffffffu, alpha, 8 * j + 4) * resc;
+              const float w0 = __shfl_sync(0xffffffffu, w, 8 * j);
+              const float w1 = __shfl_sync(0xffffffffu, w, 8 * j + 4);
 #pragma unroll
               for (int t = 0; t < 8; ++t) {
                 o[t][n][0] *= w0;
@@ -997,15 +1010,13 @@ __device__ void consumer(const DenseParams& p, const DenseTeam& tm, int bar, int
           uint32_t ph[KC / 8][NN], plo[KC / 8][NN];
 #pragma unroll
           for (int t = 0; t < KC / 8; ++t) {
-            float2 w = make_float2(1.f, 1.f);
-            if constexpr (FMT == FMT_FP8) w = mul2(vs[t], make_float2(fe, fe));
 #pragma unroll
             for (int n = 0; n < NN; ++n) {
-              const float2 x = fma2(y[t][n], make_float2(colf[n], colf[n]), make_float2(-msub[n], -msub[n]));
+              const float2 x = fma2(y[t][n], make_float2(colf[n], colf[n]), make_float2(-(SAME ? m_run : msub)[n], -(SAME ? m_run : msub)[n]));
               float2 q = make_float2(ex2(x.x), ex2(x.y));
               l_run[n] = add2(l_run[n], q);
               if constexpr (FMT == FMT_FP8) {
-                const float2 v = mul2(q, w);
+                const float2 v = mul2(mul2(q, vs[t]), make_float2(fe[n], fe[n]));
                 if (masked) {  // a masked weight stays 0 beside a scale that is not finite
                   q.x = q.x == 0.f ? 0.f : v.x;
                   q.y = q.y == 0.f ? 0.f : v.y;
@@ -1078,9 +1089,9 @@ __device__ void consumer(const DenseParams& p, const DenseTeam& tm, int bar, int
     if (lane == 0) mbar_arrive(&tm.iempty[slot]);
 
     // ---------------- the segment's result: the warps of a column group hold different keys
-    const float osc = FMT == FMT_FP8 ? pow2i(-ev) : (FMT == FMT_NVFP4 ? p.v_global : 1.f);
 #pragma unroll
     for (int n = 0; n < NN; ++n) {
+      const float osc = FMT == FMT_FP8 ? (fe[n] > 0.f ? __frcp_rn(fe[n]) : 0.f) : (FMT == FMT_NVFP4 ? p.v_global : 1.f);
       float l = l_run[n].x + l_run[n].y;
       l += __shfl_xor_sync(0xffffffffu, l, 1);
       l += __shfl_xor_sync(0xffffffffu, l, 2);
@@ -1189,7 +1200,7 @@ __device__ void consumer(const DenseParams& p, const DenseTeam& tm, int bar, int
 #pragma unroll
       for (int n = 0; n < NN; ++n) {
         const float4* own = ml + warp * LY::WROWS + 8 * n + 2 * j;
-        const float2 wc = make_float2(own[0].w, own[1].w);  // columns 2j, 2j + 1
+        const float2 oc = make_float2(own[0].z, own[1].z), wc = make_float2(own[0].w, own[1].w);  // columns 2j, 2j + 1
         // where this lane writes: BF16 lanes hold dims 8 apart and pair up with a neighbour's, one column each
         size_t at[2];
         bool live[2];
@@ -1206,10 +1217,10 @@ __device__ void consumer(const DenseParams& p, const DenseTeam& tm, int bar, int
 #pragma unroll
           for (int u = 0; u < LY::MT_OWN; ++u) {
             float(&v)[4] = o[w * LY::MT_OWN + u][n];
-            v[0] = v[0] * osc * wc.x;
-            v[1] = v[1] * osc * wc.y;
-            v[2] = v[2] * osc * wc.x;
-            v[3] = v[3] * osc * wc.y;
+            v[0] = v[0] * oc.x * wc.x;
+            v[1] = v[1] * oc.y * wc.y;
+            v[2] = v[2] * oc.x * wc.x;
+            v[3] = v[3] * oc.y * wc.y;
             if (w != me)
               mo[((warp * (KGW - 1) + (w < me ? w : w - 1)) * LY::MT_OWN + u) * 32 + lane] = make_float4(v[0], v[1], v[2], v[3]);
           }
