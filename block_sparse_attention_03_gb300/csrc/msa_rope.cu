@@ -42,7 +42,8 @@
 // RISC System/6000, 1990): with y = RN(1/s), q = RN(x y), r = RN(x - q s) exact,
 // RN(q + r y) is the correctly rounded quotient, so the codes are those of an
 // IEEE division at three operations an element; scales near the ends of fp32's
-// range, where r could underflow or y overflow, take the division itself.
+// range, where r could underflow or y overflow, and elements whose quotient is
+// infinite take the division itself.
 #include "msa_device.cuh"
 #include "msa_internal.h"
 
@@ -66,10 +67,11 @@ __device__ __forceinline__ uint32_t e4m3x4(float2 a, float2 b) {
   return (uint32_t)pack_e4m3x2(a.x, a.y) | ((uint32_t)pack_e4m3x2(b.x, b.y) << 16);
 }
 
-// y[i] / s, correctly rounded (see above).
+// y[i] / s, correctly rounded (see above).  fits: no quotient is infinite (its
+// remainder would be NaN).
 template <int N>
-__device__ __forceinline__ void divide(const float2 (&y)[N], float s, float2 (&z)[N]) {
-  if (s >= 8.27e-25f && s <= 1.2e24f) {  // 2^-80 to 2^80
+__device__ __forceinline__ void divide(const float2 (&y)[N], float s, bool fits, float2 (&z)[N]) {
+  if (s >= 8.27e-25f && s <= 1.2e24f && fits) {  // 2^-80 to 2^80
     const float r = __frcp_rn(s);
     const float2 r2 = make_float2(r, r), n2 = make_float2(-s, -s);
 #pragma unroll
@@ -126,7 +128,7 @@ __device__ __forceinline__ void put_row(const float2 (&y)[8], int dA, int dB, bo
     if (!put) return;
     const float s = m > 0.f ? __fdiv_rn(m, 448.f) : 1.f;
     float2 z[8];
-    divide(y, s, z);
+    divide(y, s, true, z);  // s follows the row's maximum: 448 at most, or s is infinite
     *reinterpret_cast<uint2*>(data + row * 128 + dA) = e4m3x8(z);
     *reinterpret_cast<uint2*>(data + row * 128 + dB) = e4m3x8(z + 4);
     if (l8 == 0) scale[row] = s;
@@ -151,7 +153,7 @@ __device__ __forceinline__ void put_row(const float2 (&y)[8], int dA, int dB, bo
       if (den > 0.f) {
         const float2 v[4] = {y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]};
         float2 z[4];
-        divide(v, den, z);
+        divide(v, den, m * __frcp_rn(den) <= 3.0e38f, z);  // the group's scale saturates
 #pragma unroll
         for (int i = 0; i < 4; ++i) w |= e2m1x2(z[i].x, z[i].y) << (8 * i);
       }
