@@ -67,8 +67,20 @@ __device__ __forceinline__ uint32_t e4m3x4(float2 a, float2 b) {
   return (uint32_t)pack_e4m3x2(a.x, a.y) | ((uint32_t)pack_e4m3x2(b.x, b.y) << 16);
 }
 
+// fma2 rounded down: a sum that is zero is -0.
+__device__ __forceinline__ float2 fma2_down(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{ .reg .b64 x, y, z, w; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mov.b64 z, {%6, %7}; fma.rm.f32x2 w, x, y, z; "
+      "mov.b64 {%0, %1}, w; }"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+
 // y[i] / s, correctly rounded (see above).  fits: no quotient is infinite (its
 // remainder would be NaN).
+// The sign of a zero is kept: the remainder is exact, and as -0 where it is zero it
+// leaves q = -0 alone.
 template <int N>
 __device__ __forceinline__ void divide(const float2 (&y)[N], float s, bool fits, float2 (&z)[N]) {
   if (s >= 8.27e-25f && s <= 1.2e24f && fits) {  // 2^-80 to 2^80
@@ -77,7 +89,7 @@ __device__ __forceinline__ void divide(const float2 (&y)[N], float s, bool fits,
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const float2 q = mul2(y[i], r2);
-      z[i] = fma2(fma2(q, n2, y[i]), r2, q);
+      z[i] = fma2(fma2_down(q, n2, y[i]), r2, q);
     }
   } else {
 #pragma unroll

@@ -50,6 +50,16 @@ def test_elements_that_are_not_finite(kv):
     _same_bytes(kv, k, x, ik)
 
 
+@pytest.mark.parametrize("kv", ["fp8", "nvfp4"])
+def test_zeros_of_either_sign(kv):
+    x, gen = _rows(256, 2, 49)
+    at = torch.rand((256, 2, 128), generator=gen).cuda()
+    x[at < 0.1] = 0.0
+    x[at > 0.9] = -0.0
+    x[5] = -0.0
+    _same_bytes(kv, _rows(256, 2, 50)[0], x, _rows(256, 1, 51)[0].squeeze(1))
+
+
 @pytest.mark.parametrize("g", [2.0 ** -8, 0.1234, 1e-10, 1e-25, 3e-30, 1e30])
 def test_nvfp4_with_elements_far_beyond_the_scale(g):
     # quotients that pass fp32's range on either side, infinities among ordinary elements
