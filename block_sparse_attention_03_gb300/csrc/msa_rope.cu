@@ -113,6 +113,11 @@ __device__ __forceinline__ uint4 bf16x8(const float2* y) {
   return make_uint4(pack_bf16x2(y[0].x, y[0].y), pack_bf16x2(y[1].x, y[1].y), pack_bf16x2(y[2].x, y[2].y),
                     pack_bf16x2(y[3].x, y[3].y));
 }
+// the same of elements that are bf16 values: their bits (the rounding has one NaN only)
+__device__ __forceinline__ uint4 bf16x8_bits(const float2* y) {
+  auto top = [](float2 v) { return __byte_perm(__float_as_uint(v.x), __float_as_uint(v.y), 0x7632); };
+  return make_uint4(top(y[0]), top(y[1]), top(y[2]), top(y[3]));
+}
 __device__ __forceinline__ uint2 e4m3x8(const float2* y) { return make_uint2(e4m3x4(y[0], y[1]), e4m3x4(y[2], y[3])); }
 __device__ __forceinline__ float amax8(const float2* y) {
   return fmaxf(fmaxf(fmaxf(fabsf(y[0].x), fabsf(y[0].y)), fmaxf(fabsf(y[1].x), fabsf(y[1].y))),
@@ -120,15 +125,16 @@ __device__ __forceinline__ float amax8(const float2* y) {
 }
 
 // One cache row of 8 lanes, elements [dA, dA + 8) (y[0..3]) and [dB, dB + 8) a lane
-// (every lane of the warp takes part in the exchanges; `put`: this row is stored).
+// (every lane of the warp takes part in the exchanges; `put`: this row is stored;
+// `raw`: as it came).
 template <int FMT>
-__device__ __forceinline__ void put_row(const float2 (&y)[8], int dA, int dB, bool put, uint8_t* __restrict__ data,
-                                        float* __restrict__ scale, uint8_t* __restrict__ sf, float g, long row,
+__device__ __forceinline__ void put_row(const float2 (&y)[8], int dA, int dB, bool put, bool raw,
+                                        uint8_t* __restrict__ data, float* __restrict__ scale, uint8_t* __restrict__ sf, float g, long row,
                                         float* chunk_max, int l8) {
   if constexpr (FMT == FMT_BF16) {
     if (put) {
-      *reinterpret_cast<uint4*>(data + row * 256 + 2 * dA) = bf16x8(y);
-      *reinterpret_cast<uint4*>(data + row * 256 + 2 * dB) = bf16x8(y + 4);
+      *reinterpret_cast<uint4*>(data + row * 256 + 2 * dA) = raw ? bf16x8_bits(y) : bf16x8(y);
+      *reinterpret_cast<uint4*>(data + row * 256 + 2 * dB) = raw ? bf16x8_bits(y + 4) : bf16x8(y + 4);
     }
     return;
   }
@@ -379,10 +385,10 @@ __global__ void __launch_bounds__(32 * kRopeWarps, kRopeCtas) rope_kernel(const 
           *reinterpret_cast<uint4*>(o + 2 * dB) = bf16x8(y + 4);
         }
       } else if (kind == KIND_IK) {
-        put_row<IF>(y, dA, dB, store && out, out, p.is, p.isf, p.ig, (long)blk * kBlock + off, s_max[warp][sub], l8);
+        put_row<IF>(y, dA, dB, store && out, false, out, p.is, p.isf, p.ig, (long)blk * kBlock + off, s_max[warp][sub], l8);
       } else {
         const bool isk = kind == KIND_K;
-        put_row<KVF>(y, dA, dB, store && out, out, isk ? p.ks : p.vs, isk ? p.ksf : p.vsf, isk ? p.kg : p.vg, row0 + d.out_step,
+        put_row<KVF>(y, dA, dB, store && out, !isk, out, isk ? p.ks : p.vs, isk ? p.ksf : p.vsf, isk ? p.kg : p.vg, row0 + d.out_step,
                      s_max[warp][sub], l8);
       }
     }

@@ -37,7 +37,7 @@ def _rows(T, H, seed, spread=1.0):
     return (x * torch.exp(spread * torch.randn((T, H, 1), generator=gen))).bfloat16().cuda(), gen
 
 
-@pytest.mark.parametrize("kv", ["fp8", "nvfp4"])
+@pytest.mark.parametrize("kv", ["bf16", "fp8", "nvfp4"])
 def test_elements_that_are_not_finite(kv):
     x, gen = _rows(256, 2, 40)
     at = torch.rand((256, 2, 128), generator=gen).cuda()
@@ -50,7 +50,12 @@ def test_elements_that_are_not_finite(kv):
     _same_bytes(kv, k, x, ik)
 
 
-@pytest.mark.parametrize("kv", ["fp8", "nvfp4"])
+def test_bf16_copies_the_bits():
+    x = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(torch.bfloat16).view(256, 2, 128).cuda()
+    _same_bytes("bf16", _rows(256, 2, 52)[0], x, _rows(256, 1, 53)[0].squeeze(1))
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8", "nvfp4"])
 def test_zeros_of_either_sign(kv):
     x, gen = _rows(256, 2, 49)
     at = torch.rand((256, 2, 128), generator=gen).cuda()
