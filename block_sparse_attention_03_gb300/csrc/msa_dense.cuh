@@ -516,13 +516,13 @@ __device__ __forceinline__ void convert_q(uint8_t* qs, float* cf, int nrows, int
     for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     int e = pow2_fit(amax, 16384.f);
     e = e < -126 ? -126 : (e > 126 ? 126 : e);
-    const float ps = pow2i(e);
+    // A query row that is not finite has no finite logits; the reduced formats
+    // would hide that, so it is NaN (the logits of masked keys are replaced all the
+    // same).  The factor is kept off zero: it multiplies -inf.
+    const float ps = __any_sync(0xffffffffu, bad) ? __int_as_float(0x7fc00000) : pow2i(e);
     *reinterpret_cast<uint32_t*>(r + 2 * q_place<FMT>(4 * lane)) = pack_f16x2(a.x * ps, a.y * ps);
     *reinterpret_cast<uint32_t*>(r + 2 * q_place<FMT>(4 * lane + 2)) = pack_f16x2(b.x * ps, b.y * ps);
-    // A query row that is not finite has no finite logits; the reduced formats
-    // would hide that.  (The factor is kept off zero: it multiplies -inf.)
-    const bool any_bad = __any_sync(0xffffffffu, bad);
-    if (lane == 0) cf[row] = any_bad ? __int_as_float(0x7fc00000) : fmaxf(pow2i(-e) * cst, 1.2e-38f);
+    if (lane == 0) cf[row] = fmaxf(pow2i(-e) * cst, 1.2e-38f);
   }
 }
 
