@@ -28,7 +28,9 @@ constexpr int kTabThreads = 512;
 // Sums saturate at kMost, past any count that can be granted, so that no set of
 // lengths wraps around (a saturating sum of sizes is associative).
 constexpr int kMost = 1 << 30;
-__device__ __forceinline__ int sat_add(int a, int b) { return min(a + b, kMost); }  // 0 <= a, b <= kMost
+__device__ __forceinline__ int sat_add(int a, int b) {  // 0 <= a, b <= kMost; two of kMost pass an int's range
+  return (int)min((unsigned)a + (unsigned)b, (unsigned)kMost);
+}
 
 // Exclusive sums in place of three arrays of n sizes <= kMost (n <= kMaxTableSeqs);
 // the totals land at [n].

@@ -381,7 +381,8 @@ msa_status_t msa_rope_insert(const msa_cache_t* cache, const msa_rope_t* rope, i
  *      the top of the stack, in the order of the requests, into its row.
  * Outputs:
  *   seq_lens       [num_seqs] cached + new (0 for an ended request): the batch's lengths
- *   token_offsets  [num_seqs + 1] exclusive sums of the new tokens
+ *   token_offsets  [num_seqs + 1] exclusive sums of the new tokens (those of the
+ *                  refused ones among them; a sum beyond 2^30 is given as 2^30)
  *   slot_mapping, positions  [max_tokens] for new token i of request s, at
  *                  token_offsets[s] + i: its slot and its position cached + i;
  *                  -1 and 0 behind the last token
