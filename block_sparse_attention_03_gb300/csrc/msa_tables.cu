@@ -123,6 +123,57 @@ __global__ void __launch_bounds__(kTabThreads) tables_kernel(const TablesParams 
   scan3(tok, want, back, S, warp_sums);
   const int count = min(max(count_in, 0), p.free_cap);
   const int room = p.free_cap - count;
+  auto ended = [&](int s) { return cached[s] >= 0 && __ldg(p.fresh + s) < 0; };
+  auto in_pool = [&](int b) { return b >= 0 && b < p.num_blocks; };
+  // Returned entries outside the pool are no blocks: they are left out, or they would
+  // come around again.  Every CTA looks at all that the stack has room for (a round of
+  // loads for each 512).
+  bool odd = false;
+  for (int r = tid; r < min(back[S], room); r += kTabThreads) {
+    const int s = owner(back, S, r);
+    odd |= !in_pool(p.block_table[(size_t)s * p.max_nb + (r - back[s])]);
+  }
+  for (int r = room + blockIdx.x * kTabThreads + tid; r < back[S]; r += gridDim.x * kTabThreads) {  // dropped: flagged only
+    const int s = owner(back, S, r), e = p.block_table[(size_t)s * p.max_nb + (r - back[s])];
+    if (!in_pool(e)) raise_flag(p.status, FLAG_BAD_BLOCK, e);
+  }
+  const bool gaps = __syncthreads_or(odd);
+  if (gaps) {
+    for (int s = tid >> 5; s < S; s += kTabThreads / 32) {  // a warp a request
+      int good = 0;
+      const int n = ended(s) ? blocks_of(cached[s]) : 0;
+      for (int b0 = 0; b0 < n; b0 += 32) {
+        const int b = b0 + (tid & 31);
+        const int e = b < n ? p.block_table[(size_t)s * p.max_nb + b] : 0;
+        if (b < n && !in_pool(e) && blockIdx.x == 0) raise_flag(p.status, FLAG_BAD_BLOCK, e);
+        good += __popc(__ballot_sync(0xffffffffu, b < n && in_pool(e)));
+      }
+      if ((tid & 31) == 0) back[s] = good;
+    }
+    __syncthreads();
+    if (tid == 0) {
+      int sum = 0;
+      for (int s = 0; s <= S; ++s) {
+        const int n = s < S ? back[s] : 0;
+        back[s] = sum;
+        sum = sat_add(sum, n);
+      }
+    }
+    __syncthreads();
+  }
+  // the r-th returned block
+  auto returned = [&](int r) -> int {
+    const int s = owner(back, S, r);
+    const int32_t* row = p.block_table + (size_t)s * p.max_nb;
+    int i = r - back[s];
+    if (gaps)
+      for (int b = 0, left = i + 1; left > 0; ++b)  // back[] counted `left` blocks or more in this row
+        if (in_pool(row[b])) {
+          i = b;
+          --left;
+        }
+    return row[i];
+  };
   if (blockIdx.x == 0 && tid == 0 && count != count_in) raise_flag(p.status, FLAG_BAD_BLOCK, count);
   const int given = min(back[S], room);  // returned blocks the stack has room for
   const int total = count + given;
@@ -141,8 +192,7 @@ __global__ void __launch_bounds__(kTabThreads) tables_kernel(const TablesParams 
     if (at < count) {
       b = __ldg(p.free_blocks_in + at);
     } else {
-      const int r = at - count, s = owner(back, S, r);
-      b = p.block_table[(size_t)s * p.max_nb + (r - back[s])];
+      b = returned(at - count);
     }
     if (b < 0 || b >= p.num_blocks) {
       raise_flag(p.status, FLAG_BAD_BLOCK, b);
@@ -156,8 +206,7 @@ __global__ void __launch_bounds__(kTabThreads) tables_kernel(const TablesParams 
   for (int s = gtid; s < S; s += gn) {
     const int add = tok[s + 1] - tok[s];
     const int c = cached[s];
-    const bool ends = back[s + 1] > back[s] || (c >= 0 && __ldg(p.fresh + s) < 0);
-    int len = c < 0 || ends ? 0 : c;
+    int len = c < 0 || ended(s) ? 0 : c;
     if (add > 0) {
       if (granted(s)) len = c + add;
       else raise_flag(p.status, FLAG_NO_ROOM, s);
@@ -202,10 +251,7 @@ __global__ void __launch_bounds__(kTabThreads) tables_kernel(const TablesParams 
   }
   // the returned blocks that stay on the stack (entries at and above `count`:
   // nothing reads those in this call)
-  for (int r = gtid; r < min(given, total - taken - count); r += gn) {
-    const int s = owner(back, S, r);
-    p.free_blocks[count + r] = p.block_table[(size_t)s * p.max_nb + (r - back[s])];
-  }
+  for (int r = gtid; r < min(given, total - taken - count); r += gn) p.free_blocks[count + r] = returned(r);
 }
 
 }  // namespace

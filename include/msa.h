@@ -376,7 +376,8 @@ msa_status_t msa_rope_insert(const msa_cache_t* cache, const msa_rope_t* rope, i
  * their blocks) and new_lens[s] new ones: 0 for a request that waits, -1 for one
  * that has ended.  free_blocks[0 .. *free_count) is a stack of free blocks.
  *   1. The blocks of the ended requests go on top of the stack, in the order of
- *      the requests; their rows of block_table are left as they are.
+ *      the requests; their rows of block_table are left as they are.  Entries
+ *      outside [0, num_blocks) are flagged and left out.
  *   2. Each request takes the blocks its new tokens need beyond those it has off
  *      the top of the stack, in the order of the requests, into its row.
  * Outputs:
