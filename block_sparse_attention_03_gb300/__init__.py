@@ -288,13 +288,15 @@ _DENSE = _Layout(_CACHE, _BATCH, _CONFIG, _QUERY)
 _ROPE = _Layout(_CACHE, _ROWS, _QUERY, _ROWS, _QUERY, _ROWS, _ROWS, _ROWS, _NORM)
 
 
-_int32 = _bf16 = _device = None
+_int32 = _bf16 = _f32 = _device = None
+_query_types = {}  # the element types of a query of each kind
 
 
 def _torch_names() -> None:
-    global _int32, _bf16, _device
+    global _int32, _bf16, _f32, _device
     import torch
-    _int32, _bf16, _device = torch.int32, torch.bfloat16, torch.cuda.current_device
+    _int32, _bf16, _f32, _device = torch.int32, torch.bfloat16, torch.float32, torch.cuda.current_device
+    _query_types.update(bf16=(torch.bfloat16,), fp8=(torch.uint8, torch.float8_e4m3fn, torch.int8))
 
 
 # The serving calls refuse what the kernels would misread: other types, strides and
@@ -417,9 +419,9 @@ def msa_dense_attend(cache, batch, cfg, q: Query, num_q_heads: int, out, lse, wo
     shape, rows, dev = table.shape, lens.numel() * batch.q_per_seq * num_q_heads, cache.k.get_device()
     if (dev < 0 or dev != _device() or len(shape) != 2 or shape[0] != lens.numel()
             or lens.dtype is not _int32 or table.dtype is not _int32 or not lens.is_contiguous() or not table.is_contiguous()
-            or data.numel() != rows * 128 or not data.is_contiguous() or data.element_size() != (1 if q.dtype == "fp8" else 2)
+            or data.numel() != rows * 128 or not data.is_contiguous() or data.dtype not in _query_types.get(q.dtype, ())
             or out.numel() != rows * 128 or not out.is_contiguous() or out.dtype is not _bf16
-            or (lse is not None and (lse.numel() != rows or not lse.is_contiguous() or lse.element_size() != 4
+            or (lse is not None and (lse.numel() != rows or not lse.is_contiguous() or lse.dtype is not _f32
                                     or lse.get_device() != dev))
             or lens.get_device() != dev or table.get_device() != dev or data.get_device() != dev or out.get_device() != dev
             or workspace.get_device() != dev):
@@ -455,7 +457,7 @@ def msa_rope_insert(cache, rope: MsaRopeT, positions, slot_mapping, q, q_out: Qu
     if (dev < 0 or dev != _device() or q.dim() != 3
             or positions.numel() != rope.axes * T or positions.dtype is not _int32 or not positions.is_contiguous()
             or slot_mapping.dtype is not _int32 or not slot_mapping.is_contiguous()
-            or qd.numel() != q.numel() or not qd.is_contiguous() or qd.element_size() != (1 if q_out.dtype == "fp8" else 2)
+            or qd.numel() != q.numel() or not qd.is_contiguous() or qd.dtype not in _query_types.get(q_out.dtype, ())
             or positions.get_device() != dev or slot_mapping.get_device() != dev or q.get_device() != dev or qd.get_device() != dev
             or workspace.get_device() != dev):
         raise MsaError(1, where)
@@ -464,7 +466,7 @@ def msa_rope_insert(cache, rope: MsaRopeT, positions, slot_mapping, q, q_out: Qu
     iqo, w = (0, 0, 0.0), (0, 0, 0, 0, 0.0, 0.0)
     if index_q_out is not None:
         x = index_q_out.data
-        if x.numel() != T * H * 128 or not x.is_contiguous() or x.element_size() != (1 if index_q_out.dtype == "fp8" else 2) \
+        if x.numel() != T * H * 128 or not x.is_contiguous() or x.dtype not in _query_types.get(index_q_out.dtype, ()) \
                 or x.get_device() != dev:
             raise MsaError(1, where)
         iqo = (x.data_ptr(), DTYPES[index_q_out.dtype], index_q_out.scale)
