@@ -182,6 +182,11 @@ class PagedCache:
     index_dim: int = 128
     nvfp4_mode: str = "exact"
 
+    def __setattr__(self, name, value):
+        # the serving calls look at the tensors once (_checked), and again when a field is set
+        self.__dict__["_seen"] = ()
+        self.__dict__[name] = value
+
     def struct(self) -> MsaCacheT:
         return MsaCacheT(DTYPES[self.kv_dtype], DTYPES[self.index_dtype], self.num_blocks, 128,
                          self.num_kv_heads, self.head_dim, self.index_dim,
@@ -278,7 +283,27 @@ def _p(t) -> int:
     return 0 if t is None else t.data_ptr()
 
 
-def _cache_values(c: PagedCache):
+def _checked(c: PagedCache, index: bool, dev: int, where: str) -> None:
+    """The cache's tensors (the index keys' too, if the call writes them): dense, on the device, of
+    their formats' types and at least num_blocks blocks long."""
+    import torch
+    codes = (torch.uint8, torch.int8, torch.float8_e4m3fn)
+    wanted = [("k", c.kv_dtype, c.num_kv_heads), ("v", c.kv_dtype, c.num_kv_heads)] + [("idx", c.index_dtype, 1)] * index
+    for name, kind, heads in wanted:
+        rows = c.num_blocks * heads * 128
+        parts = {"bf16": [(name, (torch.bfloat16,), 128)], "fp8": [(name, codes, 128), (name + "_scale", (torch.float32,), 1)],
+                 "nvfp4": [(name, (torch.uint8, torch.int8), 64), (name + "_sf", codes, 8)]}.get(kind, [])
+        for field, types, width in parts:
+            t = getattr(c, field)
+            if t is not None and (t.dtype not in types or t.numel() < rows * width or not t.is_contiguous() or t.get_device() != dev):
+                raise MsaError(1, where)
+    c.__dict__["_seen"] = (dev, index or (c._seen[:1] == (dev,) and c._seen[1]))
+
+
+def _cache_values(c: PagedCache, index: bool, dev: int, where: str):
+    seen = c._seen
+    if not seen or seen[0] != dev or (index and not seen[1]):
+        _checked(c, index, dev, where)
     return (DTYPES[c.kv_dtype], DTYPES[c.index_dtype], c.num_blocks, 128, c.num_kv_heads, c.head_dim, c.index_dim,
             c.k.data_ptr(), c.v.data_ptr(), _p(c.k_sf), _p(c.v_sf), _p(c.k_scale), _p(c.v_scale), _p(c.idx), _p(c.idx_sf),
             _p(c.idx_scale), c.k_global, c.v_global, c.idx_global, NVFP4_MODES.get(c.nvfp4_mode, -1))
@@ -426,7 +451,7 @@ def msa_dense_attend(cache, batch, cfg, q: Query, num_q_heads: int, out, lse, wo
             or lens.get_device() != dev or table.get_device() != dev or data.get_device() != dev or out.get_device() != dev
             or workspace.get_device() != dev):
         raise MsaError(1, "msa_dense_attend")
-    at = _DENSE.pack(*_cache_values(cache), shape[0], batch.q_per_seq, shape[1], lens.data_ptr(), table.data_ptr(),
+    at = _DENSE.pack(*_cache_values(cache, False, dev, "msa_dense_attend"), shape[0], batch.q_per_seq, shape[1], lens.data_ptr(), table.data_ptr(),
                      cfg.topk, cfg.init_blocks, cfg.local_blocks, cfg.index_scale, cfg.sm_scale,
                      SCORE_TYPES.get(cfg.score_type, -1), PREFILL_SELECT.get(cfg.prefill_select, -1),
                      data.data_ptr(), DTYPES[q.dtype], q.scale)
@@ -476,7 +501,7 @@ def msa_rope_insert(cache, rope: MsaRopeT, positions, slot_mapping, q, q_out: Qu
             if x is not None and (x.numel() != 128 or x.dtype is not _bf16 or not x.is_contiguous() or x.get_device() != dev):
                 raise MsaError(1, where)
         w = (_p(norm.q), _p(norm.k), _p(norm.index_q), _p(norm.index_k), norm.eps, norm.offset)
-    at = _ROPE.pack(*_cache_values(cache), *_rows(q, (T, hq, 128), where, dev), qd.data_ptr(), DTYPES[q_out.dtype], q_out.scale,
+    at = _ROPE.pack(*_cache_values(cache, index_k is not None, dev, where), *_rows(q, (T, hq, 128), where, dev), qd.data_ptr(), DTYPES[q_out.dtype], q_out.scale,
                     *(none if index_q is None else _rows(index_q, kv, where, dev)), *iqo, *_rows(k, kv, where, dev),
                     *_rows(v, kv, where, dev), *(none if index_k is None else
                                              _rows(index_k, (T, 128) if index_k.dim() == 2 else (T, 1, 128), where, dev)), *w)
