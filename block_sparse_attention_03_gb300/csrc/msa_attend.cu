@@ -305,7 +305,17 @@ __device__ __forceinline__ void attend_block(const uint8_t* stg, uint8_t* psm, u
 #pragma unroll
     for (int i = 1; i < NT; ++i) vmax = fmaxf(vmax, vsc[kw + 32 * i + lane]);
     for (int off = 16; off > 0; off >>= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, off));
-    const int e = min(126, fit448(vmax));
+    int e = min(126, fit448(vmax));
+    if (e > e_prev + 2) {
+      // Scales far below the earlier ones: o, which comes along, stays below 2^60 (and
+      // so below 2^122 with the rises of 2 a block that are not looked at).
+      float om = 0.f;
+#pragma unroll
+      for (int mm = 0; mm < 8; ++mm)
+        om = fmaxf(fmaxf(om, fmaxf(fabsf(o[mm][0]), fabsf(o[mm][1]))), fmaxf(fabsf(o[mm][2]), fabsf(o[mm][3])));
+      for (int off = 16; off > 0; off >>= 1) om = fmaxf(om, __shfl_xor_sync(0xffffffffu, om, off));
+      if (om > 0.f && om < INFINITY) e = min(e, max(e_prev, e_prev + 59 - ((int)(__float_as_uint(om) >> 23) - 127)));
+    }
     const float fe = (e >= -126) ? pow2i(e) : ldexpf(1.f, e);
     const int de = e - e_prev;
     const float resc = (de >= -126 && de <= 127) ? pow2i(de) : ldexpf(1.f, de);
@@ -800,7 +810,7 @@ __device__ __forceinline__ void attend_consumer(const AttendParams& p, uint8_t* 
     float colf[2], m_run[2], l_run[2];
     int qlim[2], qbit[2];
     float o[8][4];
-    int e_prev = 0;
+    int e_prev = 126;
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       const int col = ct * 8 + 2 * j + c;
