@@ -81,6 +81,12 @@ bool encode_unit_rows(CUtensorMap* m, const void* base, long rows, int fmt) {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// 32-bit arrays and the status word: a misaligned access would end the context
+template <typename... P>
+bool aligned4(P... p) {
+  return ((... | reinterpret_cast<uintptr_t>(static_cast<const void*>(p))) & 3u) == 0;
+}
+
 int fmt_of(msa_dtype_t d) {
   switch (d) {
     case MSA_DTYPE_BF16: return FMT_BF16;
@@ -744,7 +750,7 @@ msa_status_t msa_cache_insert(const msa_cache_t* cache, int32_t num_tokens, cons
                               size_t workspace_bytes, msa_stream_t stream) {
   msa_status_t s;
   if ((s = check_cache(cache, index_k != nullptr, true)) != MSA_OK) return s;
-  if (num_tokens < 0 || !workspace) return MSA_ERR_INVALID_ARGUMENT;
+  if (num_tokens < 0 || !workspace || !aligned4(workspace, slot_mapping)) return MSA_ERR_INVALID_ARGUMENT;
   if (cache->num_kv_heads > 8) return MSA_ERR_UNSUPPORTED;
   if (workspace_bytes < 256) return MSA_ERR_WORKSPACE_TOO_SMALL;
   if (num_tokens == 0) return MSA_OK;
@@ -793,7 +799,8 @@ msa_status_t msa_dense_attend(const msa_cache_t* cache, const msa_batch_t* batch
   if ((s = check_batch(batch)) != MSA_OK || (s = check_cfg(cfg)) != MSA_OK || (s = check_cache(cache, false, true)) != MSA_OK ||
       (s = check_query(q)) != MSA_OK)
     return s;
-  if (!out || !workspace || !aligned16(out) || !aligned16(workspace)) return MSA_ERR_INVALID_ARGUMENT;
+  if (!out || !workspace || !aligned16(out) || !aligned16(workspace) || !aligned4(batch->seq_lens, batch->block_table, lse))
+    return MSA_ERR_INVALID_ARGUMENT;
   DensePlan pl;
   if ((s = make_dense_plan(cache, batch, num_q_heads, pl)) != MSA_OK) return s;
   if (workspace_bytes < pl.total) return MSA_ERR_WORKSPACE_TOO_SMALL;
@@ -832,7 +839,7 @@ msa_status_t msa_rope_insert(const msa_cache_t* cache, const msa_rope_t* rope, i
                              size_t workspace_bytes, msa_stream_t stream) {
   msa_status_t s;
   if ((s = check_cache(cache, index_k != nullptr, true)) != MSA_OK || (s = check_rope(rope)) != MSA_OK) return s;
-  if (num_tokens < 0 || !workspace) return MSA_ERR_INVALID_ARGUMENT;
+  if (num_tokens < 0 || !workspace || !aligned4(workspace, positions, slot_mapping)) return MSA_ERR_INVALID_ARGUMENT;
   if (workspace_bytes < 256) return MSA_ERR_WORKSPACE_TOO_SMALL;
   if (num_q_heads < 1 || num_q_heads > 1024) return MSA_ERR_UNSUPPORTED;
   if (num_tokens == 0) return MSA_OK;
@@ -916,6 +923,9 @@ msa_status_t msa_build_tables(int32_t num_seqs, int32_t num_blocks, const int32_
     return MSA_ERR_UNSUPPORTED;
   if (!cached_lens || !new_lens || !block_table || !free_count || !free_count_out || !seq_lens || !token_offsets ||
       !workspace || (free_capacity > 0 && !free_blocks) || (max_tokens > 0 && (!slot_mapping || !positions)))
+    return MSA_ERR_INVALID_ARGUMENT;
+  if (!aligned4(cached_lens, new_lens, block_table, free_blocks, free_count, free_count_out, seq_lens, token_offsets, slot_mapping,
+                positions, workspace))
     return MSA_ERR_INVALID_ARGUMENT;
   // the CTAs read the inputs while others write the outputs
   if (free_count_out == free_count || seq_lens == cached_lens || seq_lens == new_lens || token_offsets == cached_lens ||
