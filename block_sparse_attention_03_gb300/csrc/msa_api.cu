@@ -927,11 +927,20 @@ msa_status_t msa_build_tables(int32_t num_seqs, int32_t num_blocks, const int32_
   if (!aligned4(cached_lens, new_lens, block_table, free_blocks, free_count, free_count_out, seq_lens, token_offsets, slot_mapping,
                 positions, workspace))
     return MSA_ERR_INVALID_ARGUMENT;
-  // the CTAs read the inputs while others write the outputs
-  if (free_count_out == free_count || seq_lens == cached_lens || seq_lens == new_lens || token_offsets == cached_lens ||
-      token_offsets == new_lens)
-    return MSA_ERR_INVALID_ARGUMENT;
   if (workspace_bytes < 256) return MSA_ERR_WORKSPACE_TOO_SMALL;
+  // the CTAs read the inputs while others write: what is written overlaps nothing else
+  const struct {
+    const int32_t* p;
+    size_t n;
+  } words[] = {{free_count_out, 1}, {seq_lens, (size_t)num_seqs}, {token_offsets, (size_t)num_seqs + 1},
+               {slot_mapping, (size_t)max_tokens}, {positions, (size_t)max_tokens},
+               {block_table, (size_t)num_seqs * max_blocks_per_seq}, {free_blocks, (size_t)free_capacity},
+               {static_cast<const int32_t*>(workspace), sizeof(DeviceStatus) / 4},
+               {free_count, 1}, {cached_lens, (size_t)num_seqs}, {new_lens, (size_t)num_seqs}};
+  for (int i = 0; i < 8; ++i)  // written: the first eight
+    for (int j = i + 1; j < 11; ++j)
+      if (words[i].n > 0 && words[j].n > 0 && words[i].p < words[j].p + words[j].n && words[j].p < words[i].p + words[i].n)
+        return MSA_ERR_INVALID_ARGUMENT;
   TablesParams p;
   p.num_seqs = num_seqs;
   p.num_blocks = num_blocks;

@@ -387,9 +387,9 @@ msa_status_t msa_rope_insert(const msa_cache_t* cache, const msa_rope_t* rope, i
  *   slot_mapping, positions  [max_tokens] for new token i of request s, at
  *                  token_offsets[s] + i: its slot and its position cached + i;
  *                  -1 and 0 behind the last token
- *   free_count_out the stack's new size.  Must not be free_count (the call reads
- *                  its inputs while it writes); seq_lens and token_offsets must not
- *                  overlap the input lengths either.
+ *   free_count_out the stack's new size
+ * The call reads its inputs while it writes: no array that it writes may overlap
+ * another one or an input (MSA_ERR_INVALID_ARGUMENT).
  * A request whose blocks are not there, or whose tokens end beyond max_tokens,
  * is refused (and so is every later one that wants tokens behind it): its length
  * stays cached_lens[s], its slots are -1, it takes no block, and the device fault

@@ -55,3 +55,18 @@ def test_misaligned_words_of_the_tables(lib, name):  # noqa: F811
     for off in (1, 2, 3):
         assert _tables(lib, **{name: 1 << 20 | off}) == 1
         assert _tables(lib, ws=ctypes.c_void_p(4096 + off)) == 1
+
+
+SIZES = dict(zip(ARRAYS, (4, 4, 40, 100, 1, 1, 4, 5, 50, 50)))  # words
+INPUTS = ("cached", "new", "count")
+
+
+@pytest.mark.parametrize("a", [n for n in ARRAYS if n not in INPUTS])
+@pytest.mark.parametrize("b", ARRAYS)
+def test_what_the_tables_write_overlaps_nothing(lib, a, b):  # noqa: F811
+    if a == b:
+        return
+    at = 1 << 20
+    for off in {0, SIZES[b] - 1, 1 - SIZES[a]}:  # the same place, the last word, the first word
+        assert _tables(lib, **{b: at, a: at + 4 * off}) == 1, off
+    assert _tables(lib, **{a: 4096 + 4}) == 1  # the workspace's status word is written too
