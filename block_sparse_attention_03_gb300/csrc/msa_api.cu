@@ -607,7 +607,8 @@ msa_status_t run_dense(const msa_cache_t* c, const msa_batch_t* b, const msa_con
   // A small cache stays in the 129 MB L2 by itself; a larger one is a stream that would push the
   // partials and the next kernels' code out, so its lines are the first to go.  Four BF16
   // sequences, default and so: 16 MB 12.6 and 14.5 us, 32 MB 16.6 and 16.5, 64 MB 22.7 and 21.7, 128 MB
-  // 32.9 and 31.4 (with a cold L2 41.5 and 37.0).  The table's width bounds what the device holds.
+  // 32.9 and 31.4 (with a cold L2 41.5 and 37.0).  The host knows no lengths: the table's width bounds
+  // them, so a small cache under a wide table counts as a large one.
   const double row = fmt == FMT_BF16 ? 512. : fmt == FMT_FP8 ? 264. : 144.;
   p.stream = (double)p.S * p.max_nb * kBlock * G * row > 32e6;
   p.info = at<int2>(ws, pl.off_info);

@@ -67,7 +67,12 @@
 // us (52%); 32 columns (8 new tokens), BF16 8 x 64K 182 us (87%), FP8 130 us (63%),
 // NVFP4 8 x 128K 226 us (40%; tensor pipe 43%, issue slots 40%, two warps a scheduler
 // waiting for each other's results); 61 ragged BF16 sequences of 48 columns 86 us
-// (48%; tensor pipe 50%); one sequence of 4K tokens 9.1 us.
+// (48%; tensor pipe 50%); one sequence of 4K tokens 9.1 us.  Products rounded to E4M3: 4
+// columns 229 us, 16 columns 107, 32 columns 273.
+//
+// Registers are what the wide instances lack: with 24 columns and more each of them spills
+// (168 to 316 bytes of stores a thread, a stack of 80 to 104), NVFP4 with 8 and 16 columns
+// too (52 and 96), the others not (FP8 with 16: 8).
 //
 // A masked key's logit is replaced, not multiplied; in units that hold masked
 // keys V is masked in registers too, so NaN or infinity in rows past the end of a

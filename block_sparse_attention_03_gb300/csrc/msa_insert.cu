@@ -2,8 +2,9 @@
 // caches -- the step just before the path (vLLM Day-0 blog, section "QKV GEMM
 // + norm + RoPE + KV 插入融合": K, V and the index key are quantized and written
 // straight into their caches; "[M3] Enable FP8 sparse GQA", items 1 and 4: FP8
-// values stored through the slot mapping).  The projections, norms and RoPE
-// that precede it need weights and are not part of this library.
+// values stored through the slot mapping).  The projections that precede it need
+// weights and are not part of this library; the per-head norm and the rotary positions
+// come with an insert of their own (msa_rope.cu), which keeps to the rules below.
 //
 // One warp per token, its rows of 128 elements (K heads, V heads, index key)
 // loaded together, four elements a lane: an 8-byte load of the bf16 row

@@ -12,15 +12,19 @@
 // format by msa_cache_insert's rules.
 //
 // The angle's fraction of a turn is the top half of p x turns_i mod 2^64
-// (turns_i: turns a position x 2^64), exact for any 32-bit position to 2^-32 of
-// a turn, with no table of cosines to read and no largest position.
+// (turns_i: turns a position x 2^64), with no table of cosines to read and no largest
+// position.  The product is exact for any 32-bit position; the fraction is then
+// rounded to fp32 (2^-25 of half a turn), and turns_i, made from a double, is off by
+// 2^-56 of a turn at most (2^-24 of half a turn at the farthest position).
 //
-// Bound: HBM (a token's rows are read once and written once), with the issue
-// slots close behind, so instructions per element are what counts: 257 for the 16
-// elements a lane has of four rows, 57 to 66% of the slots with the 24 warps an SM
-// that 80 registers allow.  Measured (one GPU, launches back to back, of 6,779
-// GB/s): 8,192 tokens into FP8 29.5 us (56%), 16,384 into BF16 51.5 us (70%), NVFP4
-// 55.9 us (57%), adjacent pairs 56.7 and 58.0 us, 24,571 into NVFP4 with three axes
+// Bound: latency.  A token's rows are read once and written once, but neither the
+// DRAM (33 to 38% of its peak cycles) nor the issue slots (59 to 66%: 257 instructions for
+// the 16 elements a lane has of four rows) are full: the 24 warps an SM that 80
+// registers allow have one quad each on its way, 24 KB an SM where the copy rate at some 800 ns
+// needs 36, and wait for shuffles and shared memory in between.  (80 registers
+// spill: up to 48 bytes a thread for halves, none for adjacent pairs.)  Measured (one GPU, launches back to back, of 6,779
+// GB/s): 8,192 tokens into FP8 29.6 us (56%), 16,384 into BF16 51.6 us (70%), NVFP4
+// 56.4 us (56%), adjacent pairs 55.9 and 58.5 us, 24,571 into NVFP4 with three axes
 // and e4m3 queries 78 us (50%), 32 tokens 4.4 us.  A quarter of
 // a warp takes a row, 16 elements a lane, chosen so that both elements of a pair
 // are in one lane (eight at i and eight at i + rotary_dim / 2; no exchange between
