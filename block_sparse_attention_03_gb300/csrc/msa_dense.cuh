@@ -55,16 +55,19 @@
 // FP8's P enters with V's scale in it, and scales may be of any size, those of
 // keys that a row does not see or that weigh nothing among them.  So every column
 // has a factor fe of its own that puts the largest p x vscale it has met (decayed
-// with m, looked at where m or the bound below moves) at 4: 2^-16 of that product
-// before f16 loses bits, off by 2^-27 of it below.  A step whose scales could
-// pass 2^15 (vscale above 2^5 times that product) has its products looked at first.  O is
-// rescaled by old over new product, never above 1, so that it cannot overflow.
+// with m, looked at where m moves) at 4: 2^-16 of that product before f16 loses bits,
+// off by 2^-27 of it below.  Where a step's scales could take a product past 2^15
+// (vscale above 2^5 times that largest one) the products themselves are looked at, and only if
+// one does the factor changes.  O is rescaled by old over new product, never above 1,
+// so that it cannot overflow.  Scales that vary: 32 columns 129 us with factors of e^0.5
+// (one standard deviation), 134 with e^1, 139 with e^2 (182 and 189 us if every such step
+// rescaled).
 //
 // Measured (one GPU, launches back to back; shares of the measured copy rate,
 // 6,779 GB/s): 4 columns, FP8 32 x 16K-32K tokens 131 us (94%), 4 x 512K 318 us
 // (103%), BF16 32 x 16K-32K 237 us (101%), NVFP4 32 x 16K-64K 173 us (65%: the
 // dequantization's issue slots); 16 columns, FP8 16 x 32K 95 us (86%), NVFP4 8 x 64K 86
-// us (52%); 32 columns (8 new tokens), BF16 8 x 64K 182 us (87%), FP8 130 us (63%),
+// us (52%); 32 columns (8 new tokens), BF16 8 x 64K 182 us (87%), FP8 129 us (63%),
 // NVFP4 8 x 128K 226 us (40%; tensor pipe 43%, issue slots 40%, two warps a scheduler
 // waiting for each other's results); 61 ragged BF16 sequences of 48 columns 86 us
 // (48%; tensor pipe 50%); one sequence of 4K tokens 9.1 us.  Products rounded to E4M3: 4
@@ -72,7 +75,7 @@
 //
 // Registers are what the wide instances lack: with 24 columns and more each of them spills
 // (168 to 316 bytes of stores a thread, a stack of 80 to 104), NVFP4 with 8 and 16 columns
-// too (52 and 96), the others not (FP8 with 16: 8).
+// too (52 and 96), the others not (FP8: 8).
 //
 // A masked key's logit is replaced, not multiplied; in units that hold masked
 // keys V is masked in registers too, so NaN or infinity in rows past the end of a
@@ -90,6 +93,7 @@ constexpr int kDenseWpg = 4;             // consumer warps of a team
 constexpr int kDenseChains = 4;
 constexpr float kDensePShift = 7.f;      // log2 of the scale of P (NVFP4)
 constexpr float kDenseTop = 4.f;         // FP8: P x vscale of a column's largest product so far
+constexpr float kDenseLeast = 6.1e-36f;  // ... which counts as 2^-117 at least: 2^8 x fe stays finite
 constexpr float kDenseLazy = 8.f;        // a logit (log2) above the reference by this moves it
 constexpr float kDenseNone = -3.0e38f;   // FP8: the reference before a row's first key
 
@@ -876,8 +880,8 @@ __device__ void consumer(const DenseParams& p, const DenseTeam& tm, int bar, int
     }
 
     // row state: the reference m_run (log2 domain), what is subtracted, and the raw logit that
-    // moves it.  (FP8 subtracts m_run itself: four registers fewer where they spill, 32 columns
-    // 130.2 us for 132.5.)
+    // moves it.  (FP8 subtracts m_run itself: four registers fewer where they spill, 2% with
+    // 32 columns.)
     constexpr bool SAME = FMT == FMT_FP8;
     float m_run[NN], msub[NN], ylim[NN], colf[NN];
     float2 l_run[NN];
@@ -951,6 +955,37 @@ __device__ void consumer(const DenseParams& p, const DenseTeam& tm, int bar, int
             for (int t = 1; t < KC / 8; ++t) mx[n] = max3(mx[n], y[t][n].x, y[t][n].y);
             over |= mx[n] > ylim[n];
           }
+          bool moved = __any_sync(0xffffffffu, over);
+          if (moved) {
+            // the row's new reference
+#pragma unroll
+            for (int n = 0; n < NN; ++n) {
+              mx[n] = fmaxf(mx[n], __shfl_xor_sync(0xffffffffu, mx[n], 1));
+              mx[n] = fmaxf(mx[n], __shfl_xor_sync(0xffffffffu, mx[n], 2));
+              const float mnew = fmaxf(m_run[n], mx[n] * colf[n]);
+              const float ref = !SAME && mnew == -INFINITY ? 0.f : mnew;
+              const float alpha = ex2(m_run[n] - ref);  // the first time 0 x 0
+              m_run[n] = mnew;
+              msub[n] = ref - SHIFT;
+              ylim[n] = (mnew + kDenseLazy) / colf[n];
+              l_run[n].x *= alpha;
+              l_run[n].y *= alpha;
+              if constexpr (FMT == FMT_FP8) {
+                fe[n] = fe[n] > 0.f ? fe[n] * __frcp_rn(alpha) : 0.f;  // O itself follows below
+              } else {
+                // the accumulators hold the columns 2j, 2j + 1
+                const float w0 = __shfl_sync(0xffffffffu, alpha, 8 * j);
+                const float w1 = __shfl_sync(0xffffffffu, alpha, 8 * j + 4);
+#pragma unroll
+                for (int t = 0; t < 8; ++t) {
+                  o[t][n][0] *= w0;
+                  o[t][n][1] *= w1;
+                  o[t][n][2] *= w0;
+                  o[t][n][3] *= w1;
+                }
+              }
+            }
+          }
           // ---- FP8: V's scales; does P x vscale x fe keep to f16's range?
           float2 vs[KC / 8];
           if constexpr (FMT == FMT_FP8) {
@@ -964,50 +999,54 @@ __device__ void consumer(const DenseParams& p, const DenseTeam& tm, int bar, int
               }
               vm = max3(vm, fabsf(vs[t].x), fabsf(vs[t].y));
             }
-            over |= vm > vlim;
-          }
-          if (__any_sync(0xffffffffu, over)) {
-            // the row's new reference and, for FP8, the column's largest product
-            if constexpr (FMT == FMT_FP8) vlim = 3.3e35f;  // 2^118: 2^8 x vscale stays finite
 #pragma unroll
-            for (int n = 0; n < NN; ++n) {
-              mx[n] = fmaxf(mx[n], __shfl_xor_sync(0xffffffffu, mx[n], 1));
-              mx[n] = fmaxf(mx[n], __shfl_xor_sync(0xffffffffu, mx[n], 2));
-              const float mnew = fmaxf(m_run[n], mx[n] * colf[n]);
-              const float ref = !SAME && mnew == -INFINITY ? 0.f : mnew;
-              const float alpha = ex2(m_run[n] - ref);  // the first time 0 x 0
-              m_run[n] = mnew;
-              msub[n] = ref - SHIFT;
-              ylim[n] = (mnew + kDenseLazy) / colf[n];
-              l_run[n].x *= alpha;
-              l_run[n].y *= alpha;
-              float w = alpha;  // of O
-              if constexpr (FMT == FMT_FP8) {
-                float top = 0.f;
+            for (int t = 0; t < KC / 8; ++t)
+#pragma unroll
+              for (int n = 0; n < NN; ++n) {
+                const float2 x = fma2(y[t][n], make_float2(colf[n], colf[n]), make_float2(-m_run[n], -m_run[n]));
+                y[t][n] = make_float2(ex2(x.x), ex2(x.y));  // the weights
+              }
+            if (moved || __any_sync(0xffffffffu, vm > vlim)) {
+              // the products themselves (times 2^-10, so that they are finite): few of the large
+              // scales meet a large weight
+              float top[NN];
+              bool grow = moved;
+#pragma unroll
+              for (int n = 0; n < NN; ++n) {
+                top[n] = 0.f;
 #pragma unroll
                 for (int t = 0; t < KC / 8; ++t) {
-                  const float2 x = fma2(y[t][n], make_float2(colf[n], colf[n]), make_float2(-(SAME ? m_run : msub)[n], -(SAME ? m_run : msub)[n]));
-                  const float a = fabsf(ex2(x.x) * vs[t].x), b = fabsf(ex2(x.y) * vs[t].y);
-                  top = max3(top, a < INFINITY ? a : 0.f, b < INFINITY ? b : 0.f);
+                  const float2 a = mul2(y[t][n], mul2(vs[t], make_float2(0x1p-10f, 0x1p-10f)));
+                  top[n] = max3(top[n], fabsf(a.x) < INFINITY ? fabsf(a.x) : 0.f, fabsf(a.y) < INFINITY ? fabsf(a.y) : 0.f);
                 }
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                const float kept = fe[n] > 0.f ? alpha * (kDenseTop * __frcp_rn(fe[n])) : 0.f;  // the former one
-                const float most = fminf(fmaxf(fmaxf(kept, top), 3.0e-36f), 3.0e38f);
-                const float inv = __frcp_rn(most);
-                w = kept == most ? 1.f : kept * inv;  // never above 1
-                if (w != 1.f || alpha != 1.f) fe[n] = fmaxf(kept, top) > 0.f ? kDenseTop * inv : 0.f;
-                vlim = fminf(vlim, fe[n] > 0.f ? 128.f * __frcp_rn(fe[n]) : -1.f);  // a weight is 2^8 at most
+                grow |= fe[n] > 0.f ? top[n] * fe[n] > 32.f : top[n] > 0.f;
               }
-              // the accumulators hold the columns 2j, 2j + 1
-              const float w0 = __shfl_sync(0xffffffffu, w, 8 * j);
-              const float w1 = __shfl_sync(0xffffffffu, w, 8 * j + 4);
+              if (__any_sync(0xffffffffu, grow)) {
+                vlim = INFINITY;
 #pragma unroll
-              for (int t = 0; t < 8; ++t) {
-                o[t][n][0] *= w0;
-                o[t][n][1] *= w1;
-                o[t][n][2] *= w0;
-                o[t][n][3] *= w1;
+                for (int n = 0; n < NN; ++n) {
+                  top[n] = fmaxf(top[n], __shfl_xor_sync(0xffffffffu, top[n], 1));
+                  top[n] = fmaxf(top[n], __shfl_xor_sync(0xffffffffu, top[n], 2));
+                  const float kept = fe[n] > 0.f ? kDenseTop * __frcp_rn(fe[n]) : 0.f;  // the former one
+                  const float most = fmaxf(kept, 1024.f * top[n]);
+                  float w = 1.f;  // of O, never above 1
+                  if (!(kept == most && kept >= kDenseLeast)) {
+                    const float inv = __frcp_rn(fminf(fmaxf(most, kDenseLeast), 3.0e38f));
+                    w = kept * inv;
+                    fe[n] = most > 0.f ? kDenseTop * inv : 0.f;
+                  }
+                  vlim = fminf(vlim, fe[n] > 0.f ? 128.f * __frcp_rn(fe[n]) : -1.f);  // a weight is 2^8 at most
+                  // the accumulators hold the columns 2j, 2j + 1
+                  const float w0 = __shfl_sync(0xffffffffu, w, 8 * j);
+                  const float w1 = __shfl_sync(0xffffffffu, w, 8 * j + 4);
+#pragma unroll
+                  for (int t = 0; t < 8; ++t) {
+                    o[t][n][0] *= w0;
+                    o[t][n][1] *= w1;
+                    o[t][n][2] *= w0;
+                    o[t][n][3] *= w1;
+                  }
+                }
               }
             }
           }
@@ -1017,11 +1056,14 @@ __device__ void consumer(const DenseParams& p, const DenseTeam& tm, int bar, int
           for (int t = 0; t < KC / 8; ++t) {
 #pragma unroll
             for (int n = 0; n < NN; ++n) {
-              const float2 x = fma2(y[t][n], make_float2(colf[n], colf[n]), make_float2(-(SAME ? m_run : msub)[n], -(SAME ? m_run : msub)[n]));
-              float2 q = make_float2(ex2(x.x), ex2(x.y));
+              float2 q = y[t][n];
+              if constexpr (FMT != FMT_FP8) {
+                const float2 x = fma2(q, make_float2(colf[n], colf[n]), make_float2(-msub[n], -msub[n]));
+                q = make_float2(ex2(x.x), ex2(x.y));
+              }
               l_run[n] = add2(l_run[n], q);
               if constexpr (FMT == FMT_FP8) {
-                const float2 v = mul2(mul2(q, vs[t]), make_float2(fe[n], fe[n]));
+                const float2 v = mul2(mul2(q, make_float2(fe[n], fe[n])), vs[t]);
                 if (masked) {  // a masked weight stays 0 beside a scale that is not finite
                   q.x = q.x == 0.f ? 0.f : v.x;
                   q.y = q.y == 0.f ? 0.f : v.y;

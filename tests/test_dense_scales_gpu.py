@@ -139,11 +139,11 @@ def test_scales_of_every_size():
     check_dense(c, *run_dense(c), _reference(c))
 
 
-@pytest.mark.parametrize("value", [2.0 ** -120, 7.0e35])
+@pytest.mark.parametrize("value", [2.0 ** -120, 7.0e35, 3.0e38])
 def test_a_cache_of_very_small_or_very_large_values(value):
     # 7e35 x 448 is close to bf16's largest number: sums of weighted rows stay below fp32's only with codes of 1
     c = paged_case([300, 17], "fp8", "fp8", Q=1, Hq=4, H=2, seed=36)
-    code = 0x38 if value > 1 else None
+    code = None if value < 1 else 0x38 if value < 1e38 else 0x01  # 1 and 2^-9
     for s, T in enumerate(c["lens"]):
         _set_scales(c, s, range(T), value=value, codes=code)
     check_dense(c, *run_dense(c), _reference(c))
