@@ -451,7 +451,8 @@ def msa_dense_attend(cache, batch, cfg, q: Query, num_q_heads: int, out, lse, wo
             or lens.get_device() != dev or table.get_device() != dev or data.get_device() != dev or out.get_device() != dev
             or workspace.get_device() != dev):
         raise MsaError(1, "msa_dense_attend")
-    at = _DENSE.pack(*_cache_values(cache, False, dev, "msa_dense_attend"), shape[0], batch.q_per_seq, shape[1], lens.data_ptr(), table.data_ptr(),
+    at = _DENSE.pack(*_cache_values(cache, False, dev, "msa_dense_attend"),
+                     shape[0], batch.q_per_seq, shape[1], lens.data_ptr(), table.data_ptr(),
                      cfg.topk, cfg.init_blocks, cfg.local_blocks, cfg.index_scale, cfg.sm_scale,
                      SCORE_TYPES.get(cfg.score_type, -1), PREFILL_SELECT.get(cfg.prefill_select, -1),
                      data.data_ptr(), DTYPES[q.dtype], q.scale)
@@ -501,7 +502,8 @@ def msa_rope_insert(cache, rope: MsaRopeT, positions, slot_mapping, q, q_out: Qu
             if x is not None and (x.numel() != 128 or x.dtype is not _bf16 or not x.is_contiguous() or x.get_device() != dev):
                 raise MsaError(1, where)
         w = (_p(norm.q), _p(norm.k), _p(norm.index_q), _p(norm.index_k), norm.eps, norm.offset)
-    at = _ROPE.pack(*_cache_values(cache, index_k is not None, dev, where), *_rows(q, (T, hq, 128), where, dev), qd.data_ptr(), DTYPES[q_out.dtype], q_out.scale,
+    at = _ROPE.pack(*_cache_values(cache, index_k is not None, dev, where),
+                    *_rows(q, (T, hq, 128), where, dev), qd.data_ptr(), DTYPES[q_out.dtype], q_out.scale,
                     *(none if index_q is None else _rows(index_q, kv, where, dev)), *iqo, *_rows(k, kv, where, dev),
                     *_rows(v, kv, where, dev), *(none if index_k is None else
                                              _rows(index_k, (T, 128) if index_k.dim() == 2 else (T, 1, 128), where, dev)), *w)

@@ -955,7 +955,7 @@ __device__ void consumer(const DenseParams& p, const DenseTeam& tm, int bar, int
             for (int t = 1; t < KC / 8; ++t) mx[n] = max3(mx[n], y[t][n].x, y[t][n].y);
             over |= mx[n] > ylim[n];
           }
-          bool moved = __any_sync(0xffffffffu, over);
+          const bool moved = __any_sync(0xffffffffu, over);
           if (moved) {
             // the row's new reference
 #pragma unroll
