@@ -24,13 +24,15 @@ MSA_OK = 0
 STATUS_NAMES = {0: "MSA_OK", 1: "MSA_ERR_INVALID_ARGUMENT", 2: "MSA_ERR_UNSUPPORTED",
                 3: "MSA_ERR_WORKSPACE_TOO_SMALL", 4: "MSA_ERR_CUDA", 5: "MSA_ERR_DEVICE_FAULT",
                 6: "MSA_ERR_TIMEOUT"}
-DTYPES = {"bf16": 0, "fp8": 1, "nvfp4": 2}
+# the block types: K / V caches only, one byte an element and one scale for a block of 128 tokens and head
+DTYPES = {"bf16": 0, "fp8": 1, "nvfp4": 2, "int8_block": 8, "fp8_block": 9}
 
 # every symbol include/msa.h declares
 EXPORTS = ("msa_workspace_size", "msa_workspace_init", "msa_indexer_score", "msa_topk_blocks",
            "msa_sparse_attend", "msa_decode", "msa_read_device_status", "msa_status_string",
            "msa_dequant_debug", "msa_decode_noalloc", "msa_cache_insert", "msa_dense_workspace_size",
-           "msa_dense_attend", "msa_rope_init", "msa_rope_insert", "msa_build_tables")
+           "msa_dense_attend", "msa_rope_init", "msa_rope_insert", "msa_build_tables",
+           "msa_block_insert", "msa_cache_read")
 
 
 class MsaError(RuntimeError):
@@ -88,6 +90,11 @@ class MsaRowsT(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("stride", ctypes.c_int64)]
 
 
+class MsaSpansT(ctypes.Structure):
+    _fields_ = [("num_seqs", ctypes.c_int32), ("max_blocks_per_seq", ctypes.c_int32), ("first", ctypes.c_void_p),
+                ("end", ctypes.c_void_p), ("token_offsets", ctypes.c_void_p), ("block_table", ctypes.c_void_p)]
+
+
 class MsaQkNormT(ctypes.Structure):
     _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("index_q", ctypes.c_void_p),
                 ("index_k", ctypes.c_void_p), ("eps", ctypes.c_float), ("offset", ctypes.c_float)]
@@ -125,6 +132,7 @@ def lib() -> ctypes.CDLL:
         h.msa_rope_init.argtypes = [P, I, ctypes.c_double, I, P, I]
         h.msa_rope_insert.argtypes = [P, P, I, P, P, I, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P]
         h.msa_build_tables.argtypes = [I, I, P, P, I, P, I, P, P, P, P, P, I, P, P, P, ctypes.c_size_t, P]
+        h.msa_block_insert.argtypes = h.msa_cache_read.argtypes = [P, P, I, P, P, P, ctypes.c_size_t, P]
         for name in EXPORTS:
             if name not in ("msa_workspace_size", "msa_status_string", "msa_dense_workspace_size"):
                 getattr(h, name).restype = ctypes.c_int
@@ -234,6 +242,16 @@ class Query:
 
 
 @dataclasses.dataclass
+class Spans:
+    """Consecutive tokens of each sequence: positions first[s] .. end[s] - 1 are rows token_offsets[s], ... of a
+    call's row tensors.  Beside msa_build_tables: its cached_lens, seq_lens, token_offsets and block_table."""
+    first: object          # int32 [S] on the device
+    end: object            # int32 [S]
+    token_offsets: object  # int32 [S] or longer
+    block_table: object    # int32 [S][max_blocks]
+
+
+@dataclasses.dataclass
 class QkNorm:
     """bf16 [128] weights of the per-head RMS norm before the rotation (None: that kind is not normed)."""
     q: object = None
@@ -255,7 +273,7 @@ def _ref(x):
 # buffer in one go (a ctypes object for each costs several microseconds a
 # call, as long as the kernels of a decode step).  The library copies what it needs before it returns.
 _tls = threading.local()
-_CACHE, _BATCH, _CONFIG, _QUERY, _ROWS, _NORM = "7i9P3fi", "3i2P", "3i2f2i", "Pif", "Pq", "4P2f"
+_CACHE, _BATCH, _CONFIG, _QUERY, _ROWS, _NORM, _SPANS = "7i9P3fi", "3i2P", "3i2f2i", "Pif", "Pq", "4P2f", "2i4P"
 
 
 class _Layout:
@@ -290,12 +308,16 @@ def _checked(c: PagedCache, index: bool, dev: int, where: str) -> None:
     codes = (torch.uint8, torch.int8, torch.float8_e4m3fn)
     wanted = [("k", c.kv_dtype, c.num_kv_heads), ("v", c.kv_dtype, c.num_kv_heads)] + [("idx", c.index_dtype, 1)] * index
     for name, kind, heads in wanted:
-        rows = c.num_blocks * heads * 128
-        parts = {"bf16": [(name, (torch.bfloat16,), 128)], "fp8": [(name, codes, 128), (name + "_scale", (torch.float32,), 1)],
-                 "nvfp4": [(name, (torch.uint8, torch.int8), 64), (name + "_sf", codes, 8)]}.get(kind, [])
-        for field, types, width in parts:
+        blocks = c.num_blocks * heads
+        rows = blocks * 128
+        scale = (name + "_scale", (torch.float32,))
+        parts = {"bf16": [(name, (torch.bfloat16,), rows * 128)], "fp8": [(name, codes, rows * 128), (*scale, rows)],
+                 "nvfp4": [(name, (torch.uint8, torch.int8), rows * 64), (name + "_sf", codes, rows * 8)],
+                 "int8_block": [(name, (torch.int8, torch.uint8), rows * 128), (*scale, blocks)],
+                 "fp8_block": [(name, codes, rows * 128), (*scale, blocks)]}.get(kind, [])
+        for field, types, least in parts:
             t = getattr(c, field)
-            if t is not None and (t.dtype not in types or t.numel() < rows * width or not t.is_contiguous() or t.get_device() != dev):
+            if t is not None and (t.dtype not in types or t.numel() < least or not t.is_contiguous() or t.get_device() != dev):
                 raise MsaError(1, where)
     c.__dict__["_seen"] = (dev, index or (c._seen[:1] == (dev,) and c._seen[1]))
 
@@ -310,6 +332,7 @@ def _cache_values(c: PagedCache, index: bool, dev: int, where: str):
 
 
 _DENSE = _Layout(_CACHE, _BATCH, _CONFIG, _QUERY)
+_SPAN = _Layout(_CACHE, _SPANS, _ROWS, _ROWS)
 _ROPE = _Layout(_CACHE, _ROWS, _QUERY, _ROWS, _QUERY, _ROWS, _ROWS, _ROWS, _NORM)
 
 
@@ -371,8 +394,15 @@ def msa_topk_blocks(batch, cfg, num_groups: int, pooled, topk_idx, topk_score, w
                                  _stream(stream)), "msa_topk_blocks")
 
 
+def _check_block_cache(cache, where: str) -> None:
+    """The tensors of a cache with block scales (whose scales are not of the shape of the other formats')."""
+    if cache.kv_dtype in ("int8_block", "fp8_block") and cache._seen[:1] != (cache.k.get_device(),):
+        _checked(cache, False, cache.k.get_device(), where)
+
+
 def msa_sparse_attend(cache, batch, cfg, q: Query, num_q_heads: int, topk_idx, out, lse, workspace,
                       stream=None) -> None:
+    _check_block_cache(cache, "msa_sparse_attend")
     c, b, f, qq = cache.struct(), batch.struct(), cfg.struct(), q.struct()
     _check(lib().msa_sparse_attend(_ref(c), _ref(b), _ref(f), _ref(qq), num_q_heads, _ptr(topk_idx), _ptr(out),
                                    _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(),
@@ -381,6 +411,7 @@ def msa_sparse_attend(cache, batch, cfg, q: Query, num_q_heads: int, topk_idx, o
 
 def msa_decode(cache, batch, cfg, index_q: Query, q: Query, num_q_heads: int, topk_idx, out, lse, workspace,
                stream=None) -> None:
+    _check_block_cache(cache, "msa_decode")
     c, b, f, iq, qq = cache.struct(), batch.struct(), cfg.struct(), index_q.struct(), q.struct()
     _check(lib().msa_decode(_ref(c), _ref(b), _ref(f), _ref(iq), _ref(qq), num_q_heads, _ptr(topk_idx),
                             _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(),
@@ -412,6 +443,7 @@ def msa_decode_noalloc(cache, batch, cfg, index_q: Query, q: Query, num_q_heads:
     workspace exceeds the scratch size are rejected; calls must not overlap on
     the GPU because they share that scratch.  status_out: optional device
     int32[2] that receives the call's device status flags."""
+    _check_block_cache(cache, "msa_decode_noalloc")
     c, b, f, iq, qq = cache.struct(), batch.struct(), cfg.struct(), index_q.struct(), q.struct()
     _check(lib().msa_decode_noalloc(_ref(c), _ref(b), _ref(f), _ref(iq), _ref(qq), num_q_heads, _ptr(topk_idx),
                                     _ptr(out), _ptr(lse), _ptr(status_out), _stream(stream)),
@@ -420,11 +452,50 @@ def msa_decode_noalloc(cache, batch, cfg, index_q: Query, q: Query, num_q_heads:
 
 def msa_cache_insert(cache, slot_mapping, k, v, index_k, workspace, stream=None) -> None:
     """Quantize and write new tokens' K, V (bf16 [T][H][128]) and index keys (bf16
-    [T][128], or None) into the paged caches at slot_mapping (int32 [T])."""
+    [T][128], or None) into the paged caches at slot_mapping (int32 [T]).  A cache with block scales: k and v are None."""
     c = cache.struct()
     _check(lib().msa_cache_insert(_ref(c), int(slot_mapping.numel()), _ptr(slot_mapping), _ptr(k), _ptr(v),
                                   _ptr(index_k), _ptr(workspace), workspace.numel() * workspace.element_size(),
                                   _stream(stream)), "msa_cache_insert")
+
+
+def _span_call(call, where: str, cache, spans, k, v, workspace, stream):
+    """Pack and make one of the two calls over spans; k, v: bf16 [T][num_kv_heads][128], any token stride."""
+    if _int32 is None:
+        _torch_names()
+    first, end, offsets, table = spans.first, spans.end, spans.token_offsets, spans.block_table
+    S, shape, dev = first.numel(), table.shape, cache.k.get_device()
+    any_rows = v if k is None else k
+    if (dev < 0 or dev != _device() or len(shape) != 2 or shape[0] != S or end.numel() != S or offsets.numel() < S
+            or first.dtype is not _int32 or end.dtype is not _int32 or offsets.dtype is not _int32 or table.dtype is not _int32
+            or not first.is_contiguous() or not end.is_contiguous() or not offsets.is_contiguous() or not table.is_contiguous()
+            or first.get_device() != dev or end.get_device() != dev or offsets.get_device() != dev or table.get_device() != dev
+            or workspace.get_device() != dev):
+        raise MsaError(1, where)
+    T = 0 if any_rows is None else any_rows.shape[0]
+    kv, none = (T, cache.num_kv_heads, 128), (0, 0)
+    at = _SPAN.pack(*_cache_values(cache, False, dev, where), S, shape[1], first.data_ptr(), end.data_ptr(), offsets.data_ptr(),
+                    table.data_ptr(), *(none if k is None else _rows(k, kv, where, dev)),
+                    *(none if v is None else _rows(v, kv, where, dev)))
+    o = _SPAN.offsets
+    _check(call(at, at + o[1], T, 0 if k is None else at + o[2], 0 if v is None else at + o[3], workspace.data_ptr(),
+                _nbytes(workspace), _stream(stream, dev)), where)
+
+
+def msa_block_insert(cache, spans: Spans, k, v, workspace, stream=None) -> None:
+    """K and V of the spans' tokens (bf16 [T][H][128], any token stride) into a cache with block scales: a block's
+    scale follows its largest element, by powers of two once it holds tokens (include/msa.h)."""
+    if k is None or v is None:
+        raise MsaError(1, "msa_block_insert")
+    _span_call(lib().msa_block_insert, "msa_block_insert", cache, spans, k, v, workspace, stream)
+
+
+def msa_cache_read(cache, spans: Spans, k_out, v_out, workspace, stream=None) -> None:
+    """The spans' tokens out of a cache of any format into bf16 rows k_out and v_out ([T][H][128], any token stride;
+    one of them may be None).  Rows of no span are left as they were."""
+    if k_out is None and v_out is None:
+        raise MsaError(1, "msa_cache_read")
+    _span_call(lib().msa_cache_read, "msa_cache_read", cache, spans, k_out, v_out, workspace, stream)
 
 
 def msa_dense_workspace_size(cache: PagedCache, batch: Batch, num_q_heads: int) -> int:
@@ -475,7 +546,7 @@ def msa_rope_insert(cache, rope: MsaRopeT, positions, slot_mapping, q, q_out: Qu
                     k, v, index_k, norm: Optional[QkNorm], workspace, stream=None) -> None:
     """Norm and rotate q, index q, k and index k (bf16 [T][H][128], any token stride), write the
     queries to q_out / index_q_out (dense) and k, v, index k into the paged caches at slot_mapping (int32 [T]).
-    positions: int32 [axes][T], or [T] for one axis."""
+    positions: int32 [axes][T], or [T] for one axis.  A cache with block scales: k and v are None (msa_block_insert)."""
     if _int32 is None:
         _torch_names()
     where = "msa_rope_insert"
@@ -504,13 +575,13 @@ def msa_rope_insert(cache, rope: MsaRopeT, positions, slot_mapping, q, q_out: Qu
         w = (_p(norm.q), _p(norm.k), _p(norm.index_q), _p(norm.index_k), norm.eps, norm.offset)
     at = _ROPE.pack(*_cache_values(cache, index_k is not None, dev, where),
                     *_rows(q, (T, hq, 128), where, dev), qd.data_ptr(), DTYPES[q_out.dtype], q_out.scale,
-                    *(none if index_q is None else _rows(index_q, kv, where, dev)), *iqo, *_rows(k, kv, where, dev),
-                    *_rows(v, kv, where, dev), *(none if index_k is None else
-                                             _rows(index_k, (T, 128) if index_k.dim() == 2 else (T, 1, 128), where, dev)), *w)
+                    *(none if index_q is None else _rows(index_q, kv, where, dev)), *iqo,
+                    *(none if k is None else _rows(k, kv, where, dev)), *(none if v is None else _rows(v, kv, where, dev)),
+                    *(none if index_k is None else _rows(index_k, (T, 128) if index_k.dim() == 2 else (T, 1, 128), where, dev)), *w)
     o = _ROPE.offsets
     _check(lib().msa_rope_insert(at, ctypes.byref(rope), T, positions.data_ptr(), slot_mapping.data_ptr(), hq, at + o[1], at + o[2],
-                                 0 if index_q is None else at + o[3], 0 if index_q_out is None else at + o[4], at + o[5],
-                                 at + o[6], 0 if index_k is None else at + o[7], 0 if norm is None else at + o[8],
+                                 0 if index_q is None else at + o[3], 0 if index_q_out is None else at + o[4],
+                                 0 if k is None else at + o[5], 0 if v is None else at + o[6], 0 if index_k is None else at + o[7], 0 if norm is None else at + o[8],
                                  workspace.data_ptr(), _nbytes(workspace), _stream(stream, dev)), where)
 
 
@@ -541,8 +612,8 @@ def default_config(topk: int = 16, head_dim: int = 128, index_dim: int = 128) ->
     return Config(topk=topk, index_scale=index_dim ** -0.5, sm_scale=head_dim ** -0.5)
 
 
-__all__ = ["PagedCache", "Batch", "Config", "Query", "QkNorm", "MsaError", "lib", "EXPORTS", "default_config",
+__all__ = ["PagedCache", "Batch", "Config", "Query", "Spans", "QkNorm", "MsaError", "lib", "EXPORTS", "default_config",
            "msa_workspace_size", "msa_workspace_init", "msa_indexer_score", "msa_topk_blocks",
            "msa_sparse_attend", "msa_decode", "msa_read_device_status", "msa_status_string",
            "msa_dequant_debug", "msa_decode_noalloc", "msa_cache_insert", "msa_dense_workspace_size", "msa_dense_attend",
-           "msa_rope_init", "msa_rope_insert", "msa_build_tables", "roofline"]
+           "msa_rope_init", "msa_rope_insert", "msa_build_tables", "msa_block_insert", "msa_cache_read", "roofline"]

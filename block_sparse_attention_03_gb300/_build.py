@@ -15,8 +15,8 @@ LIB = os.path.join(PKG, "libmsa.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["msa_api.cu", "msa_indexer.cu", "msa_pindexer.cu", "msa_topk.cu", "msa_attend.cu", "msa_k2q.cu", "msa_k2q_tc.cu", "msa_dequant.cu",
            "msa_insert.cu", "msa_dense.cu", "msa_dense_bf16.cu", "msa_dense_fp8.cu", "msa_dense_nvfp4.cu",
-           "msa_dense_nvfp4r.cu", "msa_rope.cu",
-           "msa_tables.cu"]
+           "msa_dense_nvfp4r.cu", "msa_dense_int8.cu", "msa_dense_int8_sel.cu", "msa_dense_fp8b.cu", "msa_dense_fp8b_sel.cu",
+           "msa_rope.cu", "msa_span.cu", "msa_tables.cu"]
 
 
 def _nvcc() -> str:

@@ -96,6 +96,17 @@ int fmt_of(msa_dtype_t d) {
   }
 }
 
+// formats of K and V
+int kv_fmt_of(msa_dtype_t d) {
+  switch (d) {
+    case MSA_DTYPE_INT8_BLOCK: return FMT_I8B;
+    case MSA_DTYPE_FP8_BLOCK: return FMT_F8B;
+    default: return fmt_of(d);
+  }
+}
+
+bool by_block(const msa_cache_t* c) { return fmt_by_block(kv_fmt_of(c->kv_dtype)); }
+
 int next_pow2(int x) {
   int p = 1;
   while (p < x) p <<= 1;
@@ -137,10 +148,10 @@ msa_status_t check_cache(const msa_cache_t* c, bool need_index, bool need_kv) {
     if (f == FMT_NVFP4 && (!c->idx_sf || !aligned16(c->idx_sf) || !(c->idx_global > 0.f))) return MSA_ERR_INVALID_ARGUMENT;
   }
   if (need_kv) {
-    const int f = fmt_of(c->kv_dtype);
+    const int f = kv_fmt_of(c->kv_dtype);
     if (f < 0) return MSA_ERR_UNSUPPORTED;
     if (!c->k || !c->v || !aligned16(c->k) || !aligned16(c->v)) return MSA_ERR_INVALID_ARGUMENT;
-    if (f == FMT_FP8 && (!c->k_scale || !c->v_scale || !aligned16(c->k_scale) || !aligned16(c->v_scale)))
+    if ((f == FMT_FP8 || fmt_by_block(f)) && (!c->k_scale || !c->v_scale || !aligned16(c->k_scale) || !aligned16(c->v_scale)))
       return MSA_ERR_INVALID_ARGUMENT;
     if (f == FMT_NVFP4 && (!c->k_sf || !c->v_sf || !aligned16(c->k_sf) || !aligned16(c->v_sf) ||
                            !(c->k_global > 0.f) || !(c->v_global > 0.f)))
@@ -167,6 +178,11 @@ FragGeom geom_for(int key_fmt, bool q_fp8, int cols) {
   return g;
 }
 
+struct DensePlan {
+  int cols = 0, CG = 0, cper = 0, rows = 0;
+  size_t off_info = 0, off_ml = 0, off_o = 0, total = 0;
+};
+
 struct Plan {
   int S = 0, Q = 0, chunks = 1;  // indexer: sequences / query tokens as it sees them (long chunks split)
   int Sa = 0, Qa = 0, chunks_a = 1;  // the same for the attend
@@ -183,6 +199,9 @@ struct Plan {
   // lists and a merge launch instead of the pooled scores and a top-k launch)
   bool pisel = false;
   size_t off_plists = 0;
+  // block scales: the dense attend's kernel over selection lists, its parts behind the others
+  bool blk = false;
+  DensePlan dense;
   size_t off_kcnt = 0, off_koff = 0, off_kcur = 0, off_kitem = 0, off_kent = 0, off_klist = 0, off_kpo = 0,
          off_kpml = 0, off_kq = 0, off_kqf = 0;
 };
@@ -194,6 +213,29 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 bool tc_indexer(const msa_cache_t* c, const msa_batch_t* b) {
   const int G = c->num_kv_heads;
   return fmt_of(c->index_dtype) == FMT_FP8 && b->q_per_seq > 8 && (G == 1 || G == 2 || G == 4 || G == 8);
+}
+
+// The dense attend's kernel for `seqs` sequences of q new tokens; its workspace from byte o on.
+msa_status_t dense_plan_at(const msa_cache_t* c, long seqs, int q, int hq, size_t o, DensePlan& pl) {
+  const int G = c->num_kv_heads;
+  if (hq < G || hq % G != 0) return MSA_ERR_INVALID_ARGUMENT;
+  if (hq / G > 64 || q > 8) return MSA_ERR_UNSUPPORTED;
+  pl.cols = q * (hq / G);
+  pl.CG = (pl.cols + 63) / 64;
+  pl.cper = (pl.cols + pl.CG - 1) / pl.CG;
+  const DenseShape sh = dense_shape(pl.cper);
+  pl.rows = dense_rows(sh.nn, sh.ncg);
+  if (seqs * G * pl.CG >= (1l << 31)) return MSA_ERR_UNSUPPORTED;
+  const size_t ctas = (size_t)sm_count() * dense_teams(kv_fmt_of(c->kv_dtype), sh.nn);  // runs
+  pl.off_info = o; o = align256(o + ctas * sizeof(int2));
+  pl.off_ml = o; o = align256(o + 2 * ctas * pl.rows * sizeof(float2));
+  pl.off_o = o; o = align256(o + 2 * ctas * pl.rows * kDim * sizeof(float));
+  pl.total = o;
+  return MSA_OK;
+}
+
+msa_status_t make_dense_plan(const msa_cache_t* c, const msa_batch_t* b, int hq, DensePlan& pl) {
+  return dense_plan_at(c, b->num_seqs, b->q_per_seq, hq, 256, pl);  // behind the status word
 }
 
 // Plan for the given problem.  iq_fp8 / q_fp8: query dtypes (E4M3 or bf16).
@@ -220,10 +262,18 @@ msa_status_t make_plan(const msa_cache_t* c, const msa_batch_t* b, const msa_con
   const int S = pl.Sa, Qa = pl.Qa;  // the attend's units size the buffers below
   if (hq < G || hq % G != 0) return MSA_ERR_INVALID_ARGUMENT;
   pl.r = hq / G;
-  const int fi = fmt_of(c->index_dtype), fa = fmt_of(c->kv_dtype);
+  const int fi = fmt_of(c->index_dtype), fa = kv_fmt_of(c->kv_dtype);
   pl.gi = geom_for(fi < 0 ? FMT_FP8 : fi, iq_fp8, Q * G);
   pl.ga = geom_for(fa < 0 ? FMT_FP8 : fa, q_fp8, Qa * pl.r);
   if (!tc_indexer(c, b) && (pl.gi.nt > kMaxIndexerNT || pl.gi.nt * pl.gi.sp > 8)) return MSA_ERR_UNSUPPORTED;
+  pl.blk = fmt_by_block(fa);
+  if (pl.blk) {
+    pl.off_pooled = 256;
+    const size_t pooled = (size_t)b->num_seqs * b->q_per_seq * G * b->max_blocks_per_seq * 4;
+    const msa_status_t s = dense_plan_at(c, (long)b->num_seqs * b->q_per_seq, 1, hq, align256(256 + pooled), pl.dense);
+    pl.total = pl.dense.total;
+    return s;
+  }
   if (pl.ga.cols > kMaxAttendCols || pl.ga.nt * pl.ga.sp > 8) return MSA_ERR_UNSUPPORTED;
   pl.cap = Qa * cfg->topk;
   pl.direct = (Qa == 1);
@@ -555,39 +605,20 @@ msa_status_t run_k2q(const msa_cache_t* c, const msa_batch_t* b, const msa_confi
 
 // ---------------------------------------------------------------- the dense attend
 
-struct DensePlan {
-  int cols = 0, CG = 0, cper = 0, rows = 0;
-  size_t off_info = 0, off_ml = 0, off_o = 0, total = 0;
-};
 
-msa_status_t make_dense_plan(const msa_cache_t* c, const msa_batch_t* b, int hq, DensePlan& pl) {
-  const int G = c->num_kv_heads;
-  if (hq < G || hq % G != 0) return MSA_ERR_INVALID_ARGUMENT;
-  if (hq / G > 64 || b->q_per_seq > 8) return MSA_ERR_UNSUPPORTED;
-  pl.cols = b->q_per_seq * (hq / G);
-  pl.CG = (pl.cols + 63) / 64;
-  pl.cper = (pl.cols + pl.CG - 1) / pl.CG;
-  const DenseShape sh = dense_shape(pl.cper);
-  pl.rows = dense_rows(sh.nn, sh.ncg);
-  if ((long)b->num_seqs * G * pl.CG >= (1l << 31)) return MSA_ERR_UNSUPPORTED;
-  const size_t ctas = (size_t)sm_count() * dense_teams(fmt_of(c->kv_dtype), sh.nn);  // runs
-  size_t o = 256;  // the status word
-  pl.off_info = o; o = align256(o + ctas * sizeof(int2));
-  pl.off_ml = o; o = align256(o + 2 * ctas * pl.rows * sizeof(float2));
-  pl.off_o = o; o = align256(o + 2 * ctas * pl.rows * kDim * sizeof(float));
-  pl.total = o;
-  return MSA_OK;
-}
-
+// topk_idx: the sparse attend over these selections (caches with block scales), else null.
 msa_status_t run_dense(const msa_cache_t* c, const msa_batch_t* b, const msa_config_t* cfg, const msa_query_t* q, int hq,
-                       void* out, float* lse, const DensePlan& pl, void* ws, cudaStream_t st) {
-  const int G = c->num_kv_heads, fmt = fmt_of(c->kv_dtype), sms = sm_count();
+                       const int32_t* topk_idx, void* out, float* lse, const DensePlan& pl, void* ws, cudaStream_t st) {
+  const int G = c->num_kv_heads, fmt = kv_fmt_of(c->kv_dtype), sms = sm_count();
   const long rows = (long)c->num_blocks * G * kBlock;
   CUtensorMap tk, tv;
   if (!encode_unit_rows(&tk, c->k, rows, fmt) || !encode_unit_rows(&tv, c->v, rows, fmt)) return MSA_ERR_CUDA;
   DenseParams p;
-  p.S = b->num_seqs;
-  p.Q = b->q_per_seq;
+  p.S = topk_idx ? b->num_seqs * b->q_per_seq : b->num_seqs;
+  p.Q = topk_idx ? 1 : b->q_per_seq;
+  p.topk_idx = topk_idx;
+  p.topk = cfg->topk;
+  p.q_real = b->q_per_seq;
   p.G = G;
   p.r = hq / G;
   p.cols = pl.cols;
@@ -601,16 +632,16 @@ msa_status_t run_dense(const msa_cache_t* c, const msa_batch_t* b, const msa_con
   p.q_fp8 = q->dtype == MSA_DTYPE_FP8_E4M3;
   p.q_scale = p.q_fp8 ? q->scale : 1.f;
   p.col_const = cfg->sm_scale * 1.4426950408889634f * (fmt == FMT_NVFP4 ? c->k_global : 1.f);
-  p.k_sc = static_cast<const uint8_t*>(fmt == FMT_FP8 ? static_cast<const void*>(c->k_scale) : c->k_sf);
-  p.v_sc = static_cast<const uint8_t*>(fmt == FMT_FP8 ? static_cast<const void*>(c->v_scale) : c->v_sf);
+  p.k_sc = static_cast<const uint8_t*>(fmt == FMT_NVFP4 ? c->k_sf : static_cast<const void*>(c->k_scale));
+  p.v_sc = static_cast<const uint8_t*>(fmt == FMT_NVFP4 ? c->v_sf : static_cast<const void*>(c->v_scale));
   p.v_global = c->v_global;
   // A small cache stays in the 129 MB L2 by itself; a larger one is a stream that would push the
   // partials and the next kernels' code out, so its lines are the first to go.  Four BF16
   // sequences, default and so: 16 MB 12.6 and 14.5 us, 32 MB 16.6 and 16.5, 64 MB 22.7 and 21.7, 128 MB
   // 32.9 and 31.4 (with a cold L2 41.5 and 37.0).  The host knows no lengths: the table's width bounds
   // them, so a small cache under a wide table counts as a large one.
-  const double row = fmt == FMT_BF16 ? 512. : fmt == FMT_FP8 ? 264. : 144.;
-  p.stream = (double)p.S * p.max_nb * kBlock * G * row > 32e6;
+  const double row = fmt == FMT_BF16 ? 512. : fmt == FMT_FP8 ? 264. : fmt == FMT_NVFP4 ? 144. : 256.;
+  p.stream = (double)p.S * (topk_idx ? cfg->topk : p.max_nb) * kBlock * G * row > 32e6;
   p.info = at<int2>(ws, pl.off_info);
   p.part_ml = at<float2>(ws, pl.off_ml);
   p.part_o = at<float>(ws, pl.off_o);
@@ -620,10 +651,23 @@ msa_status_t run_dense(const msa_cache_t* c, const msa_batch_t* b, const msa_con
   cudaError_t e;
   if (fmt == FMT_BF16) e = launch_dense_bf16(&tk, &tv, p, sms, st);
   else if (fmt == FMT_FP8) e = launch_dense_fp8(&tk, &tv, p, sms, st);
+  else if (fmt == FMT_I8B) e = topk_idx ? launch_dense_int8_sel(&tk, &tv, p, sms, st) : launch_dense_int8(&tk, &tv, p, sms, st);
+  else if (fmt == FMT_F8B) e = topk_idx ? launch_dense_fp8b_sel(&tk, &tv, p, sms, st) : launch_dense_fp8b(&tk, &tv, p, sms, st);
   else if (c->nvfp4_mode == MSA_NVFP4_E4M3_PRODUCT) e = launch_dense_nvfp4_rounded(&tk, &tv, p, sms, st);
   else e = launch_dense_nvfp4(&tk, &tv, p, sms, st);
   if (e != cudaSuccess) return MSA_ERR_CUDA;
   return cuda_status(launch_dense_combine(p, fmt, sms, st));
+}
+
+// The path's second half over a cache with block scales: the top-k of the pooled scores and the
+// attend over its lists.  (A warp a row for a prompt chunk's many rows, as elsewhere.)
+msa_status_t run_select_dense(const msa_cache_t* c, const msa_batch_t* b, const msa_config_t* cfg, const msa_query_t* q, int hq,
+                              const float* pooled, int32_t* topk_idx, void* out, float* lse, const Plan& pl, void* ws,
+                              cudaStream_t st) {
+  const msa_status_t s = run_topk(b, cfg, c->num_kv_heads, pooled, topk_idx, nullptr, ws, &pl, st, true, false, nullptr,
+                                  b->q_per_seq > 8);
+  if (s != MSA_OK) return s;
+  return run_dense(c, b, cfg, q, hq, topk_idx, out, lse, pl.dense, ws, st);
 }
 
 msa_status_t check_rope(const msa_rope_t* r) {
@@ -638,6 +682,41 @@ msa_status_t check_rope(const msa_rope_t* r) {
 
 // rows of one projection: tokens `stride` elements apart, heads side by side
 bool rows_ok(const msa_rows_t* r) { return r && r->data && aligned16(r->data) && r->stride >= 0 && r->stride % 8 == 0; }
+
+// What the insert and the read of spans share.
+msa_status_t span_params(const msa_cache_t* c, const msa_spans_t* sp, int num_tokens, const msa_rows_t* k, const msa_rows_t* v,
+                         void* ws, size_t ws_bytes, SpanParams& p) {
+  const msa_status_t s = check_cache(c, false, true);
+  if (s != MSA_OK) return s;
+  if (!sp || sp->num_seqs < 1 || sp->max_blocks_per_seq < 1 || num_tokens < 0 || !sp->first || !sp->end || !sp->token_offsets ||
+      !sp->block_table || !ws || !aligned4(sp->first, sp->end, sp->token_offsets, sp->block_table, ws))
+    return MSA_ERR_INVALID_ARGUMENT;
+  if ((long)sp->max_blocks_per_seq * kBlock > (1l << 30)) return MSA_ERR_UNSUPPORTED;
+  if (ws_bytes < 256) return MSA_ERR_WORKSPACE_TOO_SMALL;
+  std::memset(&p, 0, sizeof(p));
+  p.S = sp->num_seqs;
+  p.max_nb = sp->max_blocks_per_seq;
+  p.num_tokens = num_tokens;
+  p.H = c->num_kv_heads;
+  p.num_blocks = c->num_blocks;
+  p.first = sp->first;
+  p.end = sp->end;
+  p.offsets = sp->token_offsets;
+  p.block_table = sp->block_table;
+  if (k) p.k_stride = k->stride;
+  if (v) p.v_stride = v->stride;
+  p.kc = static_cast<uint8_t*>(const_cast<void*>(c->k));
+  p.vc = static_cast<uint8_t*>(const_cast<void*>(c->v));
+  p.ks = const_cast<float*>(c->k_scale);
+  p.vs = const_cast<float*>(c->v_scale);
+  p.ksf = static_cast<const uint8_t*>(c->k_sf);
+  p.vsf = static_cast<const uint8_t*>(c->v_sf);
+  p.kg = c->k_global;
+  p.vg = c->v_global;
+  p.nv_round = c->nvfp4_mode == MSA_NVFP4_E4M3_PRODUCT;
+  p.status = static_cast<DeviceStatus*>(ws);
+  return MSA_OK;
+}
 
 }  // namespace
 
@@ -712,6 +791,10 @@ msa_status_t msa_sparse_attend(const msa_cache_t* cache, const msa_batch_t* batc
   Plan pl;
   if ((s = make_plan(cache, batch, cfg, num_q_heads, true, q->dtype == MSA_DTYPE_FP8_E4M3, pl)) != MSA_OK) return s;
   if (workspace_bytes < pl.total) return MSA_ERR_WORKSPACE_TOO_SMALL;
+  if (pl.blk) {
+    if (!aligned16(workspace) || !aligned4(batch->seq_lens, batch->block_table, topk_idx, lse)) return MSA_ERR_INVALID_ARGUMENT;
+    return run_dense(cache, batch, cfg, q, num_q_heads, topk_idx, out, lse, pl.dense, workspace, (cudaStream_t)stream);
+  }
   if (pl.k2q) return run_k2q(cache, batch, cfg, q, num_q_heads, topk_idx, out, lse, pl, workspace, (cudaStream_t)stream);
   return run_attend(cache, batch, cfg, q, num_q_heads, topk_idx, out, lse, pl, workspace, (cudaStream_t)stream, false);
 }
@@ -729,9 +812,12 @@ msa_status_t msa_decode(const msa_cache_t* cache, const msa_batch_t* batch, cons
                      q->dtype == MSA_DTYPE_FP8_E4M3, pl)) != MSA_OK)
     return s;
   if (workspace_bytes < pl.total) return MSA_ERR_WORKSPACE_TOO_SMALL;
+  if (pl.blk && (!aligned16(workspace) || !aligned4(batch->seq_lens, batch->block_table, topk_idx, lse)))
+    return MSA_ERR_INVALID_ARGUMENT;
   cudaStream_t st = (cudaStream_t)stream;
   float* pooled = at<float>(workspace, pl.off_pooled);
   if ((s = run_indexer(cache, batch, cfg, index_q, pl, workspace, pooled, st, pl.pisel)) != MSA_OK) return s;
+  if (pl.blk) return run_select_dense(cache, batch, cfg, q, num_q_heads, pooled, topk_idx, out, lse, pl, workspace, st);
   if (pl.k2q) {
     if ((s = pl.pisel ? run_pisel(batch, cfg, cache->num_kv_heads, topk_idx, pl, workspace, st)
                       : run_topk(batch, cfg, cache->num_kv_heads, pooled, topk_idx, nullptr, workspace, &pl, st, true,
@@ -753,16 +839,18 @@ msa_status_t msa_cache_insert(const msa_cache_t* cache, int32_t num_tokens, cons
   if ((s = check_cache(cache, index_k != nullptr, true)) != MSA_OK) return s;
   if (num_tokens < 0 || !workspace || !aligned4(workspace, slot_mapping)) return MSA_ERR_INVALID_ARGUMENT;
   if (cache->num_kv_heads > 8) return MSA_ERR_UNSUPPORTED;
+  const bool blk = by_block(cache);  // K and V have an insert of their own
+  if (blk && (k || v)) return MSA_ERR_UNSUPPORTED;
   if (workspace_bytes < 256) return MSA_ERR_WORKSPACE_TOO_SMALL;
   if (num_tokens == 0) return MSA_OK;
-  if (!slot_mapping || !k || !v || !aligned16(k) || !aligned16(v) || (index_k && !aligned16(index_k)))
+  if (!slot_mapping || (!blk && (!k || !v)) || !aligned16(k) || !aligned16(v) || (index_k && !aligned16(index_k)))
     return MSA_ERR_INVALID_ARGUMENT;
   InsertParams p;
   std::memset(&p, 0, sizeof(p));
   p.num_tokens = num_tokens;
-  p.H = cache->num_kv_heads;
+  p.H = blk ? 0 : cache->num_kv_heads;
   p.num_blocks = cache->num_blocks;
-  p.kv_fmt = fmt_of(cache->kv_dtype);
+  p.kv_fmt = blk ? FMT_BF16 : fmt_of(cache->kv_dtype);
   p.idx_fmt = index_k ? fmt_of(cache->index_dtype) : FMT_BF16;
   p.slots = slot_mapping;
   p.k = static_cast<const __nv_bfloat16*>(k);
@@ -785,6 +873,35 @@ msa_status_t msa_cache_insert(const msa_cache_t* cache, int32_t num_tokens, cons
   return cuda_status(launch_insert(p, sm_count(), (cudaStream_t)stream));
 }
 
+msa_status_t msa_block_insert(const msa_cache_t* cache, const msa_spans_t* spans, int32_t num_tokens,
+                              const msa_rows_t* k, const msa_rows_t* v, void* workspace, size_t workspace_bytes,
+                              msa_stream_t stream) {
+  SpanParams p;
+  const msa_status_t s = span_params(cache, spans, num_tokens, k, v, workspace, workspace_bytes, p);
+  if (s != MSA_OK) return s;
+  if (!by_block(cache)) return MSA_ERR_UNSUPPORTED;
+  if (num_tokens == 0) return MSA_OK;
+  if (!rows_ok(k) || !rows_ok(v)) return MSA_ERR_INVALID_ARGUMENT;
+  p.k_in = static_cast<const __nv_bfloat16*>(k->data);
+  p.v_in = static_cast<const __nv_bfloat16*>(v->data);
+  return cuda_status(launch_block_insert(p, kv_fmt_of(cache->kv_dtype), sm_count(), (cudaStream_t)stream));
+}
+
+msa_status_t msa_cache_read(const msa_cache_t* cache, const msa_spans_t* spans, int32_t num_tokens, const msa_rows_t* k,
+                            const msa_rows_t* v, void* workspace, size_t workspace_bytes, msa_stream_t stream) {
+  SpanParams p;
+  const msa_status_t s = span_params(cache, spans, num_tokens, k, v, workspace, workspace_bytes, p);
+  if (s != MSA_OK) return s;
+  if (num_tokens == 0 || (!k && !v)) return MSA_OK;
+  // the rows are written: heads side by side, no two tokens on top of each other
+  const int64_t row = (int64_t)cache->num_kv_heads * kDim;
+  if ((k && (!rows_ok(k) || (num_tokens > 1 && k->stride < row))) || (v && (!rows_ok(v) || (num_tokens > 1 && v->stride < row))))
+    return MSA_ERR_INVALID_ARGUMENT;
+  p.k_out = k ? static_cast<__nv_bfloat16*>(const_cast<void*>(k->data)) : nullptr;
+  p.v_out = v ? static_cast<__nv_bfloat16*>(const_cast<void*>(v->data)) : nullptr;
+  return cuda_status(launch_cache_read(p, kv_fmt_of(cache->kv_dtype), sm_count(), (cudaStream_t)stream));
+}
+
 size_t msa_dense_workspace_size(const msa_cache_t* cache, const msa_batch_t* batch, int32_t num_q_heads) {
   DensePlan pl;
   if (check_batch(batch) != MSA_OK || check_cache(cache, false, false) != MSA_OK ||
@@ -805,7 +922,7 @@ msa_status_t msa_dense_attend(const msa_cache_t* cache, const msa_batch_t* batch
   DensePlan pl;
   if ((s = make_dense_plan(cache, batch, num_q_heads, pl)) != MSA_OK) return s;
   if (workspace_bytes < pl.total) return MSA_ERR_WORKSPACE_TOO_SMALL;
-  return run_dense(cache, batch, cfg, q, num_q_heads, out, lse, pl, workspace, (cudaStream_t)stream);
+  return run_dense(cache, batch, cfg, q, num_q_heads, nullptr, out, lse, pl, workspace, (cudaStream_t)stream);
 }
 
 msa_status_t msa_rope_init(msa_rope_t* rope, int32_t rotary_dim, double theta, int32_t axes, const int32_t* sections,
@@ -843,8 +960,10 @@ msa_status_t msa_rope_insert(const msa_cache_t* cache, const msa_rope_t* rope, i
   if (num_tokens < 0 || !workspace || !aligned4(workspace, positions, slot_mapping)) return MSA_ERR_INVALID_ARGUMENT;
   if (workspace_bytes < 256) return MSA_ERR_WORKSPACE_TOO_SMALL;
   if (num_q_heads < 1 || num_q_heads > 1024) return MSA_ERR_UNSUPPORTED;
+  const bool blk = by_block(cache);  // K and V have an insert of their own
+  if (blk && (k || v)) return MSA_ERR_UNSUPPORTED;
   if (num_tokens == 0) return MSA_OK;
-  if (!positions || !slot_mapping || !rows_ok(q) || !rows_ok(k) || !rows_ok(v) || (index_q && !rows_ok(index_q)) ||
+  if (!positions || !slot_mapping || !rows_ok(q) || (!blk && (!rows_ok(k) || !rows_ok(v))) || (index_q && !rows_ok(index_q)) ||
       (index_k && !rows_ok(index_k)) || (index_q != nullptr) != (index_q_out != nullptr))
     return MSA_ERR_INVALID_ARGUMENT;
   if ((s = check_query(q_out)) != MSA_OK || (index_q && (s = check_query(index_q_out)) != MSA_OK)) return s;
@@ -856,20 +975,22 @@ msa_status_t msa_rope_insert(const msa_cache_t* cache, const msa_rope_t* rope, i
     for (int b = 0; b < 2; ++b) p.axis_bits[b][i >> 5] |= (uint32_t)(rope->axis[i] >> b & 1) << (i & 31);
   p.num_tokens = num_tokens;
   p.Hq = num_q_heads;
-  p.H = cache->num_kv_heads;
+  p.H = blk ? 0 : cache->num_kv_heads;
   p.Giq = index_q ? cache->num_kv_heads : 0;
   p.Gik = index_k ? 1 : 0;
   p.num_blocks = cache->num_blocks;
-  p.kv_fmt = fmt_of(cache->kv_dtype);
+  p.kv_fmt = blk ? FMT_BF16 : fmt_of(cache->kv_dtype);
   p.idx_fmt = index_k ? fmt_of(cache->index_dtype) : FMT_BF16;
   p.positions = positions;
   p.slots = slot_mapping;
   p.q = static_cast<const __nv_bfloat16*>(q->data);
   p.q_stride = q->stride;
-  p.k = static_cast<const __nv_bfloat16*>(k->data);
-  p.k_stride = k->stride;
-  p.v = static_cast<const __nv_bfloat16*>(v->data);
-  p.v_stride = v->stride;
+  if (!blk) {
+    p.k = static_cast<const __nv_bfloat16*>(k->data);
+    p.k_stride = k->stride;
+    p.v = static_cast<const __nv_bfloat16*>(v->data);
+    p.v_stride = v->stride;
+  }
   if (index_q) {
     p.iq = static_cast<const __nv_bfloat16*>(index_q->data);
     p.iq_stride = index_q->stride;
@@ -982,7 +1103,7 @@ msa_status_t msa_dequant_debug(const msa_cache_t* cache, int32_t which, const in
   if (which < 0 || which > 2 || n < 0 || (n > 0 && (!phys_blocks || !out))) return MSA_ERR_INVALID_ARGUMENT;
   msa_status_t s = check_cache(cache, which == 2, which != 2);
   if (s != MSA_OK) return s;
-  const int f = fmt_of(which == 2 ? cache->index_dtype : cache->kv_dtype);
+  const int f = which == 2 ? fmt_of(cache->index_dtype) : kv_fmt_of(cache->kv_dtype);
   return cuda_status(launch_dequant(f, which, *cache, phys_blocks, n, out, (cudaStream_t)stream));
 }
 
@@ -1044,6 +1165,7 @@ extern "C" msa_status_t msa_decode_noalloc(const msa_cache_t* cache, const msa_b
                      q->dtype == MSA_DTYPE_FP8_E4M3, pl, false)) != MSA_OK)  // pooled scores may still fit
     return s;
   if (pl.total > MSA_NOALLOC_SCRATCH_BYTES) return MSA_ERR_WORKSPACE_TOO_SMALL;
+  if (pl.blk && !aligned4(batch->seq_lens, batch->block_table, topk_idx, lse)) return MSA_ERR_INVALID_ARGUMENT;
   void* ws = nullptr;
   if ((s = noalloc_scratch(&ws)) != MSA_OK) return s;
   cudaStream_t st = (cudaStream_t)stream;
@@ -1051,7 +1173,9 @@ extern "C" msa_status_t msa_decode_noalloc(const msa_cache_t* cache, const msa_b
   if (cudaMemsetAsync(ws, 0, 256, st) != cudaSuccess) return MSA_ERR_CUDA;
   float* pooled = at<float>(ws, pl.off_pooled);
   if ((s = run_indexer(cache, batch, cfg, index_q, pl, ws, pooled, st, pl.pisel)) != MSA_OK) return s;
-  if (pl.k2q) {
+  if (pl.blk) {
+    if ((s = run_select_dense(cache, batch, cfg, q, num_q_heads, pooled, topk_idx, out, lse, pl, ws, st)) != MSA_OK) return s;
+  } else if (pl.k2q) {
     // a prefill chunk over an FP8 cache: the same chain as msa_decode's
     if ((s = pl.pisel ? run_pisel(batch, cfg, cache->num_kv_heads, topk_idx, pl, ws, st)
                       : run_topk(batch, cfg, cache->num_kv_heads, pooled, topk_idx, nullptr, ws, &pl, st, true, false,

@@ -104,6 +104,12 @@ struct DenseTraits<FMT_FP8> {
   static constexpr int SK = 128, TILE = 128 * 128, SC = 512;  // keys, bytes of a K or V tile, of its scales
 };
 template <>
+struct DenseTraits<FMT_I8B> {  // a unit is a block: its two scales come with the stage's facts
+  static constexpr int SK = 128, TILE = 128 * 128, SC = 0;
+};
+template <>
+struct DenseTraits<FMT_F8B> : DenseTraits<FMT_I8B> {};
+template <>
 struct DenseTraits<FMT_BF16> {
   static constexpr int SK = 64, TILE = 64 * 256, SC = 0;
 };
@@ -120,6 +126,18 @@ struct DenseFacts {
   int32_t part;           // partial slot, or -1: the segment is whole
   int32_t pad;
 };
+
+// What the producer says of a stage over caches with block scales.
+struct __align__(16) DenseStage {
+  int32_t ok, key0;  // whether it holds keys, the position of the first
+  float ks, vs;
+};
+
+// Formats of one byte an element, and those with a scale for each block.
+template <int FMT>
+constexpr bool kByBlock = fmt_by_block(FMT);
+template <int FMT>
+constexpr bool kBytes = FMT == FMT_FP8 || kByBlock<FMT>;
 
 // NN: tiles of 8 query columns a warp takes; NCG: groups of such columns in a unit.
 template <int FMT, int NN, int NCG>
@@ -166,10 +184,13 @@ struct DenseLayout {
   static constexpr size_t CF = Q + 2 * QSLOT;
   static constexpr size_t FACTS = CF + CF_BYTES;
   static constexpr size_t BARS = FACTS + 2 * sizeof(DenseFacts);
-  static constexpr size_t TEAM = (BARS + 8 * (2 * NST + 4) + 4 * NST + 16 + 127) / 128 * 128;
+  static constexpr size_t STAGES = BARS + 8 * (2 * NST + 4);  // 4 bytes each, or a DenseStage
+  static constexpr size_t STAGES_BYTES = NST * (kByBlock<FMT> ? sizeof(DenseStage) : 4);
+  static constexpr size_t TEAM = (STAGES + STAGES_BYTES + 16 + 127) / 128 * 128;
   static constexpr size_t SMEM = TILES + TEAMS * TEAM + 1024;
   static_assert(SMEM <= 227 * 1024, "stages");
   static_assert(STAGE % 1024 == 0 && MERGE_BYTES % 16 == 0 && ML_BYTES % 16 == 0 && QSLOT % 16 == 0, "alignment");
+  static_assert(STAGES % 16 == 0, "DenseStage");
 };
 
 // One team's shared memory.
@@ -178,6 +199,7 @@ struct DenseTeam {
   uint8_t* mem;     // scales, merge area, queries, facts
   uint64_t *full, *empty, *ifull, *iempty;
   int* stage_ok;
+  DenseStage* stage;  // block scales: in its place
   int* dead;
   DenseFacts* facts;
   int id;           // team of the grid: the run it takes
@@ -200,6 +222,39 @@ __device__ __forceinline__ uint32_t e4m3x2_hi_to_f16x2(uint32_t w) {  // the hig
   uint32_t h;
   asm("{ .reg .b16 lo, hi; mov.b32 {lo, hi}, %1; cvt.rn.f16x2.e4m3x2 %0, hi; }" : "=r"(h) : "r"(w));
   return h;
+}
+// int8 as f16, exact: 1024 + u of u = x + 128, less 1152.  w: the codes with their top
+// bits turned; sel: the bytes taken (4: the exponent's).
+__device__ __forceinline__ uint32_t i8x2_to_f16x2(uint32_t w, uint32_t sel) {
+  uint32_t d;
+  const uint32_t h = __byte_perm(w, 0x64646464u, sel);
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(h), "r"(0x64806480u));
+  return d;
+}
+// The four bytes of w as f16: the low two in h0, the high two in h1.
+template <int FMT>
+__device__ __forceinline__ void bytes_to_f16(uint32_t w, uint32_t& h0, uint32_t& h1) {
+  if constexpr (FMT == FMT_I8B) {
+    w ^= 0x80808080u;
+    h0 = i8x2_to_f16x2(w, 0x4140);
+    h1 = i8x2_to_f16x2(w, 0x4342);
+  } else {
+    h0 = e4m3x2_to_f16x2(w);
+    h1 = e4m3x2_hi_to_f16x2(w);
+  }
+}
+// The same with the even bytes in h0, the odd ones in h1.
+template <int FMT>
+__device__ __forceinline__ void bytes_apart_to_f16(uint32_t w, uint32_t& h0, uint32_t& h1) {
+  if constexpr (FMT == FMT_I8B) {
+    w ^= 0x80808080u;
+    h0 = i8x2_to_f16x2(w, 0x4240);
+    h1 = i8x2_to_f16x2(w, 0x4341);
+  } else {
+    w = __byte_perm(w, 0u, 0x3120);
+    h0 = e4m3x2_to_f16x2(w);
+    h1 = e4m3x2_hi_to_f16x2(w);
+  }
 }
 // the four bytes of packed e2m1 codes of w as four f16 pairs (low nibble first)
 __device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&h)[4]) {
@@ -266,12 +321,13 @@ __device__ __forceinline__ long warp_scan(long v, int lane) {  // inclusive
 
 // ---------------------------------------------------------------- the producer warp
 
-template <int FMT, int NN, int NCG>
+template <int FMT, int NN, int NCG, bool SEL>
 __device__ void producer(const CUtensorMap* tmk, const CUtensorMap* tmv, const DenseParams& p, const DenseTeam& tm,
                          int lane) {
   using TR = DenseTraits<FMT>;
   using LY = DenseLayout<FMT, NN, NCG>;
   constexpr int NST = LY::NST;
+  constexpr bool BLK = kByBlock<FMT>;
   uint64_t *full = tm.full, *empty = tm.empty, *ifull = tm.ifull, *iempty = tm.iempty;
   int* dead = tm.dead;
   const int S = p.S, max_nb = p.max_nb;
@@ -282,13 +338,17 @@ __device__ void producer(const CUtensorMap* tmk, const CUtensorMap* tmv, const D
   // 61 ragged sequences of 48 columns take 14% longer.
   long total = 0;
   int mine0 = 0;  // the length of sequence `lane`: a batch of up to 32 is read once
+  if constexpr (SEL) {  // every token has the same number of places
+    total = (long)S * GC * (p.topk + LY::END);
+  } else {
 #pragma unroll 4
-  for (int s0 = 0; s0 < S; s0 += 32) {
-    const int T = s0 + lane < S ? __ldg(p.seq_lens + s0 + lane) : 0;
-    if (s0 == 0) mine0 = T;
-    total += slots_of<TR::SK, LY::END>(T, max_nb);
+    for (int s0 = 0; s0 < S; s0 += 32) {
+      const int T = s0 + lane < S ? __ldg(p.seq_lens + s0 + lane) : 0;
+      if (s0 == 0) mine0 = T;
+      total += slots_of<TR::SK, LY::END>(T, max_nb);
+    }
+    total = warp_sum(total) * GC;
   }
-  total = warp_sum(total) * GC;
   const long teams = (long)gridDim.x * LY::TEAMS;
   const long grid = total < teams ? total : teams;
   const long c = tm.id;
@@ -300,7 +360,10 @@ __device__ void producer(const CUtensorMap* tmk, const CUtensorMap* tmv, const D
   // the sequence that holds u0: sb units (x GC) come before it
   int s = 0;
   long sb = 0;
-  if (u1 > u0) {
+  if constexpr (SEL) {
+    s = (int)(u0 / (GC * (p.topk + LY::END)));
+    sb = (long)s * GC * (p.topk + LY::END);
+  } else if (u1 > u0) {
     for (int s0 = 0; s0 < S; s0 += 32) {
       const int T = s0 == 0 ? mine0 : s0 + lane < S ? __ldg(p.seq_lens + s0 + lane) : 0;
       const long mine = GC * slots_of<TR::SK, LY::END>(T, max_nb);
@@ -322,8 +385,17 @@ __device__ void producer(const CUtensorMap* tmk, const CUtensorMap* tmv, const D
   bool first = true;
 #pragma unroll 1
   while (u < u1 && ok) {
-    const int T = s < 32 ? __shfl_sync(0xffffffffu, mine0, s & 31) : __ldg(p.seq_lens + s);
-    const int un = units_of<TR::SK>(T, max_nb);
+    int T, un;
+    if constexpr (SEL) {  // keys that token s sees; 0: a malformed sequence, every entry of its lists is left out
+      T = __ldg(p.seq_lens + s / p.q_real);
+      const bool good = T >= p.q_real && T <= max_nb * kBlock;
+      if (!good && lane == 0) raise_flag(p.status, FLAG_BAD_SEQLEN, T);
+      T = good ? T - p.q_real + s % p.q_real + 1 : 0;
+      un = p.topk;
+    } else {
+      T = s < 32 ? __shfl_sync(0xffffffffu, mine0, s & 31) : __ldg(p.seq_lens + s);
+      un = units_of<TR::SK>(T, max_nb);
+    }
     if (un == 0) {  // an empty sequence holds no units
       ++s;
       continue;
@@ -346,10 +418,28 @@ __device__ void producer(const CUtensorMap* tmk, const CUtensorMap* tmv, const D
     if (first && lane == 0) p.info[c] = make_int2(sg, cut_start ? 1 : 0);
     first = false;
     // the first 32 block-table entries, on their way while the segment is published
-    const int32_t* row = p.block_table + (size_t)s * max_nb;
+    const int32_t* row = p.block_table + (size_t)(SEL ? s / p.q_real : s) * max_nb;
     constexpr int UPB = kBlock / TR::SK;  // units a block
-    int b_have = k0 / UPB;                // entries [b_have, b_have + 32), one a lane
-    int entry = (b_have + lane) * UPB < k0 + n ? __ldg(row + b_have + lane) : -1;
+    int b_have = SEL ? 0 : k0 / UPB;      // entries [b_have, b_have + 32), one a lane
+    int entry = -1, pick = -1;
+    float ks_mine = 0.f, vs_mine = 0.f;   // BLK: the scales of this lane's block
+    if constexpr (SEL) {
+      // the whole list, one entry a lane (topk <= 32)
+      if (lane < p.topk) pick = __ldg(p.topk_idx + ((size_t)s * p.G + g) * p.topk + lane);
+      const bool seen = pick >= 0 && pick <= (T - 1) >> 7;  // (an arithmetic shift: T = 0 sees none)
+      const uint32_t same = __match_any_sync(0xffffffffu, seen ? pick : -1 - lane);
+      const bool take = seen && (same & ((1u << lane) - 1u)) == 0;
+      if (pick >= 0 && !take) raise_flag(p.status, FLAG_BAD_SELECT, pick);
+      if (take) {
+        entry = __ldg(row + pick);
+        if (entry < 0 || entry >= p.num_blocks) {
+          raise_flag(p.status, FLAG_BAD_BLOCK, entry);
+          entry = -1;
+        }
+      }
+    } else {
+      entry = (b_have + lane) * UPB < k0 + n ? __ldg(row + b_have + lane) : -1;
+    }
     // publish the segment and its query rows
     const int slot = ii & 1, use = ii >> 1;
     if (use > 0 && !ring_wait(&iempty[slot], (uint32_t)((use - 1) & 1), dead)) {
@@ -385,14 +475,21 @@ __device__ void producer(const CUtensorMap* tmk, const CUtensorMap* tmv, const D
 #pragma unroll 1
     for (int k = k0; k < k0 + n; ++k) {
       const int b = k / UPB, half = k - b * UPB;
-      if (b >= b_have + 32) {
+      if (!SEL && b >= b_have + 32) {
         b_have = b;
         entry = (b + lane) * UPB < k0 + n ? __ldg(row + b + lane) : -1;
       }
-      if (b == b_have && (k == k0 || half == 0)) {  // new entries: the ones outside the pool
-        if ((b + lane) * UPB < k0 + n && (entry < 0 || entry >= p.num_blocks)) {
+      if (SEL ? k == k0 : b == b_have && (k == k0 || half == 0)) {  // new entries: the ones outside the pool
+        if (!SEL && (b + lane) * UPB < k0 + n && (entry < 0 || entry >= p.num_blocks)) {
           raise_flag(p.status, FLAG_BAD_BLOCK, entry);
           entry = -1;
+        }
+        if constexpr (BLK) {
+          if (entry >= 0) {
+            const size_t at = (size_t)entry * p.G + g;
+            ks_mine = __ldg(reinterpret_cast<const float*>(p.k_sc) + at);
+            vs_mine = __ldg(reinterpret_cast<const float*>(p.v_sc) + at);
+          }
         }
       }
       const int ph = __shfl_sync(0xffffffffu, entry, b - b_have);
@@ -402,7 +499,28 @@ __device__ void producer(const CUtensorMap* tmk, const CUtensorMap* tmv, const D
         ok = false;
         break;
       }
-      if (lane == 0) {
+      if constexpr (BLK) {
+        // The copies first; the scales may still be on their way, and the phase waits for them
+        // (this lane's arrival).
+        if (lane == 0 && ph >= 0) {
+          uint8_t* stg = tm.tiles + (size_t)st * LY::STAGE;
+          const int y = (int)(((size_t)ph * p.G + g) * kBlock);
+          fence_proxy_async();
+          mbar_expect_tx_only(&full[st], (uint32_t)LY::STAGE);
+          const uint64_t pol = p.stream ? l2_policy_evict_first() : l2_policy_evict_normal();
+          tma_load_2d_hint(stg, tmk, 0, y, &full[st], pol);
+          tma_load_2d_hint(stg + TR::TILE, tmv, 0, y, &full[st], pol);
+        }
+        DenseStage f;
+        f.ok = ph >= 0;
+        f.key0 = kBlock * (SEL ? __shfl_sync(0xffffffffu, pick, b) : k);
+        f.ks = __shfl_sync(0xffffffffu, ks_mine, b - b_have);
+        f.vs = __shfl_sync(0xffffffffu, vs_mine, b - b_have);
+        if (lane == 0) {
+          tm.stage[st] = f;
+          mbar_arrive(&full[st]);
+        }
+      } else if (lane == 0) {
         tm.stage_ok[st] = ph >= 0 ? 1 : 0;
         if (ph >= 0) {
           uint8_t* stg = tm.tiles + (size_t)st * LY::STAGE;
@@ -470,7 +588,7 @@ __device__ __forceinline__ float2 bf16x2_to_float2(uint32_t w) {
 // both agree; d even, pairs stay together.
 template <int FMT>
 __device__ __forceinline__ int q_place(int d) {
-  if constexpr (FMT == FMT_FP8) {  // K's slots 2j, 2j + 1 and 2j + 8, 2j + 9 hold dims 4j .. 4j + 3
+  if constexpr (kBytes<FMT>) {  // K's slots 2j, 2j + 1 and 2j + 8, 2j + 9 hold dims 4j .. 4j + 3
     const int ks = d >> 4, j = (d >> 2) & 3, hi = (d >> 1) & 1;
     return 16 * ks + 8 * hi + 2 * j;
   } else if constexpr (FMT == FMT_NVFP4) {  // a lane's 32 consecutive dims, four a step
@@ -613,7 +731,7 @@ __device__ __forceinline__ void logits(uint32_t kl, const uint8_t* ksc, const ui
             for (int m = 0; m < MT; ++m) mma_f16_k16(sacc[t0 + u][m], a[i][m], h[u][2 * i], h[u][2 * i + 1]);
       }
     }
-  } else if constexpr (FMT == FMT_FP8) {  // a register's four dims of a key: both halves of a k step
+  } else if constexpr (kBytes<FMT>) {  // a register's four dims of a key: both halves of a k step
 #pragma unroll
     for (int kp = 0; kp < 2; ++kp) {
       uint32_t b[NT][4];
@@ -633,7 +751,8 @@ __device__ __forceinline__ void logits(uint32_t kl, const uint8_t* ksc, const ui
         }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          const uint32_t b0 = e4m3x2_to_f16x2(b[t][i]), b1 = e4m3x2_hi_to_f16x2(b[t][i]);
+          uint32_t b0, b1;
+          bytes_to_f16<FMT>(b[t][i], b0, b1);
 #pragma unroll
           for (int m = 0; m < MT; ++m) mma_f16_k16(sacc[t][m], a[m], b0, b1);
         }
@@ -705,7 +824,7 @@ __device__ __forceinline__ void pv16(uint32_t vl, const uint8_t* vs, int kb, int
     m0 = (k <= klim ? 0xffffu : 0u) | (k + 1 <= klim ? 0xffff0000u : 0u);
     m1 = (k + 8 <= klim ? 0xffffu : 0u) | (k + 9 <= klim ? 0xffff0000u : 0u);
   }
-  if constexpr (FMT == FMT_FP8) {
+  if constexpr (kBytes<FMT>) {
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       uint32_t r[4];
@@ -713,8 +832,9 @@ __device__ __forceinline__ void pv16(uint32_t vl, const uint8_t* vs, int kb, int
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         // a register holds two dims of two keys: rows g8 take the even dim, rows g8 + 8 the odd one
-        const uint32_t x0 = __byte_perm(r[2 * q], 0u, 0x3120), x1 = __byte_perm(r[2 * q + 1], 0u, 0x3120);
-        uint32_t a[4] = {e4m3x2_to_f16x2(x0), e4m3x2_hi_to_f16x2(x0), e4m3x2_to_f16x2(x1), e4m3x2_hi_to_f16x2(x1)};
+        uint32_t a[4];
+        bytes_apart_to_f16<FMT>(r[2 * q], a[0], a[1]);
+        bytes_apart_to_f16<FMT>(r[2 * q + 1], a[2], a[3]);
         if constexpr (MASK) {
           a[0] &= m0;
           a[1] &= m0;
@@ -802,9 +922,10 @@ __device__ __forceinline__ void pv16(uint32_t vl, const uint8_t* vs, int kb, int
 template <int FMT>
 __device__ __forceinline__ bool v_not_finite(const uint8_t* stg, const uint8_t* vs, int r0, int r1, int lane) {
   using TR = DenseTraits<FMT>;
+  if constexpr (FMT == FMT_I8B) return false;
   bool bad = false;
   for (int row = r0; row < r1; ++row) {
-    if constexpr (FMT == FMT_FP8) {
+    if constexpr (kBytes<FMT>) {
       const uint32_t w = *reinterpret_cast<const uint32_t*>(stg + TR::TILE + row * 128 + 4 * lane);
 #pragma unroll
       for (int i = 0; i < 4; ++i) bad |= ((w >> (8 * i)) & 0x7fu) == 0x7fu;
@@ -824,19 +945,19 @@ __device__ __forceinline__ bool v_not_finite(const uint8_t* stg, const uint8_t* 
 // The output dim of accumulator tile mt's row g8 (half 0) or g8 + 8 (half 1).
 template <int FMT>
 __device__ __forceinline__ int out_dim(int mt, int half, int g8) {
-  if constexpr (FMT == FMT_FP8) return 16 * mt + 2 * g8 + half;
+  if constexpr (kBytes<FMT>) return 16 * mt + 2 * g8 + half;
   else if constexpr (FMT == FMT_BF16) return 16 * mt + 8 * half + g8;
   else return 32 * (mt >> 1) + 4 * g8 + 2 * (mt & 1) + half;
 }
 
-template <int FMT, int NN, int NCG, bool NVR>
+template <int FMT, int NN, int NCG, bool NVR, bool SEL>
 __device__ void consumer(const DenseParams& p, const DenseTeam& tm, int bar, int warp, int lane) {
   using TR = DenseTraits<FMT>;
   using LY = DenseLayout<FMT, NN, NCG>;
   constexpr int NST = LY::NST, MT = LY::MT, KGW = LY::KGW;
   constexpr int KW = TR::SK / KGW;             // keys of a warp in a unit
   constexpr int KC = KW < 32 ? KW : 32;        // keys a softmax step takes
-  constexpr bool F16P = FMT != FMT_BF16;
+  constexpr bool F16P = FMT != FMT_BF16, BLK = kByBlock<FMT>;
   constexpr float SHIFT = FMT == FMT_NVFP4 ? kDensePShift : 0.f;
   constexpr bool REG = NN == 1;                // query fragments held in registers
   constexpr int TEAM_THREADS = 32 * kDenseWpg;
@@ -882,7 +1003,7 @@ __device__ void consumer(const DenseParams& p, const DenseTeam& tm, int bar, int
     // row state: the reference m_run (log2 domain), what is subtracted, and the raw logit that
     // moves it.  (FP8 subtracts m_run itself: four registers fewer where they spill, 2% with
     // 32 columns.)
-    constexpr bool SAME = FMT == FMT_FP8;
+    constexpr bool SAME = kBytes<FMT>;
     float m_run[NN], msub[NN], ylim[NN], colf[NN];
     float2 l_run[NN];
 #pragma unroll
@@ -912,11 +1033,13 @@ __device__ void consumer(const DenseParams& p, const DenseTeam& tm, int bar, int
       const uint32_t stg = smem_u32(tm.tiles + (size_t)st * LY::STAGE);
       const uint8_t* ksc = tm.mem + LY::SC + (size_t)st * LY::SCALES;  // scales of K, then of V
       const uint8_t* vsb = ksc + TR::SC;
-      if (have && tm.stage_ok[st]) {
+      DenseStage sf = {};
+      if constexpr (BLK) sf = tm.stage[st];
+      if (have && (BLK ? sf.ok : tm.stage_ok[st])) {
         const uint32_t kl = k_lane<FMT>(stg, lane), vl = v_lane<FMT>(stg + TR::TILE, lane);
 #pragma unroll 1
         for (int kb = kw; kb < kw + KW; kb += KC) {
-          const int key0 = k * TR::SK + kb;  // position of the step's first key
+          const int key0 = (SEL ? sf.key0 : k * TR::SK) + kb;  // position of the step's first key
           if (key0 >= f.T) break;
           float sacc[KC / 8][MT][4];
           logits<FMT, NVR, KC, MT, REG>(kl, ksc, ql, kb, lane, aq, sacc);
@@ -933,6 +1056,15 @@ __device__ void consumer(const DenseParams& p, const DenseTeam& tm, int bar, int
               if constexpr (FMT == FMT_FP8) v = mul2(v, ks);
               y[t][n] = v;
             }
+          }
+          // a block's scale goes to the columns' factors, or, where keys are masked, to the logits
+          // (-inf times a factor that is 0 or NaN would be NaN)
+          const float kf = BLK && !masked ? sf.ks : 1.f;
+          if (BLK && masked) {
+#pragma unroll
+            for (int t = 0; t < KC / 8; ++t)
+#pragma unroll
+              for (int n = 0; n < NN; ++n) y[t][n] = mul2(y[t][n], make_float2(sf.ks, sf.ks));
           }
           if (masked) {
 #pragma unroll
@@ -953,6 +1085,7 @@ __device__ void consumer(const DenseParams& p, const DenseTeam& tm, int bar, int
             mx[n] = fmaxf(y[0][n].x, y[0][n].y);
 #pragma unroll
             for (int t = 1; t < KC / 8; ++t) mx[n] = max3(mx[n], y[t][n].x, y[t][n].y);
+            if constexpr (BLK) mx[n] *= kf;
             over |= mx[n] > ylim[n];
           }
           const bool moved = __any_sync(0xffffffffu, over);
@@ -970,7 +1103,7 @@ __device__ void consumer(const DenseParams& p, const DenseTeam& tm, int bar, int
               ylim[n] = (mnew + kDenseLazy) / colf[n];
               l_run[n].x *= alpha;
               l_run[n].y *= alpha;
-              if constexpr (FMT == FMT_FP8) {
+              if constexpr (kBytes<FMT>) {
                 fe[n] = fe[n] > 0.f ? fe[n] * __frcp_rn(alpha) : 0.f;  // O itself follows below
               } else {
                 // the accumulators hold the columns 2j, 2j + 1
@@ -987,11 +1120,16 @@ __device__ void consumer(const DenseParams& p, const DenseTeam& tm, int bar, int
             }
           }
           // ---- FP8: V's scales; does P x vscale x fe keep to f16's range?
-          float2 vs[KC / 8];
-          if constexpr (FMT == FMT_FP8) {
+          float2 vs[BLK ? 1 : KC / 8];
+          float fv[NN];  // block scales: fe x vscale
+          if constexpr (kBytes<FMT>) {
             float vm = 0.f;
+            if constexpr (BLK) {
+              vs[0] = make_float2(sf.vs, sf.vs);
+              vm = fabsf(sf.vs);
+            }
 #pragma unroll
-            for (int t = 0; t < KC / 8; ++t) {
+            for (int t = 0; t < (BLK ? 0 : KC / 8); ++t) {
               vs[t] = lds_f2(reinterpret_cast<const float*>(vsb) + kb + 8 * t + 2 * j);
               if (masked) {  // the scale of a row that holds no key may be anything
                 if (key0 + 8 * t + 2 * j >= f.T) vs[t].x = 0.f;
@@ -1003,10 +1141,13 @@ __device__ void consumer(const DenseParams& p, const DenseTeam& tm, int bar, int
             for (int t = 0; t < KC / 8; ++t)
 #pragma unroll
               for (int n = 0; n < NN; ++n) {
-                const float2 x = fma2(y[t][n], make_float2(colf[n], colf[n]), make_float2(-m_run[n], -m_run[n]));
+                const float cn = BLK ? colf[n] * kf : colf[n];
+                const float2 x = fma2(y[t][n], make_float2(cn, cn), make_float2(-m_run[n], -m_run[n]));
                 y[t][n] = make_float2(ex2(x.x), ex2(x.y));  // the weights
+                if constexpr (BLK) l_run[n] = add2(l_run[n], y[t][n]);
               }
-            if (moved || __any_sync(0xffffffffu, vm > vlim)) {
+            const bool look = moved || __any_sync(0xffffffffu, vm > vlim);
+            if (look) {
               // the products themselves (times 2^-10, so that they are finite): few of the large
               // scales meet a large weight
               float top[NN];
@@ -1016,7 +1157,7 @@ __device__ void consumer(const DenseParams& p, const DenseTeam& tm, int bar, int
                 top[n] = 0.f;
 #pragma unroll
                 for (int t = 0; t < KC / 8; ++t) {
-                  const float2 a = mul2(y[t][n], mul2(vs[t], make_float2(0x1p-10f, 0x1p-10f)));
+                  const float2 a = mul2(y[t][n], mul2(vs[BLK ? 0 : t], make_float2(0x1p-10f, 0x1p-10f)));
                   top[n] = max3(top[n], fabsf(a.x) < INFINITY ? fabsf(a.x) : 0.f, fabsf(a.y) < INFINITY ? fabsf(a.y) : 0.f);
                 }
                 grow |= fe[n] > 0.f ? top[n] * fe[n] > 32.f : top[n] > 0.f;
@@ -1049,6 +1190,19 @@ __device__ void consumer(const DenseParams& p, const DenseTeam& tm, int bar, int
                 }
               }
             }
+            if constexpr (BLK) {
+              // |vscale| <= vlim: fe x vscale is 128 at most.  Else a product with a small weight
+              // keeps to the range, but fe x vscale may not: one after the other.
+              const bool apart = look && __any_sync(0xffffffffu, vm > vlim);
+#pragma unroll
+              for (int n = 0; n < NN; ++n) {
+                fv[n] = apart ? sf.vs : fe[n] * sf.vs;
+                if (apart) {
+#pragma unroll
+                  for (int t = 0; t < KC / 8; ++t) y[t][n] = mul2(y[t][n], make_float2(fe[n], fe[n]));
+                }
+              }
+            }
           }
           // ---- P, its row sums, and P's fragments: keys 2j, 2j + 1 of tile t
           uint32_t ph[KC / 8][NN], plo[KC / 8][NN];
@@ -1057,13 +1211,13 @@ __device__ void consumer(const DenseParams& p, const DenseTeam& tm, int bar, int
 #pragma unroll
             for (int n = 0; n < NN; ++n) {
               float2 q = y[t][n];
-              if constexpr (FMT != FMT_FP8) {
+              if constexpr (!kBytes<FMT>) {
                 const float2 x = fma2(q, make_float2(colf[n], colf[n]), make_float2(-msub[n], -msub[n]));
                 q = make_float2(ex2(x.x), ex2(x.y));
               }
-              l_run[n] = add2(l_run[n], q);
-              if constexpr (FMT == FMT_FP8) {
-                const float2 v = mul2(mul2(q, make_float2(fe[n], fe[n])), vs[t]);
+              if constexpr (!BLK) l_run[n] = add2(l_run[n], q);
+              if constexpr (kBytes<FMT>) {
+                const float2 v = BLK ? mul2(q, make_float2(fv[n], fv[n])) : mul2(mul2(q, make_float2(fe[n], fe[n])), vs[BLK ? 0 : t]);
                 if (masked) {  // a masked weight stays 0 beside a scale that is not finite
                   q.x = q.x == 0.f ? 0.f : v.x;
                   q.y = q.y == 0.f ? 0.f : v.y;
@@ -1103,8 +1257,8 @@ __device__ void consumer(const DenseParams& p, const DenseTeam& tm, int bar, int
             // tile rows up to the last key of the sequence; with several new tokens a
             // row between lim0 and there is seen by some of them only, and if its V is
             // not finite each token goes by itself, up to its own position
-            const int klast = f.T - 1 - k * TR::SK;
-            int r0 = lim0 + 1 - k * TR::SK, r1 = klast + 1;
+            const int klast = f.T - 1 - (key0 - kb);
+            int r0 = lim0 + 1 - (key0 - kb), r1 = klast + 1;
             r0 = r0 < kb ? kb : r0;
             r1 = r1 > kb + KC ? kb + KC : r1;
             const bool apart =
@@ -1138,7 +1292,7 @@ __device__ void consumer(const DenseParams& p, const DenseTeam& tm, int bar, int
     // ---------------- the segment's result: the warps of a column group hold different keys
 #pragma unroll
     for (int n = 0; n < NN; ++n) {
-      const float osc = FMT == FMT_FP8 ? (fe[n] > 0.f ? __frcp_rn(fe[n]) : 0.f) : (FMT == FMT_NVFP4 ? p.v_global : 1.f);
+      const float osc = kBytes<FMT> ? (fe[n] > 0.f ? __frcp_rn(fe[n]) : 0.f) : (FMT == FMT_NVFP4 ? p.v_global : 1.f);
       float l = l_run[n].x + l_run[n].y;
       l += __shfl_xor_sync(0xffffffffu, l, 1);
       l += __shfl_xor_sync(0xffffffffu, l, 2);
@@ -1161,7 +1315,7 @@ __device__ void consumer(const DenseParams& p, const DenseTeam& tm, int bar, int
           if constexpr (FMT == FMT_NVFP4) {
             const float(&v1)[4] = o[mt | 1][0];
             if (!(mt & 1)) *reinterpret_cast<float4*>(row + d) = make_float4(v[c], v[c + 2], v1[c], v1[c + 2]);
-          } else if constexpr (FMT == FMT_FP8) {
+          } else if constexpr (kBytes<FMT>) {
             *reinterpret_cast<float2*>(row + d) = make_float2(v[c], v[c + 2]);
           } else {
             row[d] = v[c];
@@ -1316,7 +1470,7 @@ __device__ void consumer(const DenseParams& p, const DenseTeam& tm, int bar, int
 // eight take 232 (128 x 40 + 256 x 232 = 384 x 168 = 64,512 registers); three teams
 // are fifteen with up to 128, or sixteen launched with 128, the producers' four with 56
 // then and the consumers' twelve with 152 (128 x 56 + 384 x 152 = 512 x 128).
-template <int FMT, int NN, int NCG, bool NVR>
+template <int FMT, int NN, int NCG, bool NVR, bool SEL>
 __global__ void __launch_bounds__(DenseLayout<FMT, NN, NCG>::THREADS, 1)
     dense_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv, const DenseParams p) {
   using LY = DenseLayout<FMT, NN, NCG>;
@@ -1333,8 +1487,9 @@ __global__ void __launch_bounds__(DenseLayout<FMT, NN, NCG>::THREADS, 1)
   tm.empty = tm.full + NST;
   tm.ifull = tm.empty + NST;
   tm.iempty = tm.ifull + 2;
-  tm.stage_ok = reinterpret_cast<int*>(tm.iempty + 2);
-  tm.dead = tm.stage_ok + NST;
+  tm.stage_ok = reinterpret_cast<int*>(tm.mem + LY::STAGES);
+  tm.stage = reinterpret_cast<DenseStage*>(tm.mem + LY::STAGES);
+  tm.dead = reinterpret_cast<int*>(tm.mem + LY::STAGES + LY::STAGES_BYTES);
   tm.facts = reinterpret_cast<DenseFacts*>(tm.mem + LY::FACTS);
   tm.id = blockIdx.x * TEAMS + team;
   if (!consumes && team < TEAMS && lane == 0) {
@@ -1355,11 +1510,11 @@ __global__ void __launch_bounds__(DenseLayout<FMT, NN, NCG>::THREADS, 1)
   pdl_launch_dependents();  // the combine's CTAs may take their place as soon as this grid's leave room
   if (!consumes) {
     if constexpr (LY::MOVE) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(LY::REGS_P));
-    if (team < TEAMS) producer<FMT, NN, NCG>(&tmk, &tmv, p, tm, lane);
+    if (team < TEAMS) producer<FMT, NN, NCG, SEL>(&tmk, &tmv, p, tm, lane);
   } else {
     if constexpr (LY::MOVE) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(LY::REGS_C));
     // sequences without keys (and malformed ones) have no units: their rows here
-    for (int s = blockIdx.x + warp * gridDim.x; s < p.S; s += gridDim.x * TEAMS * kDenseWpg) {
+    for (int s = SEL ? p.S : blockIdx.x + warp * gridDim.x; s < p.S; s += gridDim.x * TEAMS * kDenseWpg) {
       const int T = __ldg(p.seq_lens + s);
       if (T >= 1 && T <= p.max_nb * kBlock) continue;
       if (T != 0 && lane == 0) raise_flag(p.status, FLAG_BAD_SEQLEN, T);
@@ -1369,15 +1524,15 @@ __global__ void __launch_bounds__(DenseLayout<FMT, NN, NCG>::THREADS, 1)
       if (p.lse)
         for (long x = lane; x < rows; x += 32) p.lse[(size_t)s * rows + x] = -INFINITY;
     }
-    consumer<FMT, NN, NCG, NVR>(p, tm, 1 + team, warp % kDenseWpg, lane);
+    consumer<FMT, NN, NCG, NVR, SEL>(p, tm, 1 + team, warp % kDenseWpg, lane);
   }
 }
 
-template <int FMT, int NN, int NCG, bool NVR>
+template <int FMT, int NN, int NCG, bool NVR, bool SEL = false>
 cudaError_t launch_one(const CUtensorMap* tk, const CUtensorMap* tv, const DenseParams& p, int num_sms, cudaStream_t st) {
   using LY = DenseLayout<FMT, NN, NCG>;
   static_assert(LY::ROWS == dense_rows(NN, NCG) && LY::TEAMS == dense_teams(FMT, NN), "the plan's sizes");
-  auto kern = dense_kernel<FMT, NN, NCG, NVR>;
+  auto kern = dense_kernel<FMT, NN, NCG, NVR, SEL>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)LY::SMEM);
   if (e != cudaSuccess) return e;
   if constexpr (LY::MOVE) {
@@ -1390,6 +1545,20 @@ cudaError_t launch_one(const CUtensorMap* tk, const CUtensorMap* tv, const Dense
   }
   kern<<<(unsigned)num_sms, LY::THREADS, LY::SMEM, st>>>(*tk, *tv, p);
   return cudaGetLastError();
+}
+
+// The instance for the columns of a group (dense_shape).
+template <int FMT, bool SEL>
+cudaError_t launch_shape(const CUtensorMap* tk, const CUtensorMap* tv, const DenseParams& p, int num_sms, cudaStream_t st) {
+  const DenseShape sh = dense_shape(p.cper);
+  if (sh.ncg == 2)
+    return sh.nn == 3 ? launch_one<FMT, 3, 2, false, SEL>(tk, tv, p, num_sms, st) : launch_one<FMT, 4, 2, false, SEL>(tk, tv, p, num_sms, st);
+  switch (sh.nn) {
+    case 1: return launch_one<FMT, 1, 1, false, SEL>(tk, tv, p, num_sms, st);
+    case 2: return launch_one<FMT, 2, 1, false, SEL>(tk, tv, p, num_sms, st);
+    case 3: return launch_one<FMT, 3, 1, false, SEL>(tk, tv, p, num_sms, st);
+    default: return launch_one<FMT, 4, 1, false, SEL>(tk, tv, p, num_sms, st);
+  }
 }
 
 }  // namespace dense

@@ -1,0 +1,10 @@
+// Sparse attend over FP8 caches with block scales (msa_dense.cuh).
+#include "msa_dense.cuh"
+
+namespace msa {
+
+cudaError_t launch_dense_fp8b_sel(const CUtensorMap* tk, const CUtensorMap* tv, const DenseParams& p, int num_sms, cudaStream_t st) {
+  return dense::launch_shape<FMT_F8B, true>(tk, tv, p, num_sms, st);
+}
+
+}  // namespace msa

@@ -4,6 +4,7 @@
 // NVFP4; "[M3] Enable FP8 sparse GQA" for the E4M3 KV cache):
 //   BF16   the bits widened to fp32 (exact);
 //   FP8    fp32(e4m3) * per-token fp32 scale, one round-to-nearest-even;
+//   by blocks  fp32(int8 or e4m3) * the fp32 scale of its block and head, the same;
 //   NVFP4  fp32(e2m1 * e4m3 block scale) * fp32 per-tensor scale; the inner
 //          product is exact, so again one rounding.  With the cache's
 //          MSA_NVFP4_E4M3_PRODUCT mode the product is first rounded to E4M3
@@ -44,6 +45,9 @@ __global__ void dequant_kernel(int fmt, int which, msa_cache_t c, const int32_t*
     if (fmt == FMT_BF16) {
       const uint16_t bits = static_cast<const uint16_t*>(data)[row * D + d];
       v = __uint_as_float((uint32_t)bits << 16);
+    } else if (fmt == FMT_I8B || fmt == FMT_F8B) {
+      const uint8_t code = static_cast<const uint8_t*>(data)[row * D + d];
+      v = __fmul_rn(fmt == FMT_I8B ? (float)(int8_t)code : e4m3_to_float(code), (which == 0 ? c.k_scale : c.v_scale)[row / kBlock]);
     } else if (fmt == FMT_FP8) {
       const uint8_t code = static_cast<const uint8_t*>(data)[row * D + d];
       const float* sc = is_idx ? c.idx_scale : (which == 0 ? c.k_scale : c.v_scale);

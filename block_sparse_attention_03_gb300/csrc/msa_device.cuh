@@ -55,6 +55,11 @@ __device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
                : "memory");
 }
 
+// The transaction bytes alone: the phase's arrival comes later.
+__device__ __forceinline__ void mbar_expect_tx_only(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
+
 // Plain arrival (no transaction bytes): completes a phase whose only
 // expected arrival is this one.
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
@@ -351,6 +356,40 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
       : "=f"(d.x), "=f"(d.y)
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
   return d;
+}
+
+// fma2 rounded down: a sum that is zero is -0.
+__device__ __forceinline__ float2 fma2_down(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{ .reg .b64 x, y, z, w; mov.b64 x, {%2, %3}; mov.b64 y, {%4, %5}; mov.b64 z, {%6, %7}; fma.rm.f32x2 w, x, y, z; "
+      "mov.b64 {%0, %1}, w; }"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+
+// y[i] / s, correctly rounded, by Markstein's method (Computation of elementary
+// functions on the IBM RISC System/6000, 1990): with r = RN(1/s), q = RN(y r) and
+// e = RN(y - q s) exact, RN(q + e r) is the correctly rounded quotient, three operations
+// an element; scales near the ends of fp32's range, where e could underflow or r
+// overflow, take the division itself.  fits: no quotient is infinite (its remainder
+// would be NaN).
+// The sign of a zero is kept: the remainder is exact, and as -0 where it is zero it
+// leaves q = -0 alone.
+template <int N>
+__device__ __forceinline__ void divide(const float2 (&y)[N], float s, bool fits, float2 (&z)[N]) {
+  if (s >= 8.27e-25f && s <= 1.2e24f && fits) {  // 2^-80 to 2^80
+    const float r = __frcp_rn(s);
+    const float2 r2 = make_float2(r, r), n2 = make_float2(-s, -s);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float2 q = mul2(y[i], r2);
+      z[i] = fma2(fma2_down(q, n2, y[i]), r2, q);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) z[i] = make_float2(__fdiv_rn(y[i].x, s), __fdiv_rn(y[i].y, s));
+  }
 }
 
 // Order-preserving map of a float to uint32 (NaN sorts as -inf - 1; -0 and +0

@@ -14,7 +14,9 @@ namespace msa {
 struct DeviceStatus;
 
 // Element formats as the kernels see them.
-enum Fmt : int { FMT_BF16 = 0, FMT_FP8 = 1, FMT_NVFP4 = 2 };
+// (I8B, F8B: one byte an element with a scale for each block and head)
+enum Fmt : int { FMT_BF16 = 0, FMT_FP8 = 1, FMT_NVFP4 = 2, FMT_I8B = 3, FMT_F8B = 4 };
+constexpr bool fmt_by_block(int fmt) { return fmt == FMT_I8B || fmt == FMT_F8B; }
 
 // The batch as the kernels see it.  A long chunk of new tokens (prefill) is
 // split into `chunks` virtual sequences of Q tokens each: virtual sequence s
@@ -235,9 +237,11 @@ struct DenseParams {
   int32_t q_fp8;
   float q_scale;
   float col_const;            // sm_scale * log2(e) (x NVFP4 K per-tensor scale)
-  const uint8_t* k_sc;        // per-token fp32 scales (FP8) or e4m3 group scales (NVFP4)
+  const uint8_t* k_sc;        // fp32 scales (FP8: a token and head; by blocks: a block and head) or e4m3 ones (NVFP4)
   const uint8_t* v_sc;
   float v_global;             // NVFP4 V per-tensor scale
+  const int32_t* topk_idx;    // selection lists [S][G][topk] (null: every key), topk <= 32; S counts tokens then, Q = 1,
+  int32_t topk, q_real;       // q_real of them a sequence of seq_lens and block_table
   int32_t stream;             // the cache may be larger than the L2: its lines are the first to go
   int2* info;                 // [teams] (sequence x G x CG + group) the run begins in, 1: it began before the run
   float* part_o;              // [2 x teams][rows][128] partials of cut segments
@@ -300,7 +304,25 @@ struct TablesParams {
 };
 constexpr int kMaxTableSeqs = 8192;  // four sums a request in shared memory
 
+// Spans of tokens into a cache with block scales, or out of a cache (msa_span.cu).
+struct SpanParams {
+  int32_t S, max_nb, num_tokens, H, num_blocks;
+  const int32_t *first, *end, *offsets;  // [S]
+  const int32_t* block_table;            // [S][max_nb]
+  const __nv_bfloat16 *k_in, *v_in;      // insert: [num_tokens] rows of H heads
+  __nv_bfloat16 *k_out, *v_out;          // read: the same (null: not wanted)
+  int64_t k_stride, v_stride;            // elements between tokens
+  uint8_t *kc, *vc;                      // cache data (the read writes none of these)
+  float *ks, *vs;                        // scales: of a block and head, FP8: of a row
+  const uint8_t *ksf, *vsf;              // NVFP4
+  float kg, vg;
+  int32_t nv_round;
+  DeviceStatus* status;
+};
+
 // launchers (return cudaGetLastError())
+cudaError_t launch_block_insert(const SpanParams& p, int fmt, int num_sms, cudaStream_t st);
+cudaError_t launch_cache_read(const SpanParams& p, int fmt, int num_sms, cudaStream_t st);
 cudaError_t launch_rope(const RopeParams& p, int num_sms, cudaStream_t st);
 cudaError_t launch_tables(const TablesParams& p, int num_sms, cudaStream_t st);
 cudaError_t launch_dense_bf16(const CUtensorMap* tk, const CUtensorMap* tv, const DenseParams& p, int num_sms, cudaStream_t st);
@@ -309,6 +331,13 @@ cudaError_t launch_dense_nvfp4(const CUtensorMap* tk, const CUtensorMap* tv, con
                                cudaStream_t st);
 cudaError_t launch_dense_nvfp4_rounded(const CUtensorMap* tk, const CUtensorMap* tv, const DenseParams& p, int num_sms,
                                        cudaStream_t st);
+cudaError_t launch_dense_int8(const CUtensorMap* tk, const CUtensorMap* tv, const DenseParams& p, int num_sms, cudaStream_t st);
+cudaError_t launch_dense_fp8b(const CUtensorMap* tk, const CUtensorMap* tv, const DenseParams& p, int num_sms, cudaStream_t st);
+// the sparse attend over selection lists, the tokens as sequences of their own (S tokens, Q = 1)
+cudaError_t launch_dense_int8_sel(const CUtensorMap* tk, const CUtensorMap* tv, const DenseParams& p, int num_sms,
+                                  cudaStream_t st);
+cudaError_t launch_dense_fp8b_sel(const CUtensorMap* tk, const CUtensorMap* tv, const DenseParams& p, int num_sms,
+                                  cudaStream_t st);
 cudaError_t launch_dense_combine(const DenseParams& p, int fmt, int num_sms, cudaStream_t st);
 cudaError_t launch_insert(const InsertParams& p, int num_sms, cudaStream_t st);
 cudaError_t launch_k2q_build(const K2qParams& p, int num_sms, cudaStream_t st);    // count, scan, fill

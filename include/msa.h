@@ -44,6 +44,9 @@
  *               consecutive elements), fp32 per-tensor k_global / v_global.
  *   FP8 scales  k_scale, v_scale: fp32 [num_blocks][num_kv_heads][128]
  *               (value = e4m3 * scale of its token and head).
+ *   INT8 / FP8  K, V as for FP8, one byte an element; k_scale, v_scale: fp32
+ *   by blocks   [num_blocks][num_kv_heads], positive (value = code * scale of its
+ *               block and head).  Their tokens are written by msa_block_insert.
  *   index keys  one shared head: [num_blocks][128][index_dim] (BF16 / FP8) or
  *               [num_blocks][128][index_dim/2] bytes + idx_sf
  *               [num_blocks][128][index_dim/16] (NVFP4); FP8 per-token fp32
@@ -83,7 +86,10 @@ typedef enum {
 typedef enum {
   MSA_DTYPE_BF16 = 0,
   MSA_DTYPE_FP8_E4M3 = 1,
-  MSA_DTYPE_NVFP4 = 2
+  MSA_DTYPE_NVFP4 = 2,
+  /* K / V caches only: bytes with one fp32 scale for a block of 128 tokens and head */
+  MSA_DTYPE_INT8_BLOCK = 8, /* two's complement, -127 to 127 as msa_block_insert writes them */
+  MSA_DTYPE_FP8_BLOCK = 9   /* E4M3 codes */
 } msa_dtype_t;
 
 /* How an NVFP4 element's two factors combine (vLLM Day-0 blog, "NVIDIA
@@ -114,8 +120,8 @@ typedef struct {
   const void* v;
   const void* k_sf;     /* NVFP4 only */
   const void* v_sf;     /* NVFP4 only */
-  const float* k_scale; /* FP8 only */
-  const float* v_scale; /* FP8 only */
+  const float* k_scale; /* FP8 (a token and head), INT8 / FP8 by blocks (a block and head) */
+  const float* v_scale;
   const void* idx;
   const void* idx_sf;     /* NVFP4 only */
   const float* idx_scale; /* FP8 only */
@@ -184,7 +190,8 @@ typedef struct {
  * a power-of-two scale that keeps it in range), m, l and that scale in fp32:
  * 272 bytes x tokens x q heads x topk, and with a bf16 query its rows as two
  * e4m3 terms and a factor: 260 bytes x tokens x q heads (605 MB in all for
- * 8,192 tokens x 16 heads x 16). */
+ * 8,192 tokens x 16 heads x 16).  Over a cache with block scales the attend's part
+ * does not grow with the batch. */
 size_t msa_workspace_size(const msa_cache_t* cache, const msa_batch_t* batch,
                           const msa_config_t* cfg, int32_t num_q_heads);
 
@@ -231,7 +238,9 @@ msa_status_t msa_topk_blocks(const msa_batch_t* batch, const msa_config_t* cfg,
  * A row whose selection holds no visible key gets out = 0, lse = -inf.
  * Entries naming a block the query cannot see, or repeating a block an
  * earlier entry of the same row names, are left out and raise the device
- * fault flag: the softmax runs over the selected key set, each key once. */
+ * fault flag: the softmax runs over the selected key set, each key once.
+ * Caches with block scales: num_q_heads / num_kv_heads <= 64, workspace 16-byte
+ * aligned; equal calls give equal bits on one GPU. */
 msa_status_t msa_sparse_attend(const msa_cache_t* cache, const msa_batch_t* batch,
                                const msa_config_t* cfg, const msa_query_t* q,
                                int32_t num_q_heads, const int32_t* topk_idx, void* out,
@@ -274,10 +283,67 @@ msa_status_t msa_decode(const msa_cache_t* cache, const msa_batch_t* batch,
  * The call writes through the cache struct's data and scale pointers (they are
  * declared const for the read-only entry points).  workspace: at least 256
  * bytes; only its status word is used.  Rows of one token may be written in
- * any order; two tokens mapped to one slot race. */
+ * any order; two tokens mapped to one slot race.
+ * A cache with block scales: k and v must be NULL (else MSA_ERR_UNSUPPORTED) and
+ * only the index keys are written; K and V go through msa_block_insert. */
 msa_status_t msa_cache_insert(const msa_cache_t* cache, int32_t num_tokens, const int32_t* slot_mapping,
                               const void* k, const void* v, const void* index_k, void* workspace,
                               size_t workspace_bytes, msa_stream_t stream);
+
+/* Consecutive tokens of each sequence: those at the positions first[s] to
+ * end[s] - 1 of sequence s are rows token_offsets[s], token_offsets[s] + 1, ... of
+ * the call's row tensors (none where end[s] <= first[s]).  Beside msa_build_tables
+ * first is its cached_lens, end its seq_lens and token_offsets its token_offsets: a
+ * request that waits, has ended or was refused has no tokens then. */
+typedef struct {
+  int32_t num_seqs;
+  int32_t max_blocks_per_seq;    /* row stride of block_table */
+  const int32_t* first;          /* device int32 [num_seqs] */
+  const int32_t* end;            /* device int32 [num_seqs] */
+  const int32_t* token_offsets;  /* device int32 [num_seqs] (more are not read) */
+  const int32_t* block_table;    /* device int32 [num_seqs][max_blocks_per_seq] */
+} msa_spans_t;
+
+/* bf16 rows of a projection: element d of head h of token t at data[t * stride +
+ * h * 128 + d] (a slice of a fused projection's output).  data 16-byte aligned,
+ * stride a multiple of 8 elements. */
+typedef struct {
+  const void* data;
+  int64_t stride;
+} msa_rows_t;
+
+/* Block insert: K and V of the spans' tokens (num_tokens rows of num_kv_heads heads)
+ * into a cache with block scales.  For each block and head, K and V each by itself,
+ * with Q = 127 (INT8) or 448 (E4M3), every operation one in fp32:
+ *   need  = max(amax / Q, 2^-126), amax over the finite new elements;
+ *   a block whose first row is among the call's tokens starts anew: scale = need;
+ *   another one holds the sequence's tokens up to first[s]: scale = the old one x
+ *   2^k, with the least k >= 0 that makes it need or more (an old scale that is not
+ *   a positive normal number counts as 2^-126), and where k > 0 the codes of the
+ *   tokens held become round(code x 2^-k);
+ *   code  = round(x / scale), to nearest even, saturating at +-Q; NaN becomes 0 in
+ *   INT8 and NaN in E4M3.
+ * So E4M3 codes of a block that grows move exactly down to E4M3's subnormals, and INT8
+ * codes are off by less than one step of the present scale however often it grew.
+ * Rows of a block behind end[s] are left as they were.
+ * Flagged on the device and skipped: a span with first < 0 or end beyond
+ * max_blocks_per_seq * 128, a span whose rows are not all inside num_tokens, and the
+ * tokens of a block outside the pool.  A block may be in the spans of one sequence
+ * only (two race).  k and v may not overlap the cache.
+ * The call writes through the cache's pointers.  Deterministic.  workspace: at least
+ * 256 bytes; only its status word is used. */
+msa_status_t msa_block_insert(const msa_cache_t* cache, const msa_spans_t* spans, int32_t num_tokens,
+                              const msa_rows_t* k, const msa_rows_t* v, void* workspace, size_t workspace_bytes,
+                              msa_stream_t stream);
+
+/* Cache read: the spans' tokens back as bf16 rows (num_tokens rows of num_kv_heads
+ * heads), from a cache of any format: the fp32 value of the element (msa_dequant_debug),
+ * rounded to nearest even; a BF16 cache's bits are copied.  k or v may be NULL.
+ * The call writes through their data pointers, only rows that are a span's; it
+ * flags and skips what msa_block_insert does.  Spans may share blocks, not rows.
+ * workspace: at least 256 bytes; only its status word is used. */
+msa_status_t msa_cache_read(const msa_cache_t* cache, const msa_spans_t* spans, int32_t num_tokens, const msa_rows_t* k,
+                            const msa_rows_t* v, void* workspace, size_t workspace_bytes, msa_stream_t stream);
 
 /* Dense attend: the layers of the model that select no blocks.  For query head
  * h of KV head g = h / (num_q_heads / num_kv_heads), exact softmax attention over
@@ -292,7 +358,8 @@ msa_status_t msa_cache_insert(const msa_cache_t* cache, int32_t num_tokens, cons
  * -inf.  A block-table entry outside the pool is flagged and its keys are left
  * out.  Entries past a sequence's last block are not read.
  * What the cache holds past a sequence's end (NaN or infinity among it) and what
- * the tokens after a query's own position hold reaches no output of that query.
+ * the tokens after a query's own position hold reaches no output of that query (over
+ * a cache with block scales other than through the scale of a block it sees).
  * The result does not depend on timing: equal calls give equal bits on one GPU.
  * workspace: msa_dense_workspace_size bytes, 16-byte aligned, msa_workspace_init
  * as for the other entry points (and it may be shared with them); calls that
@@ -328,14 +395,6 @@ typedef struct {
 msa_status_t msa_rope_init(msa_rope_t* rope, int32_t rotary_dim, double theta, int32_t axes, const int32_t* sections,
                            int32_t layout);
 
-/* bf16 rows of a projection: element d of head h of token t at data[t * stride +
- * h * 128 + d] (a slice of a fused projection's output).  data 16-byte aligned,
- * stride a multiple of 8 elements. */
-typedef struct {
-  const void* data;
-  int64_t stride;
-} msa_rows_t;
-
 /* Per-head RMS norm before the rotation: y = x * rsqrt(mean x^2 + eps) * (offset
  * + w), w bf16 [128], 16-byte aligned, shared by the heads of a kind (offset 1 for
  * weights stored around zero, as the model's Gemma-style norm does, else 0).  A
@@ -360,6 +419,10 @@ typedef struct {
  *   are not stored, its queries are still written; beyond the pool: the same,
  *   and flagged).  Two tokens mapped to one slot race.
  * index_q / index_q_out (num_kv_heads heads) may both be NULL, as may index_k.
+ * A cache with block scales: k and v must be NULL (else MSA_ERR_UNSUPPORTED), the
+ * queries and index keys are written as ever, and K and V go through msa_block_insert
+ * (where there is no index query, the rows of K may take its place: normed with
+ * norm->index_q, turned, and written as bf16 rows to index_q_out).
  * q_out may be q's own memory when q is dense (stride = heads * 128) and bf16.
  * The call writes through q_out's, index_q_out's and the cache's pointers.
  * workspace: at least 256 bytes; only its status word is used. */
