@@ -250,6 +250,10 @@ class Spans:
     token_offsets: object  # int32 [S] or longer
     block_table: object    # int32 [S][max_blocks]
 
+    def __setattr__(self, name, value):  # looked at once, and again when a field is set (_spans_checked)
+        self.__dict__["_seen"] = ()
+        self.__dict__[name] = value
+
 
 @dataclasses.dataclass
 class QkNorm:
@@ -459,26 +463,37 @@ def msa_cache_insert(cache, slot_mapping, k, v, index_k, workspace, stream=None)
                                   _stream(stream)), "msa_cache_insert")
 
 
+def _spans_checked(spans: Spans, dev: int, where: str):
+    """(device, sequences, width of the table) of spans whose tensors are dense int32 on the device."""
+    first, end, offsets, table = spans.first, spans.end, spans.token_offsets, spans.block_table
+    S, shape = first.numel(), table.shape
+    if len(shape) != 2 or shape[0] != S or end.numel() != S or offsets.numel() < S:
+        raise MsaError(1, where)
+    for t in (first, end, offsets, table):
+        if t.dtype is not _int32 or t.get_device() != dev or not t.is_contiguous():
+            raise MsaError(1, where)
+    spans.__dict__["_seen"] = seen = (dev, S, shape[1])
+    return seen
+
+
 def _span_call(call, where: str, cache, spans, k, v, workspace, stream):
     """Pack and make one of the two calls over spans; k, v: bf16 [T][num_kv_heads][128], any token stride."""
     if _int32 is None:
         _torch_names()
-    first, end, offsets, table = spans.first, spans.end, spans.token_offsets, spans.block_table
-    S, shape, dev = first.numel(), table.shape, cache.k.get_device()
-    any_rows = v if k is None else k
-    if (dev < 0 or dev != _device() or len(shape) != 2 or shape[0] != S or end.numel() != S or offsets.numel() < S
-            or first.dtype is not _int32 or end.dtype is not _int32 or offsets.dtype is not _int32 or table.dtype is not _int32
-            or not first.is_contiguous() or not end.is_contiguous() or not offsets.is_contiguous() or not table.is_contiguous()
-            or first.get_device() != dev or end.get_device() != dev or offsets.get_device() != dev or table.get_device() != dev
-            or workspace.get_device() != dev):
+    dev = cache.k.get_device()
+    if dev < 0 or dev != _device() or workspace.get_device() != dev:
         raise MsaError(1, where)
-    T = 0 if any_rows is None else any_rows.shape[0]
-    kv, none = (T, cache.num_kv_heads, 128), (0, 0)
-    at = _SPAN.pack(*_cache_values(cache, False, dev, where), S, shape[1], first.data_ptr(), end.data_ptr(), offsets.data_ptr(),
-                    table.data_ptr(), *(none if k is None else _rows(k, kv, where, dev)),
-                    *(none if v is None else _rows(v, kv, where, dev)))
-    o = _SPAN.offsets
-    _check(call(at, at + o[1], T, 0 if k is None else at + o[2], 0 if v is None else at + o[3], workspace.data_ptr(),
+    seen = spans._seen
+    if not seen or seen[0] != dev:
+        seen = _spans_checked(spans, dev, where)
+    T = (v if k is None else k).shape[0]
+    kv = (T, cache.num_kv_heads, 128)
+    k_at, k_step = (0, 0) if k is None else _rows(k, kv, where, dev)
+    v_at, v_step = (0, 0) if v is None else _rows(v, kv, where, dev)
+    at = _SPAN.pack(*_cache_values(cache, False, dev, where), seen[1], seen[2], spans.first.data_ptr(), spans.end.data_ptr(),
+                    spans.token_offsets.data_ptr(), spans.block_table.data_ptr(), k_at, k_step, v_at, v_step)
+    _, o_spans, o_k, o_v = _SPAN.offsets
+    _check(call(at, at + o_spans, T, 0 if k is None else at + o_k, 0 if v is None else at + o_v, workspace.data_ptr(),
                 _nbytes(workspace), _stream(stream, dev)), where)
 
 

@@ -691,7 +691,7 @@ msa_status_t span_params(const msa_cache_t* c, const msa_spans_t* sp, int num_to
   if (!sp || sp->num_seqs < 1 || sp->max_blocks_per_seq < 1 || num_tokens < 0 || !sp->first || !sp->end || !sp->token_offsets ||
       !sp->block_table || !ws || !aligned4(sp->first, sp->end, sp->token_offsets, sp->block_table, ws))
     return MSA_ERR_INVALID_ARGUMENT;
-  if ((long)sp->max_blocks_per_seq * kBlock > (1l << 30)) return MSA_ERR_UNSUPPORTED;
+  if ((long)sp->max_blocks_per_seq * kBlock > (1l << 30) || num_tokens > (1 << 27)) return MSA_ERR_UNSUPPORTED;
   if (ws_bytes < 256) return MSA_ERR_WORKSPACE_TOO_SMALL;
   std::memset(&p, 0, sizeof(p));
   p.S = sp->num_seqs;

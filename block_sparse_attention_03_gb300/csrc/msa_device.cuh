@@ -149,6 +149,17 @@ __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.w
 // Until they have completed.
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
+// 16 bytes global -> shared by this thread, past the L1, in its groups of copies.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Until at most N of this thread's groups are on their way.
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // 2-D tensor (TMA) copy global -> shared at element coordinates (x, y).
 __device__ __forceinline__ void tma_load_2d(void* dst, const void* tmap, int32_t x, int32_t y, uint64_t* bar) {
   asm volatile(
@@ -368,24 +379,25 @@ __device__ __forceinline__ float2 fma2_down(float2 a, float2 b, float2 c) {
   return d;
 }
 
-// y[i] / s, correctly rounded, by Markstein's method (Computation of elementary
+// y / s, correctly rounded, by Markstein's method (Computation of elementary
 // functions on the IBM RISC System/6000, 1990): with r = RN(1/s), q = RN(y r) and
 // e = RN(y - q s) exact, RN(q + e r) is the correctly rounded quotient, three operations
 // an element; scales near the ends of fp32's range, where e could underflow or r
-// overflow, take the division itself.  fits: no quotient is infinite (its remainder
-// would be NaN).
+// overflow, and infinite quotients (their remainder would be NaN) take the division itself.
 // The sign of a zero is kept: the remainder is exact, and as -0 where it is zero it
 // leaves q = -0 alone.
+__device__ __forceinline__ bool divides(float s) { return s >= 8.27e-25f && s <= 1.2e24f; }  // 2^-80 to 2^80
+__device__ __forceinline__ float2 divide2(float2 y, float2 r, float2 minus_s) {
+  const float2 q = mul2(y, r);
+  return fma2(fma2_down(q, minus_s, y), r, q);
+}
+// fits: no quotient is infinite
 template <int N>
 __device__ __forceinline__ void divide(const float2 (&y)[N], float s, bool fits, float2 (&z)[N]) {
-  if (s >= 8.27e-25f && s <= 1.2e24f && fits) {  // 2^-80 to 2^80
+  if (divides(s) && fits) {
     const float r = __frcp_rn(s);
-    const float2 r2 = make_float2(r, r), n2 = make_float2(-s, -s);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float2 q = mul2(y[i], r2);
-      z[i] = fma2(fma2_down(q, n2, y[i]), r2, q);
-    }
+    for (int i = 0; i < N; ++i) z[i] = divide2(y[i], make_float2(r, r), make_float2(-s, -s));
   } else {
 #pragma unroll
     for (int i = 0; i < N; ++i) z[i] = make_float2(__fdiv_rn(y[i].x, s), __fdiv_rn(y[i].y, s));

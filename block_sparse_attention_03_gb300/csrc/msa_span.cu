@@ -29,81 +29,84 @@ struct SpanChunk {
   int32_t warp_sum[kSpanWarps];
 };
 
-// One block of one span.
+// One block of one span.  (The insert looks up 32 of a CTA's blocks at once, one a lane.)
 struct SpanBlock {
-  int p0, n;     // its first token's position, tokens
-  int row;       // the row of that token in the call's tensors
-  int phys;      // the block in the pool
-  int first;     // the span's first position
+  int n, at;  // its tokens, the first one's row in the block
+  int row;    // and in the call's tensors
+  int had;    // tokens that the block held in front of the span
+  int phys;   // the block table's entry
 };
 
-// Calls f(block, sub) for the items (block touched, sub < subs) that are this CTA's:
-// item i of all, in (sequence, block, sub) order, goes to CTA i mod the grid.
-template <class F>
-__device__ __forceinline__ void walk_spans(const SpanParams& p, int subs, SpanChunk& c, const F& f) {
+// The spans s0 .. s0 + 255: returns how many blocks they touch.  Block i of those, in
+// (sequence, position) order, goes to the CTAs (i mod gridDim.x, y); y is a head and K or V.
+// (The host bounds num_tokens so that 256 spans touch fewer than 2^31 blocks.)
+__device__ __forceinline__ int load_chunk(const SpanParams& p, SpanChunk& c, int s0) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  long base = 0;  // items in front of this chunk's
-  for (int s0 = 0; s0 < p.S; s0 += kSpanThreads) {
-    const int s = s0 + tid;
-    int first = 0, end = 0, off = 0, count = 0;
-    if (s < p.S) {
-      first = __ldg(p.first + s);
-      end = __ldg(p.end + s);
-      off = __ldg(p.offsets + s);
-      if (end > first) {
-        uint32_t bad = 0;
-        if (first < 0 || end > p.max_nb * kBlock) bad = FLAG_BAD_SEQLEN;
-        else if (off < 0 || off > p.num_tokens - (end - first)) bad = FLAG_NO_ROOM;
-        if (bad == 0) count = (end - 1) / kBlock - first / kBlock + 1;
-        else if (blockIdx.x == 0) raise_flag(p.status, bad, s);
-      }
+  const int s = s0 + tid;
+  int first = 0, end = 0, off = 0, count = 0;
+  if (s < p.S) {
+    first = __ldg(p.first + s);
+    end = __ldg(p.end + s);
+    off = __ldg(p.offsets + s);
+    if (end > first) {
+      uint32_t bad = 0;
+      if (first < 0 || end > p.max_nb * kBlock) bad = FLAG_BAD_SEQLEN;
+      else if (off < 0 || off > p.num_tokens - (end - first)) bad = FLAG_NO_ROOM;
+      if (bad == 0) count = (end - 1) / kBlock - first / kBlock + 1;
+      else if (blockIdx.x == 0 && blockIdx.y == 0) raise_flag(p.status, bad, s);
     }
-    int incl = count;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
-    }
-    __syncthreads();  // the former chunk has been read
-    if (lane == 31) c.warp_sum[warp] = incl;
-    __syncthreads();
-    int total = 0;
-#pragma unroll
-    for (int w = 0; w < kSpanWarps; ++w) {
-      const int v = c.warp_sum[w];
-      if (w < warp) incl += v;
-      total += v;
-    }
-    c.first[tid] = first;
-    c.end[tid] = end;
-    c.off[tid] = off;
-    c.before[tid] = incl - count;
-    __syncthreads();
-    const long items = (long)total * subs;
-    // the first of this chunk's items that is this CTA's
-    long i = ((long)blockIdx.x - base % gridDim.x + gridDim.x) % gridDim.x;
-    for (; i < items; i += gridDim.x) {
-      const int pair = (int)(i / subs), sub = (int)(i - (long)pair * subs);
-      int at = 0;  // the last sequence with no more than `pair` blocks before it: it touches one itself
-#pragma unroll
-      for (int step = kSpanThreads / 2; step > 0; step >>= 1)
-        if (c.before[at + step] <= pair) at += step;
-      const int blk = c.first[at] / kBlock + (pair - c.before[at]);
-      SpanBlock b;
-      b.first = c.first[at];
-      b.p0 = max(b.first, blk * kBlock);
-      b.n = min(c.end[at], (blk + 1) * kBlock) - b.p0;
-      b.row = c.off[at] + (b.p0 - b.first);
-      b.phys = __ldg(p.block_table + (size_t)(s0 + at) * p.max_nb + blk);
-      if (b.phys < 0 || b.phys >= p.num_blocks) {
-        if (sub == 0 && tid == 0) raise_flag(p.status, FLAG_BAD_BLOCK, b.phys);
-        continue;
-      }
-      f(b, sub);
-    }
-    base += items;
   }
+  int incl = count;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (s0 > 0) __syncthreads();  // the former chunk has been read
+  if (lane == 31) c.warp_sum[warp] = incl;
+  c.first[tid] = first;
+  c.end[tid] = end;
+  c.off[tid] = off;
+  __syncthreads();
+  int total = 0, front = 0;
+#pragma unroll
+  for (int w = 0; w < kSpanWarps; ++w) {
+    const int v = c.warp_sum[w];
+    if (w < warp) front += v;
+    total += v;
+  }
+  c.before[tid] = front + incl - count;
+  __syncthreads();
+  return total;
 }
+
+// Block i of the chunk's.
+__device__ __forceinline__ SpanBlock find_block(const SpanParams& p, const SpanChunk& c, int s0, int i) {
+  int at = 0;  // the last sequence with no more than i blocks before it: it touches one itself
+#pragma unroll
+  for (int step = kSpanThreads / 2; step > 0; step >>= 1)
+    if (c.before[at + step] <= i) at += step;
+  const int first = c.first[at], blk = first / kBlock + (i - c.before[at]);
+  const int p0 = max(first, blk * kBlock);
+  SpanBlock b;
+  b.n = min(c.end[at], (blk + 1) * kBlock) - p0;
+  b.row = c.off[at] + (p0 - first);
+  b.at = p0 % kBlock;
+  b.had = max(0, first - blk * kBlock);
+  b.phys = __ldg(p.block_table + (size_t)(s0 + at) * p.max_nb + blk);
+  return b;
+}
+__device__ __forceinline__ SpanBlock from_lane(const SpanBlock& b, int lane) {
+  SpanBlock r;
+  r.n = __shfl_sync(0xffffffffu, b.n, lane);
+  r.at = __shfl_sync(0xffffffffu, b.at, lane);
+  r.row = __shfl_sync(0xffffffffu, b.row, lane);
+  r.had = __shfl_sync(0xffffffffu, b.had, lane);
+  r.phys = __shfl_sync(0xffffffffu, b.phys, lane);
+  return r;
+}
+
+__device__ __forceinline__ bool in_pool(const SpanParams& p, int phys) { return phys >= 0 && phys < p.num_blocks; }
 
 // ---------------------------------------------------------------- insert
 
@@ -153,54 +156,71 @@ __device__ __forceinline__ int growth(float a, float b) {
   return k > 0 ? k : 0;
 }
 
+// Items on their way at once, each in a stage of 32 KB of shared memory.  A thread copies and
+// reads the same bytes, so the copies need no barrier.
+constexpr int kInsertStages = 2;
+constexpr int kInsertCtas = 3;  // CTAs an SM
+constexpr int kStride = 2 * kSpanWarps;  // a half warp takes a row: rows between a thread's
+
 template <int FMT>
-__global__ void __launch_bounds__(kSpanThreads) block_insert_kernel(const SpanParams p) {
+__global__ void __launch_bounds__(kSpanThreads, kInsertCtas) block_insert_kernel(const SpanParams p) {
+  extern __shared__ uint4 s_rows[];  // [stages][rows of a thread][threads]
   __shared__ SpanChunk chunk;
-  __shared__ uint32_t s_max[2][kSpanWarps];
+  __shared__ __align__(16) uint32_t s_max[2][kSpanWarps];
+  static_assert(kSpanWarps == 8, "all_max");
   constexpr float Q = FMT == FMT_I8B ? 127.f : 448.f;
   constexpr float kLeast = 1.17549435e-38f;  // 2^-126
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, l16 = lane & 15;
+  const int row0 = 2 * warp + (lane >> 4);  // this thread's rows: row0 + kStride i
+  const int h = blockIdx.y >> 1;
+  const bool is_v = blockIdx.y & 1;
+  const long step = is_v ? p.v_stride : p.k_stride;
+  const __nv_bfloat16* const rows = (is_v ? p.v_in : p.k_in) + h * kDim + 8 * l16 + row0 * step;
+  uint8_t* const codes = is_v ? p.vc : p.kc;
+  float* const scales = is_v ? p.vs : p.ks;
   int turn = 0;  // the half of s_max: an item's reads end before the item after next writes
-  walk_spans(p, 2 * p.H, chunk, [&](const SpanBlock& b, int sub) {
-    const int h = sub >> 1;
-    const bool is_v = sub & 1;
-    const __nv_bfloat16* src = (is_v ? p.v_in : p.k_in) + (long)b.row * (is_v ? p.v_stride : p.k_stride) + h * kDim + 8 * l16;
-    const long step = is_v ? p.v_stride : p.k_stride;
-    const size_t head = (size_t)b.phys * p.H + h;
-    uint8_t* data = (is_v ? p.vc : p.kc) + head * (kBlock * kDim);
-    float* scale = (is_v ? p.vs : p.ks) + head;
-    const int had = max(0, b.first - b.p0 / kBlock * kBlock);
-    const float old = had > 0 ? *scale : 0.f;
-    // this half warp's rows, and the largest magnitude (as bits: they order as the values do)
+
+  auto fetch = [&](const SpanBlock& b, int stage) {
+    const __nv_bfloat16* src = rows + (long)b.row * step;
+    const uint32_t dst = smem_u32(s_rows + stage * (kRowsPerThread * kSpanThreads) + tid);
+#pragma unroll
+    for (int i = 0; i < kRowsPerThread; ++i) {
+      if (kStride * i >= b.n) break;
+      if (row0 + kStride * i < b.n) cp_async16(dst + i * (kSpanThreads * 16), src);
+      src += kStride * step;
+    }
+  };
+  auto scale_of = [&](const SpanBlock& b) { return b.had > 0 && in_pool(p, b.phys) ? scales[(size_t)b.phys * p.H + h] : 0.f; };
+  auto all_max = [&](uint32_t v) {  // of the CTA; one barrier
+    v = __reduce_max_sync(0xffffffffu, v);
+    if (lane == 0) s_max[turn][warp] = v;
+    __syncthreads();
+    const uint4 a = *reinterpret_cast<const uint4*>(s_max[turn]), c = *reinterpret_cast<const uint4*>(s_max[turn] + 4);
+    turn ^= 1;
+    return max(max(max(a.x, a.y), max(a.z, a.w)), max(max(c.x, c.y), max(c.z, c.w)));
+  };
+  auto insert = [&](const SpanBlock& b, float old, int stage) {
+    const uint4* mine = s_rows + stage * (kRowsPerThread * kSpanThreads) + tid;
+    // the largest magnitude; as bits they order as the values do, NaN above all
     uint4 x[kRowsPerThread];
-    uint32_t m = 0;
+    __nv_bfloat162 m2 = __floats2bfloat162_rn(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < kRowsPerThread; ++i) {
-      const int r = 2 * kSpanWarps * i + 2 * warp + (lane >> 4);
-      x[i] = r < b.n ? *reinterpret_cast<const uint4*>(src + r * step) : make_uint4(0u, 0u, 0u, 0u);
+      if (kStride * i >= b.n) break;
+      x[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (row0 + kStride * i < b.n) x[i] = mine[i * kSpanThreads];
+      const __nv_bfloat162* w = reinterpret_cast<const __nv_bfloat162*>(&x[i]);
+      m2 = __hmax2_nan(m2, __hmax2_nan(__hmax2_nan(__habs2(w[0]), __habs2(w[1])), __hmax2_nan(__habs2(w[2]), __habs2(w[3]))));
     }
-#pragma unroll
-    for (int i = 0; i < kRowsPerThread; ++i) {
-      const uint32_t w[4] = {x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu, x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu};
-      m = __vmaxu2(m, __vmaxu2(__vmaxu2(w[0], w[1]), __vmaxu2(w[2], w[3])));
-    }
-    auto all_max = [&](uint32_t v) {  // of the CTA; one barrier
-      v = max(v & 0xffffu, v >> 16);
-      v = __reduce_max_sync(0xffffffffu, v);
-      if (lane == 0) s_max[turn][warp] = v;
-      __syncthreads();
-#pragma unroll
-      for (int w = 0; w < kSpanWarps; ++w) v = max(v, s_max[turn][w]);
-      turn ^= 1;
-      return v;
-    };
-    m = all_max(m);
+    uint32_t m = *reinterpret_cast<uint32_t*>(&m2);
+    m = all_max(max(m & 0x7fffu, (m >> 16) & 0x7fffu));
     const bool finite = m < 0x7f80u;
     if (!finite) {  // again, over the finite elements
       uint32_t f = 0;
-#pragma unroll
-      for (int i = 0; i < kRowsPerThread; ++i) {
-        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll 1
+      for (int i = 0; row0 + kStride * i < b.n; ++i) {
+        const uint4 v = mine[i * kSpanThreads];
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const uint32_t lo = w[j] & 0x7fffu, hi = (w[j] >> 16) & 0x7fffu;
@@ -209,17 +229,18 @@ __global__ void __launch_bounds__(kSpanThreads) block_insert_kernel(const SpanPa
       }
       m = all_max(f);
     }
+    const size_t head = (size_t)b.phys * p.H + h;
+    uint8_t* const data = codes + head * (kBlock * kDim);
     const float need = fmaxf(__fdiv_rn(__uint_as_float(m << 16), Q), kLeast);
     float s = need;
-    int k = 0;
-    if (had > 0) {
+    if (b.had > 0) {
       s = normal_positive(old) ? old : kLeast;
-      k = growth(s, need);
+      const int k = growth(s, need);
       if (k > 0) {
         // (s x 2^k is below 2 need: no overflow; a factor below 2^-126 leaves nothing of a code)
         s = __uint_as_float(__float_as_uint(s) + ((uint32_t)k << 23));
         const float f = pow2i(k < 126 ? -k : -126);
-        for (int i = tid; i < had * 8; i += kSpanThreads) {
+        for (int i = tid; i < b.had * 8; i += kSpanThreads) {
           uint4 w = *reinterpret_cast<const uint4*>(data + 16 * i);
           w.x = move_codes<FMT>(w.x, f);
           w.y = move_codes<FMT>(w.y, f);
@@ -229,40 +250,105 @@ __global__ void __launch_bounds__(kSpanThreads) block_insert_kernel(const SpanPa
         }
       }
     }
-    if (tid == 0) *scale = s;
-    uint8_t* dst = data + (b.p0 % kBlock) * kDim + 8 * l16;
+    if (tid == 0) scales[head] = s;
+    uint8_t* const dst = data + (b.at + row0) * kDim + 8 * l16;
+    if (finite && divides(s)) {
+      const float inv = __frcp_rn(s);
+      const float2 r2 = make_float2(inv, inv), n2 = make_float2(-s, -s);
 #pragma unroll
-    for (int i = 0; i < kRowsPerThread; ++i) {
-      const int r = 2 * kSpanWarps * i + 2 * warp + (lane >> 4);
-      if (2 * kSpanWarps * i >= b.n) break;
-      const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-      float2 y[4], z[4];
+      for (int i = 0; i < kRowsPerThread; ++i) {
+        if (kStride * i >= b.n) break;
+        const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        float2 z[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) y[j] = make_float2(__uint_as_float(u[j] << 16), __uint_as_float(u[j] & 0xffff0000u));
-      divide(y, s, finite, z);
-      uint2 c;
-      if (finite) c = make_uint2(block_codes<FMT, false>(z[0], z[1]), block_codes<FMT, false>(z[2], z[3]));
-      else c = make_uint2(block_codes<FMT, true>(z[0], z[1]), block_codes<FMT, true>(z[2], z[3]));
-      if (r < b.n) *reinterpret_cast<uint2*>(dst + r * kDim) = c;
+        for (int j = 0; j < 4; ++j) z[j] = divide2(make_float2(__uint_as_float(u[j] << 16), __uint_as_float(u[j] & 0xffff0000u)), r2, n2);
+        const uint2 c = make_uint2(block_codes<FMT, false>(z[0], z[1]), block_codes<FMT, false>(z[2], z[3]));
+        if (row0 + kStride * i < b.n) *reinterpret_cast<uint2*>(dst + kStride * i * kDim) = c;
+      }
+    } else {  // infinities, NaN, scales near the ends of fp32's range
+#pragma unroll 1
+      for (int i = 0; row0 + kStride * i < b.n; ++i) {
+        const uint4 v = mine[i * kSpanThreads];
+        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+        float2 z[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          z[j] = make_float2(__fdiv_rn(__uint_as_float(u[j] << 16), s), __fdiv_rn(__uint_as_float(u[j] & 0xffff0000u), s));
+        *reinterpret_cast<uint2*>(dst + kStride * i * kDim) = make_uint2(block_codes<FMT, true>(z[0], z[1]), block_codes<FMT, true>(z[2], z[3]));
+      }
     }
-  });
+  };
+
+  uint32_t i = blockIdx.x;  // this CTA's next block among those of the chunk
+  for (int s0 = 0; s0 < p.S; s0 += kSpanThreads) {
+    const uint32_t total = load_chunk(p, chunk, s0), grid = gridDim.x;
+    const int count = i < total ? (int)((total - 1 - i) / grid) + 1 : 0;  // this CTA's blocks of the chunk
+    SpanBlock b[kInsertStages], some;  // what is on its way, b[0] first; the next ones, one a lane
+    auto start = [&](int k, int stage) {  // block k of the CTA's
+      if (k < count) {
+        if ((k & 31) == 0) some = find_block(p, chunk, s0, (int)min(i + (k + lane) * grid, total - 1));
+        fetch(b[kInsertStages - 1] = from_lane(some, k & 31), stage);
+      }
+      cp_async_commit();
+    };
+#pragma unroll
+    for (int k = 0; k < kInsertStages - 1; ++k) {
+      start(k, k);
+      b[k] = b[kInsertStages - 1];
+    }
+    float old = count > 0 ? scale_of(b[0]) : 0.f;
+    int stage = 0;
+#pragma unroll 1
+    for (int k = 0; k < count; ++k) {
+      start(k + kInsertStages - 1, stage == 0 ? kInsertStages - 1 : stage - 1);
+      const float next = k + 1 < count ? scale_of(b[1]) : 0.f;
+      cp_async_wait<kInsertStages - 1>();
+      if (in_pool(p, b[0].phys)) insert(b[0], old, stage);
+      else if (blockIdx.y == 0 && tid == 0) raise_flag(p.status, FLAG_BAD_BLOCK, b[0].phys);
+#pragma unroll
+      for (int j = 0; j + 1 < kInsertStages; ++j) b[j] = b[j + 1];
+      old = next;
+      stage = stage + 1 == kInsertStages ? 0 : stage + 1;
+    }
+    i = i + count * grid - total;
+  }
 }
 
 // ---------------------------------------------------------------- read
 
-// Eight elements [8 l16, 8 l16 + 8) of a cache row, as bf16.
-template <int FMT>
-__device__ __forceinline__ uint4 read_row(const uint8_t* __restrict__ data, const float* __restrict__ scale,
-                                          const uint8_t* __restrict__ sf, float g, bool nv_round, size_t row, int l16) {
-  if constexpr (FMT == FMT_BF16) return __ldg(reinterpret_cast<const uint4*>(data + row * 256) + l16);
-  float v[8];
+// A half warp takes a row of a cache, a lane its elements [8 l16, 8 l16 + 8): the bits as they
+// are stored, then as bf16.
+struct Raw {
+  uint4 w;
   float s;
+};
+template <int FMT>
+__device__ __forceinline__ Raw load_row(const uint8_t* __restrict__ data, const float* __restrict__ scale,
+                                        const uint8_t* __restrict__ sf, size_t row, int l16) {
+  Raw r;
+  if constexpr (FMT == FMT_BF16) {
+    r.w = __ldg(reinterpret_cast<const uint4*>(data + row * 256) + l16);
+  } else if constexpr (FMT == FMT_NVFP4) {
+    r.w.x = __ldg(reinterpret_cast<const uint32_t*>(data + row * 64) + l16);
+    r.w.y = __ldg(sf + row * 8 + (l16 >> 1));
+  } else {
+    const uint2 w = __ldg(reinterpret_cast<const uint2*>(data + row * 128) + l16);
+    r.w.x = w.x;
+    r.w.y = w.y;
+    if constexpr (FMT == FMT_FP8) r.s = __ldg(scale + row);
+  }
+  return r;
+}
+// s: the scale of the tensor or of the block
+template <int FMT>
+__device__ __forceinline__ uint4 row_bf16(const Raw& r, float s, bool nv_round) {
+  if constexpr (FMT == FMT_BF16) return r.w;
+  float v[8];
   if constexpr (FMT == FMT_NVFP4) {
-    const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(data + row * 64) + l16);
-    const float e = e4m3_to_float(__ldg(sf + row * 8 + (l16 >> 1)));
+    const float e = e4m3_to_float((uint8_t)r.w.y);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t h = e2m1x2_to_f16x2((w >> (8 * i)) & 0xffu);
+      const uint32_t h = e2m1x2_to_f16x2((r.w.x >> (8 * i)) & 0xffu);
       const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h));
       v[2 * i] = __fmul_rn(x.x, e);
       v[2 * i + 1] = __fmul_rn(x.y, e);
@@ -272,13 +358,11 @@ __device__ __forceinline__ uint4 read_row(const uint8_t* __restrict__ data, cons
         v[2 * i + 1] = y.y;
       }
     }
-    s = g;
   } else {
-    const uint2 w = __ldg(reinterpret_cast<const uint2*>(data + row * 128) + l16);
-    s = __ldg(scale + (FMT == FMT_FP8 ? row : row / kBlock));
+    if constexpr (FMT == FMT_FP8) s = r.s;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t h = (i < 2 ? w.x : w.y) >> (16 * (i & 1));
+      const uint32_t h = (i < 2 ? r.w.x : r.w.y) >> (16 * (i & 1));
       if constexpr (FMT == FMT_I8B) {
         v[2 * i] = (float)(int8_t)h;
         v[2 * i + 1] = (float)(int8_t)(h >> 8);
@@ -294,49 +378,67 @@ __device__ __forceinline__ uint4 read_row(const uint8_t* __restrict__ data, cons
 }
 
 template <int FMT>
-__global__ void __launch_bounds__(kSpanThreads) cache_read_kernel(const SpanParams p) {
+__global__ void __launch_bounds__(kSpanThreads, 4) cache_read_kernel(const SpanParams p) {
   __shared__ SpanChunk chunk;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l16 = lane & 15;
-  const int sides = (p.k_out != nullptr) + (p.v_out != nullptr);
-  walk_spans(p, sides * p.H, chunk, [&](const SpanBlock& b, int sub) {
-    const int h = sub / sides;
-    const bool is_v = p.k_out == nullptr || sub - h * sides == 1;
-    const size_t row0 = ((size_t)b.phys * p.H + h) * kBlock + b.p0 % kBlock;
-    const long step = is_v ? p.v_stride : p.k_stride;
-    __nv_bfloat16* dst = (is_v ? p.v_out : p.k_out) + (long)b.row * step + h * kDim + 8 * l16;
+  const int h = blockIdx.y % p.H;
+  const bool is_v = p.k_out == nullptr || (int)blockIdx.y >= p.H;
+  const long step = is_v ? p.v_stride : p.k_stride;
+  __nv_bfloat16* rows = (is_v ? p.v_out : p.k_out) + h * kDim + 8 * l16;
+  const uint8_t* data = is_v ? p.vc : p.kc;
+  const uint8_t* sf = is_v ? p.vsf : p.ksf;
+  const float* scale = is_v ? p.vs : p.ks;
+  const int row0 = 2 * warp + (lane >> 4);  // this thread's rows: row0 + 16 i
+  uint32_t i = blockIdx.x;                  // this CTA's next block among those of the chunk
+  for (int s0 = 0; s0 < p.S; s0 += kSpanThreads) {
+    const uint32_t total = load_chunk(p, chunk, s0);
+    for (; i < total; i += gridDim.x) {
+      const SpanBlock b = find_block(p, chunk, s0, i);
+      if (!in_pool(p, b.phys)) {
+        if (blockIdx.y == 0 && threadIdx.x == 0) raise_flag(p.status, FLAG_BAD_BLOCK, b.phys);
+        continue;
+      }
+      const size_t head = (size_t)b.phys * p.H + h, from = head * kBlock + b.at + row0;
+      __nv_bfloat16* dst = rows + ((long)b.row + row0) * step;
+      Raw x[kRowsPerThread];  // all of them on their way before the first is used
 #pragma unroll
-    for (int i = 0; i < kRowsPerThread; ++i) {
-      const int r = 2 * kSpanWarps * i + 2 * warp + (lane >> 4);
-      if (r < b.n)
-        *reinterpret_cast<uint4*>(dst + r * step) = read_row<FMT>(is_v ? p.vc : p.kc, is_v ? p.vs : p.ks, is_v ? p.vsf : p.ksf,
-                                                                  is_v ? p.vg : p.kg, p.nv_round, row0 + r, l16);
+      for (int k = 0; k < kRowsPerThread; ++k)
+        if (row0 + 16 * k < b.n) x[k] = load_row<FMT>(data, scale, sf, from + 16 * k, l16);
+      const float s = FMT == FMT_NVFP4 ? (is_v ? p.vg : p.kg) : FMT == FMT_I8B || FMT == FMT_F8B ? __ldg(scale + head) : 1.f;
+#pragma unroll
+      for (int k = 0; k < kRowsPerThread; ++k)
+        if (row0 + 16 * k < b.n) *reinterpret_cast<uint4*>(dst + 16 * k * step) = row_bf16<FMT>(x[k], s, p.nv_round);
     }
-  });
+    i -= total;
+  }
 }
 
-// CTAs for the items of spans with `tokens` tokens in all: a span of n tokens touches
-// at most min(n, n / 128 + 2) blocks.
-unsigned span_grid(const SpanParams& p, int subs, int num_sms, int per_sm) {
+// Blocks that spans with `tokens` tokens in all touch at most: n tokens min(n, n / 128 + 2).
+long most_blocks(const SpanParams& p) {
   const long tokens = p.num_tokens, spans = p.S < p.num_tokens ? p.S : p.num_tokens;
-  long blocks = tokens / kBlock + 2 * spans;
-  if (blocks > tokens) blocks = tokens;
-  long grid = blocks * subs;
-  const long cap = (long)num_sms * per_sm;
-  if (grid > cap) grid = cap;
-  return (unsigned)(grid < 1 ? 1 : grid);
+  const long blocks = tokens / kBlock + 2 * spans;
+  return blocks < tokens ? blocks : tokens;
+}
+
+// CTAs: (blocks, heads x K and V), no more than fit on the GPU.
+dim3 span_grid(const SpanParams& p, int subs, int ctas) {
+  const long blocks = most_blocks(p), cap = ctas > subs ? ctas / subs : 1;
+  return dim3((unsigned)(blocks > cap ? cap : blocks), (unsigned)subs);
 }
 
 }  // namespace
 
 cudaError_t launch_block_insert(const SpanParams& p, int fmt, int num_sms, cudaStream_t st) {
-  const unsigned grid = span_grid(p, 2 * p.H, num_sms, 4);
-  if (fmt == FMT_I8B) block_insert_kernel<FMT_I8B><<<grid, kSpanThreads, 0, st>>>(p);
-  else block_insert_kernel<FMT_F8B><<<grid, kSpanThreads, 0, st>>>(p);
+  const int smem = kInsertStages * kRowsPerThread * kSpanThreads * (int)sizeof(uint4);
+  auto kern = fmt == FMT_I8B ? block_insert_kernel<FMT_I8B> : block_insert_kernel<FMT_F8B>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kern<<<span_grid(p, 2 * p.H, num_sms * kInsertCtas), kSpanThreads, smem, st>>>(p);
   return cudaGetLastError();
 }
 
 cudaError_t launch_cache_read(const SpanParams& p, int fmt, int num_sms, cudaStream_t st) {
-  const unsigned grid = span_grid(p, ((p.k_out != nullptr) + (p.v_out != nullptr)) * p.H, num_sms, 8);
+  const dim3 grid = span_grid(p, ((p.k_out != nullptr) + (p.v_out != nullptr)) * p.H, num_sms * 4);
   switch (fmt) {
     case FMT_BF16: cache_read_kernel<FMT_BF16><<<grid, kSpanThreads, 0, st>>>(p); break;
     case FMT_FP8: cache_read_kernel<FMT_FP8><<<grid, kSpanThreads, 0, st>>>(p); break;

@@ -328,7 +328,7 @@ typedef struct {
  * Rows of a block behind end[s] are left as they were.
  * Flagged on the device and skipped: a span with first < 0 or end beyond
  * max_blocks_per_seq * 128, a span whose rows are not all inside num_tokens, and the
- * tokens of a block outside the pool.  A block may be in the spans of one sequence
+ * tokens of a block outside the pool.  num_tokens <= 2^27.  A block may be in the spans of one sequence
  * only (two race).  k and v may not overlap the cache.
  * The call writes through the cache's pointers.  Deterministic.  workspace: at least
  * 256 bytes; only its status word is used. */

@@ -45,7 +45,7 @@ def test_span_refusals(lib, name, kv):  # noqa: F811
                 dict(s__max_blocks_per_seq=0), dict(s__first=None), dict(s__end=None), dict(s__token_offsets=None),
                 dict(s__block_table=None), dict(s__first=18), dict(s__end=33), dict(s__token_offsets=50), dict(s__block_table=67)):
         assert call(**bad) == 1, bad
-    assert call(s__max_blocks_per_seq=(1 << 23) + 1) == 2 and call(c__num_kv_heads=9) == 2 and call(c__head_dim=64) == 2
+    assert call(tokens=(1 << 27) + 1) == 2 and call(s__max_blocks_per_seq=(1 << 23) + 1) == 2 and call(c__num_kv_heads=9) == 2 and call(c__head_dim=64) == 2
     for bad in ((None, 4096), (24, 4096), (16, 4100), (16, -8)):
         assert call(k=bad) == 1 and call(v=bad) == 1, bad
     for unknown in (3, 7, 10):
