@@ -38,7 +38,7 @@ struct SpanBlock {
 };
 
 // The spans s0 .. s0 + 255: returns how many blocks they touch.  Block i of those, in
-// (sequence, position) order, goes to the CTAs (i mod gridDim.x, y); y is a head and K or V.
+// (sequence, position) order, goes to the CTAs (x, i mod gridDim.y); x is a head and K or V.
 // (The host bounds num_tokens so that 256 spans touch fewer than 2^31 blocks.)
 __device__ __forceinline__ int load_chunk(const SpanParams& p, SpanChunk& c, int s0) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -53,7 +53,7 @@ __device__ __forceinline__ int load_chunk(const SpanParams& p, SpanChunk& c, int
       if (first < 0 || end > p.max_nb * kBlock) bad = FLAG_BAD_SEQLEN;
       else if (off < 0 || off > p.num_tokens - (end - first)) bad = FLAG_NO_ROOM;
       if (bad == 0) count = (end - 1) / kBlock - first / kBlock + 1;
-      else if (blockIdx.x == 0 && blockIdx.y == 0) raise_flag(p.status, bad, s);
+      else if (blockIdx.y == 0 && blockIdx.x == 0) raise_flag(p.status, bad, s);
     }
   }
   int incl = count;
@@ -172,8 +172,8 @@ __global__ void __launch_bounds__(kSpanThreads, kInsertCtas) block_insert_kernel
   constexpr float kLeast = 1.17549435e-38f;  // 2^-126
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, l16 = lane & 15;
   const int row0 = 2 * warp + (lane >> 4);  // this thread's rows: row0 + kStride i
-  const int h = blockIdx.y >> 1;
-  const bool is_v = blockIdx.y & 1;
+  const int h = blockIdx.x >> 1;
+  const bool is_v = blockIdx.x & 1;
   const long step = is_v ? p.v_stride : p.k_stride;
   const __nv_bfloat16* const rows = (is_v ? p.v_in : p.k_in) + h * kDim + 8 * l16 + row0 * step;
   uint8_t* const codes = is_v ? p.vc : p.kc;
@@ -279,9 +279,9 @@ __global__ void __launch_bounds__(kSpanThreads, kInsertCtas) block_insert_kernel
     }
   };
 
-  uint32_t i = blockIdx.x;  // this CTA's next block among those of the chunk
+  uint32_t i = blockIdx.y;  // this CTA's next block among those of the chunk
   for (int s0 = 0; s0 < p.S; s0 += kSpanThreads) {
-    const uint32_t total = load_chunk(p, chunk, s0), grid = gridDim.x;
+    const uint32_t total = load_chunk(p, chunk, s0), grid = gridDim.y;
     const int count = i < total ? (int)((total - 1 - i) / grid) + 1 : 0;  // this CTA's blocks of the chunk
     SpanBlock b[kInsertStages], some;  // what is on its way, b[0] first; the next ones, one a lane
     auto start = [&](int k, int stage) {  // block k of the CTA's
@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(kSpanThreads, kInsertCtas) block_insert_kernel
       const float next = k + 1 < count ? scale_of(b[1]) : 0.f;
       cp_async_wait<kInsertStages - 1>();
       if (in_pool(p, b[0].phys)) insert(b[0], old, stage);
-      else if (blockIdx.y == 0 && tid == 0) raise_flag(p.status, FLAG_BAD_BLOCK, b[0].phys);
+      else if (blockIdx.x == 0 && tid == 0) raise_flag(p.status, FLAG_BAD_BLOCK, b[0].phys);
 #pragma unroll
       for (int j = 0; j + 1 < kInsertStages; ++j) b[j] = b[j + 1];
       old = next;
@@ -377,25 +377,27 @@ __device__ __forceinline__ uint4 row_bf16(const Raw& r, float s, bool nv_round) 
                     pack_bf16x2(__fmul_rn(v[4], s), __fmul_rn(v[5], s)), pack_bf16x2(__fmul_rn(v[6], s), __fmul_rn(v[7], s)));
 }
 
+constexpr int kReadCtas = 4;  // CTAs an SM
+
 template <int FMT>
-__global__ void __launch_bounds__(kSpanThreads, 4) cache_read_kernel(const SpanParams p) {
+__global__ void __launch_bounds__(kSpanThreads, kReadCtas) cache_read_kernel(const SpanParams p) {
   __shared__ SpanChunk chunk;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l16 = lane & 15;
-  const int h = blockIdx.y % p.H;
-  const bool is_v = p.k_out == nullptr || (int)blockIdx.y >= p.H;
+  const int h = blockIdx.x % p.H;
+  const bool is_v = p.k_out == nullptr || (int)blockIdx.x >= p.H;
   const long step = is_v ? p.v_stride : p.k_stride;
   __nv_bfloat16* rows = (is_v ? p.v_out : p.k_out) + h * kDim + 8 * l16;
   const uint8_t* data = is_v ? p.vc : p.kc;
   const uint8_t* sf = is_v ? p.vsf : p.ksf;
   const float* scale = is_v ? p.vs : p.ks;
   const int row0 = 2 * warp + (lane >> 4);  // this thread's rows: row0 + 16 i
-  uint32_t i = blockIdx.x;                  // this CTA's next block among those of the chunk
+  uint32_t i = blockIdx.y;                  // this CTA's next block among those of the chunk
   for (int s0 = 0; s0 < p.S; s0 += kSpanThreads) {
     const uint32_t total = load_chunk(p, chunk, s0);
-    for (; i < total; i += gridDim.x) {
+    for (; i < total; i += gridDim.y) {
       const SpanBlock b = find_block(p, chunk, s0, i);
       if (!in_pool(p, b.phys)) {
-        if (blockIdx.y == 0 && threadIdx.x == 0) raise_flag(p.status, FLAG_BAD_BLOCK, b.phys);
+        if (blockIdx.x == 0 && threadIdx.x == 0) raise_flag(p.status, FLAG_BAD_BLOCK, b.phys);
         continue;
       }
       const size_t head = (size_t)b.phys * p.H + h, from = head * kBlock + b.at + row0;
@@ -407,7 +409,7 @@ __global__ void __launch_bounds__(kSpanThreads, 4) cache_read_kernel(const SpanP
       const float s = FMT == FMT_NVFP4 ? (is_v ? p.vg : p.kg) : FMT == FMT_I8B || FMT == FMT_F8B ? __ldg(scale + head) : 1.f;
 #pragma unroll
       for (int k = 0; k < kRowsPerThread; ++k)
-        if (row0 + 16 * k < b.n) *reinterpret_cast<uint4*>(dst + 16 * k * step) = row_bf16<FMT>(x[k], s, p.nv_round);
+        if (row0 + 16 * k < b.n) __stcs(reinterpret_cast<uint4*>(dst + 16 * k * step), row_bf16<FMT>(x[k], s, p.nv_round));
     }
     i -= total;
   }
@@ -420,10 +422,10 @@ long most_blocks(const SpanParams& p) {
   return blocks < tokens ? blocks : tokens;
 }
 
-// CTAs: (blocks, heads x K and V), no more than fit on the GPU.
+// CTAs: (heads x K and V, blocks), `ctas` at most.
 dim3 span_grid(const SpanParams& p, int subs, int ctas) {
   const long blocks = most_blocks(p), cap = ctas > subs ? ctas / subs : 1;
-  return dim3((unsigned)(blocks > cap ? cap : blocks), (unsigned)subs);
+  return dim3((unsigned)subs, (unsigned)(blocks > cap ? cap : blocks));
 }
 
 }  // namespace
@@ -438,7 +440,7 @@ cudaError_t launch_block_insert(const SpanParams& p, int fmt, int num_sms, cudaS
 }
 
 cudaError_t launch_cache_read(const SpanParams& p, int fmt, int num_sms, cudaStream_t st) {
-  const dim3 grid = span_grid(p, ((p.k_out != nullptr) + (p.v_out != nullptr)) * p.H, num_sms * 4);
+  const dim3 grid = span_grid(p, ((p.k_out != nullptr) + (p.v_out != nullptr)) * p.H, num_sms * (p.S <= kSpanThreads ? 64 : kReadCtas));
   switch (fmt) {
     case FMT_BF16: cache_read_kernel<FMT_BF16><<<grid, kSpanThreads, 0, st>>>(p); break;
     case FMT_FP8: cache_read_kernel<FMT_FP8><<<grid, kSpanThreads, 0, st>>>(p); break;
