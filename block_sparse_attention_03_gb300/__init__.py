@@ -192,7 +192,7 @@ class PagedCache:
 
     def __setattr__(self, name, value):
         # the serving calls look at the tensors once (_checked), and again when a field is set
-        self.__dict__["_seen"] = ()
+        self.__dict__["_seen"] = self.__dict__["_packed"] = ()
         self.__dict__[name] = value
 
     def struct(self) -> MsaCacheT:
@@ -335,8 +335,26 @@ def _cache_values(c: PagedCache, index: bool, dev: int, where: str):
             _p(c.idx_scale), c.k_global, c.v_global, c.idx_global, NVFP4_MODES.get(c.nvfp4_mode, -1))
 
 
-_DENSE = _Layout(_CACHE, _BATCH, _CONFIG, _QUERY)
-_SPAN = _Layout(_CACHE, _SPANS, _ROWS, _ROWS)
+_CACHE_PACKER = _struct.Struct("@" + _CACHE + "0P")
+_PACKED = f"{_CACHE_PACKER.size}s"
+
+
+def _packed_cache(c: PagedCache, dev: int, where: str) -> bytes:
+    """The cache's struct as bytes, without the index keys, for its fields and its tensors' present addresses."""
+    k, v, ks, vs = c.k.data_ptr(), c.v.data_ptr(), c.k_scale, c.v_scale
+    got, seen = c._packed, c._seen
+    if (got and got[0] == k and got[1] == v and seen and seen[0] == dev
+            and (ks is None or got[2] == ks.data_ptr()) and (vs is None or got[3] == vs.data_ptr())):
+        return got[4]
+    values = _cache_values(c, False, dev, where)
+    raw = _CACHE_PACKER.pack(*values[:13], 0, 0, 0, *values[16:])
+    if c.k_sf is None and c.v_sf is None:  # (the addresses that were compared are all there are)
+        c.__dict__["_packed"] = (k, v, _p(ks), _p(vs), raw)
+    return raw
+
+
+_ATTEND = _Layout(_PACKED, _BATCH, _CONFIG, _QUERY)
+_SPAN = _Layout(_PACKED, _SPANS, _ROWS, _ROWS)
 _ROPE = _Layout(_CACHE, _ROWS, _QUERY, _ROWS, _QUERY, _ROWS, _ROWS, _ROWS, _NORM)
 
 
@@ -347,7 +365,9 @@ _query_types = {}  # the element types of a query of each kind
 def _torch_names() -> None:
     global _int32, _bf16, _f32, _device
     import torch
-    _int32, _bf16, _f32, _device = torch.int32, torch.bfloat16, torch.float32, torch.cuda.current_device
+    # (torch.cuda.current_device without its look at whether CUDA is up: the tensors are on a GPU)
+    _device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    _int32, _bf16, _f32 = torch.int32, torch.bfloat16, torch.float32
     _query_types.update(bf16=(torch.bfloat16,), fp8=(torch.uint8, torch.float8_e4m3fn, torch.int8))
 
 
@@ -406,11 +426,42 @@ def _check_block_cache(cache, where: str) -> None:
 
 def msa_sparse_attend(cache, batch, cfg, q: Query, num_q_heads: int, topk_idx, out, lse, workspace,
                       stream=None) -> None:
-    _check_block_cache(cache, "msa_sparse_attend")
+    if cache.kv_dtype in ("int8_block", "fp8_block"):
+        _sparse_by_block(cache, batch, cfg, q, num_q_heads, topk_idx, out, lse, workspace, stream)
+        return
     c, b, f, qq = cache.struct(), batch.struct(), cfg.struct(), q.struct()
     _check(lib().msa_sparse_attend(_ref(c), _ref(b), _ref(f), _ref(qq), num_q_heads, _ptr(topk_idx), _ptr(out),
                                    _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(),
                                    _stream(stream)), "msa_sparse_attend")
+
+
+def _sparse_by_block(cache, batch, cfg, q, num_q_heads, topk_idx, out, lse, workspace, stream) -> None:
+    """The sparse attend over a cache with block scales.  topk_idx: int32 [S * q_per_seq][num_kv_heads][topk]; q.data, out:
+    [S * q_per_seq][num_q_heads][128], lse: fp32 [S * q_per_seq][num_q_heads] or None, all dense."""
+    if _int32 is None:
+        _torch_names()
+    lens, table, data = batch.seq_lens, batch.block_table, q.data
+    shape, tokens, dev = table.shape, lens.numel() * batch.q_per_seq, cache.k.get_device()
+    rows = tokens * num_q_heads
+    if (dev < 0 or dev != _device() or len(shape) != 2 or shape[0] != lens.numel()
+            or lens.dtype is not _int32 or table.dtype is not _int32 or not lens.is_contiguous() or not table.is_contiguous()
+            or topk_idx.dtype is not _int32 or topk_idx.numel() != tokens * cache.num_kv_heads * cfg.topk
+            or not topk_idx.is_contiguous() or topk_idx.get_device() != dev
+            or data.numel() != rows * 128 or not data.is_contiguous() or data.dtype not in _query_types.get(q.dtype, ())
+            or out.numel() != rows * 128 or not out.is_contiguous() or out.dtype is not _bf16
+            or (lse is not None and (lse.numel() != rows or not lse.is_contiguous() or lse.dtype is not _f32
+                                    or lse.get_device() != dev))
+            or lens.get_device() != dev or table.get_device() != dev or data.get_device() != dev or out.get_device() != dev
+            or workspace.get_device() != dev):
+        raise MsaError(1, "msa_sparse_attend")
+    at = _ATTEND.pack(_packed_cache(cache, dev, "msa_sparse_attend"),
+                      shape[0], batch.q_per_seq, shape[1], lens.data_ptr(), table.data_ptr(),
+                      cfg.topk, cfg.init_blocks, cfg.local_blocks, cfg.index_scale, cfg.sm_scale,
+                      SCORE_TYPES.get(cfg.score_type, -1), PREFILL_SELECT.get(cfg.prefill_select, -1),
+                      data.data_ptr(), DTYPES[q.dtype], q.scale)
+    _, b, f, qq = _ATTEND.offsets
+    _check(lib().msa_sparse_attend(at, at + b, at + f, at + qq, num_q_heads, topk_idx.data_ptr(), out.data_ptr(), _p(lse),
+                                   workspace.data_ptr(), workspace.nbytes, _stream(stream, dev)), "msa_sparse_attend")
 
 
 def msa_decode(cache, batch, cfg, index_q: Query, q: Query, num_q_heads: int, topk_idx, out, lse, workspace,
@@ -490,11 +541,11 @@ def _span_call(call, where: str, cache, spans, k, v, workspace, stream):
     kv = (T, cache.num_kv_heads, 128)
     k_at, k_step = (0, 0) if k is None else _rows(k, kv, where, dev)
     v_at, v_step = (0, 0) if v is None else _rows(v, kv, where, dev)
-    at = _SPAN.pack(*_cache_values(cache, False, dev, where), seen[1], seen[2], spans.first.data_ptr(), spans.end.data_ptr(),
+    at = _SPAN.pack(_packed_cache(cache, dev, where), seen[1], seen[2], spans.first.data_ptr(), spans.end.data_ptr(),
                     spans.token_offsets.data_ptr(), spans.block_table.data_ptr(), k_at, k_step, v_at, v_step)
     _, o_spans, o_k, o_v = _SPAN.offsets
     _check(call(at, at + o_spans, T, 0 if k is None else at + o_k, 0 if v is None else at + o_v, workspace.data_ptr(),
-                _nbytes(workspace), _stream(stream, dev)), where)
+                workspace.nbytes, _stream(stream, dev)), where)
 
 
 def msa_block_insert(cache, spans: Spans, k, v, workspace, stream=None) -> None:
@@ -537,14 +588,14 @@ def msa_dense_attend(cache, batch, cfg, q: Query, num_q_heads: int, out, lse, wo
             or lens.get_device() != dev or table.get_device() != dev or data.get_device() != dev or out.get_device() != dev
             or workspace.get_device() != dev):
         raise MsaError(1, "msa_dense_attend")
-    at = _DENSE.pack(*_cache_values(cache, False, dev, "msa_dense_attend"),
-                     shape[0], batch.q_per_seq, shape[1], lens.data_ptr(), table.data_ptr(),
-                     cfg.topk, cfg.init_blocks, cfg.local_blocks, cfg.index_scale, cfg.sm_scale,
-                     SCORE_TYPES.get(cfg.score_type, -1), PREFILL_SELECT.get(cfg.prefill_select, -1),
-                     data.data_ptr(), DTYPES[q.dtype], q.scale)
-    o = _DENSE.offsets
-    _check(lib().msa_dense_attend(at + o[0], at + o[1], at + o[2], at + o[3], num_q_heads, out.data_ptr(), _p(lse),
-                                  workspace.data_ptr(), _nbytes(workspace), _stream(stream, dev)), "msa_dense_attend")
+    at = _ATTEND.pack(_packed_cache(cache, dev, "msa_dense_attend"),
+                      shape[0], batch.q_per_seq, shape[1], lens.data_ptr(), table.data_ptr(),
+                      cfg.topk, cfg.init_blocks, cfg.local_blocks, cfg.index_scale, cfg.sm_scale,
+                      SCORE_TYPES.get(cfg.score_type, -1), PREFILL_SELECT.get(cfg.prefill_select, -1),
+                      data.data_ptr(), DTYPES[q.dtype], q.scale)
+    _, b, f, qq = _ATTEND.offsets
+    _check(lib().msa_dense_attend(at, at + b, at + f, at + qq, num_q_heads, out.data_ptr(), _p(lse),
+                                  workspace.data_ptr(), workspace.nbytes, _stream(stream, dev)), "msa_dense_attend")
 
 
 def msa_rope_init(rotary_dim: int, theta: float, sections=None, layout: str = "halves") -> MsaRopeT:

@@ -1533,7 +1533,8 @@ cudaError_t launch_one(const CUtensorMap* tk, const CUtensorMap* tv, const Dense
   using LY = DenseLayout<FMT, NN, NCG>;
   static_assert(LY::ROWS == dense_rows(NN, NCG) && LY::TEAMS == dense_teams(FMT, NN), "the plan's sizes");
   auto kern = dense_kernel<FMT, NN, NCG, NVR, SEL>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)LY::SMEM);
+  static std::atomic<uint64_t> allowed{0};
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), (int)LY::SMEM, allowed);
   if (e != cudaSuccess) return e;
   if constexpr (LY::MOVE) {
     // the consumers would wait for ever for registers that the launch did not bring

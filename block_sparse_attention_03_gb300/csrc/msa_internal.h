@@ -1,6 +1,7 @@
 // Internal launch interface between the C ABI (msa_api.cu) and the kernels.
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda.h>
@@ -319,6 +320,19 @@ struct SpanParams {
   int32_t nv_round;
   DeviceStatus* status;
 };
+
+// Dynamic shared memory beyond 48 KB for a kernel: asked for once a device (`done`: the kernel's own,
+// a bit a device; the call costs a third of a microsecond).
+inline cudaError_t allow_smem(const void* kern, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 // launchers (return cudaGetLastError())
 cudaError_t launch_block_insert(const SpanParams& p, int fmt, int num_sms, cudaStream_t st);

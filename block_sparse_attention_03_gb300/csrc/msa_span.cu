@@ -433,7 +433,8 @@ dim3 span_grid(const SpanParams& p, int subs, int ctas) {
 cudaError_t launch_block_insert(const SpanParams& p, int fmt, int num_sms, cudaStream_t st) {
   const int smem = kInsertStages * kRowsPerThread * kSpanThreads * (int)sizeof(uint4);
   auto kern = fmt == FMT_I8B ? block_insert_kernel<FMT_I8B> : block_insert_kernel<FMT_F8B>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<uint64_t> allowed[2];
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem, allowed[fmt == FMT_I8B]);
   if (e != cudaSuccess) return e;
   kern<<<span_grid(p, 2 * p.H, num_sms * kInsertCtas), kSpanThreads, smem, st>>>(p);
   return cudaGetLastError();

@@ -167,6 +167,24 @@ def test_python_looks_at_the_cache_in_every_attend(on_device_0, kv):  # noqa: F8
                 call(cache=_cache(msa, kv, **over))
 
 
+@pytest.mark.parametrize("kv", KINDS)
+def test_python_refuses_what_the_sparse_attend_would_misread(on_device_0, kv):  # noqa: F811
+    msa = on_device_0
+    cache = _cache(msa, kv)
+
+    def call(lens, table, q, lists, out, lse, ws, kind="bf16"):
+        msa.msa_sparse_attend(cache, msa.Batch(lens, table, 2), msa.Config(topk=8), msa.Query(q, kind), 4, lists, out, lse, ws, stream=0)
+
+    good = dict(lens=z(3, dt=i32), table=z(3, 5, dt=i32), q=z(6, 4, 128), lists=z(6, 2, 8, dt=i32), out=z(6, 4, 128), lse=z(6, 4, dt=f32),
+                ws=z(4096, dt=u8))
+    _refused(msa, call, good, [("lens", z(3, dt=torch.int64)), ("lens", cut(3)), ("table", z(2, 5, dt=i32)), ("table", z(15, dt=i32)),
+                               ("table", cut(3, 5)), ("q", z(3, 4, 128)), ("q", z(6, 4, 128, dt=u8)), ("q", z(6, 4, 128, at=1)),
+                               ("lists", z(6, 2, 16, dt=i32)), ("lists", z(6, 2, 8, dt=torch.int64)), ("lists", cut(6, 2, 8)),
+                               ("lists", z(6, 2, 8, dt=i32, at=-1)), ("out", z(6, 4, 128, dt=f32)), ("out", cut(6, 4, 128, dt=bf)),
+                               ("lse", z(3, 4, dt=f32)), ("lse", z(6, 4)), ("ws", z(4096, dt=u8, at=1)), ("kind", "fp8")])
+    _passes(call, **{**good, "lse": None})
+
+
 def test_growth_is_the_least_power_of_two():
     rng = np.random.default_rng(1)
     for a, b in np.float32(np.exp(rng.uniform(-80, 80, (500, 2)))):
