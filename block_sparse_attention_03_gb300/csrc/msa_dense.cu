@@ -29,7 +29,7 @@ template <bool BY_SEGMENT>
 __global__ void __launch_bounds__(kJoinThreads, BY_SEGMENT ? 3 : 5) dense_combine_kernel(const DenseParams p, int runs, int rows, int cta_rows,
                                                                      float shift) {
   constexpr int kJoinBatch = BY_SEGMENT ? 8 : 4;  // partials of a row a warp has in flight
-  __shared__ float so[kJoinWarps][132];
+  __shared__ __align__(16) float so[kJoinWarps][132];  // (read and written as float4)
   __shared__ float sm[kJoinWarps][2];
   __shared__ int s_first, s_end;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;

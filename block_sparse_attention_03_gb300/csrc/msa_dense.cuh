@@ -305,6 +305,11 @@ __device__ __forceinline__ int slots_of(int T, int max_nb) {
   return un > 0 ? un + END : 0;
 }
 
+// a / b of numbers from 0 up; in 32 bits where they fit (a division in 64 takes some hundred cycles).
+__device__ __forceinline__ long quotient(long a, long b) {
+  return ((a | b) >> 32) == 0 ? (long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 __device__ __forceinline__ long warp_sum(long v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -354,14 +359,14 @@ __device__ void producer(const CUtensorMap* tmk, const CUtensorMap* tmv, const D
   const long c = tm.id;
   long u0 = 0, u1 = 0;
   if (c < grid) {
-    u0 = c * total / grid;
-    u1 = (c + 1) * total / grid;
+    u0 = quotient(c * total, grid);
+    u1 = quotient((c + 1) * total, grid);
   }
   // the sequence that holds u0: sb units (x GC) come before it
   int s = 0;
   long sb = 0;
   if constexpr (SEL) {
-    s = (int)(u0 / (GC * (p.topk + LY::END)));
+    s = (int)quotient(u0, GC * (p.topk + LY::END));
     sb = (long)s * GC * (p.topk + LY::END);
   } else if (u1 > u0) {
     for (int s0 = 0; s0 < S; s0 += 32) {
@@ -386,11 +391,8 @@ __device__ void producer(const CUtensorMap* tmk, const CUtensorMap* tmv, const D
 #pragma unroll 1
   while (u < u1 && ok) {
     int T, un;
-    if constexpr (SEL) {  // keys that token s sees; 0: a malformed sequence, every entry of its lists is left out
-      T = __ldg(p.seq_lens + s / p.q_real);
-      const bool good = T >= p.q_real && T <= max_nb * kBlock;
-      if (!good && lane == 0) raise_flag(p.status, FLAG_BAD_SEQLEN, T);
-      T = good ? T - p.q_real + s % p.q_real + 1 : 0;
+    if constexpr (SEL) {
+      T = __ldg(p.seq_lens + s / p.q_real);  // (looked at once the list is on its way, too)
       un = p.topk;
     } else {
       T = s < 32 ? __shfl_sync(0xffffffffu, mine0, s & 31) : __ldg(p.seq_lens + s);
@@ -401,7 +403,7 @@ __device__ void producer(const CUtensorMap* tmk, const CUtensorMap* tmv, const D
       continue;
     }
     const long in_s = u - sb;
-    const int span = un + LY::END, gc = (int)(in_s / span), k0 = (int)(in_s - (long)gc * span);
+    const int span = un + LY::END, gc = (int)quotient(in_s, span), k0 = (int)(in_s - (long)gc * span);
     if (k0 >= un) {  // another run's segment end
       u += span - k0;
       if (gc + 1 == GC) {
@@ -426,6 +428,10 @@ __device__ void producer(const CUtensorMap* tmk, const CUtensorMap* tmv, const D
     if constexpr (SEL) {
       // the whole list, one entry a lane (topk <= 32)
       if (lane < p.topk) pick = __ldg(p.topk_idx + ((size_t)s * p.G + g) * p.topk + lane);
+      // keys that token s sees; 0: a malformed sequence, every entry of its lists is left out
+      const bool good = T >= p.q_real && T <= max_nb * kBlock;
+      if (!good && lane == 0) raise_flag(p.status, FLAG_BAD_SEQLEN, T);
+      T = good ? T - p.q_real + s % p.q_real + 1 : 0;
       const bool seen = pick >= 0 && pick <= (T - 1) >> 7;  // (an arithmetic shift: T = 0 sees none)
       const uint32_t same = __match_any_sync(0xffffffffu, seen ? pick : -1 - lane);
       const bool take = seen && (same & ((1u << lane) - 1u)) == 0;
