@@ -490,13 +490,6 @@ __device__ void producer(const CUtensorMap* tmk, const CUtensorMap* tmv, const D
           raise_flag(p.status, FLAG_BAD_BLOCK, entry);
           entry = -1;
         }
-        if constexpr (BLK) {
-          if (entry >= 0) {
-            const size_t at = (size_t)entry * p.G + g;
-            ks_mine = __ldg(reinterpret_cast<const float*>(p.k_sc) + at);
-            vs_mine = __ldg(reinterpret_cast<const float*>(p.v_sc) + at);
-          }
-        }
       }
       const int ph = __shfl_sync(0xffffffffu, entry, b - b_have);
       const int st = bi % NST, ub = bi / NST;
@@ -506,8 +499,8 @@ __device__ void producer(const CUtensorMap* tmk, const CUtensorMap* tmv, const D
         break;
       }
       if constexpr (BLK) {
-        // The copies first; the scales may still be on their way, and the phase waits for them
-        // (this lane's arrival).
+        // The copies first (their fence waits for loads on their way); then the scales of the new
+        // entries, which the phase waits for (this lane's arrival).
         if (lane == 0 && ph >= 0) {
           uint8_t* stg = tm.tiles + (size_t)st * LY::STAGE;
           const int y = (int)(((size_t)ph * p.G + g) * kBlock);
@@ -516,6 +509,13 @@ __device__ void producer(const CUtensorMap* tmk, const CUtensorMap* tmv, const D
           const uint64_t pol = p.stream ? l2_policy_evict_first() : l2_policy_evict_normal();
           tma_load_2d_hint(stg, tmk, 0, y, &full[st], pol);
           tma_load_2d_hint(stg + TR::TILE, tmv, 0, y, &full[st], pol);
+        }
+        if (SEL ? k == k0 : b == b_have && (k == k0 || half == 0)) {
+          if (entry >= 0) {
+            const size_t at = (size_t)entry * p.G + g;
+            ks_mine = __ldg(reinterpret_cast<const float*>(p.k_sc) + at);
+            vs_mine = __ldg(reinterpret_cast<const float*>(p.v_sc) + at);
+          }
         }
         DenseStage f;
         f.ok = ph >= 0;
