@@ -37,10 +37,24 @@ struct SpanBlock {
   int phys;   // the block table's entry
 };
 
+// Which chunks of 256 sequences are a CTA's, and its place among the CTAs that share them: CTA
+// (x, y) takes head and K or V x, and the chunks y mod their number, + gridDim.y, ... where there are more
+// chunks than CTAs.
+struct SpanWalk {
+  int s0, step;
+  uint32_t rank, size;
+};
+__device__ __forceinline__ SpanWalk span_walk(const SpanParams& p) {
+  const uint32_t chunks = ((uint32_t)p.S + kSpanThreads - 1) / kSpanThreads, groups = min(chunks, gridDim.y);
+  if (groups == 1) return {0, kSpanThreads, blockIdx.y, gridDim.y};
+  const uint32_t group = blockIdx.y % groups;
+  return {(int)group * kSpanThreads, (int)groups * kSpanThreads, blockIdx.y / groups, (gridDim.y - group + groups - 1) / groups};
+}
+
 // The spans s0 .. s0 + 255: returns how many blocks they touch.  Block i of those, in
-// (sequence, position) order, goes to the CTAs (x, i mod gridDim.y); x is a head and K or V.
-// (The host bounds num_tokens so that 256 spans touch fewer than 2^31 blocks.)
-__device__ __forceinline__ int load_chunk(const SpanParams& p, SpanChunk& c, int s0) {
+// (sequence, position) order, goes to worker i mod their number.  (The host bounds
+// num_tokens so that 256 spans touch fewer than 2^31 blocks.)
+__device__ __forceinline__ int load_chunk(const SpanParams& p, SpanChunk& c, int s0, bool again) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int s = s0 + tid;
   int first = 0, end = 0, off = 0, count = 0;
@@ -53,7 +67,7 @@ __device__ __forceinline__ int load_chunk(const SpanParams& p, SpanChunk& c, int
       if (first < 0 || end > p.max_nb * kBlock) bad = FLAG_BAD_SEQLEN;
       else if (off < 0 || off > p.num_tokens - (end - first)) bad = FLAG_NO_ROOM;
       if (bad == 0) count = (end - 1) / kBlock - first / kBlock + 1;
-      else if (blockIdx.y == 0 && blockIdx.x == 0) raise_flag(p.status, bad, s);
+      else if (blockIdx.x == 0) raise_flag(p.status, bad, s);
     }
   }
   int incl = count;
@@ -62,7 +76,7 @@ __device__ __forceinline__ int load_chunk(const SpanParams& p, SpanChunk& c, int
     const int v = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += v;
   }
-  if (s0 > 0) __syncthreads();  // the former chunk has been read
+  if (again) __syncthreads();  // the former chunk has been read
   if (lane == 31) c.warp_sum[warp] = incl;
   c.first[tid] = first;
   c.end[tid] = end;
@@ -156,8 +170,77 @@ __device__ __forceinline__ int growth(float a, float b) {
   return k > 0 ? k : 0;
 }
 
-// Items on their way at once, each in a stage of 32 KB of shared memory.  A thread copies and
-// reads the same bytes, so the copies need no barrier.
+// Bits of a magnitude order as the values do, NaN above all: the larger of two per half.
+__device__ __forceinline__ __nv_bfloat162 larger(__nv_bfloat162 m, const uint4& x) {
+  const __nv_bfloat162* w = reinterpret_cast<const __nv_bfloat162*>(&x);
+  return __hmax2_nan(m, __hmax2_nan(__hmax2_nan(__habs2(w[0]), __habs2(w[1])), __hmax2_nan(__habs2(w[2]), __habs2(w[3]))));
+}
+__device__ __forceinline__ uint32_t magnitude(__nv_bfloat162 m) {
+  const uint32_t u = *reinterpret_cast<const uint32_t*>(&m);
+  return max(u & 0x7fffu, (u >> 16) & 0x7fffu);
+}
+constexpr uint32_t kNotFinite = 0x7f80u;
+// The same of the finite elements only.
+__device__ __forceinline__ uint32_t larger_finite(uint32_t m, const uint4& x) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t lo = w[j] & 0x7fffu, hi = (w[j] >> 16) & 0x7fffu;
+    m = max(m, max(lo < kNotFinite ? lo : 0u, hi < kNotFinite ? hi : 0u));
+  }
+  return m;
+}
+
+// The block's scale for the largest magnitude m (bits) and, in `k`, by how many powers of two the
+// held codes shrink.
+template <int FMT>
+__device__ __forceinline__ float block_scale(uint32_t m, bool held, float old, int& k) {
+  constexpr float kLeast = 1.17549435e-38f;  // 2^-126
+  const float need = fmaxf(__fdiv_rn(__uint_as_float(m << 16), FMT == FMT_I8B ? 127.f : 448.f), kLeast);
+  k = 0;
+  if (!held) return need;
+  const float s = normal_positive(old) ? old : kLeast;
+  k = growth(s, need);
+  return __uint_as_float(__float_as_uint(s) + ((uint32_t)k << 23));  // below 2 need: no overflow
+}
+
+// `had` rows of held codes x 2^-k, by `threads` threads.
+template <int FMT>
+__device__ __forceinline__ void shrink(uint8_t* data, int had, int k, int tid, int threads) {
+  const float f = pow2i(k < 126 ? -k : -126);  // (a smaller factor leaves nothing of a code either)
+#pragma unroll 4
+  for (int i = tid; i < had * 8; i += threads) {
+    uint4 w = *reinterpret_cast<const uint4*>(data + 16 * i);
+    w.x = move_codes<FMT>(w.x, f);
+    w.y = move_codes<FMT>(w.y, f);
+    w.z = move_codes<FMT>(w.z, f);
+    w.w = move_codes<FMT>(w.w, f);
+    *reinterpret_cast<uint4*>(data + 16 * i) = w;
+  }
+}
+
+// Eight elements' codes: finite ones and a scale that divides() takes (r2: its reciprocal, n2: minus it) ...
+template <int FMT>
+__device__ __forceinline__ uint2 quantize(const uint4& x, float2 r2, float2 n2) {
+  const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+  float2 z[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) z[j] = divide2(make_float2(__uint_as_float(u[j] << 16), __uint_as_float(u[j] & 0xffff0000u)), r2, n2);
+  return make_uint2(block_codes<FMT, false>(z[0], z[1]), block_codes<FMT, false>(z[2], z[3]));
+}
+// ... and any.
+template <int FMT>
+__device__ __forceinline__ uint2 quantize_any(const uint4& x, float s) {
+  const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+  float2 z[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    z[j] = make_float2(__fdiv_rn(__uint_as_float(u[j] << 16), s), __fdiv_rn(__uint_as_float(u[j] & 0xffff0000u), s));
+  return make_uint2(block_codes<FMT, true>(z[0], z[1]), block_codes<FMT, true>(z[2], z[3]));
+}
+
+// A CTA an item.  Items on their way at once are each in a stage of 32 KB of shared memory; a
+// thread copies and reads the same bytes, so the copies need no barrier.
 constexpr int kInsertStages = 2;
 constexpr int kInsertCtas = 3;  // CTAs an SM
 constexpr int kStride = 2 * kSpanWarps;  // a half warp takes a row: rows between a thread's
@@ -168,8 +251,6 @@ __global__ void __launch_bounds__(kSpanThreads, kInsertCtas) block_insert_kernel
   __shared__ SpanChunk chunk;
   __shared__ __align__(16) uint32_t s_max[2][kSpanWarps];
   static_assert(kSpanWarps == 8, "all_max");
-  constexpr float Q = FMT == FMT_I8B ? 127.f : 448.f;
-  constexpr float kLeast = 1.17549435e-38f;  // 2^-126
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, l16 = lane & 15;
   const int row0 = 2 * warp + (lane >> 4);  // this thread's rows: row0 + kStride i
   const int h = blockIdx.x >> 1;
@@ -201,7 +282,6 @@ __global__ void __launch_bounds__(kSpanThreads, kInsertCtas) block_insert_kernel
   };
   auto insert = [&](const SpanBlock& b, float old, int stage) {
     const uint4* mine = s_rows + stage * (kRowsPerThread * kSpanThreads) + tid;
-    // the largest magnitude; as bits they order as the values do, NaN above all
     uint4 x[kRowsPerThread];
     __nv_bfloat162 m2 = __floats2bfloat162_rn(0.f, 0.f);
 #pragma unroll
@@ -209,84 +289,47 @@ __global__ void __launch_bounds__(kSpanThreads, kInsertCtas) block_insert_kernel
       if (kStride * i >= b.n) break;
       x[i] = make_uint4(0u, 0u, 0u, 0u);
       if (row0 + kStride * i < b.n) x[i] = mine[i * kSpanThreads];
-      const __nv_bfloat162* w = reinterpret_cast<const __nv_bfloat162*>(&x[i]);
-      m2 = __hmax2_nan(m2, __hmax2_nan(__hmax2_nan(__habs2(w[0]), __habs2(w[1])), __hmax2_nan(__habs2(w[2]), __habs2(w[3]))));
+      m2 = larger(m2, x[i]);
     }
-    uint32_t m = *reinterpret_cast<uint32_t*>(&m2);
-    m = all_max(max(m & 0x7fffu, (m >> 16) & 0x7fffu));
-    const bool finite = m < 0x7f80u;
-    if (!finite) {  // again, over the finite elements
-      uint32_t f = 0;
+    uint32_t m = all_max(magnitude(m2));
+    const bool finite = m < kNotFinite;
+    if (!finite) {  // again
+      m = 0;
 #pragma unroll 1
-      for (int i = 0; row0 + kStride * i < b.n; ++i) {
-        const uint4 v = mine[i * kSpanThreads];
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t lo = w[j] & 0x7fffu, hi = (w[j] >> 16) & 0x7fffu;
-          f = max(f, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
-        }
-      }
-      m = all_max(f);
+      for (int i = 0; row0 + kStride * i < b.n; ++i) m = larger_finite(m, mine[i * kSpanThreads]);
+      m = all_max(m);
     }
     const size_t head = (size_t)b.phys * p.H + h;
     uint8_t* const data = codes + head * (kBlock * kDim);
-    const float need = fmaxf(__fdiv_rn(__uint_as_float(m << 16), Q), kLeast);
-    float s = need;
-    if (b.had > 0) {
-      s = normal_positive(old) ? old : kLeast;
-      const int k = growth(s, need);
-      if (k > 0) {
-        // (s x 2^k is below 2 need: no overflow; a factor below 2^-126 leaves nothing of a code)
-        s = __uint_as_float(__float_as_uint(s) + ((uint32_t)k << 23));
-        const float f = pow2i(k < 126 ? -k : -126);
-        for (int i = tid; i < b.had * 8; i += kSpanThreads) {
-          uint4 w = *reinterpret_cast<const uint4*>(data + 16 * i);
-          w.x = move_codes<FMT>(w.x, f);
-          w.y = move_codes<FMT>(w.y, f);
-          w.z = move_codes<FMT>(w.z, f);
-          w.w = move_codes<FMT>(w.w, f);
-          *reinterpret_cast<uint4*>(data + 16 * i) = w;
-        }
-      }
-    }
+    int k;
+    const float s = block_scale<FMT>(m, b.had > 0, old, k);
+    if (k > 0) shrink<FMT>(data, b.had, k, tid, kSpanThreads);
     if (tid == 0) scales[head] = s;
     uint8_t* const dst = data + (b.at + row0) * kDim + 8 * l16;
     if (finite && divides(s)) {
       const float inv = __frcp_rn(s);
-      const float2 r2 = make_float2(inv, inv), n2 = make_float2(-s, -s);
 #pragma unroll
       for (int i = 0; i < kRowsPerThread; ++i) {
         if (kStride * i >= b.n) break;
-        const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-        float2 z[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) z[j] = divide2(make_float2(__uint_as_float(u[j] << 16), __uint_as_float(u[j] & 0xffff0000u)), r2, n2);
-        const uint2 c = make_uint2(block_codes<FMT, false>(z[0], z[1]), block_codes<FMT, false>(z[2], z[3]));
+        const uint2 c = quantize<FMT>(x[i], make_float2(inv, inv), make_float2(-s, -s));
         if (row0 + kStride * i < b.n) *reinterpret_cast<uint2*>(dst + kStride * i * kDim) = c;
       }
-    } else {  // infinities, NaN, scales near the ends of fp32's range
+    } else {
 #pragma unroll 1
-      for (int i = 0; row0 + kStride * i < b.n; ++i) {
-        const uint4 v = mine[i * kSpanThreads];
-        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-        float2 z[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          z[j] = make_float2(__fdiv_rn(__uint_as_float(u[j] << 16), s), __fdiv_rn(__uint_as_float(u[j] & 0xffff0000u), s));
-        *reinterpret_cast<uint2*>(dst + kStride * i * kDim) = make_uint2(block_codes<FMT, true>(z[0], z[1]), block_codes<FMT, true>(z[2], z[3]));
-      }
+      for (int i = 0; row0 + kStride * i < b.n; ++i)
+        *reinterpret_cast<uint2*>(dst + kStride * i * kDim) = quantize_any<FMT>(mine[i * kSpanThreads], s);
     }
   };
 
-  uint32_t i = blockIdx.y;  // this CTA's next block among those of the chunk
-  for (int s0 = 0; s0 < p.S; s0 += kSpanThreads) {
-    const uint32_t total = load_chunk(p, chunk, s0), grid = gridDim.y;
-    const int count = i < total ? (int)((total - 1 - i) / grid) + 1 : 0;  // this CTA's blocks of the chunk
+  const SpanWalk w = span_walk(p);
+  uint32_t i = w.rank;  // this CTA's next block among those of the chunk
+  for (int s0 = w.s0; s0 < p.S; s0 += w.step) {
+    const uint32_t total = load_chunk(p, chunk, s0, s0 > w.s0);
+    const int count = i < total ? (int)((total - 1 - i) / w.size) + 1 : 0;  // this CTA's blocks of the chunk
     SpanBlock b[kInsertStages], some;  // what is on its way, b[0] first; the next ones, one a lane
     auto start = [&](int k, int stage) {  // block k of the CTA's
       if (k < count) {
-        if ((k & 31) == 0) some = find_block(p, chunk, s0, (int)min(i + (k + lane) * grid, total - 1));
+        if ((k & 31) == 0) some = find_block(p, chunk, s0, (int)min(i + (k + lane) * w.size, total - 1));
         fetch(b[kInsertStages - 1] = from_lane(some, k & 31), stage);
       }
       cp_async_commit();
@@ -310,7 +353,97 @@ __global__ void __launch_bounds__(kSpanThreads, kInsertCtas) block_insert_kernel
       old = next;
       stage = stage + 1 == kInsertStages ? 0 : stage + 1;
     }
-    i = i + count * grid - total;
+    i = i + count * w.size - total;
+  }
+}
+
+// A warp an item, for spans of a step's few tokens: eight rows at a time, what one round does not
+// hold read again for the quotients.
+constexpr int kFewCtas = 4;  // CTAs an SM
+constexpr int kFewHeld = 4;  // rows a thread holds
+// Tokens a span, on average, up to which it is used: where the blocks' items are more than the CTAs of the
+// other kernel (256 spans of 16 tokens, 8 items each 5.4 us, the other 7.4; of 32 8.3 and 9.1; of 64 19.5 and
+// 14.6), and where they are not (32 spans of 8 tokens 3.3 us, the other 3.4; of 16 3.9 and 3.5).
+constexpr long kFewTokensMany = 32, kFewTokens = 8;
+
+template <int FMT>
+__global__ void __launch_bounds__(kSpanThreads, kFewCtas) block_insert_few_kernel(const SpanParams p) {
+  __shared__ SpanChunk chunk;
+  constexpr int ROUND = 2 * kFewHeld;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l16 = lane & 15, row0 = lane >> 4;
+  const int h = blockIdx.x >> 1;
+  const bool is_v = blockIdx.x & 1;
+  const long step = is_v ? p.v_stride : p.k_stride;
+  const __nv_bfloat16* const rows = (is_v ? p.v_in : p.k_in) + h * kDim + 8 * l16 + row0 * step;
+  uint8_t* const codes = is_v ? p.vc : p.kc;
+  float* const scales = is_v ? p.vs : p.ks;
+
+  auto load = [&](const __nv_bfloat16* src) { return __ldg(reinterpret_cast<const uint4*>(src)); };
+  auto insert = [&](const SpanBlock& b) {
+    const size_t head = (size_t)b.phys * p.H + h;
+    uint8_t* const data = codes + head * (kBlock * kDim);
+    const __nv_bfloat16* const src = rows + (long)b.row * step;
+    const float old = b.had > 0 ? scales[head] : 0.f;
+    uint4 x[kFewHeld];
+    __nv_bfloat162 m2 = __floats2bfloat162_rn(0.f, 0.f);
+    auto round = [&](int r) {
+#pragma unroll
+      for (int i = 0; i < kFewHeld; ++i)
+        x[i] = r + row0 + 2 * i < b.n ? load(src + (r + 2 * i) * step) : make_uint4(0u, 0u, 0u, 0u);
+    };
+#pragma unroll 1
+    for (int r = 0; r < b.n; r += ROUND) {
+      round(r);
+#pragma unroll
+      for (int i = 0; i < kFewHeld; ++i) m2 = larger(m2, x[i]);
+    }
+    uint32_t m = __reduce_max_sync(0xffffffffu, magnitude(m2));
+    const bool finite = m < kNotFinite;
+    if (!finite) {  // again
+      m = 0;
+#pragma unroll 1
+      for (int r = 0; row0 + r < b.n; r += 2) m = larger_finite(m, load(src + r * step));
+      m = __reduce_max_sync(0xffffffffu, m);
+    }
+    int k;
+    const float s = block_scale<FMT>(m, b.had > 0, old, k);
+    if (k > 0) shrink<FMT>(data, b.had, k, lane, 32);
+    __syncwarp();  // every lane has the old scale
+    if (lane == 0) scales[head] = s;
+    uint8_t* const dst = data + (b.at + row0) * kDim + 8 * l16;
+    if (finite && divides(s)) {
+      const float inv = __frcp_rn(s);
+#pragma unroll 1
+      for (int r = 0; r < b.n; r += ROUND) {
+        if (b.n > ROUND) round(r);
+#pragma unroll
+        for (int i = 0; i < kFewHeld; ++i) {
+          if (r + 2 * i >= b.n) break;
+          const uint2 c = quantize<FMT>(x[i], make_float2(inv, inv), make_float2(-s, -s));
+          if (r + row0 + 2 * i < b.n) *reinterpret_cast<uint2*>(dst + (r + 2 * i) * kDim) = c;
+        }
+      }
+    } else {
+#pragma unroll 1
+      for (int r = 0; row0 + r < b.n; r += 2) *reinterpret_cast<uint2*>(dst + r * kDim) = quantize_any<FMT>(load(src + r * step), s);
+    }
+  };
+
+  const SpanWalk w = span_walk(p);
+  const uint32_t workers = w.size * kSpanWarps;
+  uint32_t i = w.rank * kSpanWarps + warp;  // this warp's next block among those of the chunk
+  for (int s0 = w.s0; s0 < p.S; s0 += w.step) {
+    const uint32_t total = load_chunk(p, chunk, s0, s0 > w.s0);
+    const int count = i < total ? (int)((total - 1 - i) / workers) + 1 : 0;
+    SpanBlock some;  // the next ones, one a lane
+#pragma unroll 1
+    for (int k = 0; k < count; ++k) {
+      if ((k & 31) == 0) some = find_block(p, chunk, s0, (int)min(i + (uint32_t)(k + lane) * workers, total - 1));
+      const SpanBlock b = from_lane(some, k & 31);
+      if (in_pool(p, b.phys)) insert(b);
+      else if (blockIdx.x == 0 && lane == 0) raise_flag(p.status, FLAG_BAD_BLOCK, b.phys);
+    }
+    i = i + count * workers - total;
   }
 }
 
@@ -377,7 +510,8 @@ __device__ __forceinline__ uint4 row_bf16(const Raw& r, float s, bool nv_round) 
                     pack_bf16x2(__fmul_rn(v[4], s), __fmul_rn(v[5], s)), pack_bf16x2(__fmul_rn(v[6], s), __fmul_rn(v[7], s)));
 }
 
-constexpr int kReadCtas = 4;  // CTAs an SM
+constexpr int kReadCtas = 4;   // CTAs an SM
+constexpr int kReadMost = 64;  // and in all: one after the other, as SMs come free
 
 template <int FMT>
 __global__ void __launch_bounds__(kSpanThreads, kReadCtas) cache_read_kernel(const SpanParams p) {
@@ -391,10 +525,11 @@ __global__ void __launch_bounds__(kSpanThreads, kReadCtas) cache_read_kernel(con
   const uint8_t* sf = is_v ? p.vsf : p.ksf;
   const float* scale = is_v ? p.vs : p.ks;
   const int row0 = 2 * warp + (lane >> 4);  // this thread's rows: row0 + 16 i
-  uint32_t i = blockIdx.y;                  // this CTA's next block among those of the chunk
-  for (int s0 = 0; s0 < p.S; s0 += kSpanThreads) {
-    const uint32_t total = load_chunk(p, chunk, s0);
-    for (; i < total; i += gridDim.y) {
+  const SpanWalk w = span_walk(p);
+  uint32_t i = w.rank;  // this CTA's next block among those of the chunk
+  for (int s0 = w.s0; s0 < p.S; s0 += w.step) {
+    const uint32_t total = load_chunk(p, chunk, s0, s0 > w.s0);
+    for (; i < total; i += w.size) {
       const SpanBlock b = find_block(p, chunk, s0, i);
       if (!in_pool(p, b.phys)) {
         if (blockIdx.x == 0 && threadIdx.x == 0) raise_flag(p.status, FLAG_BAD_BLOCK, b.phys);
@@ -422,26 +557,35 @@ long most_blocks(const SpanParams& p) {
   return blocks < tokens ? blocks : tokens;
 }
 
-// CTAs: (heads x K and V, blocks), `ctas` at most.
-dim3 span_grid(const SpanParams& p, int subs, int ctas) {
-  const long blocks = most_blocks(p), cap = ctas > subs ? ctas / subs : 1;
+// CTAs: (heads x K and V, blocks over `each` a CTA), `ctas` in all at most.
+dim3 span_grid(const SpanParams& p, int subs, int ctas, int each = 1) {
+  const long blocks = (most_blocks(p) + each - 1) / each, cap = ctas > subs ? ctas / subs : 1;
   return dim3((unsigned)subs, (unsigned)(blocks > cap ? cap : blocks));
+}
+
+template <int FMT>
+cudaError_t launch_insert_fmt(const SpanParams& p, int num_sms, cudaStream_t st) {
+  const bool many = most_blocks(p) * 2 * p.H > (long)num_sms * kInsertCtas;
+  if (p.num_tokens <= (many ? kFewTokensMany : kFewTokens) * p.S) {
+    block_insert_few_kernel<FMT><<<span_grid(p, 2 * p.H, num_sms * kFewCtas, kSpanWarps), kSpanThreads, 0, st>>>(p);
+    return cudaGetLastError();
+  }
+  const int smem = kInsertStages * kRowsPerThread * kSpanThreads * (int)sizeof(uint4);
+  static std::atomic<uint64_t> allowed{0};
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(block_insert_kernel<FMT>), smem, allowed);
+  if (e != cudaSuccess) return e;
+  block_insert_kernel<FMT><<<span_grid(p, 2 * p.H, num_sms * kInsertCtas), kSpanThreads, smem, st>>>(p);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_block_insert(const SpanParams& p, int fmt, int num_sms, cudaStream_t st) {
-  const int smem = kInsertStages * kRowsPerThread * kSpanThreads * (int)sizeof(uint4);
-  auto kern = fmt == FMT_I8B ? block_insert_kernel<FMT_I8B> : block_insert_kernel<FMT_F8B>;
-  static std::atomic<uint64_t> allowed[2];
-  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem, allowed[fmt == FMT_I8B]);
-  if (e != cudaSuccess) return e;
-  kern<<<span_grid(p, 2 * p.H, num_sms * kInsertCtas), kSpanThreads, smem, st>>>(p);
-  return cudaGetLastError();
+  return fmt == FMT_I8B ? launch_insert_fmt<FMT_I8B>(p, num_sms, st) : launch_insert_fmt<FMT_F8B>(p, num_sms, st);
 }
 
 cudaError_t launch_cache_read(const SpanParams& p, int fmt, int num_sms, cudaStream_t st) {
-  const dim3 grid = span_grid(p, ((p.k_out != nullptr) + (p.v_out != nullptr)) * p.H, num_sms * (p.S <= kSpanThreads ? 64 : kReadCtas));
+  const dim3 grid = span_grid(p, ((p.k_out != nullptr) + (p.v_out != nullptr)) * p.H, num_sms * kReadMost);
   switch (fmt) {
     case FMT_BF16: cache_read_kernel<FMT_BF16><<<grid, kSpanThreads, 0, st>>>(p); break;
     case FMT_FP8: cache_read_kernel<FMT_FP8><<<grid, kSpanThreads, 0, st>>>(p); break;

@@ -72,6 +72,41 @@ def test_many_spans(kv, H):
 
 
 @pytest.mark.parametrize("kv", KINDS)
+@pytest.mark.parametrize("S,most", [(31, 1), (257, 3), (5000, 2), (40, 9)])
+def test_a_steps_few_tokens(kv, S, most):
+    # 1 to `most` tokens a request, and one request that brings many more; more sequences than CTAs x 256
+    rng = np.random.default_rng(S)
+    H = 1 if S > 1000 else 4
+    first = rng.integers(0, 250, S)
+    n = rng.integers(0, most + 1, S)
+    n[S // 2] = min(300, 4 * S) if most < 9 else 300
+    end = first + n
+    pool = 6 * S
+    table = rng.permutation(pool).reshape(S, 6)
+    offsets = np.cumsum(n) - n
+    cache = empty_cache(kv, pool, H, seed=S)
+    cache.k_scale.copy_(torch.rand(pool, H).cuda() * 0.03 + 0.005)
+    k, v = _rows(int(n.sum()), H, seed=S, spread=0.8)
+    _insert(cache, first, end, offsets, table, k, v)
+
+
+@pytest.mark.parametrize("kv", KINDS)
+def test_special_values_one_token_at_a_time(kv):
+    # infinities, NaN, zeros, the smallest and the largest numbers in single tokens that go on in blocks, some of which grow
+    H, S = 1, 12
+    cache = empty_cache(kv, S, H, seed=30)
+    for t in (cache.k_scale, cache.v_scale):
+        t.copy_(torch.tensor([1e-38, 1e-3, 1.0, 1e30] * 3).view(S, 1).cuda())
+    k, v = (t.clone() for t in _rows(S, H, seed=31))
+    for i, x in enumerate((0.0, -0.0, 1e-40, 3e38, float("inf"), float("-inf"), float("nan"), 1e-30, 1e20, -3.3e38, 1.0, 2.0 ** -126)):
+        k[i, 0, 3 * i] = x
+        v[i] = x
+    first = np.arange(S) * 10 + 1
+    _insert(cache, first, first + 1, np.arange(S), np.arange(S)[:, None], k, v)
+    _insert(cache, np.zeros(S), np.ones(S), np.arange(S), np.arange(S)[:, None], k, v)  # and in blocks that begin
+
+
+@pytest.mark.parametrize("kv", KINDS)
 def test_special_values(kv):
     # rows of zeros, of the smallest numbers, near the largest, with infinities and NaN, and blocks without a finite element
     H, T = 2, 8 * BLOCK
