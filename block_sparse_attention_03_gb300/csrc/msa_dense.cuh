@@ -150,8 +150,9 @@ struct DenseLayout {
   // Where an equal share is too small, the consumers take registers over from the
   // producers; their warps come in fours then (the producers' four hold idle ones).
   // Three teams of one column tile do better with equal shares (173 us, 182 so).
+  // (INT8's conversions want a few more: 64 columns 222 us, 233 so; 24 211 and 216; FP8 by blocks 200 and 197.)
   static constexpr bool WIDE = NN >= 3, MOVE = WIDE || (TEAMS == 3 && NN == 2);
-  static constexpr int REGS_P = WIDE ? 40 : 56, REGS_C = WIDE ? 232 : 152;
+  static constexpr int REGS_P = WIDE ? (FMT == FMT_I8B ? 24 : 40) : 56, REGS_C = WIDE ? (FMT == FMT_I8B ? 240 : 232) : 152;
   static constexpr int CONSUMERS = 32 * kDenseWpg * TEAMS;
   static constexpr int THREADS = CONSUMERS + (MOVE ? 128 : 32 * TEAMS);
   static_assert(!MOVE || 128 * REGS_P + CONSUMERS * REGS_C <= (65536 / THREADS / 8 * 8) * THREADS, "shares of the launch's registers");
