@@ -91,6 +91,9 @@ constexpr int kDenseWpg = 4;             // consumer warps of a team
 // An MMA's sum is ready after 21 cycles, and a scheduler could start one every 8:
 // a warp alternates this many sums (with two or eight the operator takes as long).
 constexpr int kDenseChains = 4;
+// What a segment's end takes over selection lists, in units (short segments, so that a unit's own share
+// counts more than the end's: 64 tokens of 16 blocks 29.8 us with two, 29.2 with one).
+constexpr int kSelEnd = 1;
 constexpr float kDensePShift = 7.f;      // log2 of the scale of P (NVFP4)
 constexpr float kDenseTop = 4.f;         // FP8: P x vscale of a column's largest product so far
 constexpr float kDenseLeast = 6.1e-36f;  // ... which counts as 2^-117 at least: 2^8 x fe stays finite
@@ -345,7 +348,7 @@ __device__ void producer(const CUtensorMap* tmk, const CUtensorMap* tmv, const D
   long total = 0;
   int mine0 = 0;  // the length of sequence `lane`: a batch of up to 32 is read once
   if constexpr (SEL) {  // every token has the same number of places
-    total = (long)S * GC * (p.topk + LY::END);
+    total = (long)S * GC * (p.topk + kSelEnd);
   } else {
 #pragma unroll 4
     for (int s0 = 0; s0 < S; s0 += 32) {
@@ -367,8 +370,8 @@ __device__ void producer(const CUtensorMap* tmk, const CUtensorMap* tmv, const D
   int s = 0;
   long sb = 0;
   if constexpr (SEL) {
-    s = (int)quotient(u0, GC * (p.topk + LY::END));
-    sb = (long)s * GC * (p.topk + LY::END);
+    s = (int)quotient(u0, GC * (p.topk + kSelEnd));
+    sb = (long)s * GC * (p.topk + kSelEnd);
   } else if (u1 > u0) {
     for (int s0 = 0; s0 < S; s0 += 32) {
       const int T = s0 == 0 ? mine0 : s0 + lane < S ? __ldg(p.seq_lens + s0 + lane) : 0;
@@ -404,7 +407,7 @@ __device__ void producer(const CUtensorMap* tmk, const CUtensorMap* tmv, const D
       continue;
     }
     const long in_s = u - sb;
-    const int span = un + LY::END, gc = (int)quotient(in_s, span), k0 = (int)(in_s - (long)gc * span);
+    const int span = un + (SEL ? kSelEnd : LY::END), gc = (int)quotient(in_s, span), k0 = (int)(in_s - (long)gc * span);
     if (k0 >= un) {  // another run's segment end
       u += span - k0;
       if (gc + 1 == GC) {
