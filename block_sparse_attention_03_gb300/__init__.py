@@ -204,11 +204,19 @@ class PagedCache:
                          NVFP4_MODES.get(self.nvfp4_mode, -1))
 
 
+def _looked_at_once(self, name, value):
+    """__setattr__ of holders whose tensors the serving calls look at once, and again when a field is set."""
+    self.__dict__["_seen"] = ()
+    self.__dict__[name] = value
+
+
 @dataclasses.dataclass
 class Batch:
     seq_lens: object      # int32 [S] on the device
     block_table: object   # int32 [S][max_blocks] on the device
     q_per_seq: int = 1
+
+    __setattr__ = _looked_at_once
 
     def struct(self) -> MsaBatchT:
         return MsaBatchT(self.seq_lens.shape[0], self.q_per_seq, self.block_table.shape[1],
@@ -225,6 +233,8 @@ class Config:
     score_type: str = "max"
     prefill_select: str = "topk"
 
+    __setattr__ = _looked_at_once
+
     def struct(self) -> MsaConfigT:
         # an unknown score type reaches the library as -1, which rejects it
         return MsaConfigT(self.topk, self.init_blocks, self.local_blocks, self.index_scale, self.sm_scale,
@@ -236,6 +246,8 @@ class Query:
     data: object          # bf16 tensor, or uint8 e4m3 codes
     dtype: str = "bf16"   # "bf16" | "fp8"
     scale: float = 1.0
+
+    __setattr__ = _looked_at_once
 
     def struct(self) -> MsaQueryT:
         return MsaQueryT(_ptr(self.data), DTYPES[self.dtype], self.scale)
@@ -250,9 +262,7 @@ class Spans:
     token_offsets: object  # int32 [S] or longer
     block_table: object    # int32 [S][max_blocks]
 
-    def __setattr__(self, name, value):  # looked at once, and again when a field is set (_spans_checked)
-        self.__dict__["_seen"] = ()
-        self.__dict__[name] = value
+    __setattr__ = _looked_at_once
 
 
 @dataclasses.dataclass
@@ -353,7 +363,8 @@ def _packed_cache(c: PagedCache, dev: int, where: str) -> bytes:
     return raw
 
 
-_ATTEND = _Layout(_PACKED, _BATCH, _CONFIG, _QUERY)
+_CONFIG_PACKER = _struct.Struct("@" + _CONFIG + "0P")
+_ATTEND = _Layout(_PACKED, _BATCH, f"{_CONFIG_PACKER.size}s", _QUERY)
 _SPAN = _Layout(_PACKED, _SPANS, _ROWS, _ROWS)
 _ROPE = _Layout(_CACHE, _ROWS, _QUERY, _ROWS, _QUERY, _ROWS, _ROWS, _ROWS, _NORM)
 
@@ -426,42 +437,15 @@ def _check_block_cache(cache, where: str) -> None:
 
 def msa_sparse_attend(cache, batch, cfg, q: Query, num_q_heads: int, topk_idx, out, lse, workspace,
                       stream=None) -> None:
+    """Attention over the selected blocks.  topk_idx: int32 [S * q_per_seq][num_kv_heads][topk], the other tensors as in
+    msa_dense_attend."""
     if cache.kv_dtype in ("int8_block", "fp8_block"):
-        _sparse_by_block(cache, batch, cfg, q, num_q_heads, topk_idx, out, lse, workspace, stream)
+        _attend("msa_sparse_attend", cache, batch, cfg, q, num_q_heads, topk_idx, out, lse, workspace, stream)
         return
     c, b, f, qq = cache.struct(), batch.struct(), cfg.struct(), q.struct()
     _check(lib().msa_sparse_attend(_ref(c), _ref(b), _ref(f), _ref(qq), num_q_heads, _ptr(topk_idx), _ptr(out),
                                    _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(),
                                    _stream(stream)), "msa_sparse_attend")
-
-
-def _sparse_by_block(cache, batch, cfg, q, num_q_heads, topk_idx, out, lse, workspace, stream) -> None:
-    """The sparse attend over a cache with block scales.  topk_idx: int32 [S * q_per_seq][num_kv_heads][topk]; q.data, out:
-    [S * q_per_seq][num_q_heads][128], lse: fp32 [S * q_per_seq][num_q_heads] or None, all dense."""
-    if _int32 is None:
-        _torch_names()
-    lens, table, data = batch.seq_lens, batch.block_table, q.data
-    shape, tokens, dev = table.shape, lens.numel() * batch.q_per_seq, cache.k.get_device()
-    rows = tokens * num_q_heads
-    if (dev < 0 or dev != _device() or len(shape) != 2 or shape[0] != lens.numel()
-            or lens.dtype is not _int32 or table.dtype is not _int32 or not lens.is_contiguous() or not table.is_contiguous()
-            or topk_idx.dtype is not _int32 or topk_idx.numel() != tokens * cache.num_kv_heads * cfg.topk
-            or not topk_idx.is_contiguous() or topk_idx.get_device() != dev
-            or data.numel() != rows * 128 or not data.is_contiguous() or data.dtype not in _query_types.get(q.dtype, ())
-            or out.numel() != rows * 128 or not out.is_contiguous() or out.dtype is not _bf16
-            or (lse is not None and (lse.numel() != rows or not lse.is_contiguous() or lse.dtype is not _f32
-                                    or lse.get_device() != dev))
-            or lens.get_device() != dev or table.get_device() != dev or data.get_device() != dev or out.get_device() != dev
-            or workspace.get_device() != dev):
-        raise MsaError(1, "msa_sparse_attend")
-    at = _ATTEND.pack(_packed_cache(cache, dev, "msa_sparse_attend"),
-                      shape[0], batch.q_per_seq, shape[1], lens.data_ptr(), table.data_ptr(),
-                      cfg.topk, cfg.init_blocks, cfg.local_blocks, cfg.index_scale, cfg.sm_scale,
-                      SCORE_TYPES.get(cfg.score_type, -1), PREFILL_SELECT.get(cfg.prefill_select, -1),
-                      data.data_ptr(), DTYPES[q.dtype], q.scale)
-    _, b, f, qq = _ATTEND.offsets
-    _check(lib().msa_sparse_attend(at, at + b, at + f, at + qq, num_q_heads, topk_idx.data_ptr(), out.data_ptr(), _p(lse),
-                                   workspace.data_ptr(), workspace.nbytes, _stream(stream, dev)), "msa_sparse_attend")
 
 
 def msa_decode(cache, batch, cfg, index_q: Query, q: Query, num_q_heads: int, topk_idx, out, lse, workspace,
@@ -512,6 +496,69 @@ def msa_cache_insert(cache, slot_mapping, k, v, index_k, workspace, stream=None)
     _check(lib().msa_cache_insert(_ref(c), int(slot_mapping.numel()), _ptr(slot_mapping), _ptr(k), _ptr(v),
                                   _ptr(index_k), _ptr(workspace), workspace.numel() * workspace.element_size(),
                                   _stream(stream)), "msa_cache_insert")
+
+
+def _batch_checked(batch: Batch, dev: int, where: str):
+    """(device, sequences, width of the table) of a batch whose tensors are dense int32 on the device."""
+    lens, table = batch.seq_lens, batch.block_table
+    S, shape = lens.numel(), table.shape
+    if len(shape) != 2 or shape[0] != S:
+        raise MsaError(1, where)
+    for t in (lens, table):
+        if t.dtype is not _int32 or t.get_device() != dev or not t.is_contiguous():
+            raise MsaError(1, where)
+    batch.__dict__["_seen"] = seen = (dev, S, shape[1])
+    return seen
+
+
+def _query_checked(q: Query, dev: int, where: str):
+    """(device, elements) of a query that is dense, on the device and of its kind's type."""
+    t = q.data
+    if t.dtype not in _query_types.get(q.dtype, ()) or t.get_device() != dev or not t.is_contiguous():
+        raise MsaError(1, where)
+    q.__dict__["_seen"] = seen = (dev, t.numel())
+    return seen
+
+
+def _config_bytes(cfg: Config) -> bytes:
+    raw = _CONFIG_PACKER.pack(cfg.topk, cfg.init_blocks, cfg.local_blocks, cfg.index_scale, cfg.sm_scale,
+                              SCORE_TYPES.get(cfg.score_type, -1), PREFILL_SELECT.get(cfg.prefill_select, -1))
+    cfg.__dict__["_seen"] = (raw,)
+    return raw
+
+
+def _attend(where: str, cache, batch, cfg, q, num_q_heads: int, topk_idx, out, lse, workspace, stream) -> None:
+    """The dense attend (topk_idx None), or the sparse one over a cache with block scales."""
+    if _int32 is None:
+        _torch_names()
+    dev = cache.k.get_device()
+    if dev < 0 or dev != _device():
+        raise MsaError(1, where)
+    b, qs, f = batch._seen, q._seen, cfg._seen
+    if not b or b[0] != dev:
+        b = _batch_checked(batch, dev, where)
+    if not qs or qs[0] != dev:
+        qs = _query_checked(q, dev, where)
+    tokens = b[1] * batch.q_per_seq
+    rows = tokens * num_q_heads
+    if (qs[1] != rows * 128 or out.numel() != rows * 128 or out.dtype is not _bf16 or out.get_device() != dev or not out.is_contiguous()
+            or (lse is not None and (lse.numel() != rows or lse.dtype is not _f32 or lse.get_device() != dev or not lse.is_contiguous()))
+            or workspace.get_device() != dev
+            or (topk_idx is not None and (topk_idx.numel() != tokens * cache.num_kv_heads * cfg.topk or topk_idx.dtype is not _int32
+                                          or topk_idx.get_device() != dev or not topk_idx.is_contiguous()))):
+        raise MsaError(1, where)
+    at = _ATTEND.pack(_packed_cache(cache, dev, where), b[1], batch.q_per_seq, b[2], batch.seq_lens.data_ptr(),
+                      batch.block_table.data_ptr(), f[0] if f else _config_bytes(cfg), q.data.data_ptr(), DTYPES[q.dtype], q.scale)
+    _, o_batch, o_cfg, o_q = _ATTEND.offsets
+    lse_at = 0 if lse is None else lse.data_ptr()
+    if topk_idx is None:
+        status = lib().msa_dense_attend(at, at + o_batch, at + o_cfg, at + o_q, num_q_heads, out.data_ptr(), lse_at,
+                                        workspace.data_ptr(), workspace.nbytes, _stream(stream, dev))
+    else:
+        status = lib().msa_sparse_attend(at, at + o_batch, at + o_cfg, at + o_q, num_q_heads, topk_idx.data_ptr(), out.data_ptr(),
+                                         lse_at, workspace.data_ptr(), workspace.nbytes, _stream(stream, dev))
+    if status:
+        raise MsaError(status, where)
 
 
 def _spans_checked(spans: Spans, dev: int, where: str):
@@ -575,27 +622,7 @@ def msa_dense_workspace_size(cache: PagedCache, batch: Batch, num_q_heads: int) 
 def msa_dense_attend(cache, batch, cfg, q: Query, num_q_heads: int, out, lse, workspace, stream=None) -> None:
     """Attention of each new token (up to 8 a sequence) over its whole sequence in the paged cache.
     q.data, out: [S * q_per_seq][num_q_heads][128], lse: fp32 [S * q_per_seq][num_q_heads] or None, all dense."""
-    if _int32 is None:
-        _torch_names()
-    lens, table, data = batch.seq_lens, batch.block_table, q.data
-    shape, rows, dev = table.shape, lens.numel() * batch.q_per_seq * num_q_heads, cache.k.get_device()
-    if (dev < 0 or dev != _device() or len(shape) != 2 or shape[0] != lens.numel()
-            or lens.dtype is not _int32 or table.dtype is not _int32 or not lens.is_contiguous() or not table.is_contiguous()
-            or data.numel() != rows * 128 or not data.is_contiguous() or data.dtype not in _query_types.get(q.dtype, ())
-            or out.numel() != rows * 128 or not out.is_contiguous() or out.dtype is not _bf16
-            or (lse is not None and (lse.numel() != rows or not lse.is_contiguous() or lse.dtype is not _f32
-                                    or lse.get_device() != dev))
-            or lens.get_device() != dev or table.get_device() != dev or data.get_device() != dev or out.get_device() != dev
-            or workspace.get_device() != dev):
-        raise MsaError(1, "msa_dense_attend")
-    at = _ATTEND.pack(_packed_cache(cache, dev, "msa_dense_attend"),
-                      shape[0], batch.q_per_seq, shape[1], lens.data_ptr(), table.data_ptr(),
-                      cfg.topk, cfg.init_blocks, cfg.local_blocks, cfg.index_scale, cfg.sm_scale,
-                      SCORE_TYPES.get(cfg.score_type, -1), PREFILL_SELECT.get(cfg.prefill_select, -1),
-                      data.data_ptr(), DTYPES[q.dtype], q.scale)
-    _, b, f, qq = _ATTEND.offsets
-    _check(lib().msa_dense_attend(at, at + b, at + f, at + qq, num_q_heads, out.data_ptr(), _p(lse),
-                                  workspace.data_ptr(), workspace.nbytes, _stream(stream, dev)), "msa_dense_attend")
+    _attend("msa_dense_attend", cache, batch, cfg, q, num_q_heads, None, out, lse, workspace, stream)
 
 
 def msa_rope_init(rotary_dim: int, theta: float, sections=None, layout: str = "halves") -> MsaRopeT:
