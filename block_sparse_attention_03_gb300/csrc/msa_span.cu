@@ -170,15 +170,17 @@ __device__ __forceinline__ int growth(float a, float b) {
   return k > 0 ? k : 0;
 }
 
-// Bits of a magnitude order as the values do, NaN above all: the larger of two per half.
-__device__ __forceinline__ __nv_bfloat162 larger(__nv_bfloat162 m, const uint4& x) {
-  const __nv_bfloat162* w = reinterpret_cast<const __nv_bfloat162*>(&x);
-  return __hmax2_nan(m, __hmax2_nan(__hmax2_nan(__habs2(w[0]), __habs2(w[1])), __hmax2_nan(__habs2(w[2]), __habs2(w[3]))));
+// The larger magnitude of two pairs of bf16, half by half, under any sign; NaN if either is.
+__device__ __forceinline__ uint32_t larger2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
 }
-__device__ __forceinline__ uint32_t magnitude(__nv_bfloat162 m) {
-  const uint32_t u = *reinterpret_cast<const uint32_t*>(&m);
-  return max(u & 0x7fffu, (u >> 16) & 0x7fffu);
+__device__ __forceinline__ uint32_t larger(uint32_t m, const uint4& x) {
+  return larger2(m, larger2(larger2(x.x, x.y), larger2(x.z, x.w)));
 }
+// The bits of the larger half's magnitude: they order as the values do, NaN above all.
+__device__ __forceinline__ uint32_t magnitude(uint32_t m) { return max(m & 0x7fffu, (m >> 16) & 0x7fffu); }
 constexpr uint32_t kNotFinite = 0x7f80u;
 // The same of the finite elements only.
 __device__ __forceinline__ uint32_t larger_finite(uint32_t m, const uint4& x) {
@@ -283,15 +285,16 @@ __global__ void __launch_bounds__(kSpanThreads, kInsertCtas) block_insert_kernel
   auto insert = [&](const SpanBlock& b, float old, int stage) {
     const uint4* mine = s_rows + stage * (kRowsPerThread * kSpanThreads) + tid;
     uint4 x[kRowsPerThread];
-    __nv_bfloat162 m2 = __floats2bfloat162_rn(0.f, 0.f);
+    uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < kRowsPerThread; ++i) {
       if (kStride * i >= b.n) break;
-      x[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (row0 + kStride * i < b.n) x[i] = mine[i * kSpanThreads];
-      m2 = larger(m2, x[i]);
+      if (row0 + kStride * i < b.n) {
+        x[i] = mine[i * kSpanThreads];
+        m = larger(m, x[i]);
+      }
     }
-    uint32_t m = all_max(magnitude(m2));
+    m = all_max(magnitude(m));
     const bool finite = m < kNotFinite;
     if (!finite) {  // again
       m = 0;
@@ -311,8 +314,8 @@ __global__ void __launch_bounds__(kSpanThreads, kInsertCtas) block_insert_kernel
 #pragma unroll
       for (int i = 0; i < kRowsPerThread; ++i) {
         if (kStride * i >= b.n) break;
-        const uint2 c = quantize<FMT>(x[i], make_float2(inv, inv), make_float2(-s, -s));
-        if (row0 + kStride * i < b.n) *reinterpret_cast<uint2*>(dst + kStride * i * kDim) = c;
+        if (row0 + kStride * i < b.n)
+          *reinterpret_cast<uint2*>(dst + kStride * i * kDim) = quantize<FMT>(x[i], make_float2(inv, inv), make_float2(-s, -s));
       }
     } else {
 #pragma unroll 1
@@ -385,7 +388,7 @@ __global__ void __launch_bounds__(kSpanThreads, kFewCtas) block_insert_few_kerne
     const __nv_bfloat16* const src = rows + (long)b.row * step;
     const float old = b.had > 0 ? scales[head] : 0.f;
     uint4 x[kFewHeld];
-    __nv_bfloat162 m2 = __floats2bfloat162_rn(0.f, 0.f);
+    uint32_t m = 0;
     auto round = [&](int r) {
 #pragma unroll
       for (int i = 0; i < kFewHeld; ++i)
@@ -395,9 +398,9 @@ __global__ void __launch_bounds__(kSpanThreads, kFewCtas) block_insert_few_kerne
     for (int r = 0; r < b.n; r += ROUND) {
       round(r);
 #pragma unroll
-      for (int i = 0; i < kFewHeld; ++i) m2 = larger(m2, x[i]);
+      for (int i = 0; i < kFewHeld; ++i) m = larger(m, x[i]);
     }
-    uint32_t m = __reduce_max_sync(0xffffffffu, magnitude(m2));
+    m = __reduce_max_sync(0xffffffffu, magnitude(m));
     const bool finite = m < kNotFinite;
     if (!finite) {  // again
       m = 0;
