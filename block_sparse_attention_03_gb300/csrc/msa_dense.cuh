@@ -74,8 +74,29 @@
 // columns 229 us, 16 columns 107, 32 columns 273.
 //
 // Registers are what the wide instances lack: with 24 columns and more each of them spills
-// (168 to 316 bytes of stores a thread, a stack of 80 to 104), NVFP4 with 8 and 16 columns
-// too (52 and 96), the others not (FP8: 8).
+// (176 to 324 bytes of stores a thread, a stack of 72 to 168: mostly the producers', whose share is 40 or
+// 24), NVFP4 with 8 and 16 columns too (52 and 96), INT8 with 16 (80 to 104), the others not (FP8: 8).
+//
+// Caches with one scale for each block and head (INT8, FP8).  A unit is a block, so its two
+// scales are two numbers of the stage: K's goes into the columns' factors (where keys are masked into the
+// logits), V's times fe is one factor of the weights; nothing is left of the FP8 format's work for
+// each key.  INT8 becomes f16 exactly by 1024 + (x + 128) - 1152 (5 instructions for 4 elements, E4M3's
+// 2 or 3).  The producer asks for the scales behind the block's copies and completes the stage's phase
+// when they are there.  Measured: 4 columns, FP8 32 x 16K-32K 124 us (98% of the copy rate,
+// 6,702 GB/s), INT8 4 x 512K 306 us (105%); 32 columns (8 x 128K, 8 new tokens) INT8 237 us
+// (68%; tensor pipe 42%, issue slots 40%, two warps a scheduler), FP8 226; 24 columns 211 and 197, 16 columns
+// 175 (92%); one sequence of 4K tokens 9.5 us: lengths and table 1.6, first tile 3.0, its unit 4.5, the
+// warps' join 5.5, the last CTA's end seen by the join's launch 6.2, joined 8.2.
+//
+// SEL: the sparse attend over selection lists (caches with block scales).  The new tokens are
+// sequences of their own, a (token, KV head)'s units the entries of its list, its runs cut
+// as above (every list counts topk units, so that the cut needs no sums).  The producer holds a list
+// in its lanes, leaves out what cannot be seen, is named twice or outside the pool, and says
+// where each unit's keys begin.  Measured: 32 tokens x 4 heads x 16 blocks of INT8 20.5 us in a graph (10.1 at
+// the copy rate; 4 blocks 12 us: what a call costs at least is launch, lists, first tiles and join), 64 of FP8
+// (8 x 128K, 8 new tokens) 29.1 (18.1); the kernel for FP8 with token scales takes 30 and 44.  A prompt's
+// chunk reads its blocks once for each token: 8,192 tokens on 64K 1.9 (FP8) and 2.2 ms (INT8), where the
+// key-block-major attend of the FP8 format takes 0.58.
 //
 // A masked key's logit is replaced, not multiplied; in units that hold masked
 // keys V is masked in registers too, so NaN or infinity in rows past the end of a

@@ -24,7 +24,7 @@ def kv_bytes_per_token(dtype: str, num_kv_heads: int = 4, head_dim: int = 128) -
     """K + V bytes of one token over all KV heads."""
     if dtype == "bf16":
         per = 2.0 * head_dim
-    elif dtype == "fp8":
+    elif dtype in ("fp8", "int8_block", "fp8_block"):
         per = 1.0 * head_dim
     elif dtype == "nvfp4":
         per = head_dim / 2 + head_dim / 16
@@ -34,9 +34,10 @@ def kv_bytes_per_token(dtype: str, num_kv_heads: int = 4, head_dim: int = 128) -
 
 
 def scale_bytes_per_token(kv_dtype: str, index_dtype: str, num_kv_heads: int = 4) -> tuple:
-    """(index, K/V) bytes of per-token fp32 scales (FP8 layout only)."""
+    """(index, K/V) bytes a token of fp32 scales (FP8: one for each row; block scales: one for 128)."""
     return (4.0 if index_dtype == "fp8" else 0.0,
-            8.0 * num_kv_heads if kv_dtype == "fp8" else 0.0)
+            8.0 * num_kv_heads / {"fp8": 1, "int8_block": 128, "fp8_block": 128}[kv_dtype]
+            if kv_dtype in ("fp8", "int8_block", "fp8_block") else 0.0)
 
 
 def decode_bytes_per_query(kv_dtype: str, index_dtype: str, context: int, selected_tokens: int,
