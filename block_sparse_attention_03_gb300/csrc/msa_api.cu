@@ -683,6 +683,67 @@ msa_status_t check_rope(const msa_rope_t* r) {
 // rows of one projection: tokens `stride` elements apart, heads side by side
 bool rows_ok(const msa_rows_t* r) { return r && r->data && aligned16(r->data) && r->stride >= 0 && r->stride % 8 == 0; }
 
+// Bytes from a on; whether two such pieces of memory meet.
+struct Piece {
+  const void* p;
+  size_t n;
+};
+bool meet(const Piece& a, const Piece& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return a.p && b.p && a.n > 0 && b.n > 0 && x < y + b.n && y < x + a.n;
+}
+Piece rows_piece(const msa_rows_t* r, int tokens, int heads) {
+  return {r ? r->data : nullptr, ((size_t)(tokens - 1) * r->stride + (size_t)heads * kDim) * 2};
+}
+// The K and V side of a cache: data, then scales.
+void cache_pieces(const msa_cache_t* c, Piece (&out)[4]) {
+  const size_t blocks = (size_t)c->num_blocks * c->num_kv_heads, rows = blocks * kBlock;
+  const int f = kv_fmt_of(c->kv_dtype);
+  const size_t data = rows * (f == FMT_BF16 ? 256 : f == FMT_NVFP4 ? 64 : 128);
+  const size_t scales = f == FMT_BF16 ? 0 : f == FMT_NVFP4 ? rows * 8 : f == FMT_FP8 ? rows * 4 : blocks * 4;
+  out[0] = {c->k, data};
+  out[1] = {c->v, data};
+  out[2] = {f == FMT_NVFP4 ? c->k_sf : c->k_scale, scales};
+  out[3] = {f == FMT_NVFP4 ? c->v_sf : c->v_scale, scales};
+}
+// Whether what a span call writes meets what it reads: the cache (insert) or the rows (read) against the
+// others, the lengths, the table and the status word.
+bool span_overlap(const msa_cache_t* c, const msa_spans_t* sp, int tokens, const msa_rows_t* k, const msa_rows_t* v,
+                  const void* ws, bool insert) {
+  Piece cache[4], other[8];
+  cache_pieces(c, cache);
+  int n = 0;
+  if (k) other[n++] = rows_piece(k, tokens, c->num_kv_heads);
+  if (v) other[n++] = rows_piece(v, tokens, c->num_kv_heads);
+  const int rows = n;
+  const size_t words = 4 * (size_t)sp->num_seqs;
+  other[n++] = {sp->first, words};
+  other[n++] = {sp->end, words};
+  other[n++] = {sp->token_offsets, words};
+  other[n++] = {sp->block_table, words * sp->max_blocks_per_seq};
+  other[n++] = {ws, sizeof(DeviceStatus)};
+  for (int i = 0; i < 4; ++i) {
+    for (int j = 0; j < (insert ? n : rows); ++j)
+      if (meet(cache[i], other[j])) return true;
+    for (int j = 0; insert && j < i; ++j)
+      if (meet(cache[i], cache[j])) return true;
+  }
+  if (insert) return false;
+  for (int i = 0; i < rows; ++i)
+    for (int j = rows; j < n; ++j)
+      if (meet(other[i], other[j])) return true;
+  if (rows == 2 && meet(other[0], other[1])) {
+    // slices of the same rows side by side are fine: the same stride, and no token's K on another's V
+    if (k->stride != v->stride) return true;
+    const int64_t d = (int64_t)(reinterpret_cast<intptr_t>(v->data) - reinterpret_cast<intptr_t>(k->data)) / 2;
+    const int64_t row = (int64_t)c->num_kv_heads * kDim, step = tokens > 1 ? k->stride : 0;
+    const int64_t m = step > 0 ? d / step : 0;  // the tokens whose rows are nearest
+    for (int64_t t = m - 1; t <= m + 1; ++t)
+      if (t > -tokens && t < tokens && d - t * step < row && t * step - d < row) return true;
+  }
+  return false;
+}
+
 // What the insert and the read of spans share.
 msa_status_t span_params(const msa_cache_t* c, const msa_spans_t* sp, int num_tokens, const msa_rows_t* k, const msa_rows_t* v,
                          void* ws, size_t ws_bytes, SpanParams& p) {
@@ -881,7 +942,8 @@ msa_status_t msa_block_insert(const msa_cache_t* cache, const msa_spans_t* spans
   if (s != MSA_OK) return s;
   if (!by_block(cache)) return MSA_ERR_UNSUPPORTED;
   if (num_tokens == 0) return MSA_OK;
-  if (!rows_ok(k) || !rows_ok(v)) return MSA_ERR_INVALID_ARGUMENT;
+  if (!rows_ok(k) || !rows_ok(v) || span_overlap(cache, spans, num_tokens, k, v, workspace, true))
+    return MSA_ERR_INVALID_ARGUMENT;
   p.k_in = static_cast<const __nv_bfloat16*>(k->data);
   p.v_in = static_cast<const __nv_bfloat16*>(v->data);
   return cuda_status(launch_block_insert(p, kv_fmt_of(cache->kv_dtype), sm_count(), (cudaStream_t)stream));
@@ -895,7 +957,8 @@ msa_status_t msa_cache_read(const msa_cache_t* cache, const msa_spans_t* spans, 
   if (num_tokens == 0 || (!k && !v)) return MSA_OK;
   // the rows are written: heads side by side, no two tokens on top of each other
   const int64_t row = (int64_t)cache->num_kv_heads * kDim;
-  if ((k && (!rows_ok(k) || (num_tokens > 1 && k->stride < row))) || (v && (!rows_ok(v) || (num_tokens > 1 && v->stride < row))))
+  if ((k && (!rows_ok(k) || (num_tokens > 1 && k->stride < row))) || (v && (!rows_ok(v) || (num_tokens > 1 && v->stride < row))) ||
+      span_overlap(cache, spans, num_tokens, k, v, workspace, false))
     return MSA_ERR_INVALID_ARGUMENT;
   p.k_out = k ? static_cast<__nv_bfloat16*>(const_cast<void*>(k->data)) : nullptr;
   p.v_out = v ? static_cast<__nv_bfloat16*>(const_cast<void*>(v->data)) : nullptr;

@@ -329,7 +329,8 @@ typedef struct {
  * Flagged on the device and skipped: a span with first < 0 or end beyond
  * max_blocks_per_seq * 128, a span whose rows are not all inside num_tokens, and the
  * tokens of a block outside the pool.  num_tokens <= 2^27.  A block may be in the spans of one sequence
- * only (two race).  k and v may not overlap the cache.
+ * only (two race).  What the call writes (the cache's K, V and scales) may overlap
+ * nothing that it reads, nor itself (MSA_ERR_INVALID_ARGUMENT).
  * The call writes through the cache's pointers.  Deterministic.  workspace: at least
  * 256 bytes; only its status word is used. */
 msa_status_t msa_block_insert(const msa_cache_t* cache, const msa_spans_t* spans, int32_t num_tokens,
@@ -341,6 +342,8 @@ msa_status_t msa_block_insert(const msa_cache_t* cache, const msa_spans_t* spans
  * rounded to nearest even; a BF16 cache's bits are copied.  k or v may be NULL.
  * The call writes through their data pointers, only rows that are a span's; it
  * flags and skips what msa_block_insert does.  Spans may share blocks, not rows.
+ * The rows written may overlap nothing that the call reads, nor each other (slices
+ * of one tensor side by side do not): MSA_ERR_INVALID_ARGUMENT.
  * workspace: at least 256 bytes; only its status word is used. */
 msa_status_t msa_cache_read(const msa_cache_t* cache, const msa_spans_t* spans, int32_t num_tokens, const msa_rows_t* k,
                             const msa_rows_t* v, void* workspace, size_t workspace_bytes, msa_stream_t stream);

@@ -15,12 +15,17 @@ ref = ctypes.byref
 bf, i32, u8, i8, f32 = torch.bfloat16, torch.int32, torch.uint8, torch.int8, torch.float32
 
 
+# places far from one another: the cache holds 100 blocks of 4 heads (6,553,600 bytes of codes, 1,600 of scales)
+K, V, KS, VS, ROWS_K, ROWS_V, WS = (i << 28 for i in range(1, 8))
+SPANS = tuple(i << 20 for i in range(1, 5))
+
+
 def _structs(kv=8, **over):
     import block_sparse_attention_03_gb300 as msa
-    c = msa.MsaCacheT(kv, 1, 100, 128, 4, 128, 128, 16, 32, None, None, 48, 64, 80, None, 96, 0, 0, 0)
+    c = msa.MsaCacheT(kv, 1, 100, 128, 4, 128, 128, K, V, None, None, KS, VS, 80, None, 96, 0, 0, 0)
     b = msa.MsaBatchT(2, 1, 50, 16, 32)
     f = msa.MsaConfigT(16, 0, 0, 128 ** -0.5, 128 ** -0.5, 0)
-    sp = msa.MsaSpansT(2, 50, 16, 32, 48, 64)
+    sp = msa.MsaSpansT(2, 50, *SPANS)
     for k, v in over.items():
         obj, field = k.split("__")
         setattr({"c": c, "b": b, "f": f, "s": sp}[obj], field, v)
@@ -33,29 +38,61 @@ def test_span_refusals(lib, name, kv):  # noqa: F811
     import block_sparse_attention_03_gb300 as msa
     read = name == "msa_cache_read"
 
-    def call(tokens=4, k=(16, 4096), v=(16, 4096), ws=4096, size=256, cache=True, spans=True, **over):
+    def call(tokens=4, k=(ROWS_K, 4096), v=(ROWS_V, 4096), ws=WS, size=256, cache=True, spans=True, **over):
         c, _, _, sp = _structs(kv, **over)
         rows = [None if x is None else ref(msa.MsaRowsT(*x)) for x in (k, v)]
         return getattr(lib, name)(ref(c) if cache else None, ref(sp) if spans else None, tokens, *rows, ctypes.c_void_p(ws), size, None)
 
     assert call(tokens=0) == 0 and call(tokens=0, k=None, v=None) == 0
-    assert call(cache=False) == 1 and call(spans=False) == 1 and call(tokens=-1) == 1 and call(ws=None) == 1 and call(ws=4098) == 1
+    assert call(cache=False) == 1 and call(spans=False) == 1 and call(tokens=-1) == 1 and call(ws=None) == 1 and call(ws=WS + 2) == 1
     assert call(size=255) == 3
     for bad in (dict(c__k=None), dict(c__v=17), dict(c__k_scale=None), dict(c__v_scale=20), dict(s__num_seqs=0),
                 dict(s__max_blocks_per_seq=0), dict(s__first=None), dict(s__end=None), dict(s__token_offsets=None),
                 dict(s__block_table=None), dict(s__first=18), dict(s__end=33), dict(s__token_offsets=50), dict(s__block_table=67)):
         assert call(**bad) == 1, bad
     assert call(tokens=(1 << 27) + 1) == 2 and call(s__max_blocks_per_seq=(1 << 23) + 1) == 2 and call(c__num_kv_heads=9) == 2 and call(c__head_dim=64) == 2
-    for bad in ((None, 4096), (24, 4096), (16, 4100), (16, -8)):
-        assert call(k=bad) == 1 and call(v=bad) == 1, bad
+    for bad in ((None, 4096), (24, 4096), (ROWS_K, 4100), (ROWS_K, -8)):
+        assert call(k=bad, v=bad) == 1 and call(k=bad) == 1 and call(v=(bad[0] and bad[0] + ROWS_V - ROWS_K, bad[1])) == 1, bad
     for unknown in (3, 7, 10):
         assert call(c__kv_dtype=unknown) == 2
     if read:  # one of the two is enough; the rows of two tokens may not lie on top of each other
-        assert call(k=None, v=None) == 0 and call(k=(16, 504)) == 1 and call(v=(16, 0)) == 1
+        assert call(k=None, v=None) == 0 and call(k=(ROWS_K, 504)) == 1 and call(v=(ROWS_V, 0)) == 1
     else:
         assert call(k=None) == 1 and call(v=None) == 1
         for other in (0, 1):  # the formats that msa_cache_insert writes
             assert call(c__kv_dtype=other, c__k_sf=16, c__v_sf=16) == 2
+
+
+ROW = 4 * 128  # elements of a token's heads
+
+
+@pytest.mark.parametrize("kv", [8, 9])
+def test_what_a_span_call_writes_overlaps_nothing(lib, kv):  # noqa: F811
+    import block_sparse_attention_03_gb300 as msa
+
+    def call(name, k, v, tokens=5, stride=(4096, 4096), **over):
+        c, _, _, sp = _structs(kv, **over)
+        rows = [None if x is None else ref(msa.MsaRowsT(x, n)) for x, n in zip((k, v), stride)]
+        return getattr(lib, name)(ref(c), ref(sp), tokens, *rows, ctypes.c_void_p(over.get("ws", WS)), 256, None)
+
+    codes, scales, rows = 100 * 4 * 128 * 128, 1600, (4 * 4096 + ROW) * 2
+    for name in ("msa_block_insert", "msa_cache_read"):
+        for start, size in ((K, codes), (V, codes), (KS, scales), (VS, scales)):
+            for at in (start, start + size - 16, start - rows + 16):  # inside, the last bytes, the first
+                assert call(name, at, ROWS_V) == 1 and call(name, ROWS_K, at) == 1
+    for name, start, size in (("c__k", K, codes), ("c__v", V, codes), ("c__k_scale", KS, scales), ("c__v_scale", VS, scales)):
+        for other in ("s__first", "s__end", "s__token_offsets", "s__block_table"):
+            assert call("msa_block_insert", ROWS_K, ROWS_V, **{other: start + size - 4}) == 1, (name, other)
+        for other in {"c__k", "c__v", "c__k_scale", "c__v_scale"} - {name}:
+            assert call("msa_block_insert", ROWS_K, ROWS_V, **{other: start + size - 16}) == 1, (name, other)
+    for other in ("s__first", "s__end", "s__token_offsets", "s__block_table"):
+        assert call("msa_cache_read", ROWS_K, ROWS_V, **{other: ROWS_K + rows - 4}) == 1
+        assert call("msa_cache_read", ROWS_K, ROWS_V, **{other: ROWS_V}) == 1
+    # K and V of the same rows: side by side or one behind the other, never on top of each other
+    read = lambda d, **a: call("msa_cache_read", ROWS_K, ROWS_K + 2 * d, **a)  # noqa: E731
+    for d in (0, 8, ROW - 8, 4096 - ROW + 8, 4096, 4 * 4096 - ROW + 8, 4 * 4096 + ROW - 8, -8, 8 - ROW, -4096, 8 - 4096 - ROW, -4 * 4096):
+        assert read(d) == 1, d
+    assert read(ROW, stride=(4096, 8192)) == 1 and read(0, tokens=1) == 1 and read(ROW - 8, tokens=1) == 1
 
 
 def test_what_the_other_calls_refuse_of_a_cache_with_block_scales(lib):  # noqa: F811
