@@ -168,17 +168,9 @@ cudaError_t launch_dense_combine(const DenseParams& p, int fmt, int num_sms, cud
   // few segments: each has many partials, so its rows go to CTAs of their own
   const bool by_segment = segments <= runs / 4;
   const int cta_rows = by_segment ? (p.cper <= 8 ? 1 : 4) : (p.cper < kJoinWarps ? p.cper : kJoinWarps);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(by_segment ? segments : runs - 1), (unsigned)((p.cper + cta_rows - 1) / cta_rows));
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, by_segment ? dense_combine_kernel<true> : dense_combine_kernel<false>, p, runs, rows, cta_rows,
-                            shift);
+  const dim3 grid((unsigned)(by_segment ? segments : runs - 1), (unsigned)((p.cper + cta_rows - 1) / cta_rows));
+  return launch_behind(by_segment ? dense_combine_kernel<true> : dense_combine_kernel<false>, grid, dim3(kJoinThreads), 0, st, p, runs,
+                       rows, cta_rows, shift);
 }
 
 }  // namespace msa

@@ -1538,6 +1538,7 @@ __global__ void __launch_bounds__(DenseLayout<FMT, NN, NCG>::THREADS, 1)
     prefetch_tmap(&tmv);
   }
   __syncthreads();
+  pdl_wait();               // (nothing of the memory has been touched)
   pdl_launch_dependents();  // the combine's CTAs may take their place as soon as this grid's leave room
   if (!consumes) {
     if constexpr (LY::MOVE) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(LY::REGS_P));
@@ -1575,8 +1576,7 @@ cudaError_t launch_one(const CUtensorMap* tk, const CUtensorMap* tv, const Dense
     }();
     if (regs / 8 * 8 * LY::THREADS < 128 * LY::REGS_P + LY::CONSUMERS * LY::REGS_C) return cudaErrorLaunchOutOfResources;
   }
-  kern<<<(unsigned)num_sms, LY::THREADS, LY::SMEM, st>>>(*tk, *tv, p);
-  return cudaGetLastError();
+  return launch_behind(kern, dim3((unsigned)num_sms), dim3(LY::THREADS), LY::SMEM, st, *tk, *tv, p);
 }
 
 // The instance for the columns of a group (dense_shape).

@@ -334,6 +334,24 @@ inline cudaError_t allow_smem(const void* kern, int bytes, std::atomic<uint64_t>
   return e;
 }
 
+// A programmatic launch: the grid may take its place while the one in front of it in the stream ends, and
+// waits for that by itself (pdl_wait before its first access to memory).  Behind another such
+// launch it begins some 2 us sooner than a plain one.
+template <typename... K, typename... A>
+inline cudaError_t launch_behind(void (*kern)(K...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // launchers (return cudaGetLastError())
 cudaError_t launch_block_insert(const SpanParams& p, int fmt, int num_sms, cudaStream_t st);
 cudaError_t launch_cache_read(const SpanParams& p, int fmt, int num_sms, cudaStream_t st);

@@ -346,6 +346,7 @@ __global__ void __launch_bounds__(kSpanThreads, kInsertCtas) block_insert_kernel
     }
   };
 
+  pdl_wait();
   const SpanWalk w = span_walk(p);
   uint32_t i = w.rank;  // this CTA's next block among those of the chunk
   for (int s0 = w.s0; s0 < p.S; s0 += w.step) {
@@ -454,6 +455,7 @@ __global__ void __launch_bounds__(kSpanThreads, kFewCtas) block_insert_few_kerne
     }
   };
 
+  pdl_wait();
   const SpanWalk w = span_walk(p);
   const uint32_t workers = w.size * kSpanWarps;
   uint32_t i = w.rank * kSpanWarps + warp;  // this warp's next block among those of the chunk
@@ -550,6 +552,7 @@ __global__ void __launch_bounds__(kSpanThreads, kReadCtas) cache_read_kernel(con
   const uint8_t* sf = is_v ? p.vsf : p.ksf;
   const float* scale = is_v ? p.vs : p.ks;
   const int row0 = 2 * warp + (lane >> 4);  // this thread's rows: row0 + 16 i
+  pdl_wait();
   const SpanWalk w = span_walk(p);
   uint32_t i = w.rank;  // this CTA's next block among those of the chunk
   for (int s0 = w.s0; s0 < p.S; s0 += w.step) {
@@ -592,15 +595,13 @@ template <int FMT>
 cudaError_t launch_insert_fmt(const SpanParams& p, int num_sms, cudaStream_t st) {
   const bool many = most_blocks(p) * 2 * p.H > (long)num_sms * kInsertCtas;
   if (p.num_tokens <= (many ? kFewTokensMany : kFewTokens) * p.S) {
-    block_insert_few_kernel<FMT><<<span_grid(p, 2 * p.H, num_sms * kFewCtas, kSpanWarps), kSpanThreads, 0, st>>>(p);
-    return cudaGetLastError();
+    return launch_behind(block_insert_few_kernel<FMT>, span_grid(p, 2 * p.H, num_sms * kFewCtas, kSpanWarps), dim3(kSpanThreads), 0, st, p);
   }
   const int smem = kInsertStages * kRowsPerThread * kSpanThreads * (int)sizeof(uint4);
   static std::atomic<uint64_t> allowed{0};
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(block_insert_kernel<FMT>), smem, allowed);
   if (e != cudaSuccess) return e;
-  block_insert_kernel<FMT><<<span_grid(p, 2 * p.H, num_sms * kInsertCtas), kSpanThreads, smem, st>>>(p);
-  return cudaGetLastError();
+  return launch_behind(block_insert_kernel<FMT>, span_grid(p, 2 * p.H, num_sms * kInsertCtas), dim3(kSpanThreads), smem, st, p);
 }
 
 }  // namespace
@@ -612,14 +613,13 @@ cudaError_t launch_block_insert(const SpanParams& p, int fmt, int num_sms, cudaS
 cudaError_t launch_cache_read(const SpanParams& p, int fmt, int num_sms, cudaStream_t st) {
   const dim3 grid = span_grid(p, ((p.k_out != nullptr) + (p.v_out != nullptr)) * p.H, num_sms * kReadMost);
   switch (fmt) {
-    case FMT_BF16: cache_read_kernel<FMT_BF16><<<grid, kSpanThreads, 0, st>>>(p); break;
-    case FMT_FP8: cache_read_kernel<FMT_FP8><<<grid, kSpanThreads, 0, st>>>(p); break;
-    case FMT_NVFP4: cache_read_kernel<FMT_NVFP4><<<grid, kSpanThreads, 0, st>>>(p); break;
-    case FMT_I8B: cache_read_kernel<FMT_I8B><<<grid, kSpanThreads, 0, st>>>(p); break;
-    case FMT_F8B: cache_read_kernel<FMT_F8B><<<grid, kSpanThreads, 0, st>>>(p); break;
+    case FMT_BF16: return launch_behind(cache_read_kernel<FMT_BF16>, grid, dim3(kSpanThreads), 0, st, p);
+    case FMT_FP8: return launch_behind(cache_read_kernel<FMT_FP8>, grid, dim3(kSpanThreads), 0, st, p);
+    case FMT_NVFP4: return launch_behind(cache_read_kernel<FMT_NVFP4>, grid, dim3(kSpanThreads), 0, st, p);
+    case FMT_I8B: return launch_behind(cache_read_kernel<FMT_I8B>, grid, dim3(kSpanThreads), 0, st, p);
+    case FMT_F8B: return launch_behind(cache_read_kernel<FMT_F8B>, grid, dim3(kSpanThreads), 0, st, p);
     default: return cudaErrorInvalidValue;
   }
-  return cudaGetLastError();
 }
 
 }  // namespace msa
