@@ -26,17 +26,17 @@ constexpr int kJoinThreads = 32 * kJoinWarps;
 // runs: in the grid of the attend; rows: of a partial; cta_rows: a CTA's share of
 // them (blockIdx.y); shift: log2 of P's scale, which l carries.
 template <bool BY_SEGMENT>
-__global__ void __launch_bounds__(kJoinThreads, BY_SEGMENT ? 3 : 5) dense_combine_kernel(const DenseParams p, int runs, int rows, int cta_rows,
+__global__ void __launch_bounds__(kJoinThreads, BY_SEGMENT ? 3 : 4) dense_combine_kernel(const DenseParams p, int runs, int rows, int cta_rows,
                                                                      float shift) {
   constexpr int kJoinBatch = BY_SEGMENT ? 8 : 4;  // partials of a row a warp has in flight
   __shared__ __align__(16) float so[kJoinWarps][132];  // (read and written as float4)
   __shared__ float sm[kJoinWarps][2];
-  __shared__ int s_first, s_end;
+  __shared__ int s_first, s_end, s_more;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int c, sg;  // the segment, and the first run that begins inside it
-  if (tid == 0) {
+  if (BY_SEGMENT && tid == 0) {
     s_first = runs;
-    s_end = BY_SEGMENT ? 0 : runs;
+    s_end = 0;
   }
   __syncthreads();
   pdl_wait();
@@ -54,17 +54,27 @@ __global__ void __launch_bounds__(kJoinThreads, BY_SEGMENT ? 3 : 5) dense_combin
     if (c == runs) return;  // whole: its team has written it
   } else {
     c = blockIdx.x + 1;  // nothing begins inside a segment before run 1
-    const int2 me = __ldcg(p.info + c), before = __ldcg(p.info + c - 1);
-    const int2 x = c + tid < runs ? __ldcg(p.info + c + tid) : make_int2(-1, 0);
-    sg = me.x;
-    if (sg < 0 || me.y == 0) return;
-    if (before.x == sg && before.y != 0) return;  // the segment crossed an earlier border
-    if (c + tid < runs && (x.x != sg || x.y == 0)) atomicMin(&s_end, c + tid);
-    for (int i = c + tid + kJoinThreads; i < runs; i += kJoinThreads) {
-      const int2 y = __ldcg(p.info + i);
-      if (y.x != sg || y.y == 0) atomicMin(&s_end, i);
+    if (warp == 0) {  // (all CTAs read the same few lines of notes: one warp each, 2% of a sparse call less than all of them)
+      const int2 me = __ldcg(p.info + c), before = __ldcg(p.info + c - 1);
+      const int2 x = c + 1 + lane < runs ? __ldcg(p.info + c + 1 + lane) : make_int2(-1, 0);
+      const uint32_t ends = __ballot_sync(0xffffffffu, x.x != me.x || x.y == 0);
+      if (lane == 0) {
+        // (it begins with this run, or crossed an earlier border)
+        s_first = me.x >= 0 && me.y != 0 && !(before.x == me.x && before.y != 0) ? me.x : -1;
+        s_end = ends ? c + __ffs(ends) : runs;
+        s_more = ends == 0;
+      }
     }
     __syncthreads();
+    sg = s_first;
+    if (sg < 0) return;
+    if (s_more) {  // a long one
+      for (int i = c + 33 + tid; i < runs; i += kJoinThreads) {
+        const int2 y = __ldcg(p.info + i);
+        if (y.x != sg || y.y == 0) atomicMin(&s_end, i);
+      }
+      __syncthreads();
+    }
   }
   // part 0 is the end of run c - 1, the others the starts of the runs c to s_end - 1
   const int parts = s_end - c + 1;

@@ -71,6 +71,20 @@ def test_as_many_segments_as_teams(kv, Q, r, H):
 
 
 @pytest.mark.parametrize("kv", KINDS)
+@pytest.mark.parametrize("long,short", [(30000, 90), (60000, 100), (9000, 200)])
+def test_a_long_sequence_among_many_short_ones(kv, long, short):
+    # more segments than a quarter of the runs, and some that cross more than 32 of them, first, last and in between
+    for at in (0, short // 2, short):
+        lens = [100] * short
+        lens.insert(at, long)
+        c = attend_case(kv, lens, Hq=4, H=1, seed=at)
+        out, lse = run_attend(c)
+        ref = plain_attend({**c, "lens": [t if t == long or i < 3 else 0 for i, t in enumerate(lens)]})
+        rows = [i for i, t in enumerate(lens) if t == long or i < 3]
+        check_attend(out, lse, ref, rows=rows)
+
+
+@pytest.mark.parametrize("kv", KINDS)
 @pytest.mark.parametrize("r", [4, 16])
 @pytest.mark.parametrize("qsize,scale_spread", [(6.0, 2.0), (1.0, 8.0), (0.01, 12.0)])
 def test_large_logits_and_scales_far_apart(kv, r, qsize, scale_spread):
