@@ -641,7 +641,10 @@ msa_status_t run_dense(const msa_cache_t* c, const msa_batch_t* b, const msa_con
   // 32.9 and 31.4 (with a cold L2 41.5 and 37.0).  The host knows no lengths: the table's width bounds
   // them, so a small cache under a wide table counts as a large one.
   const double row = fmt == FMT_BF16 ? 512. : fmt == FMT_FP8 ? 264. : fmt == FMT_NVFP4 ? 144. : 256.;
-  p.stream = (double)p.S * (topk_idx ? cfg->topk : p.max_nb) * kBlock * G * row > 32e6;
+  // Over selection lists the same, but for a prompt's chunk, whose tokens share blocks: they stay (1,024 tokens on
+  // 256K 281 and 262 us, 8,192 on 64K 1,940 and 1,858; a verify step's whole path, 8 x 128K x 8 tokens, 99 with its
+  // blocks the first to go and 108 without).
+  p.stream = (!topk_idx || b->q_per_seq <= 8) && (double)p.S * (topk_idx ? cfg->topk : p.max_nb) * kBlock * G * row > 32e6;
   p.info = at<int2>(ws, pl.off_info);
   p.part_ml = at<float2>(ws, pl.off_ml);
   p.part_o = at<float>(ws, pl.off_o);
