@@ -373,7 +373,7 @@ __device__ void producer(const CUtensorMap* tmk, const CUtensorMap* tmv, const D
   } else {
 #pragma unroll 4
     for (int s0 = 0; s0 < S; s0 += 32) {
-      const int T = s0 + lane < S ? __ldg(p.seq_lens + s0 + lane) : 0;
+      const int T = s0 + lane < S ? __ldcg(p.seq_lens + s0 + lane) : 0;
       if (s0 == 0) mine0 = T;
       total += slots_of<TR::SK, LY::END>(T, max_nb);
     }
@@ -395,7 +395,7 @@ __device__ void producer(const CUtensorMap* tmk, const CUtensorMap* tmv, const D
     sb = (long)s * GC * (p.topk + kSelEnd);
   } else if (u1 > u0) {
     for (int s0 = 0; s0 < S; s0 += 32) {
-      const int T = s0 == 0 ? mine0 : s0 + lane < S ? __ldg(p.seq_lens + s0 + lane) : 0;
+      const int T = s0 == 0 ? mine0 : s0 + lane < S ? __ldcg(p.seq_lens + s0 + lane) : 0;
       const long mine = GC * slots_of<TR::SK, LY::END>(T, max_nb);
       const long incl = warp_scan(mine, lane);
       const uint32_t over = __ballot_sync(0xffffffffu, sb + incl > u0);
@@ -417,10 +417,10 @@ __device__ void producer(const CUtensorMap* tmk, const CUtensorMap* tmv, const D
   while (u < u1 && ok) {
     int T, un;
     if constexpr (SEL) {
-      T = __ldg(p.seq_lens + s / p.q_real);  // (looked at once the list is on its way, too)
+      T = __ldcg(p.seq_lens + s / p.q_real);  // (looked at once the list is on its way, too)
       un = p.topk;
     } else {
-      T = s < 32 ? __shfl_sync(0xffffffffu, mine0, s & 31) : __ldg(p.seq_lens + s);
+      T = s < 32 ? __shfl_sync(0xffffffffu, mine0, s & 31) : __ldcg(p.seq_lens + s);
       un = units_of<TR::SK>(T, max_nb);
     }
     if (un == 0) {  // an empty sequence holds no units
@@ -452,7 +452,7 @@ __device__ void producer(const CUtensorMap* tmk, const CUtensorMap* tmv, const D
     float ks_mine = 0.f, vs_mine = 0.f;   // BLK: the scales of this lane's block
     if constexpr (SEL) {
       // the whole list, one entry a lane (topk <= 32)
-      if (lane < p.topk) pick = __ldg(p.topk_idx + ((size_t)s * p.G + g) * p.topk + lane);
+      if (lane < p.topk) pick = __ldcg(p.topk_idx + ((size_t)s * p.G + g) * p.topk + lane);
       // keys that token s sees; 0: a malformed sequence, every entry of its lists is left out
       const bool good = T >= p.q_real && T <= max_nb * kBlock;
       if (!good && lane == 0) raise_flag(p.status, FLAG_BAD_SEQLEN, T);
@@ -462,14 +462,14 @@ __device__ void producer(const CUtensorMap* tmk, const CUtensorMap* tmv, const D
       const bool take = seen && (same & ((1u << lane) - 1u)) == 0;
       if (pick >= 0 && !take) raise_flag(p.status, FLAG_BAD_SELECT, pick);
       if (take) {
-        entry = __ldg(row + pick);
+        entry = __ldcg(row + pick);
         if (entry < 0 || entry >= p.num_blocks) {
           raise_flag(p.status, FLAG_BAD_BLOCK, entry);
           entry = -1;
         }
       }
     } else {
-      entry = (b_have + lane) * UPB < k0 + n ? __ldg(row + b_have + lane) : -1;
+      entry = (b_have + lane) * UPB < k0 + n ? __ldcg(row + b_have + lane) : -1;
     }
     // publish the segment and its query rows
     const int slot = ii & 1, use = ii >> 1;
@@ -508,7 +508,7 @@ __device__ void producer(const CUtensorMap* tmk, const CUtensorMap* tmv, const D
       const int b = k / UPB, half = k - b * UPB;
       if (!SEL && b >= b_have + 32) {
         b_have = b;
-        entry = (b + lane) * UPB < k0 + n ? __ldg(row + b + lane) : -1;
+        entry = (b + lane) * UPB < k0 + n ? __ldcg(row + b + lane) : -1;
       }
       if (SEL ? k == k0 : b == b_have && (k == k0 || half == 0)) {  // new entries: the ones outside the pool
         if (!SEL && (b + lane) * UPB < k0 + n && (entry < 0 || entry >= p.num_blocks)) {
@@ -538,8 +538,8 @@ __device__ void producer(const CUtensorMap* tmk, const CUtensorMap* tmv, const D
         if (SEL ? k == k0 : b == b_have && (k == k0 || half == 0)) {
           if (entry >= 0) {
             const size_t at = (size_t)entry * p.G + g;
-            ks_mine = __ldg(reinterpret_cast<const float*>(p.k_sc) + at);
-            vs_mine = __ldg(reinterpret_cast<const float*>(p.v_sc) + at);
+            ks_mine = __ldcg(reinterpret_cast<const float*>(p.k_sc) + at);
+            vs_mine = __ldcg(reinterpret_cast<const float*>(p.v_sc) + at);
           }
         }
         DenseStage f;
@@ -1547,7 +1547,7 @@ __global__ void __launch_bounds__(DenseLayout<FMT, NN, NCG>::THREADS, 1)
     if constexpr (LY::MOVE) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(LY::REGS_C));
     // sequences without keys (and malformed ones) have no units: their rows here
     for (int s = SEL ? p.S : blockIdx.x + warp * gridDim.x; s < p.S; s += gridDim.x * TEAMS * kDenseWpg) {
-      const int T = __ldg(p.seq_lens + s);
+      const int T = __ldcg(p.seq_lens + s);
       if (T >= 1 && T <= p.max_nb * kBlock) continue;
       if (T != 0 && lane == 0) raise_flag(p.status, FLAG_BAD_SEQLEN, T);
       const long rows = (long)p.Q * p.G * p.r;

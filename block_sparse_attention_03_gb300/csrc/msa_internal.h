@@ -335,8 +335,9 @@ inline cudaError_t allow_smem(const void* kern, int bytes, std::atomic<uint64_t>
 }
 
 // A programmatic launch: the grid may take its place while the one in front of it in the stream ends, and
-// waits for that by itself (pdl_wait before its first access to memory).  Behind another such
-// launch it begins some 2 us sooner than a plain one.
+// waits for that by itself (pdl_wait before its first access to memory).  What it then reads may have been written
+// since it began: no __ldg, whose data may not change while the grid lives (__ldcg).  Behind another such launch it
+// begins some 2 us sooner than a plain one.
 template <typename... K, typename... A>
 inline cudaError_t launch_behind(void (*kern)(K...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, const A&... args) {
   cudaLaunchConfig_t cfg = {};

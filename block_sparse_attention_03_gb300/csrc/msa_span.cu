@@ -81,9 +81,9 @@ __device__ __forceinline__ int load_chunk(const SpanParams& p, SpanChunk& c, int
   const int s = s0 + tid;
   int first = 0, end = 0, off = 0, count = 0;
   if (s < p.S) {
-    first = __ldg(p.first + s);
-    end = __ldg(p.end + s);
-    off = __ldg(p.offsets + s);
+    first = p.first[s];
+    end = p.end[s];
+    off = p.offsets[s];
     if (end > first) {
       uint32_t bad = 0;
       if (first < 0 || end > p.max_nb * kBlock) bad = FLAG_BAD_SEQLEN;
@@ -129,7 +129,7 @@ __device__ __forceinline__ SpanBlock find_block(const SpanParams& p, const SpanC
   b.row = c.off[at] + (p0 - first);
   b.at = p0 % kBlock;
   b.had = max(0, first - blk * kBlock);
-  b.phys = __ldg(p.block_table + (size_t)(s0 + at) * p.max_nb + blk);
+  b.phys = p.block_table[(size_t)(s0 + at) * p.max_nb + blk];
   return b;
 }
 __device__ __forceinline__ SpanBlock from_lane(const SpanBlock& b, int lane) {
@@ -404,7 +404,7 @@ __global__ void __launch_bounds__(kSpanThreads, kFewCtas) block_insert_few_kerne
   uint8_t* const codes = is_v ? p.vc : p.kc;
   float* const scales = is_v ? p.vs : p.ks;
 
-  auto load = [&](const __nv_bfloat16* src) { return __ldg(reinterpret_cast<const uint4*>(src)); };
+  auto load = [&](const __nv_bfloat16* src) { return *reinterpret_cast<const uint4*>(src); };
   auto insert = [&](const SpanBlock& b) {
     const size_t head = (size_t)b.phys * p.H + h;
     uint8_t* const data = codes + head * (kBlock * kDim);
@@ -483,19 +483,18 @@ struct Raw {
   float s;
 };
 template <int FMT>
-__device__ __forceinline__ Raw load_row(const uint8_t* __restrict__ data, const float* __restrict__ scale,
-                                        const uint8_t* __restrict__ sf, size_t row, int l16) {
+__device__ __forceinline__ Raw load_row(const uint8_t* data, const float* scale, const uint8_t* sf, size_t row, int l16) {
   Raw r;
   if constexpr (FMT == FMT_BF16) {
-    r.w = __ldg(reinterpret_cast<const uint4*>(data + row * 256) + l16);
+    r.w = reinterpret_cast<const uint4*>(data + row * 256)[l16];
   } else if constexpr (FMT == FMT_NVFP4) {
-    r.w.x = __ldg(reinterpret_cast<const uint32_t*>(data + row * 64) + l16);
-    r.w.y = __ldg(sf + row * 8 + (l16 >> 1));
+    r.w.x = reinterpret_cast<const uint32_t*>(data + row * 64)[l16];
+    r.w.y = sf[row * 8 + (l16 >> 1)];
   } else {
-    const uint2 w = __ldg(reinterpret_cast<const uint2*>(data + row * 128) + l16);
+    const uint2 w = reinterpret_cast<const uint2*>(data + row * 128)[l16];
     r.w.x = w.x;
     r.w.y = w.y;
-    if constexpr (FMT == FMT_FP8) r.s = __ldg(scale + row);
+    if constexpr (FMT == FMT_FP8) r.s = scale[row];
   }
   return r;
 }
@@ -569,7 +568,7 @@ __global__ void __launch_bounds__(kSpanThreads, kReadCtas) cache_read_kernel(con
 #pragma unroll
       for (int k = 0; k < kRowsPerThread; ++k)
         if (row0 + 16 * k < b.n) x[k] = load_row<FMT>(data, scale, sf, from + 16 * k, l16);
-      const float s = FMT == FMT_NVFP4 ? (is_v ? p.vg : p.kg) : FMT == FMT_I8B || FMT == FMT_F8B ? __ldg(scale + head) : 1.f;
+      const float s = FMT == FMT_NVFP4 ? (is_v ? p.vg : p.kg) : FMT == FMT_I8B || FMT == FMT_F8B ? scale[head] : 1.f;
 #pragma unroll
       for (int k = 0; k < kRowsPerThread; ++k)
         if (row0 + 16 * k < b.n) __stcs(reinterpret_cast<uint4*>(dst + 16 * k * step), row_bf16<FMT>(x[k], s, p.nv_round));
