@@ -204,9 +204,10 @@ class PagedCache:
                          NVFP4_MODES.get(self.nvfp4_mode, -1))
 
 
-def _looked_at_once(self, name, value):
-    """__setattr__ of holders whose tensors the serving calls look at once, and again when a field is set."""
-    self.__dict__["_seen"] = ()
+def _set_field(self, name, value):
+    """__setattr__ of holders whose tensors' types and devices the serving calls look at once for a field (_seen: the
+    device), since no tensor changes them by itself; sizes and layouts, which resize_ and as_strided_ do, at every call."""
+    self.__dict__["_seen"] = None
     self.__dict__[name] = value
 
 
@@ -216,7 +217,7 @@ class Batch:
     block_table: object   # int32 [S][max_blocks] on the device
     q_per_seq: int = 1
 
-    __setattr__ = _looked_at_once
+    __setattr__ = _set_field
 
     def struct(self) -> MsaBatchT:
         return MsaBatchT(self.seq_lens.shape[0], self.q_per_seq, self.block_table.shape[1],
@@ -233,7 +234,9 @@ class Config:
     score_type: str = "max"
     prefill_select: str = "topk"
 
-    __setattr__ = _looked_at_once
+    def __setattr__(self, name, value):
+        self.__dict__["_packed"] = None  # (_config_bytes)
+        self.__dict__[name] = value
 
     def struct(self) -> MsaConfigT:
         # an unknown score type reaches the library as -1, which rejects it
@@ -247,7 +250,7 @@ class Query:
     dtype: str = "bf16"   # "bf16" | "fp8"
     scale: float = 1.0
 
-    __setattr__ = _looked_at_once
+    __setattr__ = _set_field
 
     def struct(self) -> MsaQueryT:
         return MsaQueryT(_ptr(self.data), DTYPES[self.dtype], self.scale)
@@ -262,7 +265,7 @@ class Spans:
     token_offsets: object  # int32 [S] or longer
     block_table: object    # int32 [S][max_blocks]
 
-    __setattr__ = _looked_at_once
+    __setattr__ = _set_field
 
 
 @dataclasses.dataclass
@@ -498,32 +501,28 @@ def msa_cache_insert(cache, slot_mapping, k, v, index_k, workspace, stream=None)
                                   _stream(stream)), "msa_cache_insert")
 
 
+def _int32_on(tensors, dev: int, where: str) -> None:
+    for t in tensors:
+        if t.dtype is not _int32 or t.get_device() != dev:
+            raise MsaError(1, where)
+
+
 def _batch_checked(batch: Batch, dev: int, where: str):
-    """(device, sequences, width of the table) of a batch whose tensors are dense int32 on the device."""
+    """(sequences, width of the table) of a batch whose tensors are dense int32 on the device."""
     lens, table = batch.seq_lens, batch.block_table
     S, shape = lens.numel(), table.shape
-    if len(shape) != 2 or shape[0] != S:
+    if len(shape) != 2 or shape[0] != S or not lens.is_contiguous() or not table.is_contiguous():
         raise MsaError(1, where)
-    for t in (lens, table):
-        if t.dtype is not _int32 or t.get_device() != dev or not t.is_contiguous():
-            raise MsaError(1, where)
-    batch.__dict__["_seen"] = seen = (dev, S, shape[1])
-    return seen
-
-
-def _query_checked(q: Query, dev: int, where: str):
-    """(device, elements) of a query that is dense, on the device and of its kind's type."""
-    t = q.data
-    if t.dtype not in _query_types.get(q.dtype, ()) or t.get_device() != dev or not t.is_contiguous():
-        raise MsaError(1, where)
-    q.__dict__["_seen"] = seen = (dev, t.numel())
-    return seen
+    if batch._seen != dev:
+        _int32_on((lens, table), dev, where)
+        batch.__dict__["_seen"] = dev
+    return S, shape[1]
 
 
 def _config_bytes(cfg: Config) -> bytes:
     raw = _CONFIG_PACKER.pack(cfg.topk, cfg.init_blocks, cfg.local_blocks, cfg.index_scale, cfg.sm_scale,
                               SCORE_TYPES.get(cfg.score_type, -1), PREFILL_SELECT.get(cfg.prefill_select, -1))
-    cfg.__dict__["_seen"] = (raw,)
+    cfg.__dict__["_packed"] = raw
     return raw
 
 
@@ -534,21 +533,22 @@ def _attend(where: str, cache, batch, cfg, q, num_q_heads: int, topk_idx, out, l
     dev = cache.k.get_device()
     if dev < 0 or dev != _device():
         raise MsaError(1, where)
-    b, qs, f = batch._seen, q._seen, cfg._seen
-    if not b or b[0] != dev:
-        b = _batch_checked(batch, dev, where)
-    if not qs or qs[0] != dev:
-        qs = _query_checked(q, dev, where)
-    tokens = b[1] * batch.q_per_seq
+    S, width = _batch_checked(batch, dev, where)
+    data, tokens = q.data, S * batch.q_per_seq
     rows = tokens * num_q_heads
-    if (qs[1] != rows * 128 or out.numel() != rows * 128 or out.dtype is not _bf16 or out.get_device() != dev or not out.is_contiguous()
+    if q._seen != dev:
+        if data.dtype not in _query_types.get(q.dtype, ()) or data.get_device() != dev:
+            raise MsaError(1, where)
+        q.__dict__["_seen"] = dev
+    if (data.numel() != rows * 128 or not data.is_contiguous()
+            or out.numel() != rows * 128 or out.dtype is not _bf16 or out.get_device() != dev or not out.is_contiguous()
             or (lse is not None and (lse.numel() != rows or lse.dtype is not _f32 or lse.get_device() != dev or not lse.is_contiguous()))
             or workspace.get_device() != dev
             or (topk_idx is not None and (topk_idx.numel() != tokens * cache.num_kv_heads * cfg.topk or topk_idx.dtype is not _int32
                                           or topk_idx.get_device() != dev or not topk_idx.is_contiguous()))):
         raise MsaError(1, where)
-    at = _ATTEND.pack(_packed_cache(cache, dev, where), b[1], batch.q_per_seq, b[2], batch.seq_lens.data_ptr(),
-                      batch.block_table.data_ptr(), f[0] if f else _config_bytes(cfg), q.data.data_ptr(), DTYPES[q.dtype], q.scale)
+    at = _ATTEND.pack(_packed_cache(cache, dev, where), S, batch.q_per_seq, width, batch.seq_lens.data_ptr(),
+                      batch.block_table.data_ptr(), cfg._packed or _config_bytes(cfg), data.data_ptr(), DTYPES[q.dtype], q.scale)
     _, o_batch, o_cfg, o_q = _ATTEND.offsets
     lse_at = 0 if lse is None else lse.data_ptr()
     if topk_idx is None:
@@ -562,16 +562,16 @@ def _attend(where: str, cache, batch, cfg, q, num_q_heads: int, topk_idx, out, l
 
 
 def _spans_checked(spans: Spans, dev: int, where: str):
-    """(device, sequences, width of the table) of spans whose tensors are dense int32 on the device."""
+    """(sequences, width of the table) of spans whose tensors are dense int32 on the device."""
     first, end, offsets, table = spans.first, spans.end, spans.token_offsets, spans.block_table
     S, shape = first.numel(), table.shape
-    if len(shape) != 2 or shape[0] != S or end.numel() != S or offsets.numel() < S:
+    if (len(shape) != 2 or shape[0] != S or end.numel() != S or offsets.numel() < S
+            or not (first.is_contiguous() and end.is_contiguous() and offsets.is_contiguous() and table.is_contiguous())):
         raise MsaError(1, where)
-    for t in (first, end, offsets, table):
-        if t.dtype is not _int32 or t.get_device() != dev or not t.is_contiguous():
-            raise MsaError(1, where)
-    spans.__dict__["_seen"] = seen = (dev, S, shape[1])
-    return seen
+    if spans._seen != dev:
+        _int32_on((first, end, offsets, table), dev, where)
+        spans.__dict__["_seen"] = dev
+    return S, shape[1]
 
 
 def _span_call(call, where: str, cache, spans, k, v, workspace, stream):
@@ -581,14 +581,12 @@ def _span_call(call, where: str, cache, spans, k, v, workspace, stream):
     dev = cache.k.get_device()
     if dev < 0 or dev != _device() or workspace.get_device() != dev:
         raise MsaError(1, where)
-    seen = spans._seen
-    if not seen or seen[0] != dev:
-        seen = _spans_checked(spans, dev, where)
+    S, width = _spans_checked(spans, dev, where)
     T = (v if k is None else k).shape[0]
     kv = (T, cache.num_kv_heads, 128)
     k_at, k_step = (0, 0) if k is None else _rows(k, kv, where, dev)
     v_at, v_step = (0, 0) if v is None else _rows(v, kv, where, dev)
-    at = _SPAN.pack(_packed_cache(cache, dev, where), seen[1], seen[2], spans.first.data_ptr(), spans.end.data_ptr(),
+    at = _SPAN.pack(_packed_cache(cache, dev, where), S, width, spans.first.data_ptr(), spans.end.data_ptr(),
                     spans.token_offsets.data_ptr(), spans.block_table.data_ptr(), k_at, k_step, v_at, v_step)
     _, o_spans, o_k, o_v = _SPAN.offsets
     _check(call(at, at + o_spans, T, 0 if k is None else at + o_k, 0 if v is None else at + o_v, workspace.data_ptr(),

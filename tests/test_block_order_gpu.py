@@ -129,3 +129,48 @@ def test_calls_wait_for_what_is_in_front_of_them(kv, captured):
                 step.clear()
                 step.run(news[i], join)
         _check(step, wants[i])
+
+
+@pytest.mark.parametrize("kv", KINDS)
+@pytest.mark.parametrize("change", ["lens", "table", "query", "layout", "first", "end", "offsets"])
+def test_tensors_that_change_in_place_are_looked_at_again(kv, change):
+    # holders that a call has taken before
+    step = _Step(kv)
+    x, o = step.x, step.out
+    q = msa.Query(x["q"])
+
+    def dense():
+        msa.msa_dense_attend(step.cache, step.batch, step.cfg, q, HQ, o["dense"], None, step.ws[1])
+
+    def sparse():
+        msa.msa_sparse_attend(step.cache, step.batch, step.cfg, q, HQ, o["lists"], o["sparse"], None, step.ws[2])
+
+    def insert():
+        msa.msa_block_insert(step.cache, step.spans, x["k"], x["v"], step.ws[0])
+
+    def read():
+        msa.msa_cache_read(step.cache, step.spans, o["k"], o["v"], step.ws[3])
+
+    for call in (insert, dense, sparse, read):
+        call()
+    torch.cuda.synchronize()
+    attends, moves = (dense, sparse), (insert, read)
+    if change == "lens":
+        x["lens"].resize_(4)
+        calls = attends + moves
+    elif change == "table":
+        x["table"].resize_(4, NB)
+        calls = attends + moves
+    elif change == "query":
+        x["q"].resize_(5, HQ - 1, DIM)
+        calls = attends
+    elif change == "layout":
+        x["table"].as_strided_((5, NB), (1, 5))
+        calls = attends + moves
+    else:
+        x[{"first": "first", "end": "lens", "offsets": "off"}[change]].resize_(4)
+        calls = moves
+    for call in calls:
+        with pytest.raises(msa.MsaError) as e:
+            call()
+        assert e.value.status == 1
