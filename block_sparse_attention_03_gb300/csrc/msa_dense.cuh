@@ -64,13 +64,13 @@
 // rescaled).
 //
 // Measured (one GPU, launches back to back; shares of the measured copy rate,
-// 6,779 GB/s): 4 columns, FP8 32 x 16K-32K tokens 131 us (94%), 4 x 512K 318 us
-// (103%), BF16 32 x 16K-32K 237 us (101%), NVFP4 32 x 16K-64K 173 us (65%: the
+// 6,779 GB/s): 4 columns, FP8 32 x 16K-32K tokens 127 us (98%), 4 x 512K 314 us
+// (104%), BF16 32 x 16K-32K 237 us (101%), NVFP4 32 x 16K-64K 173 us (65%: the
 // dequantization's issue slots); 16 columns, FP8 16 x 32K 95 us (86%), NVFP4 8 x 64K 86
 // us (52%); 32 columns (8 new tokens), BF16 8 x 64K 182 us (87%), FP8 129 us (63%),
-// NVFP4 8 x 128K 226 us (40%; tensor pipe 43%, issue slots 40%, two warps a scheduler
-// waiting for each other's results); 61 ragged BF16 sequences of 48 columns 86 us
-// (48%; tensor pipe 50%); one sequence of 4K tokens 9.1 us.  Products rounded to E4M3: 4
+// NVFP4 8 x 128K 224 us (40%; tensor pipe 43%, issue slots 40%, two warps a scheduler
+// waiting for each other's results); 61 ragged BF16 sequences of 48 columns 82 us
+// (51%; tensor pipe 50%); one sequence of 4K tokens 8.8 us.  Products rounded to E4M3: 4
 // columns 229 us, 16 columns 107, 32 columns 273.
 //
 // Registers are what the wide instances lack: with 24 columns and more each of them spills
@@ -82,20 +82,20 @@
 // logits), V's times fe is one factor of the weights; nothing is left of the FP8 format's work for
 // each key.  INT8 becomes f16 exactly by 1024 + (x + 128) - 1152 (5 instructions for 4 elements, E4M3's
 // 2 or 3).  The producer asks for the scales behind the block's copies and completes the stage's phase
-// when they are there.  Measured: 4 columns, FP8 32 x 16K-32K 124 us (98% of the copy rate,
+// when they are there.  Measured: 4 columns, FP8 32 x 16K-32K 123 us (99% of the copy rate,
 // 6,702 GB/s), INT8 4 x 512K 306 us (105%); 32 columns (8 x 128K, 8 new tokens) INT8 237 us
 // (68%; tensor pipe 42%, issue slots 40%, two warps a scheduler), FP8 226; 24 columns 211 and 197, 16 columns
-// 175 (92%); one sequence of 4K tokens 9.5 us: lengths and table 1.6, first tile 3.0, its unit 4.5, the
+// 175 (92%); one sequence of 4K tokens 9.4 us: lengths and table 1.6, first tile 3.0, its unit 4.5, the
 // warps' join 5.5, the last CTA's end seen by the join's launch 6.2, joined 8.2.
 //
 // SEL: the sparse attend over selection lists (caches with block scales).  The new tokens are
 // sequences of their own, a (token, KV head)'s units the entries of its list, its runs cut
 // as above (every list counts topk units, so that the cut needs no sums).  The producer holds a list
 // in its lanes, leaves out what cannot be seen, is named twice or outside the pool, and says
-// where each unit's keys begin.  Measured: 32 tokens x 4 heads x 16 blocks of INT8 20.5 us in a graph (10.1 at
+// where each unit's keys begin.  Measured: 32 tokens x 4 heads x 16 blocks of INT8 19.8 us in a graph (10.1 at
 // the copy rate; 4 blocks 12 us: what a call costs at least is launch, lists, first tiles and join), 64 of FP8
-// (8 x 128K, 8 new tokens) 29.1 (18.1); the kernel for FP8 with token scales takes 30 and 44.  A prompt's
-// chunk reads its blocks once for each token: 8,192 tokens on 64K 1.9 (FP8) and 2.2 ms (INT8), where the
+// (8 x 128K, 8 new tokens) 28.2 (18.1); the kernel for FP8 with token scales takes 30 and 44.  A prompt's
+// chunk reads its blocks once for each token: 8,192 tokens on 64K 1.85 (FP8) and 2.22 ms (INT8), where the
 // key-block-major attend of the FP8 format takes 0.58.
 //
 // A masked key's logit is replaced, not multiplied; in units that hold masked

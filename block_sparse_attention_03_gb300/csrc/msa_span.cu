@@ -21,18 +21,18 @@
 // calls give equal bits.
 //
 // Insert bound: HBM in the limit, 256 bytes in and 128 out a row.  Measured (one GPU, back to
-// back in a graph; of 6,702 GB/s copied): a prompt of 8,192 tokens x 4 heads 6.0 us (63%, of which some
+// back in a graph; of 6,702 GB/s copied): a prompt of 8,192 tokens x 4 heads 5.9 us (64%, of which some
 // 3 are the launch and the chain lengths - sums - table - rows), 64 spans of 700 to 900 tokens x 8 heads 46 us
 // (87%), 253 ragged ones of up to 200 29 us (68%: items of 55 rows on average, of whose 420 instructions
-// a warp 170 are the item's own; issue slots 69% busy), 32 requests of one token 3.1 us, 8,000 of them 23 us.
+// a warp 170 are the item's own; issue slots 69% busy), 32 requests of one token 2.8 us, 8,000 of them 23 us.
 // Two rows' copies ahead (48 KB an SM on their way) do as well as three or a ring filled as far
 // as it goes (32 and 38 us for the ragged ones: fewer CTAs, or more to do for each item); rows read twice
 // instead, out of the L2, by teams of one to four warps 34 to 56 us (a block of 128 rows is too long for one).
 //
 // Read bound: HBM, mostly the writes.  A thread has eight rows' loads on their way before it
 // stores the first; one item a CTA in hardware's order rather than a grid that stays (8 prefixes of
-// 16K to 32K tokens 94 us, 96% of the copy rate; 109 so).  One prefix of 4K tokens 3.9 us, 61 ragged
-// spans out of NVFP4 9.0 us (60%: two rounds of the chain above).
+// 16K to 32K tokens 94 us, 96% of the copy rate; 109 so).  One prefix of 4K tokens 3.5 us, 61 ragged
+// spans out of NVFP4 8.7 us (61%: two rounds of the chain above).
 #include "msa_device.cuh"
 #include "msa_internal.h"
 
