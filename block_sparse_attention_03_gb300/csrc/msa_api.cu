@@ -272,6 +272,8 @@ msa_status_t make_plan(const msa_cache_t* c, const msa_batch_t* b, const msa_con
     const size_t pooled = (size_t)b->num_seqs * b->q_per_seq * G * b->max_blocks_per_seq * 4;
     const msa_status_t s = dense_plan_at(c, (long)b->num_seqs * b->q_per_seq, 1, hq, align256(256 + pooled), pl.dense);
     pl.total = pl.dense.total;
+    // (the kernel counts the lists' places in 32 bits)
+    if (s == MSA_OK && (long)b->num_seqs * b->q_per_seq * G * pl.dense.CG * (cfg->topk + 1) >= (1l << 31)) return MSA_ERR_UNSUPPORTED;
     return s;
   }
   if (pl.ga.cols > kMaxAttendCols || pl.ga.nt * pl.ga.sp > 8) return MSA_ERR_UNSUPPORTED;

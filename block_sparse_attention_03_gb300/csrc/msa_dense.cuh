@@ -90,9 +90,10 @@
 //
 // SEL: the sparse attend over selection lists (caches with block scales).  The new tokens are
 // sequences of their own, a (token, KV head)'s units the entries of its list, its runs cut
-// as above (every list counts topk units, so that the cut needs no sums).  The producer holds a list
-// in its lanes, leaves out what cannot be seen, is named twice or outside the pool, and says
-// where each unit's keys begin.  Measured: 32 tokens x 4 heads x 16 blocks of INT8 19.8 us in a graph (10.1 at
+// as above.  A list counts topk units, or as many as its sequence has blocks where those are fewer
+// (32 tokens on 300 to 900 with 16 places 15.2 and 13.9 us, with 32 18.0 and 13.9; 64 of 32 places 21.2 and 15.1).  The
+// producer holds a list in its lanes, leaves out what cannot be seen, is named twice or outside the pool, and
+// says where each unit's keys begin.  Measured: 32 tokens x 4 heads x 16 blocks of INT8 19.8 us in a graph (10.1 at
 // the copy rate; 4 blocks 12 us: what a call costs at least is launch, lists, first tiles and join), 64 of FP8
 // (8 x 128K, 8 new tokens) 28.2 (18.1); the kernel for FP8 with token scales takes 30 and 44.  A prompt's
 // chunk reads its blocks once for each token: 8,192 tokens on 64K 1.85 (FP8) and 2.22 ms (INT8), where the
@@ -330,23 +331,62 @@ __device__ __forceinline__ int slots_of(int T, int max_nb) {
   return un > 0 ? un + END : 0;
 }
 
+// The query token of a column (SEL: tokens are sequences).  What a call fetches of code for the first time is
+// latency in its start and ends, so it is kept small.
+template <bool SEL>
+__device__ __forceinline__ int token_of(int col, int r) {
+  return SEL ? 0 : col / r;
+}
+
+// Places of a list (SEL): no more than the sequence has blocks, and one at least, whose segment writes the row.
+__device__ __forceinline__ int places_of(int T, int q, int max_nb, int topk) {
+  const int blocks = T >= q && T <= max_nb * kBlock ? (T - 1) / kBlock + 1 : 1;
+  return blocks < topk ? blocks : topk;
+}
+// The lane of the k-th set bit of a mask that has more than k (else anything from 0 to 31).
+__device__ __forceinline__ int nth_lane(uint32_t mask, int k) {
+  int at = 0;
+#pragma unroll
+  for (int step = 16; step > 0; step >>= 1)
+    if (__popc(mask & ((1u << (at + step)) - 1u)) <= k) at += step;
+  return at;
+}
+
 // a / b of numbers from 0 up; in 32 bits where they fit (a division in 64 takes some hundred cycles).
 __device__ __forceinline__ long quotient(long a, long b) {
   return ((a | b) >> 32) == 0 ? (long)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
-__device__ __forceinline__ long warp_sum(long v) {
+__device__ __forceinline__ uint32_t quotient(uint32_t a, uint32_t b) { return a / b; }
+
+template <typename U>
+__device__ __forceinline__ U warp_sum(U v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
-__device__ __forceinline__ long warp_scan(long v, int lane) {  // inclusive
+template <typename U>
+__device__ __forceinline__ U warp_scan(U v, int lane) {  // inclusive
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long t = __shfl_up_sync(0xffffffffu, v, o);
+    const U t = __shfl_up_sync(0xffffffffu, v, o);
     if (lane >= o) v += t;
   }
   return v;
+}
+
+// The run [u0, u1) of team c, of `total` units cut evenly into as many as there are teams (no unit: the last ones).
+// One division; where the runs with one unit more lie only has to be the same for all, so that fp32 will do.
+template <typename U>
+__device__ __forceinline__ void run_of(U c, U teams, U total, U& u0, U& u1) {
+  const U each = quotient(total, teams), more = total - each * teams;
+  const float rate = each == 0 ? 1.f : __fdividef((float)(int)more, (float)(int)teams);
+  auto start = [&](U i) {
+    const U extra = (U)(int)((float)(int)i * rate);
+    return i * each + (i == teams || extra > more ? more : extra);
+  };
+  u0 = start(c);
+  u1 = start(c + 1);
 }
 
 // ---------------------------------------------------------------- the producer warp
@@ -361,64 +401,102 @@ __device__ void producer(const CUtensorMap* tmk, const CUtensorMap* tmv, const D
   uint64_t *full = tm.full, *empty = tm.empty, *ifull = tm.ifull, *iempty = tm.iempty;
   int* dead = tm.dead;
   const int S = p.S, max_nb = p.max_nb;
-  const long GC = (long)p.G * p.CG;
+  using U = std::conditional_t<SEL, uint32_t, long>;  // (the host keeps the lists' places below 2^31)
+  const U GC = (U)p.G * (U)p.CG;
   // Units in all, then the run of this team: [u0, u1).  Every segment has END units
   // more than its keys, which stand for its end (the join, the output, the next
   // one's start), so that runs with many short segments are not the last: without it
   // 61 ragged sequences of 48 columns take 14% longer.
-  long total = 0;
   int mine0 = 0;  // the length of sequence `lane`: a batch of up to 32 is read once
-  if constexpr (SEL) {  // every token has the same number of places
-    total = (long)S * GC * (p.topk + kSelEnd);
+  const U teams = (U)gridDim.x * LY::TEAMS, c = (U)tm.id;
+  U u0 = 0, u1 = 0;
+  int s = 0;  // the sequence that holds u0: sb units (x GC) come before it
+  U sb = 0;
+  U pick0_row = 0;  // SEL: the list that the run begins in, on its way
+  int pick0 = -1;
+  if constexpr (SEL) {
+    // Where all sequences have topk blocks, every token has the same number of places and the first list is
+    // asked for together with the lengths; else the places follow the lengths.
+    const U R = (U)S / (U)p.q_real, list = GC * (U)(p.topk + kSelEnd);
+    run_of<U>(c, teams, (U)S * list, u0, u1);
+    s = (int)quotient(u0, list);
+    sb = (U)s * list;
+    if (u1 > u0) {
+      pick0_row = (U)s * p.G + quotient(u0 - sb, (U)(p.topk + kSelEnd) * p.CG);
+      if (lane < p.topk) pick0 = __ldcg(p.topk_idx + (size_t)pick0_row * p.topk + lane);
+    }
+    bool full = true;
+#pragma unroll 1
+    for (U at = lane; at < R; at += 32) {
+      const int T = __ldcg(p.seq_lens + at);
+      if (at < 32) mine0 = T;
+      full = full && places_of(T, p.q_real, max_nb, p.topk) == p.topk;
+    }
+    if (__builtin_expect(!__all_sync(0xffffffffu, full), 0)) {
+      const U per = GC * (U)p.q_real;
+      U total = 0;
+#pragma unroll 1
+      for (U at = lane; at < R; at += 32)
+        total += places_of(at < 32 ? mine0 : __ldcg(p.seq_lens + at), p.q_real, max_nb, p.topk) + kSelEnd;
+      __syncwarp();
+      run_of<U>(c, teams, warp_sum(total) * per, u0, u1);
+      s = 0;
+      sb = 0;
+#pragma unroll 1
+      for (U s0 = 0; s0 < R && u1 > u0; s0 += 32) {
+        const bool real = s0 + lane < R;
+        const int T = s0 == 0 ? mine0 : real ? __ldcg(p.seq_lens + s0 + lane) : 0;
+        const U mine = real ? per * (U)(places_of(T, p.q_real, max_nb, p.topk) + kSelEnd) : 0;
+        const U incl = warp_scan(mine, lane);
+        const uint32_t over = __ballot_sync(0xffffffffu, sb + incl > u0);
+        if (over) {
+          const int l = __ffs(over) - 1;
+          sb += __shfl_sync(0xffffffffu, incl - mine, l);
+          const U token = quotient(__shfl_sync(0xffffffffu, mine, l), (U)p.q_real), i = quotient(u0 - sb, token);
+          s = (int)((s0 + l) * (U)p.q_real + i);
+          sb += i * token;
+          break;
+        }
+        sb += __shfl_sync(0xffffffffu, incl, 31);
+      }
+    }
   } else {
+    U total = 0;
 #pragma unroll 4
     for (int s0 = 0; s0 < S; s0 += 32) {
       const int T = s0 + lane < S ? __ldcg(p.seq_lens + s0 + lane) : 0;
       if (s0 == 0) mine0 = T;
       total += slots_of<TR::SK, LY::END>(T, max_nb);
     }
-    total = warp_sum(total) * GC;
-  }
-  const long teams = (long)gridDim.x * LY::TEAMS;
-  const long grid = total < teams ? total : teams;
-  const long c = tm.id;
-  long u0 = 0, u1 = 0;
-  if (c < grid) {
-    u0 = quotient(c * total, grid);
-    u1 = quotient((c + 1) * total, grid);
-  }
-  // the sequence that holds u0: sb units (x GC) come before it
-  int s = 0;
-  long sb = 0;
-  if constexpr (SEL) {
-    s = (int)quotient(u0, GC * (p.topk + kSelEnd));
-    sb = (long)s * GC * (p.topk + kSelEnd);
-  } else if (u1 > u0) {
-    for (int s0 = 0; s0 < S; s0 += 32) {
-      const int T = s0 == 0 ? mine0 : s0 + lane < S ? __ldcg(p.seq_lens + s0 + lane) : 0;
-      const long mine = GC * slots_of<TR::SK, LY::END>(T, max_nb);
-      const long incl = warp_scan(mine, lane);
-      const uint32_t over = __ballot_sync(0xffffffffu, sb + incl > u0);
-      if (over) {
-        const int l = __ffs(over) - 1;
-        s = s0 + l;
-        sb += __shfl_sync(0xffffffffu, incl - mine, l);
-        break;
+    run_of<U>(c, teams, warp_sum(total) * GC, u0, u1);
+    if (u1 > u0) {
+      for (int s0 = 0; s0 < S; s0 += 32) {
+        const int T = s0 == 0 ? mine0 : s0 + lane < S ? __ldcg(p.seq_lens + s0 + lane) : 0;
+        const U mine = GC * slots_of<TR::SK, LY::END>(T, max_nb);
+        const U incl = warp_scan(mine, lane);
+        const uint32_t over = __ballot_sync(0xffffffffu, sb + incl > u0);
+        if (over) {
+          const int l = __ffs(over) - 1;
+          s = s0 + l;
+          sb += __shfl_sync(0xffffffffu, incl - mine, l);
+          break;
+        }
+        sb += __shfl_sync(0xffffffffu, incl, 31);
       }
-      sb += __shfl_sync(0xffffffffu, incl, 31);
     }
   }
   // what the combine reads: the segment the run begins in, and whether it began before
-  long u = u0;
+  U u = u0;
   int bi = 0, ii = 0;
   bool ok = true;
   bool first = true;
 #pragma unroll 1
   while (u < u1 && ok) {
-    int T, un;
+    int T, un, sr = s;
     if constexpr (SEL) {
-      T = __ldcg(p.seq_lens + s / p.q_real);  // (looked at once the list is on its way, too)
-      un = p.topk;
+      sr = (int)((uint32_t)s / (uint32_t)p.q_real);
+      T = sr < 32 ? __shfl_sync(0xffffffffu, mine0, sr & 31) : __ldcg(p.seq_lens + sr);
+      un = places_of(T, p.q_real, max_nb, p.topk);
     } else {
       T = s < 32 ? __shfl_sync(0xffffffffu, mine0, s & 31) : __ldcg(p.seq_lens + s);
       un = units_of<TR::SK>(T, max_nb);
@@ -427,36 +505,38 @@ __device__ void producer(const CUtensorMap* tmk, const CUtensorMap* tmv, const D
       ++s;
       continue;
     }
-    const long in_s = u - sb;
-    const int span = un + (SEL ? kSelEnd : LY::END), gc = (int)quotient(in_s, span), k0 = (int)(in_s - (long)gc * span);
+    const U in_s = u - sb;
+    const int span = un + (SEL ? kSelEnd : LY::END), gc = (int)quotient(in_s, (U)span), k0 = (int)(in_s - (U)gc * span);
     if (k0 >= un) {  // another run's segment end
       u += span - k0;
-      if (gc + 1 == GC) {
-        sb += (long)span * GC;
+      if ((U)gc + 1 == GC) {
+        sb += (U)span * GC;
         ++s;
       }
       continue;
     }
-    const long left = u1 - u;
-    const int n = left < (long)(un - k0) ? (int)left : un - k0;
-    const int g = gc / p.CG, cg = gc - g * p.CG;
+    const U left = u1 - u;
+    const int n = left < (U)(un - k0) ? (int)left : un - k0;
+    const int g = (int)((uint32_t)gc / (uint32_t)p.CG), cg = gc - g * p.CG;
     const bool cut_start = k0 > 0, cut_end = k0 + n < un;
-    const int sg = (int)((long)s * GC + gc);
+    const int sg = (int)((U)s * GC + gc);
     if (first && lane == 0) p.info[c] = make_int2(sg, cut_start ? 1 : 0);
     first = false;
     // the first 32 block-table entries, on their way while the segment is published
-    const int32_t* row = p.block_table + (size_t)(SEL ? s / p.q_real : s) * max_nb;
+    const int32_t* row = p.block_table + (size_t)sr * max_nb;
     constexpr int UPB = kBlock / TR::SK;  // units a block
     int b_have = SEL ? 0 : k0 / UPB;      // entries [b_have, b_have + 32), one a lane
     int entry = -1, pick = -1;
     float ks_mine = 0.f, vs_mine = 0.f;   // BLK: the scales of this lane's block
     if constexpr (SEL) {
       // the whole list, one entry a lane (topk <= 32)
-      if (lane < p.topk) pick = __ldcg(p.topk_idx + ((size_t)s * p.G + g) * p.topk + lane);
+      const U list = (U)s * p.G + g;
+      if (list == pick0_row && u == u0) pick = pick0;
+      else if (lane < p.topk) pick = __ldcg(p.topk_idx + (size_t)list * p.topk + lane);
       // keys that token s sees; 0: a malformed sequence, every entry of its lists is left out
       const bool good = T >= p.q_real && T <= max_nb * kBlock;
       if (!good && lane == 0) raise_flag(p.status, FLAG_BAD_SEQLEN, T);
-      T = good ? T - p.q_real + s % p.q_real + 1 : 0;
+      T = good ? T - p.q_real + (s - sr * p.q_real) + 1 : 0;
       const bool seen = pick >= 0 && pick <= (T - 1) >> 7;  // (an arithmetic shift: T = 0 sees none)
       const uint32_t same = __match_any_sync(0xffffffffu, seen ? pick : -1 - lane);
       const bool take = seen && (same & ((1u << lane) - 1u)) == 0;
@@ -467,6 +547,14 @@ __device__ void producer(const CUtensorMap* tmk, const CUtensorMap* tmv, const D
           raise_flag(p.status, FLAG_BAD_BLOCK, entry);
           entry = -1;
         }
+      }
+      // the entries that count to the list's first places: there are no more of them than places
+      const uint32_t taken = __ballot_sync(0xffffffffu, take);
+      if (__builtin_expect((taken & (taken + 1u)) != 0u, 0)) {
+        const int at = nth_lane(taken, lane);
+        const int e = __shfl_sync(0xffffffffu, entry, at), k = __shfl_sync(0xffffffffu, pick, at);
+        entry = lane < __popc(taken) ? e : -1;
+        pick = lane < __popc(taken) ? k : -1;
       }
     } else {
       entry = (b_have + lane) * UPB < k0 + n ? __ldcg(row + b_have + lane) : -1;
@@ -496,8 +584,8 @@ __device__ void producer(const CUtensorMap* tmk, const CUtensorMap* tmv, const D
     __syncwarp();
     fence_proxy_async();
     for (int row = lane; row < nrows; row += 32) {
-      const int col = c0 + row, i = col / p.r, h = col - i * p.r;
-      const size_t src = ((size_t)s * p.Q + i) * ((size_t)p.G * p.r) + (size_t)g * p.r + h;
+      const int col = c0 + row, i = token_of<SEL>(col, p.r), h = col - i * p.r;
+      const size_t src = ((size_t)s * (SEL ? 1 : p.Q) + i) * ((size_t)p.G * p.r) + (size_t)g * p.r + h;
       bulk_g2s(tm.mem + LY::Q + (size_t)slot * LY::QSLOT + (size_t)row * LY::QROW,
                static_cast<const uint8_t*>(p.q) + src * qrow_bytes, (uint32_t)qrow_bytes, &ifull[slot]);
     }
@@ -996,6 +1084,7 @@ __device__ void consumer(const DenseParams& p, const DenseTeam& tm, int bar, int
   const int tid = warp * 32 + lane;
   const int g8 = lane >> 2, j = lane & 3;
   const int H = p.G * p.r;
+  auto Q = [&] { return SEL ? 1 : p.Q; };  // (read where it is used: a register over the loop spills)
   int* dead = tm.dead;
   float4* ml = reinterpret_cast<float4*>(tm.mem + LY::ML);  // [warps][WROWS]: m, l, the scale of O or its weight
   float* cf = reinterpret_cast<float*>(tm.mem + LY::CF);      // [ROWS]
@@ -1055,7 +1144,7 @@ __device__ void consumer(const DenseParams& p, const DenseTeam& tm, int bar, int
     float fe[NN], vlim = -1.f;
 #pragma unroll
     for (int n = 0; n < NN; ++n) fe[n] = 0.f;
-    const int lim0 = f.T - p.Q;  // every row sees the keys up to here
+    const int lim0 = f.T - Q();  // every row sees the keys up to here
 
 #pragma unroll 1
     for (int k = f.k0; k < f.k0 + f.n; ++k) {
@@ -1101,7 +1190,7 @@ __device__ void consumer(const DenseParams& p, const DenseTeam& tm, int bar, int
 #pragma unroll
             for (int n = 0; n < NN; ++n) {
               const int row = ct * LY::WROWS + 8 * n + g8;
-              const int lim = row < nrows ? lim0 + (c0 + row) / p.r - key0 : -1;
+              const int lim = row < nrows ? lim0 + token_of<SEL>(c0 + row, p.r) - key0 : -1;
 #pragma unroll
               for (int t = 0; t < KC / 8; ++t) {
                 if (8 * t + 2 * j > lim) y[t][n].x = -INFINITY;
@@ -1293,17 +1382,17 @@ __device__ void consumer(const DenseParams& p, const DenseTeam& tm, int bar, int
             r0 = r0 < kb ? kb : r0;
             r1 = r1 > kb + KC ? kb + KC : r1;
             const bool apart =
-                p.Q > 1 && v_not_finite<FMT>(tm.tiles + (size_t)st * LY::STAGE, vsb, r0, r1, lane);
+                Q() > 1 && v_not_finite<FMT>(tm.tiles + (size_t)st * LY::STAGE, vsb, r0, r1, lane);
 #pragma unroll 1
-            for (int i = apart ? 0 : p.Q - 1; i < p.Q; ++i) {
+            for (int i = apart ? 0 : Q() - 1; i < Q(); ++i) {
               if (apart) {
 #pragma unroll
                 for (int n = 0; n < NN; ++n) {
                   const int col = c0 + ct * LY::WROWS + 8 * n + 2 * j;
-                  keep[n] = (col / p.r == i ? 1 : 0) | ((col + 1) / p.r == i ? 2 : 0);
+                  keep[n] = (token_of<SEL>(col, p.r) == i ? 1 : 0) | (token_of<SEL>(col + 1, p.r) == i ? 2 : 0);
                 }
               }
-              MSA_DENSE_PV(true, klast - (p.Q - 1 - i), keep)
+              MSA_DENSE_PV(true, klast - (Q() - 1 - i), keep)
             }
           }
 #undef MSA_DENSE_PV
@@ -1380,8 +1469,8 @@ __device__ void consumer(const DenseParams& p, const DenseTeam& tm, int bar, int
         }
         if (whole) {
           const float inv = L == 0.f ? 0.f : 1.f / L;
-          const int col = c0 + row, i = col / p.r, h = col - i * p.r;
-          const size_t orow = ((size_t)f.s * p.Q + i) * H + (size_t)f.g * p.r + h;
+          const int col = c0 + row, i = token_of<SEL>(col, p.r), h = col - i * p.r;
+          const size_t orow = ((size_t)f.s * Q() + i) * H + (size_t)f.g * p.r + h;
           uint2 pk;
           pk.x = pack_bf16x2(acc.x * inv, acc.y * inv);
           pk.y = pack_bf16x2(acc.z * inv, acc.w * inv);
@@ -1421,8 +1510,8 @@ __device__ void consumer(const DenseParams& p, const DenseTeam& tm, int bar, int
           if (!whole) {
             p.part_ml[(size_t)f.part * LY::ROWS + tid] = make_float2(M, L);
           } else if (p.lse) {
-            const int col = c0 + tid, i = col / p.r, h = col - i * p.r;
-            p.lse[((size_t)f.s * p.Q + i) * H + (size_t)f.g * p.r + h] =
+            const int col = c0 + tid, i = token_of<SEL>(col, p.r), h = col - i * p.r;
+            p.lse[((size_t)f.s * Q() + i) * H + (size_t)f.g * p.r + h] =
                 L == 0.f ? -INFINITY : (M - SHIFT + log2f(L)) * 0.69314718055994531f;
           }
         }
@@ -1440,8 +1529,8 @@ __device__ void consumer(const DenseParams& p, const DenseTeam& tm, int bar, int
         for (int c = 0; c < 2; ++c) {
           const int row = ct * LY::WROWS + 8 * n + 2 * j + (FMT == FMT_BF16 ? (g8 & 1) : c);
           live[c] = row < nrows;
-          const int col = c0 + row, i = col / p.r, h = col - i * p.r;
-          at[c] = whole ? (((size_t)f.s * p.Q + i) * H + (size_t)f.g * p.r + h) * kDim
+          const int col = c0 + row, i = token_of<SEL>(col, p.r), h = col - i * p.r;
+          at[c] = whole ? (((size_t)f.s * Q() + i) * H + (size_t)f.g * p.r + h) * kDim
                         : ((size_t)f.part * LY::ROWS + row) * kDim;
         }
 #pragma unroll

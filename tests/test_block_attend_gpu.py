@@ -45,6 +45,25 @@ def test_sparse_columns(kv, qd, Q, r, H, K):
 
 
 @pytest.mark.parametrize("kv", KINDS)
+@pytest.mark.parametrize("Q,K,r,H", [(1, 16, 4, 2), (1, 32, 1, 8), (3, 32, 2, 2), (8, 8, 5, 1), (2, 4, 33, 1)])
+@pytest.mark.parametrize("lens", ["short", "one long", "long and short"])
+def test_lists_longer_than_the_sequences(kv, Q, K, r, H, lens):
+    # more than 32 sequences, most with fewer blocks than a list has places; the entries in any order, padding among them
+    gen = np.random.default_rng(K + Q)
+    n = 37
+    got = gen.integers(Q, 700, n)
+    if lens == "one long":
+        got[n // 2] = 128 * K + 700
+    elif lens == "long and short":
+        got[::2] = 128 * K + gen.integers(0, 900, len(got[::2]))
+    got[:3] = Q, 128, 129
+    c = attend_case(kv, [0] + [int(t) for t in got] + [0], Q=Q, Hq=r * H, H=H, seed=K)
+    mine = gen.permuted(select(c, K, seed=Q), axis=-1)
+    out, lse = run_attend(c, _gpu(mine), want=2)  # (the empty sequences)
+    check_attend(out, lse, plain_attend(c, mine))
+
+
+@pytest.mark.parametrize("kv", KINDS)
 def test_many_ragged_sequences(kv):
     rng = np.random.default_rng(5)
     c = attend_case(kv, [int(x) for x in rng.integers(0, 900, 90)], Hq=4, H=2, seed=6)

@@ -151,6 +151,14 @@ def _cache(msa, kv="int8_block", **over):
     return msa.PagedCache(kv, "bf16", 2, 2, idx=None, **{**t, **over})
 
 
+@pytest.mark.parametrize("kv", [8, 9])
+def test_places_of_all_lists_are_counted_in_32_bits(lib, kv):  # noqa: F811
+    for seqs, topk, ok in ((1 << 24, 32, False), (1 << 24, 16, True), (1 << 20, 32, True), (1 << 25, 16, False)):
+        c, b, f, _ = _structs(kv, b__num_seqs=seqs, f__topk=topk)
+        assert (lib.msa_workspace_size(ref(c), ref(b), ref(f), 16) > 0) == ok
+
+
+
 @pytest.mark.parametrize("kv", KINDS)
 @pytest.mark.parametrize("name", ["msa_block_insert", "msa_cache_read"])
 def test_python_refuses_what_the_kernels_would_misread(on_device_0, kv, name):  # noqa: F811
