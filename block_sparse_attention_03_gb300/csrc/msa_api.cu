@@ -215,6 +215,13 @@ bool tc_indexer(const msa_cache_t* c, const msa_batch_t* b) {
   return fmt_of(c->index_dtype) == FMT_FP8 && b->q_per_seq > 8 && (G == 1 || G == 2 || G == 4 || G == 8);
 }
 
+// Units of a launch of the dense attend, which counts them in 32 bits (a 64-bit count takes a short call 0.2 to 0.5 us):
+// larger batches go in several.  A sequence's, by the width of its table (64 keys each at least, 4 for an end), are
+// below 2^31; so are those of a token's lists.
+constexpr long kMaxUnits = (1l << 32) - 1;
+long sequence_units(int G, const DensePlan& pl, int max_nb) { return (long)G * pl.CG * (2l * max_nb + 4); }
+long list_units(int G, const DensePlan& pl, int topk) { return (long)G * pl.CG * (topk + 1); }
+
 // The dense attend's kernel for `seqs` sequences of q new tokens; its workspace from byte o on.
 msa_status_t dense_plan_at(const msa_cache_t* c, long seqs, int q, int hq, size_t o, DensePlan& pl) {
   const int G = c->num_kv_heads;
@@ -272,8 +279,7 @@ msa_status_t make_plan(const msa_cache_t* c, const msa_batch_t* b, const msa_con
     const size_t pooled = (size_t)b->num_seqs * b->q_per_seq * G * b->max_blocks_per_seq * 4;
     const msa_status_t s = dense_plan_at(c, (long)b->num_seqs * b->q_per_seq, 1, hq, align256(256 + pooled), pl.dense);
     pl.total = pl.dense.total;
-    // (the kernel counts the lists' places in 32 bits)
-    if (s == MSA_OK && (long)b->num_seqs * b->q_per_seq * G * pl.dense.CG * (cfg->topk + 1) >= (1l << 31)) return MSA_ERR_UNSUPPORTED;
+    if (s == MSA_OK && b->q_per_seq * list_units(G, pl.dense, cfg->topk) > kMaxUnits) return MSA_ERR_UNSUPPORTED;
     return s;
   }
   if (pl.ga.cols > kMaxAttendCols || pl.ga.nt * pl.ga.sp > 8) return MSA_ERR_UNSUPPORTED;
@@ -628,9 +634,6 @@ msa_status_t run_dense(const msa_cache_t* c, const msa_batch_t* b, const msa_con
   p.cper = pl.cper;
   p.max_nb = b->max_blocks_per_seq;
   p.num_blocks = c->num_blocks;
-  p.seq_lens = b->seq_lens;
-  p.block_table = b->block_table;
-  p.q = q->data;
   p.q_fp8 = q->dtype == MSA_DTYPE_FP8_E4M3;
   p.q_scale = p.q_fp8 ? q->scale : 1.f;
   p.col_const = cfg->sm_scale * 1.4426950408889634f * (fmt == FMT_NVFP4 ? c->k_global : 1.f);
@@ -650,18 +653,30 @@ msa_status_t run_dense(const msa_cache_t* c, const msa_batch_t* b, const msa_con
   p.info = at<int2>(ws, pl.off_info);
   p.part_ml = at<float2>(ws, pl.off_ml);
   p.part_o = at<float>(ws, pl.off_o);
-  p.out = out;
-  p.lse = lse;
+  p.lse = nullptr;
   p.status = at<DeviceStatus>(ws, 0);
-  cudaError_t e;
-  if (fmt == FMT_BF16) e = launch_dense_bf16(&tk, &tv, p, sms, st);
-  else if (fmt == FMT_FP8) e = launch_dense_fp8(&tk, &tv, p, sms, st);
-  else if (fmt == FMT_I8B) e = topk_idx ? launch_dense_int8_sel(&tk, &tv, p, sms, st) : launch_dense_int8(&tk, &tv, p, sms, st);
-  else if (fmt == FMT_F8B) e = topk_idx ? launch_dense_fp8b_sel(&tk, &tv, p, sms, st) : launch_dense_fp8b(&tk, &tv, p, sms, st);
-  else if (c->nvfp4_mode == MSA_NVFP4_E4M3_PRODUCT) e = launch_dense_nvfp4_rounded(&tk, &tv, p, sms, st);
-  else e = launch_dense_nvfp4(&tk, &tv, p, sms, st);
-  if (e != cudaSuccess) return MSA_ERR_CUDA;
-  return cuda_status(launch_dense_combine(p, fmt, sms, st));
+  const long tokens = b->q_per_seq, most = kMaxUnits / (topk_idx ? tokens * list_units(G, pl, cfg->topk) : sequence_units(G, pl, p.max_nb));
+  for (long s0 = 0; s0 < b->num_seqs; s0 += most) {
+    const long n = b->num_seqs - s0 < most ? b->num_seqs - s0 : most;
+    const size_t row = (size_t)s0 * tokens * hq;
+    p.S = (int)(topk_idx ? n * tokens : n);
+    p.seq_lens = b->seq_lens + s0;
+    p.block_table = b->block_table + (size_t)s0 * p.max_nb;
+    if (topk_idx) p.topk_idx = topk_idx + (size_t)s0 * tokens * G * cfg->topk;
+    p.q = static_cast<const uint8_t*>(q->data) + row * kDim * (p.q_fp8 ? 1 : 2);
+    p.out = static_cast<uint8_t*>(out) + row * kDim * 2;
+    if (lse) p.lse = lse + row;
+    cudaError_t e;
+    if (fmt == FMT_BF16) e = launch_dense_bf16(&tk, &tv, p, sms, st);
+    else if (fmt == FMT_FP8) e = launch_dense_fp8(&tk, &tv, p, sms, st);
+    else if (fmt == FMT_I8B) e = topk_idx ? launch_dense_int8_sel(&tk, &tv, p, sms, st) : launch_dense_int8(&tk, &tv, p, sms, st);
+    else if (fmt == FMT_F8B) e = topk_idx ? launch_dense_fp8b_sel(&tk, &tv, p, sms, st) : launch_dense_fp8b(&tk, &tv, p, sms, st);
+    else if (c->nvfp4_mode == MSA_NVFP4_E4M3_PRODUCT) e = launch_dense_nvfp4_rounded(&tk, &tv, p, sms, st);
+    else e = launch_dense_nvfp4(&tk, &tv, p, sms, st);
+    if (e == cudaSuccess) e = launch_dense_combine(p, fmt, sms, st);
+    if (e != cudaSuccess) return MSA_ERR_CUDA;
+  }
+  return MSA_OK;
 }
 
 // The path's second half over a cache with block scales: the top-k of the pooled scores and the

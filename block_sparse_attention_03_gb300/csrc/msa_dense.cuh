@@ -70,12 +70,13 @@
 // us (52%); 32 columns (8 new tokens), BF16 8 x 64K 182 us (87%), FP8 129 us (63%),
 // NVFP4 8 x 128K 224 us (40%; tensor pipe 43%, issue slots 40%, two warps a scheduler
 // waiting for each other's results); 61 ragged BF16 sequences of 48 columns 82 us
-// (51%; tensor pipe 50%); one sequence of 4K tokens 8.8 us.  Products rounded to E4M3: 4
+// (51%; tensor pipe 50%); one sequence of 4K tokens 8.5 us.  Products rounded to E4M3: 4
 // columns 229 us, 16 columns 107, 32 columns 273.
 //
 // Registers are what the wide instances lack: with 24 columns and more each of them spills
-// (176 to 324 bytes of stores a thread, a stack of 72 to 168: mostly the producers', whose share is 40 or
-// 24), NVFP4 with 8 and 16 columns too (52 and 96), INT8 with 16 (80 to 104), the others not (FP8: 8).
+// (104 to 272 bytes of stores a thread, a stack of 56 to 176: mostly the producers', whose share is 40 or
+// 24), NVFP4 with 8 and 16 columns too (52 and 84), with 16 INT8 (80) and both formats over lists (132), the others
+// not (FP8: 8).
 //
 // Caches with one scale for each block and head (INT8, FP8).  A unit is a block, so its two
 // scales are two numbers of the stage: K's goes into the columns' factors (where keys are masked into the
@@ -83,9 +84,9 @@
 // each key.  INT8 becomes f16 exactly by 1024 + (x + 128) - 1152 (5 instructions for 4 elements, E4M3's
 // 2 or 3).  The producer asks for the scales behind the block's copies and completes the stage's phase
 // when they are there.  Measured: 4 columns, FP8 32 x 16K-32K 123 us (99% of the copy rate,
-// 6,702 GB/s), INT8 4 x 512K 306 us (105%); 32 columns (8 x 128K, 8 new tokens) INT8 237 us
-// (68%; tensor pipe 42%, issue slots 40%, two warps a scheduler), FP8 226; 24 columns 211 and 197, 16 columns
-// 175 (92%); one sequence of 4K tokens 9.4 us: lengths and table 1.6, first tile 3.0, its unit 4.5, the
+// 6,702 GB/s), INT8 4 x 512K 306 us (105%); 32 columns (8 x 128K, 8 new tokens) INT8 239 us
+// (67%; tensor pipe 42%, issue slots 40%, two warps a scheduler), FP8 226; 24 columns 212 and 191, 16 columns
+// 175 (92%); one sequence of 4K tokens 9.1 us: lengths and table 1.6, first tile 3.0, its unit 4.5, the
 // warps' join 5.5, the last CTA's end seen by the join's launch 6.2, joined 8.2.
 //
 // SEL: the sparse attend over selection lists (caches with block scales).  The new tokens are
@@ -175,9 +176,11 @@ struct DenseLayout {
   // Where an equal share is too small, the consumers take registers over from the
   // producers; their warps come in fours then (the producers' four hold idle ones).
   // Three teams of one column tile do better with equal shares (173 us, 182 so).
-  // (INT8's conversions want a few more: 64 columns 222 us, 233 so; 24 211 and 216; FP8 by blocks 200 and 197.)
+  // (INT8's conversions want a few more: 64 columns 221 us, 224 with the others' shares; 24 212 and 218; but one group of
+  // 32 243 and 238; FP8 by blocks, 24 columns 200 and 197.)
   static constexpr bool WIDE = NN >= 3, MOVE = WIDE || (TEAMS == 3 && NN == 2);
-  static constexpr int REGS_P = WIDE ? (FMT == FMT_I8B ? 24 : 40) : 56, REGS_C = WIDE ? (FMT == FMT_I8B ? 240 : 232) : 152;
+  static constexpr bool MORE = FMT == FMT_I8B && !(NN == 4 && NCG == 1);
+  static constexpr int REGS_P = WIDE ? (MORE ? 24 : 40) : 56, REGS_C = WIDE ? (MORE ? 240 : 232) : 152;
   static constexpr int CONSUMERS = 32 * kDenseWpg * TEAMS;
   static constexpr int THREADS = CONSUMERS + (MOVE ? 128 : 32 * TEAMS);
   static_assert(!MOVE || 128 * REGS_P + CONSUMERS * REGS_C <= (65536 / THREADS / 8 * 8) * THREADS, "shares of the launch's registers");
@@ -352,24 +355,15 @@ __device__ __forceinline__ int nth_lane(uint32_t mask, int k) {
   return at;
 }
 
-// a / b of numbers from 0 up; in 32 bits where they fit (a division in 64 takes some hundred cycles).
-__device__ __forceinline__ long quotient(long a, long b) {
-  return ((a | b) >> 32) == 0 ? (long)((uint32_t)a / (uint32_t)b) : a / b;
-}
-
-__device__ __forceinline__ uint32_t quotient(uint32_t a, uint32_t b) { return a / b; }
-
-template <typename U>
-__device__ __forceinline__ U warp_sum(U v) {
+__device__ __forceinline__ uint32_t warp_sum(uint32_t v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
-template <typename U>
-__device__ __forceinline__ U warp_scan(U v, int lane) {  // inclusive
+__device__ __forceinline__ uint32_t warp_scan(uint32_t v, int lane) {  // inclusive
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const U t = __shfl_up_sync(0xffffffffu, v, o);
+    const uint32_t t = __shfl_up_sync(0xffffffffu, v, o);
     if (lane >= o) v += t;
   }
   return v;
@@ -377,12 +371,11 @@ __device__ __forceinline__ U warp_scan(U v, int lane) {  // inclusive
 
 // The run [u0, u1) of team c, of `total` units cut evenly into as many as there are teams (no unit: the last ones).
 // One division; where the runs with one unit more lie only has to be the same for all, so that fp32 will do.
-template <typename U>
-__device__ __forceinline__ void run_of(U c, U teams, U total, U& u0, U& u1) {
-  const U each = quotient(total, teams), more = total - each * teams;
+__device__ __forceinline__ void run_of(uint32_t c, uint32_t teams, uint32_t total, uint32_t& u0, uint32_t& u1) {
+  const uint32_t each = total / teams, more = total - each * teams;
   const float rate = each == 0 ? 1.f : __fdividef((float)(int)more, (float)(int)teams);
-  auto start = [&](U i) {
-    const U extra = (U)(int)((float)(int)i * rate);
+  auto start = [&](uint32_t i) {
+    const uint32_t extra = (uint32_t)(int)((float)(int)i * rate);
     return i * each + (i == teams || extra > more ? more : extra);
   };
   u0 = start(c);
@@ -401,7 +394,7 @@ __device__ void producer(const CUtensorMap* tmk, const CUtensorMap* tmv, const D
   uint64_t *full = tm.full, *empty = tm.empty, *ifull = tm.ifull, *iempty = tm.iempty;
   int* dead = tm.dead;
   const int S = p.S, max_nb = p.max_nb;
-  using U = std::conditional_t<SEL, uint32_t, long>;  // (the host keeps the lists' places below 2^31)
+  using U = uint32_t;  // (the host launches no more units at once)
   const U GC = (U)p.G * (U)p.CG;
   // Units in all, then the run of this team: [u0, u1).  Every segment has END units
   // more than its keys, which stand for its end (the join, the output, the next
@@ -418,11 +411,11 @@ __device__ void producer(const CUtensorMap* tmk, const CUtensorMap* tmv, const D
     // Where all sequences have topk blocks, every token has the same number of places and the first list is
     // asked for together with the lengths; else the places follow the lengths.
     const U R = (U)S / (U)p.q_real, list = GC * (U)(p.topk + kSelEnd);
-    run_of<U>(c, teams, (U)S * list, u0, u1);
-    s = (int)quotient(u0, list);
+    run_of(c, teams, (U)S * list, u0, u1);
+    s = (int)(u0 / list);
     sb = (U)s * list;
     if (u1 > u0) {
-      pick0_row = (U)s * p.G + quotient(u0 - sb, (U)(p.topk + kSelEnd) * p.CG);
+      pick0_row = (U)s * p.G + (u0 - sb) / ((U)(p.topk + kSelEnd) * p.CG);
       if (lane < p.topk) pick0 = __ldcg(p.topk_idx + (size_t)pick0_row * p.topk + lane);
     }
     bool full = true;
@@ -439,7 +432,7 @@ __device__ void producer(const CUtensorMap* tmk, const CUtensorMap* tmv, const D
       for (U at = lane; at < R; at += 32)
         total += places_of(at < 32 ? mine0 : __ldcg(p.seq_lens + at), p.q_real, max_nb, p.topk) + kSelEnd;
       __syncwarp();
-      run_of<U>(c, teams, warp_sum(total) * per, u0, u1);
+      run_of(c, teams, warp_sum(total) * per, u0, u1);
       s = 0;
       sb = 0;
 #pragma unroll 1
@@ -452,7 +445,7 @@ __device__ void producer(const CUtensorMap* tmk, const CUtensorMap* tmv, const D
         if (over) {
           const int l = __ffs(over) - 1;
           sb += __shfl_sync(0xffffffffu, incl - mine, l);
-          const U token = quotient(__shfl_sync(0xffffffffu, mine, l), (U)p.q_real), i = quotient(u0 - sb, token);
+          const U token = __shfl_sync(0xffffffffu, mine, l) / (U)p.q_real, i = (u0 - sb) / token;
           s = (int)((s0 + l) * (U)p.q_real + i);
           sb += i * token;
           break;
@@ -468,7 +461,7 @@ __device__ void producer(const CUtensorMap* tmk, const CUtensorMap* tmv, const D
       if (s0 == 0) mine0 = T;
       total += slots_of<TR::SK, LY::END>(T, max_nb);
     }
-    run_of<U>(c, teams, warp_sum(total) * GC, u0, u1);
+    run_of(c, teams, warp_sum(total) * GC, u0, u1);
     if (u1 > u0) {
       for (int s0 = 0; s0 < S; s0 += 32) {
         const int T = s0 == 0 ? mine0 : s0 + lane < S ? __ldcg(p.seq_lens + s0 + lane) : 0;
@@ -506,7 +499,7 @@ __device__ void producer(const CUtensorMap* tmk, const CUtensorMap* tmv, const D
       continue;
     }
     const U in_s = u - sb;
-    const int span = un + (SEL ? kSelEnd : LY::END), gc = (int)quotient(in_s, (U)span), k0 = (int)(in_s - (U)gc * span);
+    const int span = un + (SEL ? kSelEnd : LY::END), gc = (int)(in_s / (U)span), k0 = (int)(in_s - (U)gc * span);
     if (k0 >= un) {  // another run's segment end
       u += span - k0;
       if ((U)gc + 1 == GC) {

@@ -239,9 +239,8 @@ msa_status_t msa_topk_blocks(const msa_batch_t* batch, const msa_config_t* cfg,
  * Entries naming a block the query cannot see, or repeating a block an
  * earlier entry of the same row names, are left out and raise the device
  * fault flag: the softmax runs over the selected key set, each key once.
- * Caches with block scales: num_q_heads / num_kv_heads <= 64, num_seqs * q_per_seq *
- * num_kv_heads * (topk + 1) < 2^31, workspace 16-byte aligned; equal calls give equal bits
- * on one GPU. */
+ * Caches with block scales: num_q_heads / num_kv_heads <= 64, q_per_seq * num_kv_heads *
+ * (topk + 1) < 2^32, workspace 16-byte aligned; equal calls give equal bits on one GPU. */
 msa_status_t msa_sparse_attend(const msa_cache_t* cache, const msa_batch_t* batch,
                                const msa_config_t* cfg, const msa_query_t* q,
                                int32_t num_q_heads, const int32_t* topk_idx, void* out,

@@ -309,3 +309,31 @@ def test_the_whole_path(kv, Q, index):
     msa.msa_decode_noalloc(cache, batch, cfg, iq, q, 8, topk2, out2, lse2, status)
     assert status.cpu().tolist()[0] == 0
     assert torch.equal(topk2, topk) and torch.equal(out2, out) and torch.equal(lse2, lse)
+
+
+@pytest.mark.parametrize("kv", KINDS)
+def test_tables_so_wide_that_a_batch_takes_several_launches(kv):
+    # units of a launch are counted in 32 bits, by the width of the table: 31 sequences of 64 segments and 2^20 blocks
+    wide, most, Q, r, H = 1 << 20, 31, 8, 64, 8
+    lens = [int(t) for t in np.random.default_rng(5).integers(Q, 300, 40)]
+    lens[3] = lens[35] = 0
+    c = attend_case(kv, lens, Q=Q, Hq=r * H, H=H, seed=23)
+    cache, batch, q = bind(c)
+    cfg = msa.default_config(16)
+    table = torch.full((len(lens), wide), -(1 << 30), dtype=torch.int32, device="cuda")
+    table[:, :c["table"].shape[1]] = c["table"].cuda()
+
+    def call(a, b, table):
+        part = msa.Batch(batch.seq_lens[a:b], table[a:b].contiguous(), Q)
+        out = torch.full(((b - a) * Q, r * H, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+        lse = torch.full(((b - a) * Q, r * H), 7.0, device="cuda")
+        ws = workspace(msa.msa_dense_workspace_size(cache, part, r * H))
+        msa.msa_dense_attend(cache, part, cfg, msa.Query(q.data[a * Q:b * Q]), r * H, out, lse, ws)
+        assert msa.msa_read_device_status(ws)[1] == 0
+        return out, lse
+
+    out, lse = call(0, len(lens), table)
+    for a, b in ((0, most), (most, len(lens))):
+        want, want_lse = call(a, b, c["table"].cuda())  # (the same segments, so the same runs)
+        assert torch.equal(out[a * Q:b * Q], want) and torch.equal(lse[a * Q:b * Q], want_lse)
+    assert (out[3 * Q:4 * Q] == 0).all() and torch.isfinite(lse[:3 * Q]).all()

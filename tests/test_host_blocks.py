@@ -152,10 +152,11 @@ def _cache(msa, kv="int8_block", **over):
 
 
 @pytest.mark.parametrize("kv", [8, 9])
-def test_places_of_all_lists_are_counted_in_32_bits(lib, kv):  # noqa: F811
-    for seqs, topk, ok in ((1 << 24, 32, False), (1 << 24, 16, True), (1 << 20, 32, True), (1 << 25, 16, False)):
-        c, b, f, _ = _structs(kv, b__num_seqs=seqs, f__topk=topk)
-        assert (lib.msa_workspace_size(ref(c), ref(b), ref(f), 16) > 0) == ok
+def test_places_of_a_sequences_lists_are_counted_in_32_bits(lib, kv):  # noqa: F811
+    for tokens, topk, ok in ((1 << 25, 32, False), (1 << 25, 16, True), (1 << 24, 32, True), (1 << 26, 16, False)):
+        c, b, f, _ = _structs(kv, b__num_seqs=1, b__q_per_seq=tokens, b__max_blocks_per_seq=1 << 19, f__topk=topk)
+        assert (lib.msa_workspace_size(ref(c), ref(b), ref(f), 16) > 0) == ok, (tokens, topk)
+
 
 
 
