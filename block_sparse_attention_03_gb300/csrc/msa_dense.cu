@@ -42,11 +42,16 @@ __global__ void __launch_bounds__(kJoinThreads, BY_SEGMENT ? 3 : 4) dense_combin
   pdl_wait();
   if constexpr (BY_SEGMENT) {
     sg = blockIdx.x;
-    for (int i = tid; i < runs; i += kJoinThreads) {
-      const int2 x = __ldcg(p.info + i);
+#pragma unroll 1
+    for (int i = tid; i < runs; i += 2 * kJoinThreads) {  // (two loads at once, for some 300 notes: 0.3 us)
+      const int2 x = __ldcg(p.info + i), y = i + kJoinThreads < runs ? __ldcg(p.info + i + kJoinThreads) : make_int2(-1, 0);
       if (x.x == sg && x.y != 0) {
         atomicMin(&s_first, i);
         atomicMax(&s_end, i + 1);
+      }
+      if (y.x == sg && y.y != 0) {
+        atomicMin(&s_first, i + kJoinThreads);
+        atomicMax(&s_end, i + kJoinThreads + 1);
       }
     }
     __syncthreads();

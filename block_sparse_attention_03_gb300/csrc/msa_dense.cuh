@@ -70,7 +70,7 @@
 // us (52%); 32 columns (8 new tokens), BF16 8 x 64K 182 us (87%), FP8 129 us (63%),
 // NVFP4 8 x 128K 224 us (40%; tensor pipe 43%, issue slots 40%, two warps a scheduler
 // waiting for each other's results); 61 ragged BF16 sequences of 48 columns 82 us
-// (51%; tensor pipe 50%); one sequence of 4K tokens 8.5 us.  Products rounded to E4M3: 4
+// (51%; tensor pipe 50%); one sequence of 4K tokens 8.1 us.  Products rounded to E4M3: 4
 // columns 229 us, 16 columns 107, 32 columns 273.
 //
 // Registers are what the wide instances lack: with 24 columns and more each of them spills
@@ -86,8 +86,8 @@
 // when they are there.  Measured: 4 columns, FP8 32 x 16K-32K 123 us (99% of the copy rate,
 // 6,702 GB/s), INT8 4 x 512K 306 us (105%); 32 columns (8 x 128K, 8 new tokens) INT8 239 us
 // (67%; tensor pipe 42%, issue slots 40%, two warps a scheduler), FP8 226; 24 columns 212 and 191, 16 columns
-// 175 (92%); one sequence of 4K tokens 9.1 us: lengths and table 1.6, first tile 3.0, its unit 4.5, the
-// warps' join 5.5, the last CTA's end seen by the join's launch 6.2, joined 8.2.
+// 175 (92%); one sequence of 4K tokens 8.9 us: lengths and table 1.6, first tile 3.0, its unit 4.5, the
+// warps' join 5.5, the last CTA's end seen by the join's launch 6.2, joined 8.2 (when it took 9.4).
 //
 // SEL: the sparse attend over selection lists (caches with block scales).  The new tokens are
 // sequences of their own, a (token, KV head)'s units the entries of its list, its runs cut
