@@ -85,8 +85,8 @@
 // 2 or 3).  The producer asks for the scales behind the block's copies and completes the stage's phase
 // when they are there.  Measured: 4 columns, FP8 32 x 16K-32K 123 us (99% of the copy rate,
 // 6,702 GB/s), INT8 4 x 512K 306 us (105%); 32 columns (8 x 128K, 8 new tokens) INT8 239 us
-// (67%; tensor pipe 42%, issue slots 40%, two warps a scheduler), FP8 226; 24 columns 212 and 191, 16 columns
-// 175 (92%); one sequence of 4K tokens 8.9 us: lengths and table 1.6, first tile 3.0, its unit 4.5, the
+// (67%; tensor pipe 42%, issue slots 40%, two warps a scheduler), FP8 226; 24 columns 209 and 191, 16 columns
+// 175 (92%); one sequence of 4K tokens 8.8 us: lengths and table 1.6, first tile 3.0, its unit 4.5, the
 // warps' join 5.5, the last CTA's end seen by the join's launch 6.2, joined 8.2 (when it took 9.4).
 //
 // SEL: the sparse attend over selection lists (caches with block scales).  The new tokens are
@@ -97,7 +97,7 @@
 // says where each unit's keys begin.  Measured: 32 tokens x 4 heads x 16 blocks of INT8 19.8 us in a graph (10.1 at
 // the copy rate; 4 blocks 12 us: what a call costs at least is launch, lists, first tiles and join), 64 of FP8
 // (8 x 128K, 8 new tokens) 28.2 (18.1); the kernel for FP8 with token scales takes 30 and 44.  A prompt's
-// chunk reads its blocks once for each token: 8,192 tokens on 64K 1.85 (FP8) and 2.22 ms (INT8), where the
+// chunk reads its blocks once for each token: 8,192 tokens on 64K 1.73 (FP8) and 2.13 ms (INT8), where the
 // key-block-major attend of the FP8 format takes 0.58.
 //
 // A masked key's logit is replaced, not multiplied; in units that hold masked
@@ -176,7 +176,7 @@ struct DenseLayout {
   // Where an equal share is too small, the consumers take registers over from the
   // producers; their warps come in fours then (the producers' four hold idle ones).
   // Three teams of one column tile do better with equal shares (173 us, 182 so).
-  // (INT8's conversions want a few more: 64 columns 221 us, 224 with the others' shares; 24 212 and 218; but one group of
+  // (INT8's conversions want a few more: 64 columns 221 us, 224 with the others' shares; 24 209 and 218; but one group of
   // 32 243 and 238; FP8 by blocks, 24 columns 200 and 197.)
   static constexpr bool WIDE = NN >= 3, MOVE = WIDE || (TEAMS == 3 && NN == 2);
   static constexpr bool MORE = FMT == FMT_I8B && !(NN == 4 && NCG == 1);
@@ -455,12 +455,12 @@ __device__ void producer(const CUtensorMap* tmk, const CUtensorMap* tmv, const D
     }
   } else {
     U total = 0;
-#pragma unroll 4
-    for (int s0 = 0; s0 < S; s0 += 32) {
-      const int T = s0 + lane < S ? __ldcg(p.seq_lens + s0 + lane) : 0;
-      if (s0 == 0) mine0 = T;
-      total += slots_of<TR::SK, LY::END>(T, max_nb);
-    }
+    mine0 = lane < S ? __ldcg(p.seq_lens + lane) : 0;
+    total = slots_of<TR::SK, LY::END>(mine0, max_nb);
+    // (1,000 short sequences 61 us, 64 with one load at a time; more of this code is more to fetch for all)
+#pragma unroll 2
+    for (int at = lane + 32; at < S; at += 32) total += slots_of<TR::SK, LY::END>(__ldcg(p.seq_lens + at), max_nb);
+    __syncwarp();
     run_of(c, teams, warp_sum(total) * GC, u0, u1);
     if (u1 > u0) {
       for (int s0 = 0; s0 < S; s0 += 32) {
@@ -749,16 +749,17 @@ __device__ __forceinline__ void convert_q(uint8_t* qs, float* cf, int nrows, int
     const uint2 w = *reinterpret_cast<const uint2*>(r + 8 * lane);
     __syncwarp();
     const float2 a = bf16x2_to_float2(w.x), b = bf16x2_to_float2(w.y);
-    float amax = fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(b.x), fabsf(b.y)));
-    const bool bad = !(fabsf(a.x) <= 3.4e38f) || !(fabsf(a.y) <= 3.4e38f) || !(fabsf(b.x) <= 3.4e38f) || !(fabsf(b.y) <= 3.4e38f);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    int e = pow2_fit(amax, 16384.f);
-    e = e < -126 ? -126 : (e > 126 ? 126 : e);
+    // The largest e with amax 2^e <= 2^14, from the exponent and mantissa (magnitudes' bits order as they do, infinity and
+    // NaN above all): on the way of every segment's first logits (three short sequences of 40 columns 13.2 us; 15.0 by divisions and ldexpf).
+    uint32_t m = max(max(__float_as_uint(a.x) & 0x7fffffffu, __float_as_uint(a.y) & 0x7fffffffu),
+                     max(__float_as_uint(b.x) & 0x7fffffffu, __float_as_uint(b.y) & 0x7fffffffu));
+    m = __reduce_max_sync(0xffffffffu, m);
+    const bool bad = m >= 0x7f800000u;
+    const int e = bad || m == 0u ? 0 : min(126, 141 - (int)(m >> 23) - ((m & 0x7fffffu) != 0u ? 1 : 0));
     // A query row that is not finite has no finite logits; the reduced formats
     // would hide that, so it is NaN (the logits of masked keys are replaced all the
     // same).  The factor is kept off zero: it multiplies -inf.
-    const float ps = __any_sync(0xffffffffu, bad) ? __int_as_float(0x7fc00000) : pow2i(e);
+    const float ps = bad ? __int_as_float(0x7fc00000) : pow2i(e);
     *reinterpret_cast<uint32_t*>(r + 2 * q_place<FMT>(4 * lane)) = pack_f16x2(a.x * ps, a.y * ps);
     *reinterpret_cast<uint32_t*>(r + 2 * q_place<FMT>(4 * lane + 2)) = pack_f16x2(b.x * ps, b.y * ps);
     if (lane == 0) cf[row] = fmaxf(pow2i(-e) * cst, 1.2e-38f);
