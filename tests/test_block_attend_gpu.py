@@ -337,3 +337,15 @@ def test_tables_so_wide_that_a_batch_takes_several_launches(kv):
         want, want_lse = call(a, b, c["table"].cuda())  # (the same segments, so the same runs)
         assert torch.equal(out[a * Q:b * Q], want) and torch.equal(lse[a * Q:b * Q], want_lse)
     assert (out[3 * Q:4 * Q] == 0).all() and torch.isfinite(lse[:3 * Q]).all()
+
+
+@pytest.mark.parametrize("kv", KINDS)
+def test_queries_near_the_largest_bf16(kv):
+    c = attend_case(kv, [300, 131], Q=2, Hq=8, H=2, seed=29)
+    c["q"] = (c["q"].float().clamp(-3, 3) * 1.1e38).bfloat16()
+    assert c["q"].abs().max() > 3e38 and torch.isfinite(c["q"]).all()
+    for name in ("k_scale", "rows_k_scale"):
+        c[name] = c[name] * 2e-36
+    check_attend(*run_attend(c), plain_attend(c))
+    lists = select(c, 4, seed=3)
+    check_attend(*run_attend(c, _gpu(lists)), plain_attend(c, lists))
