@@ -443,6 +443,8 @@ def msa_sparse_attend(cache, batch, cfg, q: Query, num_q_heads: int, topk_idx, o
     """Attention over the selected blocks.  topk_idx: int32 [S * q_per_seq][num_kv_heads][topk], the other tensors as in
     msa_dense_attend."""
     if cache.kv_dtype in ("int8_block", "fp8_block"):
+        if topk_idx is None:  # (_attend's dense form)
+            raise MsaError(1, "msa_sparse_attend")
         _attend("msa_sparse_attend", cache, batch, cfg, q, num_q_heads, topk_idx, out, lse, workspace, stream)
         return
     c, b, f, qq = cache.struct(), batch.struct(), cfg.struct(), q.struct()
