@@ -204,20 +204,11 @@ class PagedCache:
                          NVFP4_MODES.get(self.nvfp4_mode, -1))
 
 
-def _set_field(self, name, value):
-    """__setattr__ of holders whose tensors' types and devices the serving calls look at once for a field (_seen: the
-    device), since no tensor changes them by itself; sizes and layouts, which resize_ and as_strided_ do, at every call."""
-    self.__dict__["_seen"] = None
-    self.__dict__[name] = value
-
-
 @dataclasses.dataclass
 class Batch:
     seq_lens: object      # int32 [S] on the device
     block_table: object   # int32 [S][max_blocks] on the device
     q_per_seq: int = 1
-
-    __setattr__ = _set_field
 
     def struct(self) -> MsaBatchT:
         return MsaBatchT(self.seq_lens.shape[0], self.q_per_seq, self.block_table.shape[1],
@@ -250,8 +241,6 @@ class Query:
     dtype: str = "bf16"   # "bf16" | "fp8"
     scale: float = 1.0
 
-    __setattr__ = _set_field
-
     def struct(self) -> MsaQueryT:
         return MsaQueryT(_ptr(self.data), DTYPES[self.dtype], self.scale)
 
@@ -264,8 +253,6 @@ class Spans:
     end: object            # int32 [S]
     token_offsets: object  # int32 [S] or longer
     block_table: object    # int32 [S][max_blocks]
-
-    __setattr__ = _set_field
 
 
 @dataclasses.dataclass
@@ -503,21 +490,13 @@ def msa_cache_insert(cache, slot_mapping, k, v, index_k, workspace, stream=None)
                                   _stream(stream)), "msa_cache_insert")
 
 
-def _int32_on(tensors, dev: int, where: str) -> None:
-    for t in tensors:
-        if t.dtype is not _int32 or t.get_device() != dev:
-            raise MsaError(1, where)
-
-
 def _batch_checked(batch: Batch, dev: int, where: str):
     """(sequences, width of the table) of a batch whose tensors are dense int32 on the device."""
     lens, table = batch.seq_lens, batch.block_table
     S, shape = lens.numel(), table.shape
-    if len(shape) != 2 or shape[0] != S or not lens.is_contiguous() or not table.is_contiguous():
+    if (len(shape) != 2 or shape[0] != S or lens.dtype is not _int32 or table.dtype is not _int32
+            or not lens.is_contiguous() or not table.is_contiguous() or lens.get_device() != dev or table.get_device() != dev):
         raise MsaError(1, where)
-    if batch._seen != dev:
-        _int32_on((lens, table), dev, where)
-        batch.__dict__["_seen"] = dev
     return S, shape[1]
 
 
@@ -538,11 +517,8 @@ def _attend(where: str, cache, batch, cfg, q, num_q_heads: int, topk_idx, out, l
     S, width = _batch_checked(batch, dev, where)
     data, tokens = q.data, S * batch.q_per_seq
     rows = tokens * num_q_heads
-    if q._seen != dev:
-        if data.dtype not in _query_types.get(q.dtype, ()) or data.get_device() != dev:
-            raise MsaError(1, where)
-        q.__dict__["_seen"] = dev
     if (data.numel() != rows * 128 or not data.is_contiguous()
+            or data.dtype not in _query_types.get(q.dtype, ()) or data.get_device() != dev
             or out.numel() != rows * 128 or out.dtype is not _bf16 or out.get_device() != dev or not out.is_contiguous()
             or (lse is not None and (lse.numel() != rows or lse.dtype is not _f32 or lse.get_device() != dev or not lse.is_contiguous()))
             or workspace.get_device() != dev
@@ -568,11 +544,10 @@ def _spans_checked(spans: Spans, dev: int, where: str):
     first, end, offsets, table = spans.first, spans.end, spans.token_offsets, spans.block_table
     S, shape = first.numel(), table.shape
     if (len(shape) != 2 or shape[0] != S or end.numel() != S or offsets.numel() < S
-            or not (first.is_contiguous() and end.is_contiguous() and offsets.is_contiguous() and table.is_contiguous())):
+            or first.dtype is not _int32 or end.dtype is not _int32 or offsets.dtype is not _int32 or table.dtype is not _int32
+            or not (first.is_contiguous() and end.is_contiguous() and offsets.is_contiguous() and table.is_contiguous())
+            or first.get_device() != dev or end.get_device() != dev or offsets.get_device() != dev or table.get_device() != dev):
         raise MsaError(1, where)
-    if spans._seen != dev:
-        _int32_on((first, end, offsets, table), dev, where)
-        spans.__dict__["_seen"] = dev
     return S, shape[1]
 
 
