@@ -191,8 +191,8 @@ class PagedCache:
     nvfp4_mode: str = "exact"
 
     def __setattr__(self, name, value):
-        # the serving calls look at the tensors once (_checked), and again when a field is set
-        self.__dict__["_seen"] = self.__dict__["_packed"] = ()
+        # what the serving calls derive from the fields (_parts, _packed_cache): anew when one is set
+        self.__dict__.update(_kv=None, _idx=None, _packed=None)
         self.__dict__[name] = value
 
     def struct(self) -> MsaCacheT:
@@ -305,31 +305,40 @@ def _p(t) -> int:
     return 0 if t is None else t.data_ptr()
 
 
-def _checked(c: PagedCache, index: bool, dev: int, where: str) -> None:
-    """The cache's tensors (the index keys' too, if the call writes them): dense, on the device, of
-    their formats' types and at least num_blocks blocks long."""
+def _parts(c: PagedCache, index: bool):
+    """(tensor, its types, its least number of elements) of the tensors of K and V, or of the index keys: for the cache's fields."""
     import torch
     codes = (torch.uint8, torch.int8, torch.float8_e4m3fn)
-    wanted = [("k", c.kv_dtype, c.num_kv_heads), ("v", c.kv_dtype, c.num_kv_heads)] + [("idx", c.index_dtype, 1)] * index
+    wanted = [("idx", c.index_dtype, 1)] if index else [("k", c.kv_dtype, c.num_kv_heads), ("v", c.kv_dtype, c.num_kv_heads)]
+    got = []
     for name, kind, heads in wanted:
         blocks = c.num_blocks * heads
         rows = blocks * 128
         scale = (name + "_scale", (torch.float32,))
-        parts = {"bf16": [(name, (torch.bfloat16,), rows * 128)], "fp8": [(name, codes, rows * 128), (*scale, rows)],
-                 "nvfp4": [(name, (torch.uint8, torch.int8), rows * 64), (name + "_sf", codes, rows * 8)],
-                 "int8_block": [(name, (torch.int8, torch.uint8), rows * 128), (*scale, blocks)],
-                 "fp8_block": [(name, codes, rows * 128), (*scale, blocks)]}.get(kind, [])
-        for field, types, least in parts:
-            t = getattr(c, field)
-            if t is not None and (t.dtype not in types or t.numel() < least or not t.is_contiguous() or t.get_device() != dev):
-                raise MsaError(1, where)
-    c.__dict__["_seen"] = (dev, index or (c._seen[:1] == (dev,) and c._seen[1]))
+        fields = {"bf16": [(name, (torch.bfloat16,), rows * 128)], "fp8": [(name, codes, rows * 128), (*scale, rows)],
+                  "nvfp4": [(name, (torch.uint8, torch.int8), rows * 64), (name + "_sf", codes, rows * 8)],
+                  "int8_block": [(name, (torch.int8, torch.uint8), rows * 128), (*scale, blocks)],
+                  "fp8_block": [(name, codes, rows * 128), (*scale, blocks)]}.get(kind, [])
+        got += [(getattr(c, field), types, least) for field, types, least in fields if getattr(c, field) is not None]
+    c.__dict__["_idx" if index else "_kv"] = got
+    return got
+
+
+def _addresses(parts, dev: int, where: str) -> list:
+    """The tensors' addresses.  They have to be dense, on the device, of their formats' types and at least num_blocks blocks
+    long: looked at in every call, since a tensor changes in place (resize_, as_strided_, t.data = other)."""
+    at = []
+    for t, types, least in parts:
+        if t.dtype not in types or t.numel() < least or not t.is_contiguous() or t.get_device() != dev:
+            raise MsaError(1, where)
+        at.append(t.data_ptr())
+    return at
 
 
 def _cache_values(c: PagedCache, index: bool, dev: int, where: str):
-    seen = c._seen
-    if not seen or seen[0] != dev or (index and not seen[1]):
-        _checked(c, index, dev, where)
+    _addresses(c._kv or _parts(c, False), dev, where)
+    if index:
+        _addresses(c._idx or _parts(c, True), dev, where)
     return (DTYPES[c.kv_dtype], DTYPES[c.index_dtype], c.num_blocks, 128, c.num_kv_heads, c.head_dim, c.index_dim,
             c.k.data_ptr(), c.v.data_ptr(), _p(c.k_sf), _p(c.v_sf), _p(c.k_scale), _p(c.v_scale), _p(c.idx), _p(c.idx_sf),
             _p(c.idx_scale), c.k_global, c.v_global, c.idx_global, NVFP4_MODES.get(c.nvfp4_mode, -1))
@@ -341,15 +350,12 @@ _PACKED = f"{_CACHE_PACKER.size}s"
 
 def _packed_cache(c: PagedCache, dev: int, where: str) -> bytes:
     """The cache's struct as bytes, without the index keys, for its fields and its tensors' present addresses."""
-    k, v, ks, vs = c.k.data_ptr(), c.v.data_ptr(), c.k_scale, c.v_scale
-    got, seen = c._packed, c._seen
-    if (got and got[0] == k and got[1] == v and seen and seen[0] == dev
-            and (ks is None or got[2] == ks.data_ptr()) and (vs is None or got[3] == vs.data_ptr())):
-        return got[4]
+    at, got = _addresses(c._kv or _parts(c, False), dev, where), c._packed
+    if got and got[0] == at:
+        return got[1]
     values = _cache_values(c, False, dev, where)
     raw = _CACHE_PACKER.pack(*values[:13], 0, 0, 0, *values[16:])
-    if c.k_sf is None and c.v_sf is None:  # (the addresses that were compared are all there are)
-        c.__dict__["_packed"] = (k, v, _p(ks), _p(vs), raw)
+    c.__dict__["_packed"] = (at, raw)
     return raw
 
 
@@ -421,8 +427,8 @@ def msa_topk_blocks(batch, cfg, num_groups: int, pooled, topk_idx, topk_score, w
 
 def _check_block_cache(cache, where: str) -> None:
     """The tensors of a cache with block scales (whose scales are not of the shape of the other formats')."""
-    if cache.kv_dtype in ("int8_block", "fp8_block") and cache._seen[:1] != (cache.k.get_device(),):
-        _checked(cache, False, cache.k.get_device(), where)
+    if cache.kv_dtype in ("int8_block", "fp8_block"):
+        _addresses(cache._kv or _parts(cache, False), cache.k.get_device(), where)
 
 
 def msa_sparse_attend(cache, batch, cfg, q: Query, num_q_heads: int, topk_idx, out, lse, workspace,

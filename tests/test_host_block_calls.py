@@ -5,7 +5,7 @@ import torch
 
 from test_host_blocks import KINDS, _cache, f32, i32, u8, z
 from test_host_serving import on_device_0  # noqa: F401  (a fixture)
-from test_host_types import _passes
+from test_host_types import _passes, _tensors
 
 
 @pytest.mark.parametrize("kv", KINDS)
@@ -62,3 +62,65 @@ def test_types_and_devices_are_looked_at_in_every_call(on_device_0, kv):  # noqa
                 call()
             t._at = 0
         _passes(call)
+
+
+def _cache_calls(msa, kv):
+    """Each call that looks at the cache's K and V, as a function of the cache."""
+    batch, cfg, q = msa.Batch(z(3, dt=i32), z(3, 5, dt=i32)), msa.Config(), msa.Query(z(3, 4, 128))
+    lists, out, ws, rope = z(3, 2, 16, dt=i32), z(3, 4, 128), z(4096, dt=u8), msa.MsaRopeT()
+    rope.axes = 1
+    spans = msa.Spans(z(3, dt=i32), z(3, dt=i32), z(4, dt=i32), z(3, 5, dt=i32))
+    rows = z(3, 2, 128)
+    yield lambda c: msa.msa_dense_attend(c, batch, cfg, q, 4, out, None, ws, stream=0)
+    yield lambda c: msa.msa_cache_read(c, spans, rows, None, ws, stream=0)
+    blk = kv in KINDS
+    kv_rows = None if blk else rows
+    yield lambda c: msa.msa_rope_insert(c, rope, z(3, dt=i32), z(3, dt=i32), z(3, 4, 128), msa.Query(z(3, 4, 128)), None, None, kv_rows,
+                                        kv_rows, None, None, ws, stream=0)
+    if blk:
+        yield lambda c: msa.msa_block_insert(c, spans, rows, rows, ws, stream=0)
+        yield lambda c: msa.msa_sparse_attend(c, batch, cfg, q, 4, lists, out, None, ws, stream=0)
+        yield lambda c: msa.msa_decode(c, batch, cfg, msa.Query(rows), q, 4, lists, out, None, ws, stream=0)
+        yield lambda c: msa.msa_decode_noalloc(c, batch, cfg, msa.Query(rows), q, 4, lists, out, None, stream=0)
+
+
+def _taken(msa, kv):
+    """A cache whose tensors may change in place."""
+    if kv in KINDS:
+        return _cache(msa, kv), ("k", "v", "k_scale", "v_scale")
+    t = _tensors(kv, "bf16")
+    return msa.PagedCache(kv, "bf16", 2, 2, **t, k_global=1.0, v_global=1.0), [n for n in t if n != "idx"]
+
+
+@pytest.mark.parametrize("kv", [*KINDS, "bf16", "fp8", "nvfp4"])
+def test_the_caches_tensors_are_looked_at_in_every_call(on_device_0, kv):  # noqa: F811
+    msa = on_device_0
+    for i in range(len(list(_cache_calls(msa, kv)))):
+        cache, names = _taken(msa, kv)
+        call = list(_cache_calls(msa, kv))[i]
+        for name in names:
+            t = getattr(cache, name)
+            real, shape = t._t, t.shape
+            address = real.data_ptr()
+            _passes(call, c=cache)
+            t._t.resize_(1, *shape[1:])  # at the same address
+            assert real.data_ptr() == address
+            with pytest.raises(msa.MsaError):
+                call(cache)
+            t._t.resize_(shape)
+            _passes(call, c=cache)
+            t._t.as_strided_(shape, [0] * len(shape))
+            assert real.data_ptr() == address
+            with pytest.raises(msa.MsaError):
+                call(cache)
+            t._t = real.new_zeros(shape)
+            _passes(call, c=cache)  # at another address
+            t._t.data = torch.zeros(shape, dtype=torch.float64)
+            with pytest.raises(msa.MsaError):
+                call(cache)
+            t._t = real.new_zeros(shape)
+            t._at = 1
+            with pytest.raises(msa.MsaError):
+                call(cache)
+            t._at = 0
+            _passes(call, c=cache)
