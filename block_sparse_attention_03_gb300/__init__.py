@@ -428,7 +428,12 @@ def msa_topk_blocks(batch, cfg, num_groups: int, pooled, topk_idx, topk_score, w
 def _check_block_cache(cache, where: str) -> None:
     """The tensors of a cache with block scales (whose scales are not of the shape of the other formats')."""
     if cache.kv_dtype in ("int8_block", "fp8_block"):
-        _addresses(cache._kv or _parts(cache, False), cache.k.get_device(), where)
+        if _int32 is None:
+            _torch_names()
+        dev = cache.k.get_device()
+        if dev < 0 or dev != _device():
+            raise MsaError(1, where)
+        _addresses(cache._kv or _parts(cache, False), dev, where)
 
 
 def msa_sparse_attend(cache, batch, cfg, q: Query, num_q_heads: int, topk_idx, out, lse, workspace,

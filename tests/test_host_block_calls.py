@@ -124,3 +124,16 @@ def test_the_caches_tensors_are_looked_at_in_every_call(on_device_0, kv):  # noq
                 call(cache)
             t._at = 0
             _passes(call, c=cache)
+
+
+@pytest.mark.parametrize("at", [-1, 1])
+@pytest.mark.parametrize("kv", KINDS)
+def test_a_cache_that_is_not_on_the_current_device(on_device_0, kv, at):  # noqa: F811
+    msa = on_device_0
+    for call in _cache_calls(msa, kv):
+        cache = _cache(msa, kv)
+        _passes(call, c=cache)
+        for name in ("k", "v", "k_scale", "v_scale"):
+            getattr(cache, name)._at = at
+        with pytest.raises(msa.MsaError):
+            call(cache)
