@@ -1,5 +1,8 @@
 """What the binding looks at in every call over caches with block scales, beside test_host_blocks.py (no GPU is touched)."""
 
+import dataclasses
+from types import SimpleNamespace
+
 import pytest
 import torch
 
@@ -137,3 +140,21 @@ def test_a_cache_that_is_not_on_the_current_device(on_device_0, kv, at):  # noqa
             getattr(cache, name)._at = at
         with pytest.raises(msa.MsaError):
             call(cache)
+
+
+def test_holders_of_a_callers_own(on_device_0):  # noqa: F811
+    # anything with the fields will do, changed in place or not
+    msa = on_device_0
+    cfg = SimpleNamespace(**{f.name: f.default for f in dataclasses.fields(msa.Config)})
+    batch, q = SimpleNamespace(seq_lens=z(3, dt=i32), block_table=z(3, 5, dt=i32), q_per_seq=1), SimpleNamespace(data=z(3, 4, 128), dtype="bf16", scale=1.0)
+
+    def call(kv="bf16"):
+        msa.msa_dense_attend(_plain_cache(msa, kv), batch, cfg, q, 4, z(3, 4, 128), None, z(4096, dt=u8), stream=0)
+
+    for kv in (*KINDS, "bf16"):
+        _passes(call, kv=kv)
+    batch.seq_lens = z(2, dt=i32)
+    with pytest.raises(msa.MsaError):
+        call()
+    spans = SimpleNamespace(first=z(3, dt=i32), end=z(3, dt=i32), token_offsets=z(4, dt=i32), block_table=z(3, 5, dt=i32))
+    _passes(lambda: msa.msa_cache_read(_cache(msa), spans, z(7, 2, 128), None, z(256, dt=u8), stream=0))
