@@ -4,6 +4,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "msa_cut.h"
 #include "msa_device.cuh"
 #include "msa_internal.h"
 
@@ -655,17 +656,17 @@ msa_status_t run_dense(const msa_cache_t* c, const msa_batch_t* b, const msa_con
   p.part_o = at<float>(ws, pl.off_o);
   p.lse = nullptr;
   p.status = at<DeviceStatus>(ws, 0);
-  const long tokens = b->q_per_seq, most = kMaxUnits / (topk_idx ? tokens * list_units(G, pl, cfg->topk) : sequence_units(G, pl, p.max_nb));
-  for (long s0 = 0; s0 < b->num_seqs; s0 += most) {
-    const long n = b->num_seqs - s0 < most ? b->num_seqs - s0 : most;
-    const size_t row = (size_t)s0 * tokens * hq;
-    p.S = (int)(topk_idx ? n * tokens : n);
-    p.seq_lens = b->seq_lens + s0;
-    p.block_table = b->block_table + (size_t)s0 * p.max_nb;
-    if (topk_idx) p.topk_idx = topk_idx + (size_t)s0 * tokens * G * cfg->topk;
-    p.q = static_cast<const uint8_t*>(q->data) + row * kDim * (p.q_fp8 ? 1 : 2);
-    p.out = static_cast<uint8_t*>(out) + row * kDim * 2;
-    if (lse) p.lse = lse + row;
+  const long tokens = b->q_per_seq, units = topk_idx ? tokens * list_units(G, pl, cfg->topk) : sequence_units(G, pl, p.max_nb);
+  for (long s0 = 0; s0 < b->num_seqs;) {
+    const DenseCut cut = dense_cut(s0, b->num_seqs, units, kMaxUnits, tokens, hq, p.max_nb, G, cfg->topk);
+    s0 += cut.n;
+    p.S = (int)(topk_idx ? cut.n * tokens : cut.n);
+    p.seq_lens = b->seq_lens + cut.s0;
+    p.block_table = b->block_table + cut.table;
+    if (topk_idx) p.topk_idx = topk_idx + cut.lists;
+    p.q = static_cast<const uint8_t*>(q->data) + (size_t)cut.row * kDim * (p.q_fp8 ? 1 : 2);
+    p.out = static_cast<uint8_t*>(out) + (size_t)cut.row * kDim * 2;
+    if (lse) p.lse = lse + cut.row;
     cudaError_t e;
     if (fmt == FMT_BF16) e = launch_dense_bf16(&tk, &tv, p, sms, st);
     else if (fmt == FMT_FP8) e = launch_dense_fp8(&tk, &tv, p, sms, st);
