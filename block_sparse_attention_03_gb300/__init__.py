@@ -225,6 +225,10 @@ class Config:
     score_type: str = "max"
     prefill_select: str = "topk"
 
+    def __setattr__(self, name, value):
+        self.__dict__["_packed"] = None  # (_config_bytes)
+        self.__dict__[name] = value
+
     def struct(self) -> MsaConfigT:
         # an unknown score type reaches the library as -1, which rejects it
         return MsaConfigT(self.topk, self.init_blocks, self.local_blocks, self.index_scale, self.sm_scale,
@@ -355,7 +359,8 @@ def _packed_cache(c: PagedCache, dev: int, where: str) -> bytes:
     return raw
 
 
-_ATTEND = _Layout(_PACKED, _BATCH, _CONFIG, _QUERY)
+_CONFIG_PACKER = _struct.Struct("@" + _CONFIG + "0P")
+_ATTEND = _Layout(_PACKED, _BATCH, f"{_CONFIG_PACKER.size}s", _QUERY)
 _SPAN = _Layout(_PACKED, _SPANS, _ROWS, _ROWS)
 _ROPE = _Layout(_CACHE, _ROWS, _QUERY, _ROWS, _QUERY, _ROWS, _ROWS, _ROWS, _NORM)
 
@@ -506,6 +511,17 @@ def _batch_checked(batch: Batch, dev: int, where: str):
     return S, shape[1]
 
 
+def _config_bytes(cfg) -> bytes:
+    """The settings' struct as bytes: of a Config packed once for its fields, of a caller's own object in every call."""
+    if type(cfg) is Config and cfg._packed:
+        return cfg._packed
+    raw = _CONFIG_PACKER.pack(cfg.topk, cfg.init_blocks, cfg.local_blocks, cfg.index_scale, cfg.sm_scale,
+                              SCORE_TYPES.get(cfg.score_type, -1), PREFILL_SELECT.get(cfg.prefill_select, -1))
+    if type(cfg) is Config:
+        cfg.__dict__["_packed"] = raw
+    return raw
+
+
 def _attend(where: str, cache, batch, cfg, q, num_q_heads: int, topk_idx, out, lse, workspace, stream) -> None:
     """The dense attend (topk_idx None), or the sparse one over a cache with block scales."""
     if _int32 is None:
@@ -525,9 +541,7 @@ def _attend(where: str, cache, batch, cfg, q, num_q_heads: int, topk_idx, out, l
                                           or topk_idx.get_device() != dev or not topk_idx.is_contiguous()))):
         raise MsaError(1, where)
     at = _ATTEND.pack(_packed_cache(cache, dev, where), S, batch.q_per_seq, width, batch.seq_lens.data_ptr(),
-                      batch.block_table.data_ptr(), cfg.topk, cfg.init_blocks, cfg.local_blocks, cfg.index_scale, cfg.sm_scale,
-                      SCORE_TYPES.get(cfg.score_type, -1), PREFILL_SELECT.get(cfg.prefill_select, -1),
-                      data.data_ptr(), DTYPES[q.dtype], q.scale)
+                      batch.block_table.data_ptr(), _config_bytes(cfg), data.data_ptr(), DTYPES[q.dtype], q.scale)
     _, o_batch, o_cfg, o_q = _ATTEND.offsets
     lse_at = 0 if lse is None else lse.data_ptr()
     if topk_idx is None:

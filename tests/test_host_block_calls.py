@@ -158,3 +158,23 @@ def test_holders_of_a_callers_own(on_device_0):  # noqa: F811
         call()
     spans = SimpleNamespace(first=z(3, dt=i32), end=z(3, dt=i32), token_offsets=z(4, dt=i32), block_table=z(3, 5, dt=i32))
     _passes(lambda: msa.msa_cache_read(_cache(msa), spans, z(7, 2, 128), None, z(256, dt=u8), stream=0))
+
+
+def test_settings_follow_their_fields():
+    import block_sparse_attention_03_gb300 as msa
+    cfg = msa.Config()
+    own = SimpleNamespace(**{f.name: f.default for f in dataclasses.fields(msa.Config)})
+    seen = set()
+
+    def same():  # (behind the struct: padding up to the next one's place)
+        want = bytes(cfg.struct())
+        assert msa._config_bytes(cfg) == msa._config_bytes(own) == want.ljust(len(msa._config_bytes(own)), b"\0")
+
+    for name, value in (("topk", 8), ("init_blocks", 1), ("local_blocks", 2), ("index_scale", 0.5), ("sm_scale", 0.25),
+                        ("score_type", "other"), ("prefill_select", "indexer")):
+        same()
+        seen.add(msa._config_bytes(cfg))
+        setattr(cfg, name, value)
+        setattr(own, name, value)
+    same()
+    assert len(seen) == 7
