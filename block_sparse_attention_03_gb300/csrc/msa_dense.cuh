@@ -74,9 +74,9 @@
 // columns 229 us, 16 columns 107, 32 columns 273.
 //
 // Registers are what the wide instances lack: with 24 columns and more each of them spills
-// (104 to 272 bytes of stores a thread, a stack of 56 to 176: mostly the producers', whose share is 40 or
-// 24), NVFP4 with 8 and 16 columns too (52 and 84), with 16 INT8 (80) and both formats over lists (132), the others
-// not (FP8: 8).
+// (92 to 268 bytes of stores a thread, a stack of 56 to 176: mostly the producers', whose share is 40 or
+// 24), with 16 all but BF16 (FP8 44, by blocks 28, INT8 80, over lists 124 and 132, NVFP4 84), with 8 NVFP4 (44, products
+// rounded 60) and FP8 (8).
 //
 // Caches with one scale for each block and head (INT8, FP8).  A unit is a block, so its two
 // scales are two numbers of the stage: K's goes into the columns' factors (where keys are masked into the
@@ -1581,7 +1581,7 @@ __device__ void consumer(const DenseParams& p, const DenseTeam& tm, int bar, int
 
 // One CTA an SM.  Two teams are ten warps with up to 168 registers a thread, or, WIDE,
 // twelve launched with 168, of which the producers' four keep 40 and the consumers'
-// eight take 232 (128 x 40 + 256 x 232 = 384 x 168 = 64,512 registers); three teams
+// eight take 232 (128 x 40 + 256 x 232 = 384 x 168 = 64,512 registers; MORE: 24 and 240); three teams
 // are fifteen with up to 128, or sixteen launched with 128, the producers' four with 56
 // then and the consumers' twelve with 152 (128 x 56 + 384 x 152 = 512 x 128).
 template <int FMT, int NN, int NCG, bool NVR, bool SEL>

@@ -322,7 +322,7 @@ struct SpanParams {
 };
 
 // Dynamic shared memory beyond 48 KB for a kernel: asked for once a device (`done`: the kernel's own,
-// a bit a device; the call costs a third of a microsecond).
+// a bit a device; the call costs a third of a microsecond; a device reset and a second context keep it).
 inline cudaError_t allow_smem(const void* kern, int bytes, std::atomic<uint64_t>& done) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);

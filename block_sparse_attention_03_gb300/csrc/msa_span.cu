@@ -25,6 +25,8 @@
 // 3 are the launch and the chain lengths - sums - table - rows), 64 spans of 700 to 900 tokens x 8 heads 46 us
 // (87%), 253 ragged ones of up to 200 29 us (68%: items of 55 rows on average, of whose 420 instructions
 // a warp 170 are the item's own; issue slots 69% busy), 32 requests of one token 2.8 us, 8,000 of them 23 us.
+// All of these without growth.  A block that grows has its held codes read and written once the maximum is known: where
+// every block does, 32 requests of one token 11.5 us (a warp moves up to 16 KB), the 253 ragged ones 51, the prompt 5.8.
 // Two rows' copies ahead (48 KB an SM on their way) do as well as three or a ring filled as far
 // as it goes (32 and 38 us for the ragged ones: fewer CTAs, or more to do for each item); rows read twice
 // instead, out of the L2, by teams of one to four warps 34 to 56 us (a block of 128 rows is too long for one).
@@ -387,7 +389,9 @@ __global__ void __launch_bounds__(kSpanThreads, kInsertCtas) block_insert_kernel
 // hold read again for the quotients.
 constexpr int kFewCtas = 4;  // CTAs an SM
 constexpr int kFewHeld = 4;  // rows a thread holds
-// Tokens a span, on average, up to which it is used: where the blocks' items are more than the CTAs of the
+// Tokens a span, on average over all of the call's, empty ones too (the lengths are on the device), up to which it
+// is used, so that a prompt among many empty spans goes through it: 16,384 tokens in one of 512 spans 24 us, by itself 8.5 (4 heads);
+// 2,048 in one of 64 16.3, by itself 3.6.  Spans alike: where the blocks' items are more than the CTAs of the
 // other kernel (256 spans of 16 tokens, 8 items each 5.4 us, the other 7.4; of 32 8.3 and 9.1; of 64 19.5 and
 // 14.6), and where they are not (32 spans of 8 tokens 3.3 us, the other 3.4; of 16 3.9 and 3.5).
 constexpr long kFewTokensMany = 32, kFewTokens = 8;

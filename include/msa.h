@@ -325,6 +325,9 @@ typedef struct {
  *   INT8 and NaN in E4M3.
  * So E4M3 codes of a block that grows move exactly down to E4M3's subnormals, and INT8
  * codes are off by less than one step of the present scale however often it grew.
+ * A scale does not shrink while its block holds tokens: where tokens are written again
+ * (first[s] moved back, as behind a draft that was refused), the scale and the codes that
+ * were rounded for it stay as they became, unless the block's first row is written again too.
  * Rows of a block behind end[s] are left as they were.
  * Flagged on the device and skipped: a span with first < 0 or end beyond
  * max_blocks_per_seq * 128, a span whose rows are not all inside num_tokens, and the
@@ -425,7 +428,8 @@ typedef struct {
  * A cache with block scales: k and v must be NULL (else MSA_ERR_UNSUPPORTED), the
  * queries and index keys are written as ever, and K and V go through msa_block_insert
  * (where there is no index query, the rows of K may take its place: normed with
- * norm->index_q, turned, and written as bf16 rows to index_q_out).
+ * norm->index_q, turned, and written as bf16 rows to index_q_out).  K is rounded to
+ * bf16 on that way (2^-8 of an element), before the block's own rounding.
  * q_out may be q's own memory when q is dense (stride = heads * 128) and bf16.
  * The call writes through q_out's, index_q_out's and the cache's pointers.
  * workspace: at least 256 bytes; only its status word is used. */
